@@ -275,6 +275,120 @@ ffn_status ffn_nvfp4_linear(const void* x, int64_t m, const ffn_nvfp4_weight* w,
 ffn_status ffn_nvfp4_linear_noalloc(const void* x, int64_t m, const ffn_nvfp4_weight* w,
                                     void* y, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Mixture of experts: routing, products by expert, the experts' layer.  The
+ * same NVFP4 weights and bf16 activations; the conventions above hold.
+ * ("metrale_model_layers/layers/mod.rs" names a MoeLayer beside the dense
+ * layer; its body is not on the pages, so the definitions below are this
+ * library's.)
+ * ------------------------------------------------------------------------- */
+#define FFN_MOE_MAX_EXPERTS 1024
+#define FFN_MOE_MAX_TOP_K 32
+#define FFN_MOE_MAX_GROUPS 32
+
+typedef enum ffn_logits_type { FFN_LOGITS_F32 = 0, FFN_LOGITS_BF16 = 1 } ffn_logits_type;
+typedef enum ffn_moe_scoring { FFN_MOE_SOFTMAX = 0, FFN_MOE_SIGMOID = 1 } ffn_moe_scoring;
+typedef enum ffn_moe_group_score {
+  FFN_MOE_GROUP_MAX = 0,  /* a group's best key                               */
+  FFN_MOE_GROUP_TOP2 = 1  /* the sum of its two best keys                     */
+} ffn_moe_group_score;
+
+typedef struct ffn_moe_router {
+  int scoring;      /* ffn_moe_scoring                                        */
+  int top_k;        /* experts per row, 1 .. FFN_MOE_MAX_TOP_K                */
+  int groups;       /* groups of experts / groups consecutive experts; 1: none */
+  int top_groups;   /* groups a row may choose from, 1 .. groups              */
+  int group_score;  /* ffn_moe_group_score                                    */
+  int renormalize;  /* not 0: the weights of a row sum to `scale`             */
+  float scale;      /* factor of every weight; finite                         */
+} ffn_moe_router;
+
+/* The top_k experts of each of m rows and their weights.
+ *   logits   [m, experts] of `type`, row i at i * row_stride elements
+ *            (row_stride >= experts; aligned to one element)
+ *   bias     [experts] fp32 or NULL: added to the scores for the choice only
+ *   ids      int32 [m, top_k] (output), the best expert first
+ *   weights  fp32 [m, top_k] (output)
+ * With s = softmax(logits) or sigmoid(logits) of a row, the choice goes by the
+ * keys s + bias: with groups > 1 the top_groups groups of the highest score
+ * stay open; ids are the top_k open experts of the highest keys, in descending
+ * order, equal keys by the lower id (groups likewise).  weights = scale * s of
+ * the chosen experts, or scale * s / (sum of s over the chosen ones).
+ * The choice is the one that 64-bit arithmetic makes; weights are accurate to
+ * a few fp32 steps.
+ * An expert whose logit is -inf or NaN, or whose key is, is never chosen; where
+ * fewer than top_k are left, the remaining ids are -1 with weight 0 (a row
+ * without any open expert: all of them).  A group's score counts only such
+ * experts as can be chosen.  A row that holds a NaN logit, or a +inf one under
+ * softmax, has NaN for every weight; its ids are still valid or -1.
+ * Errors: FFN_ERR_SHAPE unless groups divides experts and top_k experts fit
+ * into top_groups groups; FFN_ERR_UNSUPPORTED beyond the limits above. */
+ffn_status ffn_nvfp4_moe_route(const void* logits, ffn_logits_type type, int64_t m, int64_t experts,
+                               int64_t row_stride, const float* bias, const ffn_moe_router* router,
+                               int32_t* ids, float* weights, void* stream);
+
+/* Opaque stack of E experts' NVFP4 weights of one projection, [n, k] each:
+ * owns a re-tiled device copy (0.5625 bytes per weight plus tile padding).
+ * Immutable after creation; may be shared by concurrent calls. */
+typedef struct ffn_nvfp4_experts ffn_nvfp4_experts;
+
+/* Build a stack from NVFP4 tensors: codes uint8 [experts, n, k/2], block_scales
+ * uint8 [experts, n, k/16] (layout and meaning as for a single weight),
+ * global_scales fp32 [experts].  With gate_up = 1, n = 2 * inter: rows
+ * [0, inter) of each expert are its gate and rows [inter, 2 * inter) its up
+ * weight, and global_scales is [experts, 2] (gate, up).  Reads the caller's
+ * buffers, which it may free once the stream has run the work; allocates
+ * device memory; the stack is usable by later work on `stream` (other streams:
+ * synchronise first).  Errors: FFN_ERR_SHAPE unless n > 0, k (and inter) are
+ * positive multiples of 32; FFN_ERR_UNSUPPORTED for experts >
+ * FFN_MOE_MAX_EXPERTS. */
+ffn_status ffn_nvfp4_experts_create(const void* codes, const void* block_scales, const float* global_scales,
+                                    int64_t experts, int64_t n, int64_t k, int gate_up, void* stream,
+                                    ffn_nvfp4_experts** out);
+
+/* Release a stack (synchronises the device first).  NULL is accepted. */
+ffn_status ffn_nvfp4_experts_destroy(ffn_nvfp4_experts* w);
+
+/* Dims of a stack and the device bytes it holds (any pointer may be NULL). */
+ffn_status ffn_nvfp4_experts_info(const ffn_nvfp4_experts* w, int64_t* experts, int64_t* n, int64_t* k,
+                                  int* is_gate_up, size_t* device_bytes);
+
+/* Each row through the projections of the experts picked for it:
+ *   y[i, j, :] = bf16(gs_e * sum_k x[i, k] * w_e[:, k]),  e = ids[i, j]
+ *   x    [m, k] bf16;  ids int32 [m, top_k];  y bf16 [m, top_k, n]
+ * w is a plain (not gate and up) stack.  An id outside [0, experts) writes
+ * zeros; equal ids in a row are computed each.  fp32 accumulation; a row's
+ * result does not depend on which other rows share its expert as long as the
+ * same kernels run (they are chosen by m, top_k and the shapes).  m == 0 is a
+ * no-op.  The workspace holds the rows sorted by expert; it may be shared by
+ * calls on one stream.  Errors: FFN_ERR_UNSUPPORTED for a gate and up stack;
+ * FFN_ERR_SHAPE when 2 * m * top_k exceeds 2^31 - 1. */
+ffn_status ffn_nvfp4_experts_workspace_size(int64_t m, int top_k, int64_t experts, int64_t n, int64_t k,
+                                            size_t* bytes);
+ffn_status ffn_nvfp4_experts_linear(const void* x, int64_t m, const ffn_nvfp4_experts* w, const int32_t* ids,
+                                    int top_k, void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The experts' SwiGLU layer and its weighted sum:
+ *   out[i, :] = bf16(sum_j weights[i, j] * down_e(h)),  e = ids[i, j]
+ *   h = bf16(silu(gate_e(x[i])) * up_e(x[i]))
+ *   x [m, hidden] bf16; gate_up a stack of [2 * inter, hidden] built with
+ *   gate_up = 1; down a plain stack of [hidden, inter] of as many experts;
+ *   ids int32 [m, top_k], weights fp32 [m, top_k] (ffn_nvfp4_moe_route's, or
+ *   the caller's); out bf16 [m, hidden], only rows 0 .. m-1 are written.
+ * Numerics: gate, up and the down products stay fp32; h is rounded once, to
+ * bf16 (the down projection's operand), and the sum over j (ascending) once.
+ * (ffn_nvfp4_forward also rounds gate and up, following its source page.)
+ * An id outside [0, experts) contributes weights[i, j] * 0, so padding rows
+ * (all ids -1, weights 0) give zeros.  Deterministic: the same call gives the
+ * same bits.  m == 0 is a no-op.  Allocates nothing and does not synchronise;
+ * the workspace may be shared by calls on one stream. */
+ffn_status ffn_nvfp4_moe_workspace_size(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter,
+                                        size_t* bytes);
+ffn_status ffn_nvfp4_moe_forward(const void* x, int64_t m, int64_t hidden, int64_t inter,
+                                 const ffn_nvfp4_experts* gate_up, const ffn_nvfp4_experts* down,
+                                 const int32_t* ids, const float* weights, int top_k, void* out, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
 /* Kernel configuration a projection of m rows would use (the m-dispatch),
  * without launching anything; callable without a GPU (the SM count of the
  * current device is used when there is one, else 148).  Lets callers and

@@ -1,0 +1,232 @@
+// Mixture-of-experts part of the C ABI: the handle of stacked NVFP4 experts,
+// argument checks, workspace carving and dispatch of ffn_nvfp4_experts_linear
+// and ffn_nvfp4_moe_forward.
+#include <new>
+
+#include "ffn_nvfp4.h"
+#include "internal.h"
+#include "moe.h"
+
+struct ffn_nvfp4_experts {
+  int64_t experts = 0, n = 0, k = 0;
+  int gate_up = 0;
+  int device = 0;
+  size_t bytes = 0;
+  uint8_t* tiles = nullptr;
+  float* gs = nullptr;
+  ffn::ExpertsView view() const {
+    ffn::ExpertsView v;
+    v.tiles = tiles;
+    v.gs = gs;
+    v.experts = (int)experts;
+    v.wtiles = (int)(gate_up ? (n / 2 + 63) / 64 : (n + 127) / 128);
+    v.kc = (int)((k + 63) / 64);
+    v.n = n;
+    v.k = k;
+    v.gate_up = gate_up != 0;
+    return v;
+  }
+};
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+bool valid_k(int64_t k) { return k > 0 && k % 32 == 0; }
+
+ffn_status check_device(const ffn_nvfp4_experts* w) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return FFN_ERR_CUDA;
+  }
+  return dev == w->device ? FFN_OK : FFN_ERR_INVALID_ARG;
+}
+
+// m * top_k pairs must fit an int, and so must the rows of every product.
+bool valid_pairs(int64_t m, int top_k) { return m <= (int64_t)INT32_MAX / 2 / top_k; }
+
+struct Carve {
+  size_t offsets = 0, order = 0, tiles = 0, h = 0, y = 0, total = 0;
+};
+
+size_t take(size_t& off, size_t bytes) {
+  const size_t at = off;
+  off += round_up(bytes, 256);
+  return at;
+}
+
+// inter = 0: one projection, whose output is the caller's.
+Carve carve(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter) {
+  Carve c;
+  const int64_t pairs = m * top_k;
+  if (pairs == 0) return c;
+  size_t off = 0;
+  c.offsets = take(off, sizeof(int) * (experts + 1));
+  c.order = take(off, sizeof(int) * pairs);
+  c.tiles = take(off, sizeof(int) * (1 + 3 * ffn::moe_max_tiles(pairs, experts, ffn::kRowsTile)));
+  if (inter > 0) {
+    c.h = take(off, (size_t)pairs * inter * 2);
+    c.y = take(off, (size_t)pairs * hidden * 4);
+  }
+  c.total = off;
+  return c;
+}
+
+ffn::MoePlan plan_at(uint8_t* ws, const Carve& c) {
+  ffn::MoePlan p;
+  p.offsets = reinterpret_cast<int*>(ws + c.offsets);
+  p.order = reinterpret_cast<int*>(ws + c.order);
+  p.tiles = reinterpret_cast<int*>(ws + c.tiles);
+  return p;
+}
+
+void free_experts(ffn_nvfp4_experts* w) {
+  if (!w) return;
+  cudaFree(w->tiles);
+  cudaFree(w->gs);
+  delete w;
+}
+
+}  // namespace
+
+extern "C" {
+
+ffn_status ffn_nvfp4_experts_create(const void* codes, const void* block_scales, const float* global_scales,
+                                    int64_t experts, int64_t n, int64_t k, int gate_up, void* stream,
+                                    ffn_nvfp4_experts** out) {
+  if (!out) return FFN_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!codes || !block_scales || !global_scales || (gate_up != 0 && gate_up != 1)) return FFN_ERR_INVALID_ARG;
+  if (experts < 1 || n < 1 || !valid_k(k) || (gate_up && n % 2)) return FFN_ERR_SHAPE;
+  if (gate_up && (n / 2) % 32) return FFN_ERR_SHAPE;  // inter is the down projection's K
+  if (experts > FFN_MOE_MAX_EXPERTS) return FFN_ERR_UNSUPPORTED;
+  if (n > INT32_MAX / 2 || k > INT32_MAX / 2) return FFN_ERR_SHAPE;
+  if (!aligned16(codes) || !aligned16(block_scales) || !aligned4(global_scales)) return FFN_ERR_ALIGNMENT;
+  if (ffn_status st = ffn::moe_precheck()) return st;
+  auto* w = new (std::nothrow) ffn_nvfp4_experts;
+  if (!w) return FFN_ERR_OOM;
+  w->experts = experts;
+  w->n = n;
+  w->k = k;
+  w->gate_up = gate_up;
+  const size_t tile_bytes = (size_t)ffn::tc_tiled_bytes(n, k, gate_up != 0);
+  const size_t gs_bytes = sizeof(float) * experts * (gate_up ? 2 : 1);
+  w->bytes = tile_bytes * experts + gs_bytes;
+  if (cudaGetDevice(&w->device) != cudaSuccess) {
+    delete w;
+    cudaGetLastError();
+    return FFN_ERR_CUDA;
+  }
+  if (cudaMalloc(reinterpret_cast<void**>(&w->tiles), tile_bytes * experts) != cudaSuccess ||
+      cudaMalloc(reinterpret_cast<void**>(&w->gs), gs_bytes) != cudaSuccess) {
+    cudaGetLastError();
+    free_experts(w);
+    return FFN_ERR_OOM;
+  }
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(w->gs, global_scales, gs_bytes, cudaMemcpyDeviceToDevice, s);
+  for (int64_t i = 0; e == cudaSuccess && i < experts; ++i)
+    e = ffn::launch_tile_weight(static_cast<const uint8_t*>(codes) + i * n * (k / 2),
+                                static_cast<const uint8_t*>(block_scales) + i * n * (k / 16), n, k, gate_up != 0,
+                                true, w->tiles + i * tile_bytes, s);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    free_experts(w);
+    return FFN_ERR_CUDA;
+  }
+  *out = w;
+  return FFN_OK;
+}
+
+ffn_status ffn_nvfp4_experts_destroy(ffn_nvfp4_experts* w) {
+  if (!w) return FFN_OK;
+  const cudaError_t e = cudaDeviceSynchronize();
+  free_experts(w);
+  return e == cudaSuccess ? FFN_OK : FFN_ERR_CUDA;
+}
+
+ffn_status ffn_nvfp4_experts_info(const ffn_nvfp4_experts* w, int64_t* experts, int64_t* n, int64_t* k,
+                                  int* is_gate_up, size_t* device_bytes) {
+  if (!w) return FFN_ERR_INVALID_ARG;
+  if (experts) *experts = w->experts;
+  if (n) *n = w->n;
+  if (k) *k = w->k;
+  if (is_gate_up) *is_gate_up = w->gate_up;
+  if (device_bytes) *device_bytes = w->bytes;
+  return FFN_OK;
+}
+
+ffn_status ffn_nvfp4_experts_workspace_size(int64_t m, int top_k, int64_t experts, int64_t n, int64_t k,
+                                            size_t* bytes) {
+  if (!bytes || m < 0 || top_k < 1 || experts < 1 || n < 1) return FFN_ERR_INVALID_ARG;
+  if (!valid_k(k) || !valid_pairs(m, top_k)) return FFN_ERR_SHAPE;
+  *bytes = carve(m, top_k, experts, n, 0).total;
+  return FFN_OK;
+}
+
+ffn_status ffn_nvfp4_experts_linear(const void* x, int64_t m, const ffn_nvfp4_experts* w, const int32_t* ids,
+                                    int top_k, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  if (m < 0 || !w || top_k < 1) return FFN_ERR_INVALID_ARG;
+  if (w->gate_up) return FFN_ERR_UNSUPPORTED;
+  if (!valid_pairs(m, top_k)) return FFN_ERR_SHAPE;
+  if (m == 0) return FFN_OK;
+  if (!x || !ids || !y) return FFN_ERR_INVALID_ARG;
+  if (ffn_status st = check_device(w)) return st;
+  const Carve c = carve(m, top_k, w->experts, w->n, 0);
+  if (!workspace || workspace_bytes < c.total) return FFN_ERR_WORKSPACE;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(workspace) || !aligned4(ids)) return FFN_ERR_ALIGNMENT;
+  if (ffn_status st = ffn::moe_precheck()) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const ffn::ExpertsView v = w->view();
+  const ffn::MoePlan p = plan_at(static_cast<uint8_t*>(workspace), c);
+  const int64_t pairs = m * top_k;
+  cudaError_t e = ffn::launch_moe_plan(ids, pairs, v.experts, ffn::kRowsTile, p, s);
+  if (e == cudaSuccess) e = ffn::launch_experts_rows(x, top_k, v, p, pairs, ffn::ExpertsOut::kBf16, y, s);
+  if (e == cudaSuccess) e = ffn::launch_experts_zero(ids, pairs, v.experts, v.n, y, s);
+  return ffn::moe_status(e);
+}
+
+ffn_status ffn_nvfp4_moe_workspace_size(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter,
+                                        size_t* bytes) {
+  if (!bytes || m < 0 || top_k < 1 || experts < 1) return FFN_ERR_INVALID_ARG;
+  if (!valid_k(hidden) || !valid_k(inter) || !valid_pairs(m, top_k)) return FFN_ERR_SHAPE;
+  *bytes = carve(m, top_k, experts, hidden, inter).total;
+  return FFN_OK;
+}
+
+ffn_status ffn_nvfp4_moe_forward(const void* x, int64_t m, int64_t hidden, int64_t inter,
+                                 const ffn_nvfp4_experts* gate_up, const ffn_nvfp4_experts* down,
+                                 const int32_t* ids, const float* weights, int top_k, void* out, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (m < 0 || !gate_up || !down || top_k < 1) return FFN_ERR_INVALID_ARG;
+  if (!valid_k(hidden) || !valid_k(inter)) return FFN_ERR_SHAPE;
+  if (!gate_up->gate_up || down->gate_up) return FFN_ERR_INVALID_ARG;
+  if (gate_up->n != 2 * inter || gate_up->k != hidden || down->n != hidden || down->k != inter ||
+      gate_up->experts != down->experts || !valid_pairs(m, top_k))
+    return FFN_ERR_SHAPE;
+  if (m == 0) return FFN_OK;
+  if (!x || !ids || !weights || !out) return FFN_ERR_INVALID_ARG;
+  if (ffn_status st = check_device(gate_up)) return st;
+  if (ffn_status st = check_device(down)) return st;
+  const Carve c = carve(m, top_k, down->experts, hidden, inter);
+  if (!workspace || workspace_bytes < c.total) return FFN_ERR_WORKSPACE;
+  if (!aligned16(x) || !aligned16(out) || !aligned16(workspace) || !aligned4(ids) || !aligned4(weights))
+    return FFN_ERR_ALIGNMENT;
+  if (ffn_status st = ffn::moe_precheck()) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const ffn::ExpertsView gu = gate_up->view(), dn = down->view();
+  const ffn::MoePlan p = plan_at(ws, c);
+  const int64_t pairs = m * top_k;
+  cudaError_t e = ffn::launch_moe_plan(ids, pairs, dn.experts, ffn::kRowsTile, p, s);
+  if (e == cudaSuccess) e = ffn::launch_experts_rows(x, top_k, gu, p, pairs, ffn::ExpertsOut::kSiluMul, ws + c.h, s);
+  if (e == cudaSuccess) e = ffn::launch_experts_rows(ws + c.h, 1, dn, p, pairs, ffn::ExpertsOut::kF32, ws + c.y, s);
+  if (e == cudaSuccess)
+    e = ffn::launch_moe_combine(reinterpret_cast<const float*>(ws + c.y), ids, weights, m, top_k, dn.experts, hidden,
+                                out, s);
+  return ffn::moe_status(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,64 @@
+// Host-side declarations of the mixture-of-experts operators (routing,
+// products by expert, the experts' layer).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ffn_nvfp4.h"
+
+namespace ffn {
+
+inline ffn_status moe_status(cudaError_t e) {
+  if (e == cudaSuccess) return FFN_OK;
+  cudaGetLastError();
+  return FFN_ERR_CUDA;
+}
+
+// Pick up errors of earlier asynchronous work before enqueuing more.
+inline ffn_status moe_precheck() { return moe_status(cudaPeekAtLastError()); }
+
+// Stacked experts as the kernels read them: E times the 128-row x 64-element
+// tiles of the bf16 activation format (launch_tile_weight with for_w4a16).
+struct ExpertsView {
+  const uint8_t* tiles = nullptr;  // [E][wtiles][kc][4608]
+  const float* gs = nullptr;       // [E], or [E][2] (gate, up)
+  int experts = 0, wtiles = 0, kc = 0;
+  int64_t n = 0, k = 0;            // logical dims (n = 2 * inter for gate and up)
+  bool gate_up = false;
+};
+
+// Which rows go to which expert, for pairs p = row * top_k + slot with an id
+// in [0, E): device arrays in the caller's workspace.
+struct MoePlan {
+  int* offsets;  // [E + 1]: expert e owns order[offsets[e] .. offsets[e + 1])
+  int* order;    // [pairs]: the pairs, expert by expert
+  int* tiles;    // [0]: number of tiles; then per tile {expert, first, rows}
+};
+
+// Most tiles of `rows` rows that `pairs` pairs over E experts can fill.
+inline int64_t moe_max_tiles(int64_t pairs, int64_t experts, int rows) {
+  return pairs / rows + (pairs < experts ? pairs : experts);
+}
+
+cudaError_t launch_moe_plan(const int32_t* ids, int64_t pairs, int experts, int tile_rows, const MoePlan& p,
+                            cudaStream_t s);
+
+enum class ExpertsOut : int {
+  kBf16 = 0,     // y[p, :] = bf16(gs * acc)
+  kSiluMul = 1,  // h[p, :] = bf16(silu(g) * u), gate and up weights
+  kF32 = 2       // y[p, :] = gs * acc, fp32
+};
+
+// Products of few rows per expert: row p of the input is x[p / row_div].
+cudaError_t launch_experts_rows(const void* x, int row_div, const ExpertsView& w, const MoePlan& p, int64_t pairs,
+                                ExpertsOut mode, void* out, cudaStream_t s);
+// out[i, :] = bf16(sum_j weights[i, j] * y[i * top_k + j, :]), j ascending.
+cudaError_t launch_moe_combine(const float* y, const int32_t* ids, const float* weights, int64_t m, int top_k,
+                               int experts, int64_t hidden, void* out, cudaStream_t s);
+// Rows of y [pairs, n] bf16 whose id is outside [0, E): zeros.
+cudaError_t launch_experts_zero(const int32_t* ids, int64_t pairs, int experts, int64_t n, void* y, cudaStream_t s);
+
+constexpr int kRowsTile = 8;  // rows of one expert that launch_experts_rows takes at a time
+
+}  // namespace ffn

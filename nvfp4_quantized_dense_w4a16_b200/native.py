@@ -43,6 +43,17 @@ KERNEL_FAMILIES = {0: "none", 1: "tc_w4a16", 2: "tc_w4a4", 3: "gemv_w4a16", 4: "
 ROLES = {"linear": 0, "gate_up": 1, "down": 2}
 
 
+class MoeRouter(ctypes.Structure):
+    _fields_ = [("scoring", ctypes.c_int), ("top_k", ctypes.c_int), ("groups", ctypes.c_int),
+                ("top_groups", ctypes.c_int), ("group_score", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+MOE_SCORINGS = {"softmax": 0, "sigmoid": 1}
+MOE_GROUP_SCORES = {"max": 0, "top2": 1}
+_LOGITS_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
 class KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("launches", ctypes.c_int), ("total_ms", ctypes.c_double)]
 
@@ -79,6 +90,14 @@ def _load() -> ctypes.CDLL:
                                                      P(ProjectionPlan)]),
         "ffn_nvfp4_tensor_peak": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                  P(ctypes.c_double)]),
+        "ffn_nvfp4_moe_route": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, P(MoeRouter), vp, vp, vp]),
+        "ffn_nvfp4_experts_create": (ctypes.c_int, [vp, vp, vp, i64, i64, i64, ctypes.c_int, vp, P(vp)]),
+        "ffn_nvfp4_experts_destroy": (ctypes.c_int, [vp]),
+        "ffn_nvfp4_experts_info": (ctypes.c_int, [vp, P(i64), P(i64), P(i64), P(ctypes.c_int), P(sz)]),
+        "ffn_nvfp4_experts_workspace_size": (ctypes.c_int, [i64, ctypes.c_int, i64, i64, i64, P(sz)]),
+        "ffn_nvfp4_experts_linear": (ctypes.c_int, [vp, i64, vp, vp, ctypes.c_int, vp, vp, sz, vp]),
+        "ffn_nvfp4_moe_workspace_size": (ctypes.c_int, [i64, ctypes.c_int, i64, i64, i64, P(sz)]),
+        "ffn_nvfp4_moe_forward": (ctypes.c_int, [vp, i64, i64, i64, vp, vp, vp, vp, ctypes.c_int, vp, vp, sz, vp]),
         "ffn_nvfp4_profile_begin": (ctypes.c_int, []),
         "ffn_nvfp4_device_error": (ctypes.c_int, [P(ctypes.c_int), ctypes.c_int]),
         "ffn_nvfp4_profile_end": (ctypes.c_int, [P(KernelTime), ctypes.c_int, P(ctypes.c_int)]),
@@ -327,6 +346,144 @@ def ffn_nvfp4_linear(x: torch.Tensor, w: Weight, fmt="bf16", y=None, workspace=N
         _ptr(x), m, w.handle, _fmt(fmt), _ptr(y), _ptr(workspace), workspace.numel(),
         _stream(stream)))
     return y
+
+
+def ffn_nvfp4_moe_route(logits: torch.Tensor, top_k: int, scoring="softmax", bias=None, groups: int = 1,
+                        top_groups: int = 1, group_score="max", renormalize: bool = True, scale: float = 1.0,
+                        ids=None, weights=None, stream=None):
+    """[m, experts] float32 or bfloat16 logits -> (ids int32 [m, top_k], weights float32 [m, top_k]).
+    The rows may be strided (a slice of wider rows), each row contiguous."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor (the library has no CPU path)")
+    if logits.dtype not in _LOGITS_TYPES:
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    m, experts = logits.shape
+    ld, step = logits.stride()
+    if experts > 1 and step != 1 or m > 1 and ld < experts:
+        raise ValueError("logits must have contiguous, non-overlapping rows")
+    dev = logits.device
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (experts,))
+    ids = torch.empty((m, top_k), dtype=torch.int32, device=dev) if ids is None else ids
+    weights = torch.empty((m, top_k), dtype=torch.float32, device=dev) if weights is None else weights
+    _need(ids, "ids", torch.int32, (m, top_k))
+    _need(weights, "weights", torch.float32, (m, top_k))
+    router = MoeRouter(MOE_SCORINGS[scoring], top_k, groups, top_groups, MOE_GROUP_SCORES[group_score],
+                       int(renormalize), scale)
+    _check("ffn_nvfp4_moe_route", lib.ffn_nvfp4_moe_route(
+        logits.data_ptr(), _LOGITS_TYPES[logits.dtype], m, experts, ld if m > 1 else max(ld, experts),
+        None if bias is None else bias.data_ptr(), ctypes.byref(router), ids.data_ptr(), weights.data_ptr(),
+        _stream(stream)))
+    return ids, weights
+
+
+class Experts:
+    """Owning wrapper of an ``ffn_nvfp4_experts*`` stack."""
+
+    def __init__(self, handle: ctypes.c_void_p):
+        self._h = handle
+        e, n, k = ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int64()
+        gu, b = ctypes.c_int(), ctypes.c_size_t()
+        _check("ffn_nvfp4_experts_info", lib.ffn_nvfp4_experts_info(
+            self._h, ctypes.byref(e), ctypes.byref(n), ctypes.byref(k), ctypes.byref(gu), ctypes.byref(b)))
+        self.experts, self.n, self.k, self.is_gate_up = e.value, n.value, k.value, bool(gu.value)
+        self.device_bytes = b.value
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if self._h:
+            _check("ffn_nvfp4_experts_destroy", lib.ffn_nvfp4_experts_destroy(self._h))
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def ffn_nvfp4_experts_create(codes: torch.Tensor, block_scales: torch.Tensor, global_scales: torch.Tensor,
+                             gate_up: bool = False, stream=None) -> Experts:
+    """Stack of experts from codes uint8 [E, n, k/2], block_scales uint8 [E, n, k/16] and global_scales
+    float32 of E values; with gate_up, n = 2 * inter (gate rows, then up rows) and 2 * E values [E, 2]."""
+    _need(codes, "codes", torch.uint8)
+    e, n, half_k = codes.shape
+    k = 2 * half_k
+    _need(block_scales, "block_scales", torch.uint8, (e, n, k // 16))
+    _need(global_scales, "global_scales", torch.float32)
+    if gate_up and tuple(global_scales.shape) != (e, 2) or not gate_up and global_scales.numel() != e:
+        raise ValueError(f"global_scales must hold {'[E, 2]' if gate_up else 'E'} values for {e} experts, "
+                         f"got shape {tuple(global_scales.shape)}")
+    h = ctypes.c_void_p()
+    _check("ffn_nvfp4_experts_create", lib.ffn_nvfp4_experts_create(
+        _ptr(codes), _ptr(block_scales), _ptr(global_scales), e, n, k, int(gate_up), _stream(stream),
+        ctypes.byref(h)))
+    return Experts(h)
+
+
+def ffn_nvfp4_experts_workspace_size(m: int, top_k: int, experts: int, n: int, k: int) -> int:
+    out = ctypes.c_size_t()
+    _check("ffn_nvfp4_experts_workspace_size", lib.ffn_nvfp4_experts_workspace_size(
+        m, top_k, experts, n, k, ctypes.byref(out)))
+    return out.value
+
+
+def ffn_nvfp4_moe_workspace_size(m: int, top_k: int, experts: int, hidden: int, inter: int) -> int:
+    out = ctypes.c_size_t()
+    _check("ffn_nvfp4_moe_workspace_size", lib.ffn_nvfp4_moe_workspace_size(
+        m, top_k, experts, hidden, inter, ctypes.byref(out)))
+    return out.value
+
+
+def ffn_nvfp4_experts_linear(x: torch.Tensor, w: Experts, ids: torch.Tensor, y=None, workspace=None,
+                             stream=None) -> torch.Tensor:
+    """y[m, top_k, n]: row i of x through the weight of every expert in ids[i] (zeros for ids outside the stack)."""
+    _need(x, "x", torch.bfloat16)
+    m, k = x.shape
+    if k != w.k:
+        raise ValueError(f"x has {k} columns, the experts expect {w.k}")
+    _need(ids, "ids", torch.int32)
+    if ids.dim() != 2 or ids.shape[0] != m:
+        raise ValueError(f"ids must have shape ({m}, top_k), got {tuple(ids.shape)}")
+    top_k = ids.shape[1]
+    y = torch.empty((m, top_k, w.n), dtype=torch.bfloat16, device=x.device) if y is None else y
+    _need(y, "y", torch.bfloat16, (m, top_k, w.n))
+    if workspace is None:
+        workspace = _workspace(ffn_nvfp4_experts_workspace_size(m, top_k, w.experts, w.n, k), x.device, None)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    _check("ffn_nvfp4_experts_linear", lib.ffn_nvfp4_experts_linear(
+        x.data_ptr(), m, w.handle, ids.data_ptr(), top_k, y.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _stream(stream)))
+    return y
+
+
+def ffn_nvfp4_moe_forward(x: torch.Tensor, gate_up: Experts, down: Experts, ids: torch.Tensor,
+                          weights: torch.Tensor, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """out[m, hidden] = sum over j of weights[:, j] * down_e(silu(gate_e(x)) * up_e(x)), e = ids[:, j]."""
+    _need(x, "x", torch.bfloat16)
+    m, hidden = x.shape
+    _need(ids, "ids", torch.int32)
+    if ids.dim() != 2 or ids.shape[0] != m:
+        raise ValueError(f"ids must have shape ({m}, top_k), got {tuple(ids.shape)}")
+    top_k = ids.shape[1]
+    _need(weights, "weights", torch.float32, (m, top_k))
+    out = torch.empty((m, hidden), dtype=torch.bfloat16, device=x.device) if out is None else out
+    _need(out, "out", torch.bfloat16, (m, hidden))
+    inter = down.k
+    if workspace is None:
+        workspace = _workspace(ffn_nvfp4_moe_workspace_size(m, top_k, down.experts, hidden, inter), x.device, None)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    _check("ffn_nvfp4_moe_forward", lib.ffn_nvfp4_moe_forward(
+        x.data_ptr(), m, hidden, inter, gate_up.handle, down.handle, ids.data_ptr(), weights.data_ptr(), top_k,
+        out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return out
 
 
 def ffn_nvfp4_profile_begin():

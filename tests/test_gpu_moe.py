@@ -1,0 +1,471 @@
+"""Mixture of experts on the GPU against the fp64 oracle: routing decisions and
+weights, products by expert, the layer, and the three of them together."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import moe as M
+from oracle import nvfp4_ffn as O
+from nvfp4_quantized_dense_w4a16_b200 import synth
+
+pytestmark = pytest.mark.gpu
+
+from gpu_helpers import bf16_to_f64, to_dev_bf16
+
+
+@pytest.fixture(scope="module")
+def native():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from nvfp4_quantized_dense_w4a16_b200 import build
+    build.build()
+    from nvfp4_quantized_dense_w4a16_b200 import native as N
+    return N
+
+
+@pytest.fixture(autouse=True)
+def no_device_error(native):
+    yield
+    torch.cuda.synchronize()
+    assert native.ffn_nvfp4_device_error(clear=False) == 0
+
+
+# ------------------------------------------------------------------- routing
+
+def check_route(native, logits, bias=None, dtype=torch.float32, **kw):
+    """Ids equal the oracle's, weights within their rounding.
+
+    Tolerance of a weight, in half steps of fp32 (2^-24 relative): exp in fp32
+    of a rounded difference l - max costs |d| e^d <= 1/e of a half step of the
+    sum and 4 for the function, the tree of the sum E/32 + 5 additions, the
+    quotient, the scale and the last rounding 3: E/32 + 13.
+    """
+    l = torch.as_tensor(np.asarray(logits, dtype=np.float32)).to(dtype)
+    b = None if bias is None else torch.as_tensor(np.asarray(bias, dtype=np.float32))
+    ids, w = native.ffn_nvfp4_moe_route(l.cuda(), bias=None if b is None else b.cuda(), **kw)
+    torch.cuda.synchronize()
+    rid, rw = M.route(l.double().numpy(), None if b is None else b.double().numpy(), **kw)
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    got = w.double().cpu().numpy()
+    tol = (l.shape[1] / 32 + 13) * 2.0 ** -24
+    assert np.all(np.abs(got - rw) <= tol * np.abs(rw) + 2.0 ** -149), np.max(np.abs(got - rw) / np.maximum(np.abs(rw), 1e-300))
+    return ids, w
+
+
+@pytest.mark.parametrize("m,experts,kw", [
+    (1, 1, dict(top_k=1)),
+    (1, 64, dict(top_k=8)),
+    (5, 31, dict(top_k=31)),
+    (37, 33, dict(top_k=5, scoring="sigmoid", renormalize=False, scale=2.5)),
+    (64, 128, dict(top_k=8, renormalize=False)),
+    (70, 160, dict(top_k=6, groups=8, top_groups=3, group_score="max")),
+    (129, 256, dict(top_k=8, scoring="sigmoid", groups=8, top_groups=4, group_score="top2", scale=2.5)),
+    (33, 96, dict(top_k=4, groups=32, top_groups=2, group_score="top2")),
+    (9, 257, dict(top_k=32, scoring="sigmoid")),
+    (3, 1024, dict(top_k=32)),
+])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_route_matches_oracle(native, m, experts, kw, dtype, with_bias):
+    rng = np.random.default_rng(1000 + m + experts)
+    logits = 2.0 * rng.standard_normal((m, experts))
+    bias = 0.1 * rng.standard_normal(experts) if with_bias else None
+    check_route(native, logits, bias, dtype, **kw)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_ties_go_to_the_lowest_id(native, scoring):
+    rng = np.random.default_rng(7)
+    logits = rng.integers(-2, 3, (64, 96)).astype(np.float64)  # many equal logits
+    check_route(native, logits, None, top_k=9, scoring=scoring)
+    check_route(native, logits, np.zeros(96), top_k=9, scoring=scoring, groups=6, top_groups=2, group_score="top2")
+    check_route(native, np.zeros((3, 64)), None, top_k=8, scoring=scoring, groups=4, top_groups=2)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_decides_as_64_bits(native, scoring):
+    """Keys a few fp32 steps apart, or less than one: the bias cancels the score up to a remainder."""
+    rng = np.random.default_rng(8)
+    experts = 64
+    logits = np.sort(rng.standard_normal((256, experts)).astype(np.float32), axis=1)
+    score = np.exp(M.log_score(logits[0], scoring))
+    bias = (1.0 - score).astype(np.float32)  # row 0: all keys within 2^-24 of one another
+    logits[1:128] = logits[0]
+    step = np.float32(2.0 ** -23)
+    logits[1:64] *= 1 + step * rng.integers(-1, 2, (63, experts)).astype(np.float32)
+    check_route(native, logits, bias, top_k=8, scoring=scoring)
+    check_route(native, logits, bias, top_k=6, scoring=scoring, groups=8, top_groups=3, group_score="top2")
+    check_route(native, logits, bias, top_k=6, scoring=scoring, groups=8, top_groups=3, group_score="max")
+    # sigmoids that round to one in fp32
+    big = rng.uniform(15.0, 22.0, (64, experts)).astype(np.float32)
+    check_route(native, big, None, top_k=8, scoring=scoring)
+    check_route(native, big, np.zeros(experts), top_k=8, scoring=scoring, groups=4, top_groups=2, group_score="top2")
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_route_masked_experts(native, scoring, groups):
+    rng = np.random.default_rng(9)
+    logits = rng.standard_normal((40, 32))
+    logits[rng.random((40, 32)) < 0.85] = -np.inf
+    logits[0] = -np.inf
+    logits[1] = -np.inf
+    logits[1, 17] = 0.5
+    logits[2] = np.finfo(np.float32).min
+    logits[3, :] = -np.inf
+    logits[3, :8] = -200.0 - np.arange(8)  # scores that underflow keep their ratio
+    kw = dict(top_k=6, scoring=scoring, groups=groups, top_groups=max(1, groups // 2), group_score="top2")
+    check_route(native, logits, None, **kw)
+    bias = 0.1 * rng.standard_normal(32)
+    bias[5] = -np.inf
+    check_route(native, logits, bias, **kw)
+    check_route(native, logits, None, renormalize=False, **kw)
+
+
+def test_route_non_finite_rows(native):
+    logits = np.random.default_rng(10).standard_normal((6, 40)).astype(np.float32)
+    logits[1, 3] = np.nan
+    logits[2] = np.nan
+    logits[4, 7] = np.inf
+    for scoring in ("softmax", "sigmoid"):
+        ids, w = native.ffn_nvfp4_moe_route(torch.from_numpy(logits).cuda(), 4, scoring=scoring)
+        ids, w = ids.cpu().numpy(), w.cpu().numpy()
+        bad = [1, 2, 4] if scoring == "softmax" else [1, 2]
+        for i in range(6):
+            assert np.all(np.isnan(w[i])) if i in bad else np.all(np.isfinite(w[i]))
+        assert ids[2].tolist() == [-1] * 4 and 3 not in ids[1] and ids[4, 0] == 7
+        good = [i for i in range(6) if i not in bad]
+        rid, _ = M.route(logits[good].astype(np.float64), None, 4, scoring=scoring)
+        assert np.array_equal(ids[good], rid)
+    nan_bias = np.zeros(32, np.float32)
+    nan_bias[11] = np.nan
+    ids, w = native.ffn_nvfp4_moe_route(torch.from_numpy(logits[:1, :32]).cuda(), 32, bias=torch.from_numpy(nan_bias).cuda())
+    assert 11 not in ids.cpu().numpy() and ids[0, 31].item() == -1 and bool(torch.isfinite(w).all())
+
+
+def test_route_strided_rows_and_streams(native):
+    wide = torch.randn((50, 200), generator=torch.Generator().manual_seed(3))
+    part = wide.cuda()[:, 3:67]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ids, w = native.ffn_nvfp4_moe_route(part, 8, stream=s)
+    s.synchronize()
+    rid, _ = M.route(wide[:, 3:67].double().numpy(), None, 8)
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    empty = native.ffn_nvfp4_moe_route(part[:0], 8)
+    assert empty[0].shape == (0, 8)
+
+
+def test_route_refusals(native):
+    l = torch.zeros((4, 32), device="cuda")
+    with pytest.raises(TypeError):
+        native.ffn_nvfp4_moe_route(l.half(), 4)
+    with pytest.raises(ValueError):
+        native.ffn_nvfp4_moe_route(l.cpu(), 4)
+    with pytest.raises(ValueError):
+        native.ffn_nvfp4_moe_route(l.t(), 4)
+    with pytest.raises(ValueError):
+        native.ffn_nvfp4_moe_route(l, 4, bias=torch.zeros(31, device="cuda"))
+    with pytest.raises(native.FfnError) as e:
+        native.ffn_nvfp4_moe_route(l, 33)
+    assert e.value.status_name == "FFN_ERR_SHAPE"
+
+
+# ------------------------------------------------------------ experts' products
+
+class Stack:
+    """Random NVFP4 experts on both sides: any code, scales over several binades (some zero), tensor scales."""
+
+    def __init__(self, native, experts, n, k, seed, gate_up=False):
+        rng = np.random.default_rng(seed)
+        codes = rng.integers(0, 256, (experts, n, k // 2), dtype=np.uint8)
+        scales = rng.integers(0x28, 0x48, (experts, n, k // 16), dtype=np.uint8)
+        scales[rng.random(scales.shape) < 0.02] = 0
+        parts = 2 if gate_up else 1
+        gs = (rng.uniform(0.5, 2.0, (experts, parts)) / (5.0 * np.sqrt(k))).astype(np.float32)
+        self.w = M.experts_dequant(codes, scales, gs)
+        dev = lambda a: torch.from_numpy(a).cuda()
+        self.handle = native.ffn_nvfp4_experts_create(dev(codes), dev(scales), dev(gs if gate_up else gs[:, 0].copy()),
+                                                      gate_up=gate_up)
+
+
+def rows(m, k, seed):
+    bits = synth.random_bf16((m, k), seed)
+    return to_dev_bf16(bits), synth.bf16_bits_to_f32(bits).astype(np.float64)
+
+
+def pick(rng, m, experts, top_k, padding=0.0, favourite=None):
+    ids = np.stack([rng.choice(experts, top_k, replace=False) for _ in range(m)]).astype(np.int32) if m else np.zeros((0, top_k), np.int32)
+    if favourite is not None:
+        ids[:, 0] = favourite
+    ids[rng.random(m) < padding] = -1
+    return ids
+
+
+def sum_error(k):
+    """Relative error of a product's fp32 sum to the sum of the terms' magnitudes.
+
+    The terms (8-bit times 6-bit significands) are exact; the tensor core adds 16 (or 64) at a time, each such step
+    losing at most one step of fp32 in alignment and one in rounding (2^-22 together); the partial sums of at most 64
+    ranges of K, the tensor scale and its product add 66 half steps."""
+    return (k / 16 + 33) * 2.0 ** -22
+
+
+HALF = 2.0 ** -8  # half a step of bf16, relative
+
+
+def check_linear(native, stack, x, x64, ids, **kw):
+    y = native.ffn_nvfp4_experts_linear(x, stack.handle, torch.from_numpy(ids).cuda(), **kw)
+    torch.cuda.synchronize()
+    ref = M.experts_linear(x64, stack.w, ids)
+    tol = sum_error(x64.shape[1]) * M.experts_linear(np.abs(x64), np.abs(stack.w), ids)
+    got = bf16_to_f64(y)
+    err = np.abs(got - ref)
+    bound = HALF * np.abs(ref) + (1 + HALF) * tol + 2.0 ** -133
+    assert np.all(err <= bound), (float((err / np.maximum(bound, 1e-300)).max()), np.unravel_index(np.argmax(err - bound), err.shape))
+    return y
+
+
+@pytest.mark.parametrize("m,experts,top_k,n,k,padding", [
+    (1, 1, 1, 8, 32, 0.0), (1, 4, 4, 128, 64, 0.0), (1, 8, 2, 200, 96, 0.0), (2, 5, 3, 129, 160, 0.0),
+    (9, 3, 2, 64, 1056, 0.3), (17, 20, 3, 1000, 256, 0.1), (40, 2, 2, 384, 512, 0.0), (70, 6, 1, 33, 128, 0.2),
+    (130, 3, 2, 256, 320, 0.1), (300, 2, 1, 136, 2048, 0.0), (600, 7, 4, 128, 192, 0.05),
+])
+def test_linear_matches_oracle(native, m, experts, top_k, n, k, padding):
+    rng = np.random.default_rng(2000 + m)
+    s = Stack(native, experts, n, k, 2100 + m)
+    x, x64 = rows(m, k, 2200 + m)
+    check_linear(native, s, x, x64, pick(rng, m, experts, top_k, padding))
+
+
+@pytest.mark.parametrize("m", [1, 5, 64, 300])
+def test_linear_uneven_experts(native, m):
+    """All rows at one expert, none at most others; ids outside the stack; the same id twice in a row."""
+    s = Stack(native, 9, 144, 224, 31)
+    x, x64 = rows(m, 224, 32)
+    ids = np.full((m, 3), 6, np.int32)
+    check_linear(native, s, x, x64, ids)
+    ids[:, 1] = 9
+    ids[:, 2] = -2**31
+    check_linear(native, s, x, x64, ids)
+    none = torch.full((m, 3), -1, dtype=torch.int32, device="cuda")
+    y = torch.full((m, 3, 144), float("nan"), dtype=torch.bfloat16, device="cuda")
+    native.ffn_nvfp4_experts_linear(x, s.handle, none, y=y)
+    assert int(torch.count_nonzero(y.view(torch.int16))) == 0
+
+
+def test_linear_exact_integers(native):
+    """Small whole numbers: every product and sum is exact, so the bits are the oracle's."""
+    rng = np.random.default_rng(41)
+    s = Stack(native, 4, 96, 128, 42)
+    codes = rng.integers(0, 256, (4, 96, 64), dtype=np.uint8)
+    scales = np.full((4, 96, 8), 0x38, np.uint8)  # 1.0
+    gs = np.ones(4, np.float32)
+    h = native.ffn_nvfp4_experts_create(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), torch.from_numpy(gs).cuda())
+    w = M.experts_dequant(codes, scales, gs)
+    for m in (1, 3, 90, 400):
+        xi = rng.integers(-3, 4, (m, 128)).astype(np.float64)
+        x = torch.from_numpy(xi).to(torch.bfloat16).cuda()
+        ids = pick(rng, m, 4, 2)
+        y = native.ffn_nvfp4_experts_linear(x, h, torch.from_numpy(ids).cuda())
+        assert np.array_equal(bf16_to_f64(y), O.round_to_bf16(M.experts_linear(xi, w, ids)))
+
+
+def test_linear_non_finite_rows_stay_their_own(native):
+    s = Stack(native, 3, 128, 256, 51)
+    for m in (2, 12, 200):
+        x, x64 = rows(m, 256, 52)
+        x[1, 17] = float("nan")
+        ids = np.zeros((m, 2), np.int32)
+        ids[:, 1] = 2
+        y = native.ffn_nvfp4_experts_linear(x, s.handle, torch.from_numpy(ids).cuda())
+        assert bool(torch.isnan(y[1]).all())
+        assert bool(torch.isfinite(torch.cat([y[:1], y[2:]])).all())
+
+
+# ------------------------------------------------------------------- the layer
+
+class Layer:
+    def __init__(self, native, experts, hidden, inter, seed):
+        self.native, self.hidden, self.inter, self.experts = native, hidden, inter, experts
+        self.gu = Stack(native, experts, 2 * inter, hidden, seed, gate_up=True)
+        self.dn = Stack(native, experts, hidden, inter, seed + 1)
+
+    def run(self, x, ids, weights, **kw):
+        d = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+        return self.native.ffn_nvfp4_moe_forward(x, self.gu.handle, self.dn.handle, d(ids), d(weights), **kw)
+
+    def check(self, out, x64, ids, weights):
+        """Error carried through the layer: the products' sums, silu (slope at most 1.1, a few steps of fp32), the
+        rounding of h, the down sums, the weighted sum (top_k + 1 half steps) and the last rounding."""
+        top_k = ids.shape[1]
+        ref = M.moe_forward(x64, self.gu.w, self.dn.w, ids, weights)
+        g, u, h = M.moe_hidden(x64, self.gu.w, ids)
+        mag = sum_error(self.hidden) * M.experts_linear(np.abs(x64), np.abs(self.gu.w), ids)
+        dg, du = mag[:, :, :self.inter], mag[:, :, self.inter:]
+        sg = np.abs(g / (1 + np.exp(-g)))
+        # the bf16 value of h may fall to the other side of a midpoint: a whole step from the oracle's
+        dh = (1.1 * dg * np.abs(u) + sg * du + 1.1 * dg * du + 16 * 2.0 ** -24 * np.abs(h)) * (1 + 2 * HALF) + 2 * HALF * np.abs(h)
+        ref_h = h
+        wd, aw = np.abs(self.dn.w), np.abs(np.asarray(weights, np.float64))
+        bound = np.zeros_like(ref)
+        mag_out = np.zeros_like(ref)
+        for j in range(top_k):
+            for i, e in enumerate(ids[:, j]):
+                if 0 <= e < self.experts:
+                    terms = wd[e] @ (np.abs(ref_h[i, j]) + dh[i, j])
+                    bound[i] += aw[i, j] * (wd[e] @ dh[i, j] + sum_error(self.inter) * terms)
+                    mag_out[i] += aw[i, j] * terms
+        bound += (top_k + 1) * 2.0 ** -24 * mag_out
+        bound = (1 + HALF) * bound + HALF * np.abs(ref) + 2.0 ** -133
+        got = bf16_to_f64(out)
+        err = np.abs(got - ref)
+        assert np.all(err <= bound), float((err / bound).max())
+        # the bound adds magnitudes; errors of either sign mostly cancel: two roundings to bf16 in the 2-norm
+        n = np.linalg.norm(ref)
+        assert n == 0 or np.linalg.norm(got - ref) <= 2 * HALF * n
+
+
+@pytest.mark.parametrize("m,experts,top_k,hidden,inter,padding", [
+    (1, 1, 1, 32, 32, 0.0), (1, 8, 2, 256, 96, 0.0), (1, 16, 8, 512, 160, 0.0), (1, 3, 3, 1056, 32, 0.0),
+    (2, 4, 2, 128, 704, 0.0), (7, 20, 3, 352, 224, 0.2), (24, 16, 4, 256, 128, 0.0), (33, 2, 2, 160, 288, 0.1),
+    (64, 5, 1, 384, 64, 0.3), (128, 4, 2, 256, 320, 0.0), (257, 3, 2, 192, 96, 0.1), (520, 2, 1, 128, 128, 0.0),
+])
+def test_layer_matches_oracle(native, m, experts, top_k, hidden, inter, padding):
+    rng = np.random.default_rng(3000 + m)
+    layer = Layer(native, experts, hidden, inter, 3100 + m)
+    x, x64 = rows(m, hidden, 3200 + m)
+    ids = pick(rng, m, experts, top_k, padding)
+    weights = rng.uniform(0.0, 1.0, (m, top_k)).astype(np.float32)
+    layer.check(layer.run(x, ids, weights), x64, ids, weights)
+
+
+@pytest.mark.parametrize("m", [1, 20, 150])
+def test_layer_padding_rows_and_canaries(native, m):
+    """Rows without an expert are zeros; nothing behind row m is written; the workspace's size is enough."""
+    layer = Layer(native, 4, 128, 96, 61)
+    x, x64 = rows(m, 128, 62)
+    ids = np.full((m, 2), -1, np.int32)
+    w = np.zeros((m, 2), np.float32)
+    out = torch.full((m + 3, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    size = native.ffn_nvfp4_moe_workspace_size(m, 2, 4, 128, 96)
+    ws = torch.full((size + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    layer.run(x, ids, w, out=out[:m], workspace=ws[:size])
+    assert int(torch.count_nonzero(out[:m].view(torch.int16))) == 0
+    ids[m // 2] = (3, 1)
+    w[m // 2] = (0.25, 0.75)
+    layer.run(x, ids, w, out=out[:m], workspace=ws[:size])
+    torch.cuda.synchronize()
+    assert bool((out[m:] == 7.0).all()) and bool((ws[size:] == 0xA5).all())
+    layer.check(out[:m], x64, ids, w)
+    other = [i for i in range(m) if i != m // 2]
+    assert int(torch.count_nonzero(out[other].view(torch.int16))) == 0
+
+
+def test_layer_weight_signs_nan_and_zero(native):
+    layer = Layer(native, 4, 128, 96, 63)
+    x, x64 = rows(6, 128, 64)
+    ids = pick(np.random.default_rng(65), 6, 4, 2)
+    w = np.array([[1, -1], [0, 2], [-3, 0], [0, 0], [1, 1], [2, 2]], np.float32)
+    layer.check(layer.run(x, ids, w), x64, ids, w)
+    w[4, 0] = np.nan
+    ids[5] = -1
+    w[5, 1] = np.nan  # a NaN weight of an id that picks nothing still shows
+    out = layer.run(x, ids, w)
+    assert bool(torch.isnan(out[4:]).all()) and bool(torch.isfinite(out[:4]).all())
+
+
+@pytest.mark.parametrize("m", [1, 40, 300])
+def test_layer_repeats_its_bits_and_rows_are_independent(native, m):
+    layer = Layer(native, 6, 256, 160, 71)
+    x, _ = rows(m, 256, 72)
+    rng = np.random.default_rng(73)
+    ids, w = pick(rng, m, 6, 3), rng.uniform(0, 1, (m, 3)).astype(np.float32)
+    a = layer.run(x, ids, w)
+    assert torch.equal(a, layer.run(x, ids, w))
+    order = rng.permutation(m)
+    b = layer.run(x[torch.from_numpy(order).cuda()].contiguous(), ids[order], w[order])
+    assert torch.equal(b, a[torch.from_numpy(order).cuda()])
+
+
+@pytest.mark.parametrize("m", [1, 24, 200])
+def test_route_then_layer_in_a_graph_on_its_own_stream(native, m):
+    """The three operators as a serving step uses them: routed, computed and replayed with new rows."""
+    layer = Layer(native, 8, 256, 128, 81)
+    proj = Stack(native, 8, 64, 256, 83)
+    s = torch.cuda.Stream()
+    x = torch.empty((m, 256), dtype=torch.bfloat16, device="cuda")
+    logits = torch.empty((m, 8), device="cuda")
+    bias = torch.linspace(-0.1, 0.1, 8, device="cuda")
+    ids = torch.empty((m, 2), dtype=torch.int32, device="cuda")
+    w = torch.empty((m, 2), device="cuda")
+    out = torch.empty((m, 256), dtype=torch.bfloat16, device="cuda")
+    y = torch.empty((m, 2, 64), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(native.ffn_nvfp4_moe_workspace_size(m, 2, 8, 256, 128), dtype=torch.uint8, device="cuda")
+
+    def step():
+        native.ffn_nvfp4_moe_route(logits, 2, scoring="sigmoid", bias=bias, groups=4, top_groups=2, group_score="top2",
+                                   ids=ids, weights=w)
+        native.ffn_nvfp4_moe_forward(x, layer.gu.handle, layer.dn.handle, ids, w, out=out, workspace=ws)
+        native.ffn_nvfp4_experts_linear(x, proj.handle, ids, y=y, workspace=ws)
+
+    x.zero_()
+    logits.zero_()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            step()
+    torch.cuda.synchronize()
+    for seed in (1, 2):
+        xd, x64 = rows(m, 256, 90 + seed)
+        l = np.random.default_rng(seed).standard_normal((m, 8)).astype(np.float32)
+        x.copy_(xd)
+        logits.copy_(torch.from_numpy(l))
+        for t in (out, y, w):
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        rid, rw = M.route(l.astype(np.float64), bias.double().cpu().numpy(), 2, scoring="sigmoid", groups=4, top_groups=2,
+                          group_score="top2")
+        assert np.array_equal(ids.cpu().numpy(), rid) and np.allclose(w.cpu().numpy(), rw, rtol=14 * 2.0 ** -24)
+        layer.check(out, x64, rid, w.cpu().numpy())
+        ref = M.experts_linear(x64, proj.w, rid)
+        tol = HALF * np.abs(ref) + 1.01 * sum_error(256) * M.experts_linear(np.abs(x64), np.abs(proj.w), rid)
+        assert np.all(np.abs(bf16_to_f64(y) - ref) <= tol)
+
+
+def test_layer_refusals(native):
+    layer = Layer(native, 4, 128, 96, 91)
+    x, _ = rows(3, 128, 92)
+    ids = torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    w = torch.ones((3, 2), device="cuda")
+    run = lambda gu, dn, **kw: native.ffn_nvfp4_moe_forward(x, gu, dn, ids, w, **kw)
+
+    def status(f):
+        with pytest.raises(native.FfnError) as e:
+            f()
+        return e.value.status_name
+
+    other = Stack(native, 5, 128, 96, 93).handle
+    assert status(lambda: run(layer.dn.handle, layer.gu.handle)) in ("FFN_ERR_INVALID_ARG", "FFN_ERR_SHAPE")
+    assert status(lambda: run(layer.gu.handle, other)) == "FFN_ERR_SHAPE"
+    assert status(lambda: run(layer.gu.handle, layer.dn.handle, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))) == "FFN_ERR_WORKSPACE"
+    assert status(lambda: native.ffn_nvfp4_experts_linear(x, layer.gu.handle, ids)) == "FFN_ERR_UNSUPPORTED"
+    with pytest.raises(TypeError):
+        native.ffn_nvfp4_moe_forward(x.float(), layer.gu.handle, layer.dn.handle, ids, w)
+    with pytest.raises(TypeError):
+        native.ffn_nvfp4_moe_forward(x, layer.gu.handle, layer.dn.handle, ids.long(), w)
+    with pytest.raises(ValueError):
+        native.ffn_nvfp4_moe_forward(x, layer.gu.handle, layer.dn.handle, ids[:2], w)
+    with pytest.raises(ValueError):
+        native.ffn_nvfp4_experts_linear(x[:, :64].contiguous(), layer.dn.handle, ids)
+    with pytest.raises(ValueError):
+        native.ffn_nvfp4_experts_create(torch.zeros((2, 64, 32), dtype=torch.uint8, device="cuda"),
+                                        torch.zeros((2, 64, 4), dtype=torch.uint8, device="cuda"), torch.ones(3, device="cuda"))
+    empty = native.ffn_nvfp4_moe_forward(x[:0], layer.gu.handle, layer.dn.handle, ids[:0], w[:0])
+    assert empty.shape == (0, 128)
