@@ -7,6 +7,7 @@
 
 #include "ffn_nvfp4.h"
 #include "internal.h"
+#include "moe.h"
 
 using ffn::Epilogue;
 using ffn::WeightView;
@@ -664,7 +665,11 @@ ffn_status ffn_nvfp4_device_error(int* flags, int clear) {
     cudaGetLastError();
     return FFN_ERR_CUDA;
   }
-  return cuda_status(ffn::read_device_error(flags, clear != 0));
+  int moe = 0;
+  cudaError_t e = ffn::read_device_error(flags, clear != 0);
+  if (e == cudaSuccess) e = ffn::read_moe_device_error(&moe, clear != 0);
+  *flags |= moe;
+  return cuda_status(e);
 }
 
 ffn_status ffn_nvfp4_linear_workspace_size(int64_t m, int64_t n, int64_t k,

@@ -19,7 +19,7 @@ struct ffn_nvfp4_experts {
     v.tiles = tiles;
     v.gs = gs;
     v.experts = (int)experts;
-    v.wtiles = (int)(gate_up ? (n / 2 + 63) / 64 : (n + 127) / 128);
+    v.wtiles = (int)((n / (gate_up ? 2 : 1) + 127) / 128);
     v.kc = (int)((k + 63) / 64);
     v.n = n;
     v.k = k;
@@ -48,8 +48,12 @@ ffn_status check_device(const ffn_nvfp4_experts* w) {
 bool valid_pairs(int64_t m, int top_k) { return m <= (int64_t)INT32_MAX / 2 / top_k; }
 
 struct Carve {
-  size_t offsets = 0, order = 0, tiles = 0, h = 0, y = 0, total = 0;
+  size_t offsets = 0, order = 0, tiles = 0, xs = 0, h = 0, y = 0, total = 0;
+  bool tc = false;
 };
+
+// From how many rows an expert (on average) the tensor cores take over.
+bool use_tc(int64_t pairs, int64_t experts) { return pairs > 16 * experts; }
 
 size_t take(size_t& off, size_t bytes) {
   const size_t at = off;
@@ -57,19 +61,21 @@ size_t take(size_t& off, size_t bytes) {
   return at;
 }
 
-// inter = 0: one projection, whose output is the caller's.
-Carve carve(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter) {
+// inter = 0: one projection of `hidden` columns and k, whose output is the caller's.
+Carve carve(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter, int64_t k) {
   Carve c;
   const int64_t pairs = m * top_k;
   if (pairs == 0) return c;
+  c.tc = use_tc(pairs, experts);
+  const int64_t padded = pairs + ffn::kTcTile;
   size_t off = 0;
   c.offsets = take(off, sizeof(int) * (experts + 1));
   c.order = take(off, sizeof(int) * pairs);
-  c.tiles = take(off, sizeof(int) * (1 + 3 * ffn::moe_max_tiles(pairs, experts, ffn::kRowsTile)));
-  if (inter > 0) {
-    c.h = take(off, (size_t)pairs * inter * 2);
-    c.y = take(off, (size_t)pairs * hidden * 4);
-  }
+  c.tiles = take(off, sizeof(int) * (1 + 3 * ffn::moe_max_tiles(pairs, experts, c.tc ? ffn::kTcTile : ffn::kRowsTile)));
+  // the sorted rows are read before the down products are written: one buffer
+  const size_t xs = c.tc ? (size_t)padded * k * 2 : 0, y = inter > 0 ? (size_t)pairs * hidden * 4 : 0;
+  c.xs = c.y = take(off, xs > y ? xs : y);
+  if (inter > 0) c.h = take(off, (size_t)padded * inter * 2);
   c.total = off;
   return c;
 }
@@ -111,15 +117,16 @@ ffn_status ffn_nvfp4_experts_create(const void* codes, const void* block_scales,
   w->n = n;
   w->k = k;
   w->gate_up = gate_up;
-  const size_t tile_bytes = (size_t)ffn::tc_tiled_bytes(n, k, gate_up != 0);
+  const int64_t parts = gate_up ? 2 : 1, rows = n / parts;  // gate and up are tiled apart
+  const size_t tile_bytes = (size_t)ffn::tc_tiled_bytes(rows, k, false);
   const size_t gs_bytes = sizeof(float) * experts * (gate_up ? 2 : 1);
-  w->bytes = tile_bytes * experts + gs_bytes;
+  w->bytes = tile_bytes * parts * experts + gs_bytes;
   if (cudaGetDevice(&w->device) != cudaSuccess) {
     delete w;
     cudaGetLastError();
     return FFN_ERR_CUDA;
   }
-  if (cudaMalloc(reinterpret_cast<void**>(&w->tiles), tile_bytes * experts) != cudaSuccess ||
+  if (cudaMalloc(reinterpret_cast<void**>(&w->tiles), tile_bytes * parts * experts) != cudaSuccess ||
       cudaMalloc(reinterpret_cast<void**>(&w->gs), gs_bytes) != cudaSuccess) {
     cudaGetLastError();
     free_experts(w);
@@ -127,10 +134,10 @@ ffn_status ffn_nvfp4_experts_create(const void* codes, const void* block_scales,
   }
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaMemcpyAsync(w->gs, global_scales, gs_bytes, cudaMemcpyDeviceToDevice, s);
-  for (int64_t i = 0; e == cudaSuccess && i < experts; ++i)
-    e = ffn::launch_tile_weight(static_cast<const uint8_t*>(codes) + i * n * (k / 2),
-                                static_cast<const uint8_t*>(block_scales) + i * n * (k / 16), n, k, gate_up != 0,
-                                true, w->tiles + i * tile_bytes, s);
+  for (int64_t i = 0; e == cudaSuccess && i < experts * parts; ++i)
+    e = ffn::launch_tile_weight(static_cast<const uint8_t*>(codes) + i * rows * (k / 2),
+                                static_cast<const uint8_t*>(block_scales) + i * rows * (k / 16), rows, k, false, true,
+                                w->tiles + i * tile_bytes, s);
   if (e != cudaSuccess) {
     cudaGetLastError();
     free_experts(w);
@@ -162,7 +169,7 @@ ffn_status ffn_nvfp4_experts_workspace_size(int64_t m, int top_k, int64_t expert
                                             size_t* bytes) {
   if (!bytes || m < 0 || top_k < 1 || experts < 1 || n < 1) return FFN_ERR_INVALID_ARG;
   if (!valid_k(k) || !valid_pairs(m, top_k)) return FFN_ERR_SHAPE;
-  *bytes = carve(m, top_k, experts, n, 0).total;
+  *bytes = carve(m, top_k, experts, n, 0, k).total;
   return FFN_OK;
 }
 
@@ -174,16 +181,22 @@ ffn_status ffn_nvfp4_experts_linear(const void* x, int64_t m, const ffn_nvfp4_ex
   if (m == 0) return FFN_OK;
   if (!x || !ids || !y) return FFN_ERR_INVALID_ARG;
   if (ffn_status st = check_device(w)) return st;
-  const Carve c = carve(m, top_k, w->experts, w->n, 0);
+  const Carve c = carve(m, top_k, w->experts, w->n, 0, w->k);
   if (!workspace || workspace_bytes < c.total) return FFN_ERR_WORKSPACE;
   if (!aligned16(x) || !aligned16(y) || !aligned16(workspace) || !aligned4(ids)) return FFN_ERR_ALIGNMENT;
   if (ffn_status st = ffn::moe_precheck()) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const ffn::ExpertsView v = w->view();
-  const ffn::MoePlan p = plan_at(static_cast<uint8_t*>(workspace), c);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const ffn::MoePlan p = plan_at(ws, c);
   const int64_t pairs = m * top_k;
-  cudaError_t e = ffn::launch_moe_plan(ids, pairs, v.experts, ffn::kRowsTile, p, s);
-  if (e == cudaSuccess) e = ffn::launch_experts_rows(x, top_k, v, p, pairs, ffn::ExpertsOut::kBf16, y, s);
+  cudaError_t e = ffn::launch_moe_plan(ids, pairs, v.experts, c.tc ? ffn::kTcTile : ffn::kRowsTile, p, s);
+  if (c.tc) {
+    if (e == cudaSuccess) e = ffn::launch_moe_gather(x, top_k, p, v.experts, pairs, v.k, ws + c.xs, s);
+    if (e == cudaSuccess) e = ffn::launch_experts_tc(ws + c.xs, v, p, pairs, ffn::ExpertsOut::kBf16, y, s);
+  } else {
+    if (e == cudaSuccess) e = ffn::launch_experts_rows(x, top_k, v, p, pairs, ffn::ExpertsOut::kBf16, y, s);
+  }
   if (e == cudaSuccess) e = ffn::launch_experts_zero(ids, pairs, v.experts, v.n, y, s);
   return ffn::moe_status(e);
 }
@@ -192,7 +205,7 @@ ffn_status ffn_nvfp4_moe_workspace_size(int64_t m, int top_k, int64_t experts, i
                                         size_t* bytes) {
   if (!bytes || m < 0 || top_k < 1 || experts < 1) return FFN_ERR_INVALID_ARG;
   if (!valid_k(hidden) || !valid_k(inter) || !valid_pairs(m, top_k)) return FFN_ERR_SHAPE;
-  *bytes = carve(m, top_k, experts, hidden, inter).total;
+  *bytes = carve(m, top_k, experts, hidden, inter, hidden).total;
   return FFN_OK;
 }
 
@@ -210,7 +223,7 @@ ffn_status ffn_nvfp4_moe_forward(const void* x, int64_t m, int64_t hidden, int64
   if (!x || !ids || !weights || !out) return FFN_ERR_INVALID_ARG;
   if (ffn_status st = check_device(gate_up)) return st;
   if (ffn_status st = check_device(down)) return st;
-  const Carve c = carve(m, top_k, down->experts, hidden, inter);
+  const Carve c = carve(m, top_k, down->experts, hidden, inter, hidden);
   if (!workspace || workspace_bytes < c.total) return FFN_ERR_WORKSPACE;
   if (!aligned16(x) || !aligned16(out) || !aligned16(workspace) || !aligned4(ids) || !aligned4(weights))
     return FFN_ERR_ALIGNMENT;
@@ -220,9 +233,15 @@ ffn_status ffn_nvfp4_moe_forward(const void* x, int64_t m, int64_t hidden, int64
   const ffn::ExpertsView gu = gate_up->view(), dn = down->view();
   const ffn::MoePlan p = plan_at(ws, c);
   const int64_t pairs = m * top_k;
-  cudaError_t e = ffn::launch_moe_plan(ids, pairs, dn.experts, ffn::kRowsTile, p, s);
-  if (e == cudaSuccess) e = ffn::launch_experts_rows(x, top_k, gu, p, pairs, ffn::ExpertsOut::kSiluMul, ws + c.h, s);
-  if (e == cudaSuccess) e = ffn::launch_experts_rows(ws + c.h, 1, dn, p, pairs, ffn::ExpertsOut::kF32, ws + c.y, s);
+  cudaError_t e = ffn::launch_moe_plan(ids, pairs, dn.experts, c.tc ? ffn::kTcTile : ffn::kRowsTile, p, s);
+  if (c.tc) {
+    if (e == cudaSuccess) e = ffn::launch_moe_gather(x, top_k, p, dn.experts, pairs, hidden, ws + c.xs, s);
+    if (e == cudaSuccess) e = ffn::launch_experts_tc(ws + c.xs, gu, p, pairs, ffn::ExpertsOut::kSiluMul, ws + c.h, s);
+    if (e == cudaSuccess) e = ffn::launch_experts_tc(ws + c.h, dn, p, pairs, ffn::ExpertsOut::kF32, ws + c.y, s);
+  } else {
+    if (e == cudaSuccess) e = ffn::launch_experts_rows(x, top_k, gu, p, pairs, ffn::ExpertsOut::kSiluMul, ws + c.h, s);
+    if (e == cudaSuccess) e = ffn::launch_experts_rows(ws + c.h, 1, dn, p, pairs, ffn::ExpertsOut::kF32, ws + c.y, s);
+  }
   if (e == cudaSuccess)
     e = ffn::launch_moe_combine(reinterpret_cast<const float*>(ws + c.y), ids, weights, m, top_k, dn.experts, hidden,
                                 out, s);

@@ -86,12 +86,11 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One CTA: 32 weight rows of one expert times up to 8 of its rows, all of K;
-// the warps take 128-element steps of K in turn and their sums are added in
-// warp order.  Lane (g, t) = (lane / 4, lane % 4) reads 32 consecutive K
-// elements of weight rows 8a + g + {0, 32, 64, 96} straight into registers (of
-// a gate and up tile: two gate rows and their up rows) and the same elements
-// of row g of x.  The MMA sums over K in any order, so "k" of the fragments is
+// One CTA: 32 weight rows of one expert (16 gate rows and their up rows) times
+// up to 8 of its rows, all of K; the warps take 128-element steps of K in turn
+// and their sums are added in warp order.  Lane (g, t) = (lane / 4, lane % 4)
+// reads 32 consecutive K elements of four weight rows, 32 apart in the tile,
+// straight into registers and the same elements of row g of x.  The MMA sums over K in any order, so "k" of the fragments is
 // whatever the four lanes of a quad hold, and no data moves between lanes.
 template <int MODE>
 __global__ void __launch_bounds__(kRowsWarps * 32) experts_rows_kernel(const RowsArgs a) {
@@ -99,13 +98,18 @@ __global__ void __launch_bounds__(kRowsWarps * 32) experts_rows_kernel(const Row
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int unit = blockIdx.x, tile = unit >> 2, r8 = 8 * (unit & 3);
+  constexpr bool kPair = MODE == (int)ExpertsOut::kSiluMul;
+  // tile rows of the four weight rows: r0 + 32 * j, j = 0..3; gate and up: r0 + 32 * (j & 1) of either tile
+  const int tile = blockIdx.x / (kPair ? 8 : 4), r8 = 8 * (blockIdx.x & 3), j64 = kPair ? 64 * ((blockIdx.x >> 2) & 1) : 0;
+  const int r0 = r8 + g + j64;
   const int ntiles = a.plan.tiles[0];
   const int64_t k = a.w.k;
   const int steps = (a.w.kc + 1) / 2;
   for (int slot = blockIdx.y; slot < ntiles; slot += gridDim.y) {
     const int e = a.plan.tiles[1 + 3 * slot], first = a.plan.tiles[2 + 3 * slot], rows = a.plan.tiles[3 + 3 * slot];
-    const uint8_t* wt = a.w.tiles + ((size_t)e * a.w.wtiles + tile) * a.w.kc * kChunkBytes;
+    const size_t tile_bytes = (size_t)a.w.kc * kChunkBytes;
+    const uint8_t* wt = a.w.tiles + ((size_t)e * (kPair ? 2 : 1) * a.w.wtiles + tile) * tile_bytes;
+    const size_t second = kPair ? a.w.wtiles * tile_bytes : 64 * 16;  // from rows j = 0, 1 to rows j = 2, 3
     const uint16_t* xr = g < rows ? a.x + (size_t)(a.plan.order[first + g] / a.row_div) * k : nullptr;
     float acc[2][4] = {};
     for (int s = warp; s < steps; s += kRowsWarps) {
@@ -117,8 +121,14 @@ __global__ void __launch_bounds__(kRowsWarps * 32) experts_rows_kernel(const Row
         const uint8_t* base = wt + (size_t)c * kChunkBytes;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          cw[j] = __ldg(reinterpret_cast<const uint4*>(base + (t & 1) * 2048 + 16 * (r8 + g + 32 * j)));
-        sc = __ldg(reinterpret_cast<const uint4*>(base + 4096 + 16 * (r8 + g)));
+          cw[j] = __ldg(reinterpret_cast<const uint4*>(base + (t & 1) * 2048 + 16 * (r0 + 32 * (j & 1)) + (j >> 1) * second));
+        if (kPair) {  // the scales of rows r8 + g + {0, 32, 64, 96} stand together
+          const uint2 s0 = __ldg(reinterpret_cast<const uint2*>(base + 4096 + 16 * (r8 + g) + j64 / 8));
+          const uint2 s1 = __ldg(reinterpret_cast<const uint2*>(base + second + 4096 + 16 * (r8 + g) + j64 / 8));
+          sc = make_uint4(s0.x, s0.y, s1.x, s1.y);
+        } else {
+          sc = __ldg(reinterpret_cast<const uint4*>(base + 4096 + 16 * (r8 + g)));
+        }
         const int64_t k0 = 128 * (int64_t)s + 32 * t;
         if (xr && k0 < k)
 #pragma unroll
@@ -149,17 +159,17 @@ __global__ void __launch_bounds__(kRowsWarps * 32) experts_rows_kernel(const Row
     __syncthreads();
     // accumulator i of lane (g, t): weight row 8a + g + 32 * (i / 2), x row 2t + (i & 1)
     const int og = threadIdx.x & 7, on = (threadIdx.x >> 3) & 7, oj = threadIdx.x >> 6;  // row, token, 32-row group
-    if (on < rows && (MODE != (int)ExpertsOut::kSiluMul || oj < 2)) {
+    if (on < rows && (!kPair || oj < 2)) {
       const int src = 4 * og + (on >> 1), i = 2 * oj + (on & 1);
       const int64_t p = a.plan.order[first + on];
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < kRowsWarps; ++w) v += red[w][i][src];
-      if (MODE == (int)ExpertsOut::kSiluMul) {
+      if (kPair) {
         float u = 0.0f;
 #pragma unroll
         for (int w = 0; w < kRowsWarps; ++w) u += red[w][i + 4][src];
-        const int64_t inter = a.w.n / 2, col = 64 * (int64_t)tile + r8 + og + 32 * oj;
+        const int64_t inter = a.w.n / 2, col = kTileRows * (int64_t)tile + r8 + og + j64 + 32 * oj;
         if (col < inter)
           static_cast<uint16_t*>(a.out)[p * inter + col] =
               f32_to_bf16_bits(silu_f32(a.w.gs[2 * e] * kUnscale * v) * (a.w.gs[2 * e + 1] * kUnscale * u));
@@ -236,7 +246,7 @@ cudaError_t launch_experts_rows(const void* x, int row_div, const ExpertsView& w
   a.plan = p;
   a.out = out;
   const int64_t tiles = moe_max_tiles(pairs, w.experts, kRowsTile);
-  const dim3 grid((unsigned)(4 * w.wtiles), (unsigned)(tiles < 65535 ? tiles : 65535)), block(kRowsWarps * 32);
+  const dim3 grid((unsigned)((w.gate_up ? 8 : 4) * w.wtiles), (unsigned)(tiles < 65535 ? tiles : 65535)), block(kRowsWarps * 32);
   ProfScope prof(s, mode == ExpertsOut::kSiluMul ? "experts_rows_silu" : "experts_rows");
   switch (mode) {
     case ExpertsOut::kSiluMul: return launch_pdl(experts_rows_kernel<(int)ExpertsOut::kSiluMul>, grid, block, 0, s, a);

@@ -21,9 +21,10 @@ inline ffn_status moe_precheck() { return moe_status(cudaPeekAtLastError()); }
 // Stacked experts as the kernels read them: E times the 128-row x 64-element
 // tiles of the bf16 activation format (launch_tile_weight with for_w4a16).
 struct ExpertsView {
-  const uint8_t* tiles = nullptr;  // [E][wtiles][kc][4608]
+  const uint8_t* tiles = nullptr;  // [E][wtiles][kc][4608]; gate and up: [E][2][wtiles][kc][4608]
   const float* gs = nullptr;       // [E], or [E][2] (gate, up)
-  int experts = 0, wtiles = 0, kc = 0;
+  int experts = 0, kc = 0;
+  int wtiles = 0;                  // 128-row tiles of n (gate and up: of inter)
   int64_t n = 0, k = 0;            // logical dims (n = 2 * inter for gate and up)
   bool gate_up = false;
 };
@@ -60,5 +61,17 @@ cudaError_t launch_moe_combine(const float* y, const int32_t* ids, const float* 
 cudaError_t launch_experts_zero(const int32_t* ids, int64_t pairs, int experts, int64_t n, void* y, cudaStream_t s);
 
 constexpr int kRowsTile = 8;  // rows of one expert that launch_experts_rows takes at a time
+
+// Many rows per expert, on the tensor cores (plan with kTcTile rows a tile).
+// xs holds the rows sorted by expert, and kTcTile more rows of any content;
+// kSiluMul writes h in the same order, the others write row p of the pair.
+constexpr int kTcTile = 128;
+cudaError_t launch_experts_tc(const void* xs, const ExpertsView& w, const MoePlan& p, int64_t pairs, ExpertsOut mode,
+                              void* out, cudaStream_t s);
+// xs[q, :] = x[order[q] / row_div, :]
+cudaError_t launch_moe_gather(const void* x, int row_div, const MoePlan& p, int experts, int64_t pairs, int64_t k,
+                              void* xs, cudaStream_t s);
+// Error bits of these kernels' bounded waits, as read_device_error.
+cudaError_t read_moe_device_error(int* flags, bool clear);
 
 }  // namespace ffn
