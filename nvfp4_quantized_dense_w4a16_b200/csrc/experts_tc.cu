@@ -4,20 +4,24 @@
 //
 // A persistent CTA per SM walks the tiles (128 rows of one expert) x (a pair
 // of 128-row weight tiles: the gate and up tiles of the same columns, or two
-// consecutive tiles of a plain weight).  Per 64-element K chunk:
-//   * one warp streams the two weight tiles' chunks (9216 B) by bulk copies
-//     and one the rows' chunk (128 x 128 B, 128-byte swizzle) by TMA;
+// consecutive tiles of a plain weight).  Per unit of two 64-element K chunks:
+//   * one warp streams the two weight tiles' chunks (18432 B) by bulk copies
+//     and one the rows' chunks (2 x 128 x 128 B, 128-byte swizzle) by TMA;
 //   * two warpgroups, one per weight tile, decode the codes to bf16 and write
 //     them to tensor memory, where they are the MMA's A operand (M = 128);
-//   * one thread issues tcgen05.mma kind::f16 of both halves against the same
-//     row tile in shared memory (N = 128), into two fp32 accumulators;
-//   * two further warpgroups read a finished tile's accumulators (64 rows
-//     each), and run the epilogue while the next tile's MMAs proceed.
+//   * two threads, one per weight tile, issue tcgen05.mma kind::f16 against
+//     the same rows in shared memory (N = 128), each into its own fp32
+//     accumulator.  A barrier wait, a fence and a commit cost an issuing thread
+//     about 0.1 us each while its MMAs of 64 cycles drain: one thread with
+//     one-chunk units kept the tensor pipe busy for half of the time;
+//   * two further warpgroups (64 rows each) read a finished tile's
+//     accumulators, one into registers and one into shared memory, hand them
+//     back and run the epilogue while the next tile's MMAs proceed.
 // The pair is what bounds the traffic: a row tile is read from L2 once per 256
-// weight rows, 25 KB per chunk of 512 MMA cycles (50 B/clk per SM).
-// Tensor memory: accumulators in columns 0..255, four A slots of both halves
-// in columns 256..511.  Every wait is bounded; on expiry a device error bit is
-// raised and the CTA frees its tensor memory and exits.
+// weight rows, 50 KB per unit of 1024 MMA cycles (50 B/clk per SM).
+// Tensor memory: accumulators in columns 0..255, two A slots of a unit and
+// tile each in columns 256..511.  Every wait is bounded; on expiry a device
+// error bit is raised and the CTA frees its tensor memory and exits.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -42,21 +46,18 @@ __device__ int g_moe_device_error = 0;
 __device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
 
 constexpr int kThreads = 640;
-constexpr int kXStages = 6, kWStages = 6, kASlots = 4;
-constexpr int kWStageBytes = 2 * kChunkBytes;
-
-template <int BN>
-struct Cfg {
-  static constexpr int kXStageBytes = BN * 128;
-  static constexpr int kSmemW = kXStages * kXStageBytes;
-  static constexpr int kSmemStage = kSmemW + kWStages * kWStageBytes;  // epilogue staging, two warpgroups
-  static constexpr int kStageBytes = (BN / 2) * 256;
-  static constexpr int kSmemBar = kSmemStage + 2 * kStageBytes;
-  static constexpr int kNumBars = 2 * kXStages + 2 * kWStages + 2 * kASlots + 2;
-  static constexpr int kSmemBytes = kSmemBar + kNumBars * 8 + 16;
-  static constexpr int kSmemAlloc = kSmemBytes + 1024;
-  static_assert(kSmemAlloc <= 232448, "shared memory budget");
-};
+constexpr int kUnit = 2;  // K chunks per unit
+constexpr int kXStages = 3, kWStages = 3, kASlots = 2;
+constexpr int kWStageBytes = 2 * kUnit * kChunkBytes;  // [chunk][tile of the pair]
+constexpr int kXChunkBytes = kTcTile * 128, kXStageBytes = kUnit * kXChunkBytes;
+constexpr int kMine = kTcTile / 2;                      // rows of a tile per epilogue warpgroup
+constexpr int kParkBytes = kMine * kTileRows * 4;       // one warpgroup's half of an accumulator
+constexpr int kSmemW = kXStages * kXStageBytes;
+constexpr int kSmemPark = kSmemW + kWStages * kWStageBytes;
+constexpr int kSmemBar = kSmemPark + 2 * kParkBytes;
+constexpr int kNumBars = 2 * kXStages + 2 * kWStages + 4 * kASlots + 2;
+constexpr int kSmemAlloc = kSmemBar + kNumBars * 8 + 16 + 1024;  // slack for 1024-byte alignment
+static_assert(kSmemAlloc <= 232448, "shared memory budget");
 constexpr int kAColBase = 256;
 
 struct TcExpertsArgs {
@@ -87,43 +88,42 @@ __device__ __forceinline__ bool drain(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
-template <int BN, int MODE>
+template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_constant__ CUtensorMap xmap,
                                                                 const TcExpertsArgs a) {
-  using C = Cfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* xs = smem;
-  uint8_t* wsm = smem + C::kSmemW;
-  uint64_t* xfull = reinterpret_cast<uint64_t*>(smem + C::kSmemBar);
+  uint8_t* wsm = smem + kSmemW;
+  uint64_t* xfull = reinterpret_cast<uint64_t*>(smem + kSmemBar);
   uint64_t* xempty = xfull + kXStages;
   uint64_t* wfull = xempty + kXStages;
   uint64_t* wempty = wfull + kWStages;
-  uint64_t* afull = wempty + kWStages;
-  uint64_t* aempty = afull + kASlots;
-  uint64_t* accfull = aempty + kASlots;
+  uint64_t* afull = wempty + kWStages;     // [tile of the pair][slot]
+  uint64_t* aempty = afull + 2 * kASlots;  // likewise
+  uint64_t* accfull = aempty + 2 * kASlots;
   uint64_t* accempty = accfull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accempty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* err = &g_moe_device_error;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kc = a.w.kc;
+  const int kc = a.w.kc, units = (kc + kUnit - 1) / kUnit;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kXStages; ++s) {
       mbar_init(&xfull[s], 1);
-      mbar_init(&xempty[s], 1);
+      mbar_init(&xempty[s], 2);  // one commit per MMA thread
     }
     for (int s = 0; s < kWStages; ++s) {
       mbar_init(&wfull[s], 1);
       mbar_init(&wempty[s], 8);
     }
-    for (int s = 0; s < kASlots; ++s) {
-      mbar_init(&afull[s], 8);
+    for (int s = 0; s < 2 * kASlots; ++s) {
+      mbar_init(&afull[s], 4);
       mbar_init(&aempty[s], 1);
     }
-    mbar_init(accfull, 1);
+    mbar_init(accfull, 2);
     mbar_init(accempty, 8);
     *abort_flag = 0;
     fence_mbar_init();
@@ -155,18 +155,19 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
           w1 = w0 + a.w.wtiles * tile_bytes;
         } else {
           w0 = a.w.tiles + ((size_t)ti.e * a.w.wtiles + 2 * ti.wt) * tile_bytes;
-          // an odd last tile: its chunks stand in for the missing half, whose sums are not stored
+          // an odd last tile stands in for the missing one, whose sums are not stored
           w1 = 2 * ti.wt + 1 < a.w.wtiles ? w0 + tile_bytes : w0;
         }
-        for (int c = 0; c < kc; ++c, ++u) {
+        for (int c = 0; c < kc; c += kUnit, ++u) {
           const int s = u % kWStages;
           if (u >= kWStages && !mbar_wait(&wempty[s], ((u / kWStages) - 1) & 1, abort_flag, err, 1)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&wfull[s], kWStageBytes);
-          bulk_load(wsm + s * kWStageBytes, w0 + (size_t)c * kChunkBytes, kChunkBytes, &wfull[s]);
-          bulk_load(wsm + s * kWStageBytes + kChunkBytes, w1 + (size_t)c * kChunkBytes, kChunkBytes, &wfull[s]);
+          const uint32_t bytes = min(kUnit, kc - c) * kChunkBytes;
+          mbar_arrive_expect_tx(&wfull[s], 2 * bytes);
+          bulk_load(wsm + s * kWStageBytes, w0 + (size_t)c * kChunkBytes, bytes, &wfull[s]);
+          bulk_load(wsm + s * kWStageBytes + kUnit * kChunkBytes, w1 + (size_t)c * kChunkBytes, bytes, &wfull[s]);
         }
       }
       for (int r = max(0, u - kWStages); r < u; ++r) drain(&wfull[r % kWStages], (r / kWStages) & 1);
@@ -178,167 +179,182 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
       bool ok = true;
       for (int T = blockIdx.x; ok && T < total; T += gridDim.x) {
         const TileInfo ti = tile_at(a, T);
-        for (int c = 0; c < kc; ++c, ++u) {
-          const int s = u % kXStages;
+        for (int c = 0; c < kc; c += kUnit, ++u) {
+          const int s = u % kXStages, nc = min(kUnit, kc - c);
           if (u >= kXStages && !mbar_wait(&xempty[s], ((u / kXStages) - 1) & 1, abort_flag, err, 1)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&xfull[s], C::kXStageBytes);
-          tma_load_2d(xs + s * C::kXStageBytes, &xmap, c * kChunkK, ti.first, &xfull[s]);
+          mbar_arrive_expect_tx(&xfull[s], nc * kXChunkBytes);
+          for (int j = 0; j < nc; ++j)
+            tma_load_2d(xs + s * kXStageBytes + j * kXChunkBytes, &xmap, (c + j) * kChunkK, ti.first, &xfull[s]);
         }
       }
       for (int r = max(0, u - kXStages); r < u; ++r) drain(&xfull[r % kXStages], (r / kXStages) & 1);
     }
-  } else if (warp == 2) {
-    // ----------------------------------------------------------- MMA issuer
+  } else if (warp < 4) {
+    // ----------------------------------------------------------- MMA issuers
     if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(kTileRows, BN);
+      const int half = warp - 2;
+      const uint32_t idesc = idesc_bf16_f32(kTileRows, kTcTile), d = tmem + 128 * half;
       int u = 0, i = 0;
       bool ok = true;
       for (int T = blockIdx.x; ok && T < total; T += gridDim.x, ++i) {
         if (i > 0 && !mbar_wait(accempty, (i - 1) & 1, abort_flag, err, 2)) break;
-        tc_fence_after();
-        for (int c = 0; c < kc; ++c, ++u) {
-          const int sx = u % kXStages, sa = u % kASlots;
-          if (!mbar_wait(&xfull[sx], (u / kXStages) & 1, abort_flag, err, 2) ||
-              !mbar_wait(&afull[sa], (u / kASlots) & 1, abort_flag, err, 2)) {
+        for (int c = 0; c < kc; c += kUnit, ++u) {
+          const int sx = u % kXStages, sa = u % kASlots, nc = min(kUnit, kc - c);
+          // (the decode warps have waited for the rows as well)
+          if (!mbar_wait(&afull[half * kASlots + sa], (u / kASlots) & 1, abort_flag, err, 2)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t b = smem_desc_sw128(smem_u32(xs + sx * C::kXStageBytes));
-          const uint32_t aslot = tmem + kAColBase + 64 * sa;
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
+          for (int j = 0; j < nc; ++j) {
+            const uint64_t b = smem_desc_sw128(smem_u32(xs + sx * kXStageBytes + j * kXChunkBytes));
+            const uint32_t aslot = tmem + kAColBase + 128 * sa + 64 * half + 32 * j;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ts(tmem + 128 * half, aslot + 32 * half + 8 * kk, b + 2 * kk, idesc, (c == 0 && kk == 0) ? 0u : 1u);
-          mma_commit(&aempty[sa]);
+              mma_bf16_ts(d, aslot + 8 * kk, b + 2 * kk, idesc, (c == 0 && j == 0 && kk == 0) ? 0u : 1u);
+          }
+          mma_commit(&aempty[half * kASlots + sa]);
           mma_commit(&xempty[sx]);
         }
         if (ok) mma_commit(accfull);
       }
     }
-  } else if (warp >= 4 && warp < 12) {
+  } else if (warp < 12) {
     // --------------------------------------------------------------- decode
     const int half = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane;
-    const uint32_t col = tmem + ((uint32_t)(32 * q) << 16) + kAColBase + 32 * half;
+    const uint32_t col = tmem + ((uint32_t)(32 * q) << 16) + kAColBase + 64 * half;
     int u = 0;
     bool ok = true;
     for (int T = blockIdx.x; ok && T < total; T += gridDim.x) {
-      for (int c = 0; c < kc; ++c, ++u) {
-        const int sw = u % kWStages, sa = u % kASlots;
+      for (int c = 0; c < kc; c += kUnit, ++u) {
+        const int sw = u % kWStages, sa = u % kASlots, nc = min(kUnit, kc - c);
         ok = mbar_wait(&wfull[sw], (u / kWStages) & 1, abort_flag, err, 4);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint8_t* w = wsm + sw * kWStageBytes + half * kChunkBytes;
-        const uint4 lo = *reinterpret_cast<const uint4*>(w + 16 * row);
-        const uint4 hi = *reinterpret_cast<const uint4*>(w + 2048 + 16 * row);
-        const uint32_t sc = *reinterpret_cast<const uint32_t*>(w + 4096 + 16 * lane + 4 * q);
+        uint4 lo[kUnit], hi[kUnit];
+        uint32_t sc[kUnit];
+        const uint8_t* w = wsm + sw * kWStageBytes + half * kUnit * kChunkBytes;
+#pragma unroll
+        for (int j = 0; j < kUnit; ++j) {  // (a missing second chunk reads what the stage held before)
+          lo[j] = *reinterpret_cast<const uint4*>(w + j * kChunkBytes + 16 * row);
+          hi[j] = *reinterpret_cast<const uint4*>(w + j * kChunkBytes + 2048 + 16 * row);
+          sc[j] = *reinterpret_cast<const uint32_t*>(w + j * kChunkBytes + 4096 + 16 * lane + 4 * q);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&wempty[sw]);
-        const uint32_t s01 = scale_pair(sc & 0xffffu), s23 = scale_pair(sc >> 16);
-        const uint32_t words[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        uint32_t v[32];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t o[4];
-          decode8(words[j], __byte_perm(j < 4 ? s01 : s23, 0, (j & 2) ? 0x3232 : 0x1010), o);
+        for (int j = 0; j < kUnit; ++j) {
+          if (j >= nc) break;
+          const uint32_t s01 = scale_pair(sc[j] & 0xffffu), s23 = scale_pair(sc[j] >> 16);
+          const uint32_t words[8] = {lo[j].x, lo[j].y, lo[j].z, lo[j].w, hi[j].x, hi[j].y, hi[j].z, hi[j].w};
+          uint32_t v[32];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[4 * j + i] = o[i];
+          for (int i = 0; i < 8; ++i) {
+            uint32_t o[4];
+            decode8(words[i], __byte_perm(i < 4 ? s01 : s23, 0, (i & 2) ? 0x3232 : 0x1010), o);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[4 * i + k] = o[k];
+          }
+          if (j == 0 && u >= kASlots) {  // the MMAs that read this slot two units ago are done
+            ok = mbar_wait(&aempty[half * kASlots + sa], ((u / kASlots) - 1) & 1, abort_flag, err, 4);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          tmem_st32(col + 128 * sa + 32 * j, v);
         }
-        if (u >= kASlots) {  // the MMAs that read this slot four chunks ago are done
-          ok = mbar_wait(&aempty[sa], ((u / kASlots) - 1) & 1, abort_flag, err, 4);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-        }
-        tmem_st32(col + 64 * sa, v);
+        if (!ok) break;
+        // the unit's rows, on the MMA thread's behalf
+        ok = mbar_wait(&xfull[u % kXStages], (u / kXStages) & 1, abort_flag, err, 4);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&afull[sa]);
+        if (lane == 0) mbar_arrive(&afull[half * kASlots + sa]);
       }
     }
-  } else if (warp >= 12) {
+  } else {
     // ------------------------------------------------------------- epilogue
     const int g = (warp - 12) >> 2, q = warp & 3, row = 32 * q + lane;
     const int et = threadIdx.x - 384 - 128 * g;  // 0..127 within this warpgroup
-    constexpr int kMine = BN / 2;                // rows of the tile this warpgroup takes
-    uint16_t* stage = reinterpret_cast<uint16_t*>(smem + C::kSmemStage + g * C::kStageBytes);  // [kMine][128]
-    const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16);
+    float* park = reinterpret_cast<float*>(smem + kSmemPark + g * kParkBytes);  // [kMine][128]
+    const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + kMine * g;
     int i = 0;
-    bool ok = true;
-    for (int T = blockIdx.x; ok && T < total; T += gridDim.x, ++i) {
+    for (int T = blockIdx.x; T < total; T += gridDim.x, ++i) {
       const TileInfo ti = tile_at(a, T);
-      const int j0 = kMine * g;                       // first row of the tile
-      const int mine = min(kMine, ti.rows - j0);      // may be <= 0
-      float gs0, gs1;
-      if (MODE == (int)ExpertsOut::kSiluMul) {
-        gs0 = a.w.gs[2 * ti.e] * kUnscale;
-        gs1 = a.w.gs[2 * ti.e + 1] * kUnscale;
-      } else {
-        gs0 = gs1 = a.w.gs[ti.e] * kUnscale;
-      }
-      ok = mbar_wait(accfull, i & 1, abort_flag, err, 8);
+      const int first = ti.first + kMine * g, mine = min(kMine, ti.rows - kMine * g);  // may be <= 0
+      const bool silu = MODE == (int)ExpertsOut::kSiluMul;
+      const float gs0 = a.w.gs[silu ? 2 * ti.e : ti.e] * kUnscale;
+      const float gs1 = silu ? a.w.gs[2 * ti.e + 1] * kUnscale : gs0;
+      int pr[2] = {0, 0};  // the rows' pairs
+      if (!silu)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (32 * h + lane < mine) pr[h] = a.plan.order[first + 32 * h + lane];
+      bool ok = mbar_wait(accfull, i & 1, abort_flag, err, 8);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      for (int c = 0; c < kMine; c += 32) {
-        uint32_t v0[32], v1[32];
-        tmem_ld32(lane_addr + j0 + c, v0);
-        tmem_ld32(lane_addr + 128 + j0 + c, v1);
+      float v[kMine];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t t[32];
+        tmem_ld32(lane_addr + 128 + 32 * h, t);
         tmem_ld_wait();
-        if (c + 32 >= kMine) {  // the accumulators are read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(accempty);
-        }
-        if (c >= mine) continue;
-        const int n = min(32, mine - c);
-        if (MODE == (int)ExpertsOut::kSiluMul) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float z = gs0 * __uint_as_float(v0[j]);
-            stage[(c + j) * 128 + row] = f32_to_bf16_bits(silu_fast(z) * (gs1 * __uint_as_float(v1[j])));
-          }
-        } else if (MODE == (int)ExpertsOut::kF32) {
-          float* y = static_cast<float*>(a.out);
-          const int p = lane < n ? a.plan.order[ti.first + j0 + c + lane] : 0;
-          const int64_t col0 = 256 * (int64_t)ti.wt + row, col1 = col0 + 128;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (j >= n) break;
-            float* yr = y + (int64_t)__shfl_sync(0xffffffffu, p, j) * a.w.n;
-            if (col0 < a.w.n) yr[col0] = gs0 * __uint_as_float(v0[j]);
-            if (col1 < a.w.n) yr[col1] = gs0 * __uint_as_float(v1[j]);
-          }
-        } else {
-          uint16_t* y = static_cast<uint16_t*>(a.out);
-          const int p = lane < n ? a.plan.order[ti.first + j0 + c + lane] : 0;
-          const int64_t col0 = 256 * (int64_t)ti.wt + row, col1 = col0 + 128;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (j >= n) break;
-            uint16_t* yr = y + (int64_t)__shfl_sync(0xffffffffu, p, j) * a.w.n;
-            if (col0 < a.w.n) yr[col0] = f32_to_bf16_bits(gs0 * __uint_as_float(v0[j]));
-            if (col1 < a.w.n) yr[col1] = f32_to_bf16_bits(gs0 * __uint_as_float(v1[j]));
-          }
-        }
+        for (int j = 0; j < 32; ++j) park[(32 * h + j) * kTileRows + row] = gs1 * __uint_as_float(t[j]);
       }
-      if (MODE == (int)ExpertsOut::kSiluMul) {
-        // h rows in sorted order, 16 bytes at a time (inter is a multiple of 32)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t t[32];
+        tmem_ld32(lane_addr + 32 * h, t);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[32 * h + j] = gs0 * __uint_as_float(t[j]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(accempty);
+      if (silu) {
+        // h = silu(g) * u, left as bf16 in the low half of u's own word
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+          float* u = park + j * kTileRows + row;
+          *reinterpret_cast<uint32_t*>(u) = f32_to_bf16_bits(silu_fast(v[j]) * *u);
+        }
+        // rows in sorted order, 16 bytes at a time (inter is a multiple of 32)
         named_bar_sync(1 + g, 128);
-        const int64_t inter = a.w.n / 2;
-        uint16_t* h = static_cast<uint16_t*>(a.out) + (int64_t)(ti.first + j0) * inter + 128 * (int64_t)ti.wt;
+        const int64_t inter = a.w.n / 2, c0 = kTileRows * (int64_t)ti.wt;
+        uint16_t* h = static_cast<uint16_t*>(a.out) + first * inter + c0;
         for (int idx = et; idx < mine * 16; idx += 128) {
           const int j = idx >> 4, ch = idx & 15;
-          if (128 * (int64_t)ti.wt + 8 * ch < inter)
-            *reinterpret_cast<uint4*>(h + j * inter + 8 * ch) =
-                *reinterpret_cast<const uint4*>(stage + j * 128 + 8 * ch);
+          if (c0 + 8 * ch >= inter) continue;
+          const uint4 p0 = *reinterpret_cast<const uint4*>(park + j * kTileRows + 8 * ch);
+          const uint4 p1 = *reinterpret_cast<const uint4*>(park + j * kTileRows + 8 * ch + 4);
+          *reinterpret_cast<uint4*>(h + j * inter + 8 * ch) =
+              make_uint4(p0.x | (p0.y << 16), p0.z | (p0.w << 16), p1.x | (p1.y << 16), p1.z | (p1.w << 16));
         }
         named_bar_sync(1 + g, 128);
+      } else {
+        const int64_t c0 = 2 * kTileRows * (int64_t)ti.wt + row, c1 = c0 + kTileRows, n = a.w.n;
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+          if (j >= mine) break;
+          const int64_t at = (int64_t)__shfl_sync(0xffffffffu, pr[j >> 5], j & 31) * n;
+          if (MODE == (int)ExpertsOut::kF32) {
+            float* y = static_cast<float*>(a.out) + at;
+            if (c0 < n) y[c0] = v[j];
+            if (c1 < n) y[c1] = park[j * kTileRows + row];
+          } else {
+            uint16_t* y = static_cast<uint16_t*>(a.out) + at;
+            if (c0 < n) y[c0] = f32_to_bf16_bits(v[j]);
+            if (c1 < n) y[c1] = f32_to_bf16_bits(park[j * kTileRows + row]);
+          }
+        }
       }
     }
   }
@@ -386,13 +402,13 @@ int sm_count() {
   return n;
 }
 
-template <int BN, int MODE>
+template <int MODE>
 cudaError_t launch_one(const CUtensorMap& map, const TcExpertsArgs& a, int grid, cudaStream_t s) {
-  auto kern = experts_tc_kernel<BN, MODE>;
+  auto kern = experts_tc_kernel<MODE>;
   // set on every launch: the attribute belongs to the current device's context
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::kSmemAlloc);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), Cfg<BN>::kSmemAlloc, s, map, a);
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), kSmemAlloc, s, map, a);
 }
 
 }  // namespace
@@ -406,14 +422,13 @@ cudaError_t launch_moe_gather(const void* x, int row_div, const MoePlan& p, int 
 
 cudaError_t launch_experts_tc(const void* xs, const ExpertsView& w, const MoePlan& p, int64_t pairs, ExpertsOut mode,
                               void* out, cudaStream_t s) {
-  constexpr int BN = kTcTile;
   auto enc = encode_fn();
   if (!enc) return cudaErrorInvalidValue;
   CUtensorMap map;
   // kTcTile rows behind the last pair belong to the buffer: no box leaves it
   cuuint64_t dims[2] = {(cuuint64_t)w.k, (cuuint64_t)(pairs + kTcTile)};
   cuuint64_t strides[1] = {(cuuint64_t)w.k * 2};
-  cuuint32_t box[2] = {(cuuint32_t)kChunkK, (cuuint32_t)BN};
+  cuuint32_t box[2] = {(cuuint32_t)kChunkK, (cuuint32_t)kTcTile};
   cuuint32_t estr[2] = {1, 1};
   if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(xs), dims, strides, box, estr,
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -424,14 +439,14 @@ cudaError_t launch_experts_tc(const void* xs, const ExpertsView& w, const MoePla
   a.plan = p;
   a.out = out;
   a.pairs_n = mode == ExpertsOut::kSiluMul ? w.wtiles : (w.wtiles + 1) / 2;
-  const int64_t most = moe_max_tiles(pairs, w.experts, BN) * a.pairs_n;
+  const int64_t most = moe_max_tiles(pairs, w.experts, kTcTile) * a.pairs_n;
   const int sms = sm_count();
   const int grid = (int)(most < sms ? most : sms);
   ProfScope prof(s, mode == ExpertsOut::kSiluMul ? "experts_tc_silu" : "experts_tc");
   switch (mode) {
-    case ExpertsOut::kSiluMul: return launch_one<BN, (int)ExpertsOut::kSiluMul>(map, a, grid, s);
-    case ExpertsOut::kF32: return launch_one<BN, (int)ExpertsOut::kF32>(map, a, grid, s);
-    default: return launch_one<BN, (int)ExpertsOut::kBf16>(map, a, grid, s);
+    case ExpertsOut::kSiluMul: return launch_one<(int)ExpertsOut::kSiluMul>(map, a, grid, s);
+    case ExpertsOut::kF32: return launch_one<(int)ExpertsOut::kF32>(map, a, grid, s);
+    default: return launch_one<(int)ExpertsOut::kBf16>(map, a, grid, s);
   }
 }
 
