@@ -665,10 +665,11 @@ ffn_status ffn_nvfp4_device_error(int* flags, int clear) {
     cudaGetLastError();
     return FFN_ERR_CUDA;
   }
-  int moe = 0;
+  int moe = 0, rows = 0;
   cudaError_t e = ffn::read_device_error(flags, clear != 0);
   if (e == cudaSuccess) e = ffn::read_moe_device_error(&moe, clear != 0);
-  *flags |= moe;
+  if (e == cudaSuccess) e = ffn::read_rows_device_error(&rows, clear != 0);
+  *flags |= moe | rows;
   return cuda_status(e);
 }
 

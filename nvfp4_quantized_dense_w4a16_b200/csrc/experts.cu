@@ -4,7 +4,6 @@
 #include <new>
 
 #include "ffn_nvfp4.h"
-#include "internal.h"
 #include "moe.h"
 
 struct ffn_nvfp4_experts {
@@ -19,7 +18,7 @@ struct ffn_nvfp4_experts {
     v.tiles = tiles;
     v.gs = gs;
     v.experts = (int)experts;
-    v.wtiles = (int)((n / (gate_up ? 2 : 1) + 127) / 128);
+    v.wtiles = ffn::experts_tiles(n / (gate_up ? 2 : 1));
     v.kc = (int)((k + 63) / 64);
     v.n = n;
     v.k = k;
@@ -48,12 +47,13 @@ ffn_status check_device(const ffn_nvfp4_experts* w) {
 bool valid_pairs(int64_t m, int top_k) { return m <= (int64_t)INT32_MAX / 2 / top_k; }
 
 struct Carve {
-  size_t offsets = 0, order = 0, tiles = 0, xs = 0, h = 0, y = 0, total = 0;
+  size_t offsets = 0, order = 0, tiles = 0, arrived = 0, xs = 0, h = 0, y = 0, total = 0;
   bool tc = false;
+  int splits = 1;  // of the down products' K
 };
 
 // From how many rows an expert (on average) the tensor cores take over.
-bool use_tc(int64_t pairs, int64_t experts) { return pairs > 16 * experts; }
+bool use_tc(int64_t pairs, int64_t experts) { return pairs > ffn::kFewPairs && pairs > 16 * experts; }
 
 size_t take(size_t& off, size_t bytes) {
   const size_t at = off;
@@ -72,8 +72,16 @@ Carve carve(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter
   c.offsets = take(off, sizeof(int) * (experts + 1));
   c.order = take(off, sizeof(int) * pairs);
   c.tiles = take(off, sizeof(int) * (1 + 3 * ffn::moe_max_tiles(pairs, experts, c.tc ? ffn::kTcTile : ffn::kRowsTile)));
+  c.arrived = take(off, sizeof(int) * ((hidden + 127) / 128));
+  if (inter > 0 && !c.tc) {
+    ffn::ExpertsView down;
+    down.wtiles = ffn::experts_tiles(hidden);
+    down.kc = (int)((inter + 63) / 64);
+    // every pair has an expert of its own with few pairs of one row; a batch spreads over all experts
+    c.splits = ffn::rows_splits(down, pairs < experts ? pairs : experts);
+  }
   // the sorted rows are read before the down products are written: one buffer
-  const size_t xs = c.tc ? (size_t)padded * k * 2 : 0, y = inter > 0 ? (size_t)pairs * hidden * 4 : 0;
+  const size_t xs = c.tc ? (size_t)padded * k * 2 : 0, y = inter > 0 ? (size_t)c.splits * pairs * hidden * 4 : 0;
   c.xs = c.y = take(off, xs > y ? xs : y);
   if (inter > 0) c.h = take(off, (size_t)padded * inter * 2);
   c.total = off;
@@ -118,7 +126,7 @@ ffn_status ffn_nvfp4_experts_create(const void* codes, const void* block_scales,
   w->k = k;
   w->gate_up = gate_up;
   const int64_t parts = gate_up ? 2 : 1, rows = n / parts;  // gate and up are tiled apart
-  const size_t tile_bytes = (size_t)ffn::tc_tiled_bytes(rows, k, false);
+  const size_t tile_bytes = ffn::experts_tile_bytes(rows, k);
   const size_t gs_bytes = sizeof(float) * experts * (gate_up ? 2 : 1);
   w->bytes = tile_bytes * parts * experts + gs_bytes;
   if (cudaGetDevice(&w->device) != cudaSuccess) {
@@ -134,10 +142,8 @@ ffn_status ffn_nvfp4_experts_create(const void* codes, const void* block_scales,
   }
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaMemcpyAsync(w->gs, global_scales, gs_bytes, cudaMemcpyDeviceToDevice, s);
-  for (int64_t i = 0; e == cudaSuccess && i < experts * parts; ++i)
-    e = ffn::launch_tile_weight(static_cast<const uint8_t*>(codes) + i * rows * (k / 2),
-                                static_cast<const uint8_t*>(block_scales) + i * rows * (k / 16), rows, k, false, true,
-                                w->tiles + i * tile_bytes, s);
+  if (e == cudaSuccess)
+    e = ffn::launch_tile_experts(codes, block_scales, experts * parts, rows, k, w->tiles, s);
   if (e != cudaSuccess) {
     cudaGetLastError();
     free_experts(w);
@@ -190,14 +196,16 @@ ffn_status ffn_nvfp4_experts_linear(const void* x, int64_t m, const ffn_nvfp4_ex
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const ffn::MoePlan p = plan_at(ws, c);
   const int64_t pairs = m * top_k;
-  cudaError_t e = ffn::launch_moe_plan(ids, pairs, v.experts, c.tc ? ffn::kTcTile : ffn::kRowsTile, p, s);
+  cudaError_t e = cudaSuccess;
+  if (pairs > ffn::kFewPairs)
+    e = ffn::launch_moe_plan(ids, pairs, v.experts, c.tc ? ffn::kTcTile : ffn::kRowsTile, p, s);
   if (c.tc) {
     if (e == cudaSuccess) e = ffn::launch_moe_gather(x, top_k, p, v.experts, pairs, v.k, ws + c.xs, s);
     if (e == cudaSuccess) e = ffn::launch_experts_tc(ws + c.xs, v, p, pairs, ffn::ExpertsOut::kBf16, y, s);
-  } else {
-    if (e == cudaSuccess) e = ffn::launch_experts_rows(x, top_k, v, p, pairs, ffn::ExpertsOut::kBf16, y, s);
+    if (e == cudaSuccess) e = ffn::launch_experts_zero(ids, pairs, v.experts, v.n, y, s);
+  } else if (e == cudaSuccess) {
+    e = ffn::launch_experts_rows(x, top_k, v, ids, p, pairs, top_k, ffn::ExpertsOut::kBf16, 1, y, nullptr, 0, nullptr, s);
   }
-  if (e == cudaSuccess) e = ffn::launch_experts_zero(ids, pairs, v.experts, v.n, y, s);
   return ffn::moe_status(e);
 }
 
@@ -233,18 +241,28 @@ ffn_status ffn_nvfp4_moe_forward(const void* x, int64_t m, int64_t hidden, int64
   const ffn::ExpertsView gu = gate_up->view(), dn = down->view();
   const ffn::MoePlan p = plan_at(ws, c);
   const int64_t pairs = m * top_k;
-  cudaError_t e = ffn::launch_moe_plan(ids, pairs, dn.experts, c.tc ? ffn::kTcTile : ffn::kRowsTile, p, s);
+  const ffn::ExpertsOut kSilu = ffn::ExpertsOut::kSiluMul, kF32 = ffn::ExpertsOut::kF32;
+  float* y = reinterpret_cast<float*>(ws + c.y);
+  cudaError_t e = cudaSuccess;
+  if (pairs <= ffn::kFewPairs) {
+    const ffn::RowsSum sum{weights, out, reinterpret_cast<int*>(ws + c.arrived)};
+    e = ffn::launch_experts_rows(x, top_k, gu, ids, p, pairs, top_k, kSilu, 1, ws + c.h, sum.arrived, ffn::rows_units(dn),
+                                 nullptr, s);
+    if (e == cudaSuccess) e = ffn::launch_experts_rows(ws + c.h, 1, dn, ids, p, pairs, top_k, kF32, c.splits, y, nullptr, 0, &sum, s);
+    return ffn::moe_status(e);
+  }
+  e = ffn::launch_moe_plan(ids, pairs, dn.experts, c.tc ? ffn::kTcTile : ffn::kRowsTile, p, s);
   if (c.tc) {
     if (e == cudaSuccess) e = ffn::launch_moe_gather(x, top_k, p, dn.experts, pairs, hidden, ws + c.xs, s);
-    if (e == cudaSuccess) e = ffn::launch_experts_tc(ws + c.xs, gu, p, pairs, ffn::ExpertsOut::kSiluMul, ws + c.h, s);
-    if (e == cudaSuccess) e = ffn::launch_experts_tc(ws + c.h, dn, p, pairs, ffn::ExpertsOut::kF32, ws + c.y, s);
+    if (e == cudaSuccess) e = ffn::launch_experts_tc(ws + c.xs, gu, p, pairs, kSilu, ws + c.h, s);
+    if (e == cudaSuccess) e = ffn::launch_experts_tc(ws + c.h, dn, p, pairs, kF32, y, s);
   } else {
-    if (e == cudaSuccess) e = ffn::launch_experts_rows(x, top_k, gu, p, pairs, ffn::ExpertsOut::kSiluMul, ws + c.h, s);
-    if (e == cudaSuccess) e = ffn::launch_experts_rows(ws + c.h, 1, dn, p, pairs, ffn::ExpertsOut::kF32, ws + c.y, s);
+    if (e == cudaSuccess)
+      e = ffn::launch_experts_rows(x, top_k, gu, ids, p, pairs, top_k, kSilu, 1, ws + c.h, nullptr, 0, nullptr, s);
+    if (e == cudaSuccess)
+      e = ffn::launch_experts_rows(ws + c.h, 1, dn, ids, p, pairs, top_k, kF32, c.splits, y, nullptr, 0, nullptr, s);
   }
-  if (e == cudaSuccess)
-    e = ffn::launch_moe_combine(reinterpret_cast<const float*>(ws + c.y), ids, weights, m, top_k, dn.experts, hidden,
-                                out, s);
+  if (e == cudaSuccess) e = ffn::launch_moe_combine(y, c.splits, ids, weights, m, top_k, dn.experts, hidden, out, s);
   return ffn::moe_status(e);
 }
 

@@ -3,13 +3,13 @@
 // its NVFP4 weight.
 //
 // A persistent CTA per SM walks the tiles (128 rows of one expert) x (a pair
-// of 128-row weight tiles: the gate and up tiles of the same columns, or two
-// consecutive tiles of a plain weight).  Per unit of two 64-element K chunks:
-//   * one warp streams the two weight tiles' chunks (18432 B) by bulk copies
+// of MMA operands of 128 weight rows: gate and up rows of the same columns, or
+// 256 consecutive rows of a plain weight).  Per unit of two 64-element K chunks:
+//   * one warp streams the weights' chunks (18432 B) by bulk copies
 //     and one the rows' chunks (2 x 128 x 128 B, 128-byte swizzle) by TMA;
-//   * two warpgroups, one per weight tile, decode the codes to bf16 and write
+//   * two warpgroups, one per operand, decode the codes to bf16 and write
 //     them to tensor memory, where they are the MMA's A operand (M = 128);
-//   * two threads, one per weight tile, issue tcgen05.mma kind::f16 against
+//   * two threads, one per operand, issue tcgen05.mma kind::f16 against
 //     the same rows in shared memory (N = 128), each into its own fp32
 //     accumulator.  A barrier wait, a fence and a commit cost an issuing thread
 //     about 0.1 us each while its MMAs of 64 cycles drain: one thread with
@@ -19,8 +19,8 @@
 //     back and run the epilogue while the next tile's MMAs proceed.
 // The pair is what bounds the traffic: a row tile is read from L2 once per 256
 // weight rows, 50 KB per unit of 1024 MMA cycles (50 B/clk per SM).
-// Tensor memory: accumulators in columns 0..255, two A slots of a unit and
-// tile each in columns 256..511.  Every wait is bounded; on expiry a device
+// Tensor memory: accumulators in columns 0..255, two A slots of a unit per
+// operand in columns 256..511.  Every wait is bounded; on expiry a device
 // error bit is raised and the CTA frees its tensor memory and exits.
 #include <cudaTypedefs.h>
 
@@ -48,10 +48,12 @@ __device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f 
 constexpr int kThreads = 640;
 constexpr int kUnit = 2;  // K chunks per unit
 constexpr int kXStages = 3, kWStages = 3, kASlots = 2;
-constexpr int kWStageBytes = 2 * kUnit * kChunkBytes;  // [chunk][tile of the pair]
+constexpr int kTiles = 4;  // weight tiles of 64 rows per CTA tile: two per MMA operand
+constexpr int kWStageBytes = kTiles * kUnit * kChunkBytes;  // [tile][chunk]
 constexpr int kXChunkBytes = kTcTile * 128, kXStageBytes = kUnit * kXChunkBytes;
 constexpr int kMine = kTcTile / 2;                      // rows of a tile per epilogue warpgroup
-constexpr int kParkBytes = kMine * kTileRows * 4;       // one warpgroup's half of an accumulator
+constexpr int kOpRows = 2 * kTileRows;                  // weight rows of an MMA operand
+constexpr int kParkBytes = kMine * kOpRows * 4;       // one warpgroup's half of an accumulator
 constexpr int kSmemW = kXStages * kXStageBytes;
 constexpr int kSmemPark = kSmemW + kWStages * kWStageBytes;
 constexpr int kSmemBar = kSmemPark + 2 * kParkBytes;
@@ -64,7 +66,7 @@ struct TcExpertsArgs {
   ExpertsView w;
   MoePlan plan;
   void* out;
-  int pairs_n;  // weight tile pairs per expert
+  int pairs_n;  // CTA tiles (two MMA operands) along the weight of an expert
 };
 
 struct TileInfo {
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
   uint64_t* xempty = xfull + kXStages;
   uint64_t* wfull = xempty + kXStages;
   uint64_t* wempty = wfull + kWStages;
-  uint64_t* afull = wempty + kWStages;     // [tile of the pair][slot]
+  uint64_t* afull = wempty + kWStages;     // [operand][slot]
   uint64_t* aempty = afull + 2 * kASlots;  // likewise
   uint64_t* accfull = aempty + 2 * kASlots;
   uint64_t* accempty = accfull + 1;
@@ -149,14 +151,13 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
       for (int T = blockIdx.x; ok && T < total; T += gridDim.x) {
         const TileInfo ti = tile_at(a, T);
         const size_t tile_bytes = (size_t)kc * kChunkBytes;
-        const uint8_t *w0, *w1;
-        if (MODE == (int)ExpertsOut::kSiluMul) {
-          w0 = a.w.tiles + ((size_t)ti.e * 2 * a.w.wtiles + ti.wt) * tile_bytes;
-          w1 = w0 + a.w.wtiles * tile_bytes;
-        } else {
-          w0 = a.w.tiles + ((size_t)ti.e * a.w.wtiles + 2 * ti.wt) * tile_bytes;
-          // an odd last tile stands in for the missing one, whose sums are not stored
-          w1 = 2 * ti.wt + 1 < a.w.wtiles ? w0 + tile_bytes : w0;
+        // Past the last tile, that tile stands in: its sums are not stored.
+        const uint8_t* w[kTiles];
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+          const bool silu = MODE == (int)ExpertsOut::kSiluMul;
+          const int tile = min(silu ? 2 * ti.wt + (i & 1) : kTiles * ti.wt + i, a.w.wtiles - 1);
+          w[i] = a.w.tiles + ((size_t)(silu ? 2 * ti.e + (i >> 1) : ti.e) * a.w.wtiles + tile) * tile_bytes;
         }
         for (int c = 0; c < kc; c += kUnit, ++u) {
           const int s = u % kWStages;
@@ -165,9 +166,10 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
             break;
           }
           const uint32_t bytes = min(kUnit, kc - c) * kChunkBytes;
-          mbar_arrive_expect_tx(&wfull[s], 2 * bytes);
-          bulk_load(wsm + s * kWStageBytes, w0 + (size_t)c * kChunkBytes, bytes, &wfull[s]);
-          bulk_load(wsm + s * kWStageBytes + kUnit * kChunkBytes, w1 + (size_t)c * kChunkBytes, bytes, &wfull[s]);
+          mbar_arrive_expect_tx(&wfull[s], kTiles * bytes);
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i)
+            bulk_load(wsm + s * kWStageBytes + i * kUnit * kChunkBytes, w[i] + (size_t)c * kChunkBytes, bytes, &wfull[s]);
         }
       }
       for (int r = max(0, u - kWStages); r < u; ++r) drain(&wfull[r % kWStages], (r / kWStages) & 1);
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
     // ----------------------------------------------------------- MMA issuers
     if (lane == 0) {
       const int half = warp - 2;
-      const uint32_t idesc = idesc_bf16_f32(kTileRows, kTcTile), d = tmem + 128 * half;
+      const uint32_t idesc = idesc_bf16_f32(kOpRows, kTcTile), d = tmem + 128 * half;
       int u = 0, i = 0;
       bool ok = true;
       for (int T = blockIdx.x; ok && T < total; T += gridDim.x, ++i) {
@@ -236,12 +238,13 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
         if (!ok) break;
         uint4 lo[kUnit], hi[kUnit];
         uint32_t sc[kUnit];
-        const uint8_t* w = wsm + sw * kWStageBytes + half * kUnit * kChunkBytes;
+        const uint8_t* w = wsm + sw * kWStageBytes + (2 * half + (row >> 6)) * kUnit * kChunkBytes;
+        const int r = row & 63;
 #pragma unroll
         for (int j = 0; j < kUnit; ++j) {  // (a missing second chunk reads what the stage held before)
-          lo[j] = *reinterpret_cast<const uint4*>(w + j * kChunkBytes + 16 * row);
-          hi[j] = *reinterpret_cast<const uint4*>(w + j * kChunkBytes + 2048 + 16 * row);
-          sc[j] = *reinterpret_cast<const uint32_t*>(w + j * kChunkBytes + 4096 + 16 * lane + 4 * q);
+          lo[j] = *reinterpret_cast<const uint4*>(w + j * kChunkBytes + code_offset(r, 0, j));
+          hi[j] = *reinterpret_cast<const uint4*>(w + j * kChunkBytes + code_offset(r, 1, j));
+          sc[j] = *reinterpret_cast<const uint32_t*>(w + j * kChunkBytes + scale_offset(r, j));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&wempty[sw]);
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
         tmem_ld32(lane_addr + 128 + 32 * h, t);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) park[(32 * h + j) * kTileRows + row] = gs1 * __uint_as_float(t[j]);
+        for (int j = 0; j < 32; ++j) park[(32 * h + j) * kOpRows + row] = gs1 * __uint_as_float(t[j]);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -323,24 +326,24 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
         // h = silu(g) * u, left as bf16 in the low half of u's own word
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {
-          float* u = park + j * kTileRows + row;
+          float* u = park + j * kOpRows + row;
           *reinterpret_cast<uint32_t*>(u) = f32_to_bf16_bits(silu_fast(v[j]) * *u);
         }
         // rows in sorted order, 16 bytes at a time (inter is a multiple of 32)
         named_bar_sync(1 + g, 128);
-        const int64_t inter = a.w.n / 2, c0 = kTileRows * (int64_t)ti.wt;
+        const int64_t inter = a.w.n / 2, c0 = kOpRows * (int64_t)ti.wt;
         uint16_t* h = static_cast<uint16_t*>(a.out) + first * inter + c0;
         for (int idx = et; idx < mine * 16; idx += 128) {
           const int j = idx >> 4, ch = idx & 15;
           if (c0 + 8 * ch >= inter) continue;
-          const uint4 p0 = *reinterpret_cast<const uint4*>(park + j * kTileRows + 8 * ch);
-          const uint4 p1 = *reinterpret_cast<const uint4*>(park + j * kTileRows + 8 * ch + 4);
+          const uint4 p0 = *reinterpret_cast<const uint4*>(park + j * kOpRows + 8 * ch);
+          const uint4 p1 = *reinterpret_cast<const uint4*>(park + j * kOpRows + 8 * ch + 4);
           *reinterpret_cast<uint4*>(h + j * inter + 8 * ch) =
               make_uint4(p0.x | (p0.y << 16), p0.z | (p0.w << 16), p1.x | (p1.y << 16), p1.z | (p1.w << 16));
         }
         named_bar_sync(1 + g, 128);
       } else {
-        const int64_t c0 = 2 * kTileRows * (int64_t)ti.wt + row, c1 = c0 + kTileRows, n = a.w.n;
+        const int64_t c0 = 2 * kOpRows * (int64_t)ti.wt + row, c1 = c0 + kOpRows, n = a.w.n;
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {
           if (j >= mine) break;
@@ -348,11 +351,11 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
           if (MODE == (int)ExpertsOut::kF32) {
             float* y = static_cast<float*>(a.out) + at;
             if (c0 < n) y[c0] = v[j];
-            if (c1 < n) y[c1] = park[j * kTileRows + row];
+            if (c1 < n) y[c1] = park[j * kOpRows + row];
           } else {
             uint16_t* y = static_cast<uint16_t*>(a.out) + at;
             if (c0 < n) y[c0] = f32_to_bf16_bits(v[j]);
-            if (c1 < n) y[c1] = f32_to_bf16_bits(park[j * kTileRows + row]);
+            if (c1 < n) y[c1] = f32_to_bf16_bits(park[j * kOpRows + row]);
           }
         }
       }
@@ -392,16 +395,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-    cudaGetLastError();
-    return 148;
-  }
-  return n;
-}
-
 template <int MODE>
 cudaError_t launch_one(const CUtensorMap& map, const TcExpertsArgs& a, int grid, cudaStream_t s) {
   auto kern = experts_tc_kernel<MODE>;
@@ -438,9 +431,9 @@ cudaError_t launch_experts_tc(const void* xs, const ExpertsView& w, const MoePla
   a.w = w;
   a.plan = p;
   a.out = out;
-  a.pairs_n = mode == ExpertsOut::kSiluMul ? w.wtiles : (w.wtiles + 1) / 2;
+  a.pairs_n = mode == ExpertsOut::kSiluMul ? (w.wtiles + 1) / 2 : (w.wtiles + kTiles - 1) / kTiles;
   const int64_t most = moe_max_tiles(pairs, w.experts, kTcTile) * a.pairs_n;
-  const int sms = sm_count();
+  const int sms = device_sms();
   const int grid = (int)(most < sms ? most : sms);
   ProfScope prof(s, mode == ExpertsOut::kSiluMul ? "experts_tc_silu" : "experts_tc");
   switch (mode) {

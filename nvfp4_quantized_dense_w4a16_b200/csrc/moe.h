@@ -18,13 +18,27 @@ inline ffn_status moe_status(cudaError_t e) {
 // Pick up errors of earlier asynchronous work before enqueuing more.
 inline ffn_status moe_precheck() { return moe_status(cudaPeekAtLastError()); }
 
-// Stacked experts as the kernels read them: E times the 128-row x 64-element
-// tiles of the bf16 activation format (launch_tile_weight with for_w4a16).
+// SMs of the current device (B200's, where there is none).
+inline int device_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    return 148;
+  }
+  return n;
+}
+
+// Stacked experts as the kernels read them: tiles of 64 rows (moe_decode.cuh).
+int experts_tiles(int64_t rows);
+size_t experts_tile_bytes(int64_t rows, int64_t k);
+cudaError_t launch_tile_experts(const void* codes, const void* scales, int64_t weights, int64_t rows, int64_t k,
+                                uint8_t* out, cudaStream_t s);
 struct ExpertsView {
-  const uint8_t* tiles = nullptr;  // [E][wtiles][kc][4608]; gate and up: [E][2][wtiles][kc][4608]
+  const uint8_t* tiles = nullptr;  // [E][wtiles][kc][2304]; gate and up: [E][2][wtiles][kc][2304]
   const float* gs = nullptr;       // [E], or [E][2] (gate, up)
   int experts = 0, kc = 0;
-  int wtiles = 0;                  // 128-row tiles of n (gate and up: of inter)
+  int wtiles = 0;                  // 64-row tiles of n (gate and up: of inter)
   int64_t n = 0, k = 0;            // logical dims (n = 2 * inter for gate and up)
   bool gate_up = false;
 };
@@ -51,16 +65,36 @@ enum class ExpertsOut : int {
   kF32 = 2       // y[p, :] = gs * acc, fp32
 };
 
+// Up to this many pairs the kernels for few rows read the ids themselves: no
+// plan is needed.
+constexpr int kFewPairs = 32;
+constexpr int kRowsTile = 16;  // rows of a plan's tiles for launch_experts_rows
+
+// How many ranges of K the down products are cut into for `tiles` tiles of
+// rows, so that the items fill the SMs evenly; each range leaves its own sums.
+constexpr int kMaxSplits = 8;
+int rows_splits(const ExpertsView& w, int64_t tiles);
+
+// The weighted sum over a row's experts, made by the down products themselves
+// (kF32, at most kFewPairs pairs): out = bf16(sum_j weights[j] * y[j]).
+struct RowsSum {
+  const float* weights;
+  void* out;
+  int* arrived;  // [rows_units(w)] zeroed words
+};
+inline int rows_units(const ExpertsView& w) { return w.gate_up ? w.wtiles : (w.wtiles + 1) / 2; }
+
 // Products of few rows per expert: row p of the input is x[p / row_div].
-cudaError_t launch_experts_rows(const void* x, int row_div, const ExpertsView& w, const MoePlan& p, int64_t pairs,
-                                ExpertsOut mode, void* out, cudaStream_t s);
-// out[i, :] = bf16(sum_j weights[i, j] * y[i * top_k + j, :]), j ascending.
-cudaError_t launch_moe_combine(const float* y, const int32_t* ids, const float* weights, int64_t m, int top_k,
-                               int experts, int64_t hidden, void* out, cudaStream_t s);
+// kF32 writes y [splits, pairs, n].  kBf16 also writes zeros for the pairs
+// without an expert.  `zero`: words that kSiluMul clears for a later launch.
+cudaError_t launch_experts_rows(const void* x, int row_div, const ExpertsView& w, const int32_t* ids, const MoePlan& p,
+                                int64_t pairs, int top_k, ExpertsOut mode, int splits, void* out, int* zero,
+                                int zero_count, const RowsSum* sum, cudaStream_t s);
+// out[i, :] = bf16(sum_j weights[i, j] * y[i * top_k + j, :]), j ascending, y the sum of its splits.
+cudaError_t launch_moe_combine(const float* y, int splits, const int32_t* ids, const float* weights, int64_t m,
+                               int top_k, int experts, int64_t hidden, void* out, cudaStream_t s);
 // Rows of y [pairs, n] bf16 whose id is outside [0, E): zeros.
 cudaError_t launch_experts_zero(const int32_t* ids, int64_t pairs, int experts, int64_t n, void* y, cudaStream_t s);
-
-constexpr int kRowsTile = 8;  // rows of one expert that launch_experts_rows takes at a time
 
 // Many rows per expert, on the tensor cores (plan with kTcTile rows a tile).
 // xs holds the rows sorted by expert, and kTcTile more rows of any content;
@@ -73,5 +107,6 @@ cudaError_t launch_moe_gather(const void* x, int row_div, const MoePlan& p, int 
                               void* xs, cudaStream_t s);
 // Error bits of these kernels' bounded waits, as read_device_error.
 cudaError_t read_moe_device_error(int* flags, bool clear);
+cudaError_t read_rows_device_error(int* flags, bool clear);
 
 }  // namespace ffn
