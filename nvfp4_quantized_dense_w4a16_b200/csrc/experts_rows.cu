@@ -114,22 +114,39 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// out[., col] = bf16(sum_j weights[., j] * y[., j, col]), j ascending, for the
-// rows first, first + step, ...: which CTA runs it changes no bit.
-__device__ __forceinline__ void rows_sum(const RowsArgs& a, int64_t col, int first, int step) {
-  if (col >= a.w.n) return;
-  const float* y = static_cast<const float*>(a.out) + col;
-  for (int row = first; row < a.pairs / a.top_k; row += step) {
-    float s = 0.0f;
-    for (int j = 0; j < a.top_k; ++j) {
-      const int64_t p = (int64_t)row * a.top_k + j;
-      const int id = __ldcg(a.ids + p);
-      float v = 0.0f;
-      if (id >= 0 && id < a.w.experts)
-        for (int i = 0; i < a.splits; ++i) v += __ldcg(y + ((int64_t)i * a.pairs + p) * a.w.n);
-      s = fmaf(__ldcg(a.weights + p), v, s);
+// out[., col] = bf16(sum_j weights[., j] * y[., j, col]), j ascending and y the
+// sum of its splits, for the rows first, first + step, ...: which CTA runs it
+// changes no bit.  With few pairs: lane p of every warp holds pair p's weight,
+// and in `there` the pairs that have an expert.
+__device__ __forceinline__ void rows_sum(const RowsArgs& a, int64_t col, int first, int step, uint32_t there,
+                                         float weight) {
+  const float* y = static_cast<const float*>(a.out) + min(col, a.w.n - 1);
+  const int64_t stride = (int64_t)a.pairs * a.w.n;
+  const int rows = a.pairs / a.top_k, terms = a.top_k * a.splits;
+  for (int row = first; row < rows; row += step) {
+    float sum = 0.0f, v = 0.0f;
+    int j = 0, i = 0;  // slot and split of the next term
+    for (int f = 0; f < terms; f += 8) {  // eight loads in flight
+      float t[8];
+      int jj = j, ii = i;
+#pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        const int p = row * a.top_k + jj;
+        t[z] = f + z < terms && ((there >> (p & 31)) & 1) ? __ldcg(y + ii * stride + (int64_t)p * a.w.n) : 0.0f;
+        if (++ii == a.splits) ii = 0, ++jj;
+      }
+#pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        v += t[z];
+        if (++i < a.splits) continue;
+        const float w = __shfl_sync(0xffffffffu, weight, (row * a.top_k + j) & 31);
+        if (j < a.top_k) sum = fmaf(w, v, sum);
+        v = 0.0f;
+        i = 0;
+        ++j;
+      }
     }
-    a.sum_out[row * a.w.n + col] = f32_to_bf16_bits(s);
+    if (col < a.w.n) a.sum_out[row * a.w.n + col] = f32_to_bf16_bits(sum);
   }
 }
 
@@ -351,6 +368,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1) experts_rows_kernel(const Row
     griddep_launch_dependents();
   }
 
+  uint32_t there = 0;  // for the sum
+  float weight = 0.0f;
+  if (SUM) {
+    there = __ballot_sync(0xffffffffu, tiles.id >= 0);
+    weight = lane < a.pairs ? __ldcg(a.weights + lane) : 0.0f;
+  }
+
   // ------------------------------------------------------------------ products
   const int row0 = 16 * own + g, h = t & 1, cc = t >> 1;  // first row, half and chunk of this lane's elements
   // offsets in a stage of this lane's codes (rows row0, row0 + 8), their scales and its elements of x
@@ -475,7 +499,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) experts_rows_kernel(const Row
       named_bar_sync(5, 32 * kRowsWarps);
       if (*last) {
         __threadfence();
-        rows_sum(a, 2 * kTileRows * (int64_t)unit + (threadIdx.x & 127), threadIdx.x >> 7, kRowsWarps / 4);
+        rows_sum(a, 2 * kTileRows * (int64_t)unit + (threadIdx.x & 127), threadIdx.x >> 7, kRowsWarps / 4, there, weight);
       }
     }
   }
@@ -488,8 +512,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) experts_rows_kernel(const Row
   if (a.zero && blockIdx.x == 0)
     for (int i = threadIdx.x; i < a.zero_count; i += 32 * kRowsWarps) a.zero[i] = 0;
   if (SUM && tiles.count == 0)  // no row has an expert
-    for (int64_t c = 128 * (int64_t)blockIdx.x + (threadIdx.x & 127); c < a.w.n; c += 128 * (int64_t)gridDim.x)
-      rows_sum(a, c, threadIdx.x >> 7, kRowsWarps / 4);
+    for (int64_t c = 128 * (int64_t)blockIdx.x; c < a.w.n; c += 128 * (int64_t)gridDim.x)
+      rows_sum(a, c + (threadIdx.x & 127), threadIdx.x >> 7, kRowsWarps / 4, there, weight);
 }
 
 // ----------------------------------------------------------- weighted sum
