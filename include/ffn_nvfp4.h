@@ -370,13 +370,14 @@ ffn_status ffn_nvfp4_experts_linear(const void* x, int64_t m, const ffn_nvfp4_ex
 
 /* The experts' SwiGLU layer and its weighted sum:
  *   out[i, :] = bf16(sum_j weights[i, j] * down_e(h)),  e = ids[i, j]
- *   h = bf16(silu(gate_e(x[i])) * up_e(x[i]))
+ *   h = silu(gate_e(x[i])) * up_e(x[i])
  *   x [m, hidden] bf16; gate_up a stack of [2 * inter, hidden] built with
  *   gate_up = 1; down a plain stack of [hidden, inter] of as many experts;
  *   ids int32 [m, top_k], weights fp32 [m, top_k] (ffn_nvfp4_moe_route's, or
  *   the caller's); out bf16 [m, hidden], only rows 0 .. m-1 are written.
  * Numerics: gate, up and the down products stay fp32; h is rounded once, to
- * bf16 (the down projection's operand), and the sum over j (ascending) once.
+ * bf16 (the down projection's operand; for m * top_k <= 32 to a pair of bf16
+ * numbers, 16 bits), and the sum over j (ascending) once.
  * (ffn_nvfp4_forward also rounds gate and up, following its source page.)
  * An id outside [0, experts) contributes weights[i, j] * 0, so padding rows
  * (all ids -1, weights 0) give zeros.  Deterministic: the same call gives the

@@ -73,6 +73,14 @@ constexpr int kStepChunks = 2;
 constexpr int kTileStep = kStepChunks * kChunkBytes;  // one tile's bytes of a step
 constexpr int kXRow = 256 + 16;                       // a row of x's bytes of a step, and 16 that spread the banks
 
+// With few pairs the hidden rows go to the down products as two bf16 parts (the
+// rounded value and what it lost), two columns of the MMA that are idle there
+// anyway, so that the sum over experts is rounded once.
+template <bool SUM>
+__host__ __device__ constexpr int parts_of() {
+  return SUM ? 2 : 1;
+}
+
 template <int NT>
 struct RowsCfg {
   static constexpr int kDepth = NT == 1 ? 4 : 3;  // stages of a group
@@ -255,7 +263,8 @@ template <int MODE, int NT, int FROM, bool SUM>
 __global__ void __launch_bounds__(kRowsThreads, 1) experts_rows_kernel(const RowsArgs a) {
   using C = RowsCfg<NT>;
   constexpr bool kPair = MODE == (int)ExpertsOut::kSiluMul;
-  constexpr int kRows = 8 * NT;
+  constexpr int kParts = parts_of<SUM>();         // columns of the MMA per row of x
+  constexpr int kRows = 8 * NT / kParts;
   extern __shared__ __align__(128) uint8_t rows_smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(rows_smem + C::kBars);  // [group][stage]
   uint64_t* empty = full + C::kStages;
@@ -299,13 +308,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1) experts_rows_kernel(const Row
     // ---------------------------------------------- stream of the group's steps
     int n = 0, step0 = 0, slot = -1;
     RowTile rt{0, 0, 0};
-    const uint16_t* xrow = nullptr;  // lane i: row i of x
+    const uint16_t* xrow = nullptr;  // lane i: row (and part) i of x
     bool ok = true, waited = !SUM;
     int held_rows[C::kDepth];        // x's part of the steps whose weights were fetched ahead of the wait
     const uint16_t* held_src[C::kDepth];
     uint32_t held_bytes[C::kDepth];
     auto fetch_x = [&](int s, const uint16_t* src, int rows, uint32_t bytes) {
-      if (lane < rows) bulk_load(ring + s * C::kStageBytes + 2 * kTileStep + lane * kXRow, src, bytes, &full[s]);
+      if (lane < rows * kParts) bulk_load(ring + s * C::kStageBytes + 2 * kTileStep + lane * kXRow, src, bytes, &full[s]);
     };
     auto wait = [&] {
       griddep_wait();
@@ -321,7 +330,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) experts_rows_kernel(const Row
       if (it.slot != slot) {
         slot = it.slot;
         rt = tiles.tile(slot, kRows);
-        xrow = a.x + (size_t)(FROM == kFromOneRow && a.row_div > 1 ? 0 : rt.pair / a.row_div) * k;
+        const int p = kParts == 1 ? rt.pair : __shfl_sync(0xffffffffu, rt.pair, lane / kParts);
+        xrow = a.x + (size_t)(FROM == kFromOneRow && a.row_div > 1 ? 0 : p / a.row_div * kParts + lane % kParts) * k;
       }
       const size_t tile_bytes = (size_t)a.w.kc * kChunkBytes;
       // a plain weight's missing second tile: the first stands in, its sums are not stored
@@ -337,7 +347,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) experts_rows_kernel(const Row
         const uint32_t bytes = min(kStepChunks, a.w.kc - kStepChunks * c) * kChunkBytes;
         const uint32_t xbytes = 2 * min(128, k - 128 * c);
         if (lane == 0) {
-          mbar_arrive_expect_tx(&full[s], 2 * bytes + rt.rows * xbytes);
+          mbar_arrive_expect_tx(&full[s], 2 * bytes + rt.rows * kParts * xbytes);
           bulk_load(ring + s * C::kStageBytes, w0 + (size_t)c * kTileStep, bytes, &full[s]);
           bulk_load(ring + s * C::kStageBytes + kTileStep, w1 + (size_t)c * kTileStep, bytes, &full[s]);
         }
@@ -464,20 +474,28 @@ __global__ void __launch_bounds__(kRowsThreads, 1) experts_rows_kernel(const Row
     const bool live = !*abort_flag;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int64_t p = __shfl_sync(0xffffffffu, rt.pair, 8 * i + on);
-      if (8 * i + on >= rt.rows || !live) continue;
+      const int row = (8 * i + on) / kParts;  // (of two parts, the first one's threads add both)
+      const int64_t p = __shfl_sync(0xffffffffu, rt.pair, row);
+      if (row >= rt.rows || on % kParts || !live) continue;
       const float* src = red + (i * 8 + 2 * oh + (on & 1)) * 32 + 4 * og + (on >> 1);
       float v = 0.0f, u = 0.0f;
 #pragma unroll
       for (int j = 0; j < kPhases; ++j) {
-        v += src[j * 4 * NT * 256];
-        u += src[j * 4 * NT * 256 + 4 * 32];
+#pragma unroll
+        for (int z = 0; z < kParts; ++z) {
+          v += src[j * 4 * NT * 256 + 32 * z];
+          u += src[j * 4 * NT * 256 + 4 * 32 + 32 * z];
+        }
       }
       const int r = 16 * own + 8 * oh + og;
       if (kPair) {
         const int64_t inter = a.w.n / 2, col = kTileRows * (int64_t)unit + r;
-        if (col < inter)
-          static_cast<uint16_t*>(a.out)[p * inter + col] = f32_to_bf16_bits(silu_f32(gs0 * v) * (gs1 * u));
+        const float hv = silu_f32(gs0 * v) * (gs1 * u), hi = bf16_round(hv);
+        uint16_t* o = static_cast<uint16_t*>(a.out) + p * (FROM == kFromPlan ? 1 : 2) * inter + col;
+        if (col < inter) {
+          o[0] = f32_to_bf16_bits(hi);
+          if (FROM != kFromPlan) o[inter] = f32_to_bf16_bits(isfinite(hi) ? hv - hi : 0.0f);
+        }
       } else {
         const int64_t col = 2 * kTileRows * (int64_t)unit + r;
         if (MODE == (int)ExpertsOut::kF32) {
@@ -583,7 +601,7 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s) {
   // set on every launch: the attribute belongs to the current device's context
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t most = moe_max_tiles(a.pairs, a.w.experts, 8 * NT) * rows_units(a.w) * a.splits;
+  const int64_t most = moe_max_tiles(a.pairs, a.w.experts, 8 * NT / parts_of<SUM>()) * rows_units(a.w) * a.splits;
   if (most > INT32_MAX) return cudaErrorInvalidValue;
   const int sms = device_sms();
   return launch_pdl(kern, dim3((unsigned)(most < sms ? most : sms)), dim3(kRowsThreads), kSmem, s, a);
@@ -595,9 +613,9 @@ cudaError_t launch_rows_from(const RowsArgs& a, cudaStream_t s) {
   constexpr int kNT = kRowsTile / 8;
   if (a.pairs > kFewPairs) return launch_rows<MODE, kNT, kFromPlan, false>(a, s);
   if (a.pairs == a.top_k) return launch_rows<MODE, 1, kFromOneRow, SUM>(a, s);
-  // an expert has at most one row per row of x where a row's ids differ: up to
-  // eight rows fill one tile of 8
-  return a.pairs / a.top_k <= 8 ? launch_rows<MODE, 1, kFromFew, SUM>(a, s) : launch_rows<MODE, kNT, kFromFew, SUM>(a, s);
+  // an expert has at most one row per row of x where a row's ids differ: so few
+  // rows fill one tile
+  return a.pairs / a.top_k <= 8 / parts_of<SUM>() ? launch_rows<MODE, 1, kFromFew, SUM>(a, s) : launch_rows<MODE, kNT, kFromFew, SUM>(a, s);
 }
 
 }  // namespace

@@ -84,7 +84,9 @@ struct RowsSum {
 };
 inline int rows_units(const ExpertsView& w) { return w.gate_up ? w.wtiles : (w.wtiles + 1) / 2; }
 
-// Products of few rows per expert: row p of the input is x[p / row_div].
+// Products of few rows per expert: row p of the input is x[p / row_div].  With
+// at most kFewPairs pairs kSiluMul writes h [pairs, 2, inter], the bf16 value
+// and (bf16) what it lost, and a kF32 launch with `sum` reads it so.
 // kF32 writes y [splits, pairs, n].  kBf16 also writes zeros for the pairs
 // without an expert.  `zero`: words that kSiluMul clears for a later launch.
 cudaError_t launch_experts_rows(const void* x, int row_div, const ExpertsView& w, const int32_t* ids, const MoePlan& p,

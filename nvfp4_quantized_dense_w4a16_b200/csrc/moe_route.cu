@@ -5,7 +5,17 @@
 // keys c = s + bias (optionally only inside the best groups of experts) and
 // the weights by s alone, renormalised over the chosen experts on request.
 //
-// One warp owns one row; lane l holds experts l, l + 32, ... in registers.
+// One warp owns one row; lane l holds experts l * EPL .. l * EPL + EPL - 1 in
+// registers.  Without a bias (and with group scores that are maxima) the keys
+// are monotone in the logits, which are compared as they are: exact.  Else the
+// keys are computed in fp32, and the row is computed again in 64 bits where two
+// keys whose order matters are closer than their error: the choice is always
+// that of 64-bit arithmetic, and few rows in a thousand pay for it.
+//
+// Bound by instructions: the logits of 16384 rows of 128 experts are 0.6 us of
+// memory traffic; top_k rounds of a warp-wide maximum (one redux instruction
+// and one vote each, the winner's lane then rescans its registers) take most
+// of the time.
 #include <math.h>
 
 #include "common.cuh"
@@ -46,148 +56,329 @@ __device__ __forceinline__ double warp_sum64(double v) {
   return v;
 }
 
-// log(sigmoid(l)), finite for every finite l.
-__device__ __forceinline__ double log_sigmoid(double l) {
-  return l < 0.0 ? l - log1p(exp(l)) : -log1p(exp(-l));
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
-template <int EPL, bool BF16>
-__global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteArgs a) {
-  extern __shared__ double route_smem[];  // [warps][experts] keys, only with groups
-  griddep_wait();
-  griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kRouteWarps + warp;
-  if (row >= a.m) return;
-  const int E = a.experts;
-  const bool softmax = a.scoring == FFN_MOE_SOFTMAX;
+// exp(a - b) for a <= b, to about two fp32 steps: the difference's rounding
+// error multiplies the result.  Zero for a far below b.
+__device__ __forceinline__ float exp_diff(float a, float b) {
+  const float d = a - b, bb = a - d;  // a - b = d + lo, lo = (a - (d + bb)) + (bb - b)
+  const float lo = (a - (d + bb)) + (bb - b);
+  return d > -200.0f ? expf(d) * (1.0f + lo) : 0.0f;
+}
 
-  float l[EPL];
-  double key[EPL];
-  bool bad = false;
-  double mx = -INFINITY;
+// sigmoid to about three fp32 steps.
+__device__ __forceinline__ float sigmoid_f32(float l) {
+  const float e = expf(-fabsf(l));
+  return (l >= 0.0f ? 1.0f : e) / (1.0f + e);
+}
+
+// The experts of the row that may be chosen after the groups: keys of the
+// others become -inf.  Key is float or double.  Returns how near the worst
+// group kept and the best one left out are (infinity: no matter).
+template <int EPL, typename Key>
+__device__ __forceinline__ Key keep_best_groups(const RouteArgs& a, Key (&key)[EPL], int lane, Key* smem) {
+  const int size = a.experts / a.groups;
+  const bool top2 = a.group_score == FFN_MOE_GROUP_TOP2;
+  Key best = -INFINITY, second = -INFINITY;  // of group `lane` (or of the lane's group)
+  auto take = [&](Key c) {
+    second = fmax(second, fmin(best, c));
+    best = fmax(best, c);
+  };
+  const int span = size / EPL;  // lanes of a group, where it is whole lanes
+  const bool whole = size % EPL == 0 && (span & (span - 1)) == 0;
+  if (whole) {
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 32 * i;
-    l[i] = -INFINITY;
-    if (e < E) {
-      l[i] = BF16 ? bf16_bits_to_float(static_cast<const uint16_t*>(a.logits)[row * a.ld + e])
-                  : static_cast<const float*>(a.logits)[row * a.ld + e];
-      bad |= isnan(l[i]) || (softmax && l[i] == INFINITY);
+    for (int i = 0; i < EPL; ++i) take(key[i]);
+    for (int o = 1; o < span; o <<= 1) {
+      const Key ob = __shfl_xor_sync(0xffffffffu, best, o), os = __shfl_xor_sync(0xffffffffu, second, o);
+      second = fmax(fmax(second, os), fmin(best, ob));
+      best = fmax(best, ob);
     }
-    if (!isnan(l[i])) mx = fmax(mx, (double)l[i]);
-  }
-  bad = __any_sync(0xffffffffu, bad);
-  mx = warp_max(mx);
-  double lse = 0.0;
-  if (softmax) {
-    double sum = 0.0;
+  } else {
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (l[i] > -INFINITY) sum += exp((double)l[i] - mx);
-    lse = mx + log(warp_sum64(sum));
+      if (lane * EPL + i < a.experts) smem[lane * EPL + i] = key[i];
+    __syncwarp();
+    if (lane < a.groups)
+      for (int i = 0; i < size; ++i) take(smem[lane * size + i]);
+    __syncwarp();
+  }
+  if (top2 && second > -INFINITY) best += second;
+  // rank among the groups: ties to the lower one
+  const int step = whole ? span : 1, mine = whole ? lane / span : lane;
+  int rank = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const Key o = __shfl_sync(0xffffffffu, best, g * step);
+    rank += o > best || (o == best && g < mine);
+  }
+  const bool in = mine < a.groups, kept = in && rank < a.top_groups;
+  Key low = kept ? best : (Key)INFINITY, high = in && !kept ? best : (Key)-INFINITY;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    low = fmin(low, __shfl_xor_sync(0xffffffffu, low, o));
+    high = fmax(high, __shfl_xor_sync(0xffffffffu, high, o));
+  }
+  const uint32_t open = __ballot_sync(0xffffffffu, kept);
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int g = whole ? lane : min((lane * EPL + i) / size, 31);
+    if (!((open >> g) & 1u)) key[i] = -INFINITY;
+  }
+  return high > -INFINITY && low < INFINITY ? low - high : (Key)INFINITY;
+}
+
+// The row's choice in 64 bits: lane j gets the j-th id (-1: none).
+template <int EPL>
+__device__ __noinline__ int choose_64(const RouteArgs& a, const float (&l)[EPL], int lane, double* smem) {
+  const bool softmax = a.scoring == FFN_MOE_SOFTMAX;
+  double key[EPL];
+  double top = -INFINITY, sum = 0.0;
+  if (softmax) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) top = fmax(top, (double)l[i]);
+    top = warp_max(top);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (l[i] > -INFINITY) sum += exp((double)l[i] - top);
+    sum = warp_sum64(sum);
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 32 * i;
     key[i] = -INFINITY;
-    if (e < E && l[i] > -INFINITY) {
-      double c = softmax ? (l[i] == INFINITY ? 1.0 : exp((double)l[i] - lse)) : 1.0 / (1.0 + exp(-(double)l[i]));
-      if (isnan(c)) c = 0.0;  // another expert's +inf: the row's weights are NaN, its ids go by the keys all the same
-      if (a.bias) c += (double)a.bias[e];
+    if (l[i] > -INFINITY) {
+      double c = softmax ? (l[i] == INFINITY ? 1.0 : exp((double)l[i] - top) / sum) : 1.0 / (1.0 + exp(-(double)l[i]));
+      if (isnan(c)) c = 0.0;  // beside a logit of +inf
+      if (a.bias) c += (double)a.bias[lane * EPL + i];
       if (c > -INFINITY) key[i] = c;
     }
   }
-
-  if (a.groups > 1) {
-    double* keys = route_smem + (size_t)warp * E;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (lane + 32 * i < E) keys[lane + 32 * i] = key[i];
-    __syncwarp();
-    const int size = E / a.groups;
-    double best = -INFINITY, second = -INFINITY;
-    if (lane < a.groups)
-      for (int i = 0; i < size; ++i) {
-        const double c = keys[lane * size + i];
-        second = fmax(second, fmin(best, c));
-        best = fmax(best, c);
-      }
-    if (a.group_score == FFN_MOE_GROUP_TOP2 && second > -INFINITY) best += second;
-    int rank = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const double o = __shfl_sync(0xffffffffu, best, g);
-      rank += o > best || (o == best && g < lane);
-    }
-    const uint32_t open = __ballot_sync(0xffffffffu, lane < a.groups && rank < a.top_groups);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E && !((open >> (e / size)) & 1u)) key[i] = -INFINITY;
-    }
-  }
-
-  // top_k rounds of a warp-wide maximum; lane j keeps the j-th choice
-  int my_id = -1;
-  float my_l = -INFINITY;
+  if (a.groups > 1) keep_best_groups<EPL, double>(a, key, lane, smem);
+  int mine = -1;
   for (int j = 0; j < a.top_k; ++j) {
     double best = -INFINITY;
     int at = 0x7fffffff;
-    float bl = -INFINITY;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
       if (key[i] > best) {
         best = key[i];
-        at = lane + 32 * i;
-        bl = l[i];
+        at = lane * EPL + i;
       }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const double ob = __shfl_xor_sync(0xffffffffu, best, o);
       const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-      const float ol = __shfl_xor_sync(0xffffffffu, bl, o);
       if (ob > best || (ob == best && oa < at)) {
         best = ob;
         at = oa;
-        bl = ol;
       }
     }
     if (best == -INFINITY) break;  // nothing is left
-    if (lane == j) {
-      my_id = at;
-      my_l = bl;
+    if (lane == j) mine = at;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (at == lane * EPL + i) key[i] = -INFINITY;
+  }
+  return mine;
+}
+
+// EPL logits of the row from expert lane * EPL on; -inf past the last expert.
+template <int EPL, bool BF16, bool WIDE>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t row, int lane, float (&l)[EPL]) {
+  constexpr int kBytes = EPL * (BF16 ? 2 : 4);
+  const char* p = static_cast<const char*>(a.logits) + (row * a.ld + lane * EPL) * (BF16 ? 2 : 4);
+  if (WIDE && lane * EPL < a.experts) {  // E is a multiple of EPL and every lane's logits are aligned
+    uint32_t w[(kBytes + 3) / 4];
+    if (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    } else if (kBytes == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      w[0] = kBytes == 4 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (at == lane + 32 * i) key[i] = -INFINITY;
+      l[i] = BF16 ? bf16_bits_to_float((w[i / 2] >> (16 * (i & 1))) & 0xffffu) : __uint_as_float(w[i]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    l[i] = -INFINITY;
+    if (!WIDE && lane * EPL + i < a.experts)
+      l[i] = BF16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
+  }
+}
+
+template <int EPL, bool BF16, bool WIDE>
+__global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteArgs a) {
+  extern __shared__ double route_smem[];  // [warps][experts], only with groups that are not whole lanes
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * kRouteWarps + warp;
+  if (row >= a.m) return;
+  const bool softmax = a.scoring == FFN_MOE_SOFTMAX;
+  // do the keys need more than the logits' order, does anything need the sum?
+  const bool scored = a.bias || (a.groups > 1 && a.group_score == FFN_MOE_GROUP_TOP2);
+  const bool summed = softmax && (scored || !a.renormalize);
+
+  float l[EPL], key[EPL];
+  load_logits<EPL, BF16, WIDE>(a, row, lane, l);
+  bool bad = false;
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    bad |= isnan(l[i]) || (softmax && l[i] == INFINITY);
+    if (isnan(l[i])) l[i] = -INFINITY;
+    top = fmaxf(top, l[i]);
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  float sum = 0.0f;
+  if (summed) {
+    top = redux_max(top);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      key[i] = l[i] == INFINITY ? 1.0f : l[i] > -INFINITY ? exp_diff(l[i], top) : 0.0f;
+      sum += key[i];
+    }
+    sum = warp_sum(sum);
+  }
+  if (scored) {
+    const float inv = summed ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      float c = softmax ? key[i] * inv : sigmoid_f32(l[i]);
+      if (a.bias && l[i] > -INFINITY) c += a.bias[lane * EPL + i];
+      key[i] = l[i] > -INFINITY && c > -INFINITY ? c : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = l[i];
+  }
+  // An upper bound of a key's error: EPL + 5 additions of the sum and about ten
+  // steps of the exponential, the quotient and the bias.
+  const float err = (EPL + 16) * 1.1920929e-7f;
+  bool close = false;
+  if (a.groups > 1) {
+    const float gap =
+        keep_best_groups<EPL, float>(a, key, lane, reinterpret_cast<float*>(route_smem + (size_t)warp * a.experts));
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) most = fmaxf(most, key[i] > -INFINITY ? fabsf(key[i]) : 0.0f);
+    close = scored && gap <= 4.0f * err * (1.0f + redux_max(most));
   }
 
-  // Renormalised weights go through the logarithms, so that scores that
-  // underflow still have their ratio.
-  double log_s = -INFINITY, w = 0.0;
-  if (my_id >= 0) log_s = softmax ? (double)my_l - lse : log_sigmoid((double)my_l);
+  // top_k rounds of a warp-wide maximum, and one for the runner-up; lane j
+  // keeps the j-th choice
+  int my_id = -1;
+  float my_l = -INFINITY, my_c = -INFINITY, next_c = -INFINITY, next_l = 0.0f, next_b = 0.0f;
+  float best = -INFINITY, best_l = -INFINITY;
+  int at = 0;
+  auto rescan = [&] {
+    best = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        best_l = l[i];
+        at = i;
+      }
+  };
+  rescan();
+  const int rounds = a.top_k + scored;
+  for (int j = 0; j < rounds; ++j) {
+    const float c = redux_max(best);
+    if (c == -INFINITY) break;  // nothing is left
+    const int w = __ffs(__ballot_sync(0xffffffffu, best == c)) - 1;  // the lowest lane: the lowest id
+    const int id = __shfl_sync(0xffffffffu, lane * EPL + at, w);
+    const float wl = __shfl_sync(0xffffffffu, best_l, w);
+    if (j == a.top_k) {
+      next_c = c;
+      next_l = wl;
+      next_b = a.bias ? a.bias[id] : 0.0f;
+      break;
+    }
+    if (lane == j) {
+      my_id = id;
+      my_l = wl;
+      my_c = c;
+    }
+    if (lane == w) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (i == at) key[i] = -INFINITY;
+      rescan();
+    }
+  }
+  if (scored) {
+    // Is a choice nearer to the next one than their errors?  (Equal logits with
+    // equal biases have equal keys.)
+    const float my_b = a.bias && my_id >= 0 ? a.bias[my_id] : 0.0f;
+    float c = __shfl_down_sync(0xffffffffu, my_c, 1), cl = __shfl_down_sync(0xffffffffu, my_l, 1),
+          cb = __shfl_down_sync(0xffffffffu, my_b, 1);
+    if (lane == a.top_k - 1) c = next_c, cl = next_l, cb = next_b;
+    close |= lane < a.top_k && c > -INFINITY && my_c - c <= 2.0f * err * (1.0f + fmaxf(fabsf(my_c), fabsf(c))) &&
+             !(cl == my_l && cb == my_b);
+    if (__any_sync(0xffffffffu, close)) {
+      my_id = choose_64<EPL>(a, l, lane, route_smem + (size_t)warp * a.experts);
+      // the chosen logits, from the lanes that hold them
+      my_l = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const float v = __shfl_sync(0xffffffffu, l[i], my_id >= 0 ? my_id / EPL : 0);
+        if (my_id >= 0 && my_id % EPL == i) my_l = v;
+      }
+    }
+  }
+
+  float w = 0.0f;
   if (a.renormalize) {
-    const double top = warp_max(log_s);
-    const double s = my_id >= 0 ? exp(log_s - top) : 0.0;
-    const double sum = warp_sum64(s);
-    if (my_id >= 0) w = s / sum;
+    // Ratios of exponentials where the scores are so (softmax; sigmoids of
+    // logits below -60, to e^-60): scores that underflow keep their ratio.
+    const float high = redux_max(my_l);
+    if (my_id >= 0) w = softmax || high < -60.0f ? exp_diff(my_l, high) : sigmoid_f32(my_l);
+    const float total = warp_sum(w);
+    if (my_id >= 0) w /= total;
   } else if (my_id >= 0) {
-    w = exp(log_s);
+    w = softmax ? exp_diff(my_l, top) / sum : sigmoid_f32(my_l);
   }
   if (lane < a.top_k) {
     a.ids[row * a.top_k + lane] = my_id;
-    a.weights[row * a.top_k + lane] = bad ? NAN : (float)(w * (double)a.scale);
+    a.weights[row * a.top_k + lane] = bad ? NAN : w * a.scale;
   }
+}
+
+template <int EPL, bool BF16>
+cudaError_t launch_epl(const RouteArgs& a, cudaStream_t s) {
+  const dim3 grid((unsigned)((a.m + kRouteWarps - 1) / kRouteWarps)), block(kRouteWarps * 32);
+  const int size = a.experts / a.groups, span = size / EPL;
+  const bool whole = size % EPL == 0 && (span & (span - 1)) == 0;
+  const size_t smem = a.groups > 1 && !whole ? sizeof(double) * kRouteWarps * a.experts : 0;
+  // one load of up to 16 bytes a time, where every lane's logits start on its boundary
+  constexpr int kElem = BF16 ? 2 : 4, kLoad = EPL * kElem < 16 ? EPL * kElem : 16;
+  const bool wide = a.experts % EPL == 0 && reinterpret_cast<uintptr_t>(a.logits) % kLoad == 0 &&
+                    (a.m == 1 || a.ld * kElem % kLoad == 0);
+  return wide ? launch_pdl(moe_route_kernel<EPL, BF16, true>, grid, block, smem, s, a)
+              : launch_pdl(moe_route_kernel<EPL, BF16, false>, grid, block, smem, s, a);
 }
 
 template <bool BF16>
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
-  const dim3 grid((unsigned)((a.m + kRouteWarps - 1) / kRouteWarps)), block(kRouteWarps * 32);
-  const size_t smem = a.groups > 1 ? sizeof(double) * kRouteWarps * a.experts : 0;
   ProfScope prof(s, "moe_route");
-  if (a.experts <= 64) return launch_pdl(moe_route_kernel<2, BF16>, grid, block, smem, s, a);
-  if (a.experts <= 256) return launch_pdl(moe_route_kernel<8, BF16>, grid, block, smem, s, a);
-  return launch_pdl(moe_route_kernel<32, BF16>, grid, block, smem, s, a);
+  if (a.experts <= 32) return launch_epl<1, BF16>(a, s);
+  if (a.experts <= 64) return launch_epl<2, BF16>(a, s);
+  if (a.experts <= 128) return launch_epl<4, BF16>(a, s);
+  if (a.experts <= 256) return launch_epl<8, BF16>(a, s);
+  if (a.experts <= 512) return launch_epl<16, BF16>(a, s);
+  return launch_epl<32, BF16>(a, s);
 }
 
 }  // namespace

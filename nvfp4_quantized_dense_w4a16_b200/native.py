@@ -9,6 +9,7 @@ fails loudly when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -134,9 +135,17 @@ def _fmt(fmt) -> int:
     return _FORMATS[fmt]
 
 
+# The raw handle of the current stream, without a Stream object around it
+# (which takes 3 us to make).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _ptr(t: torch.Tensor | None):
@@ -144,6 +153,9 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -348,6 +360,22 @@ def ffn_nvfp4_linear(x: torch.Tensor, w: Weight, fmt="bf16", y=None, workspace=N
     return y
 
 
+def _on_current_device(first: torch.Tensor, *others):
+    """Refuse tensors of another device than the current one: their pointers would mean nothing there."""
+    dev = first.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors are on cuda:{dev} and cuda:{t.get_device()}")
+
+
+@functools.lru_cache(maxsize=256)
+def _router(scoring, top_k, groups, top_groups, group_score, renormalize, scale):
+    return MoeRouter(MOE_SCORINGS[scoring], top_k, groups, top_groups, MOE_GROUP_SCORES[group_score],
+                     int(renormalize), scale)
+
+
 def ffn_nvfp4_moe_route(logits: torch.Tensor, top_k: int, scoring="softmax", bias=None, groups: int = 1,
                         top_groups: int = 1, group_score="max", renormalize: bool = True, scale: float = 1.0,
                         ids=None, weights=None, stream=None):
@@ -357,25 +385,26 @@ def ffn_nvfp4_moe_route(logits: torch.Tensor, top_k: int, scoring="softmax", bia
         raise TypeError("logits must be a torch.Tensor")
     if not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor (the library has no CPU path)")
-    if logits.dtype not in _LOGITS_TYPES:
+    kind = _LOGITS_TYPES.get(logits.dtype)
+    if kind is None:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     m, experts = logits.shape
     ld, step = logits.stride()
     if experts > 1 and step != 1 or m > 1 and ld < experts:
         raise ValueError("logits must have contiguous, non-overlapping rows")
-    dev = logits.device
     if bias is not None:
         _need(bias, "bias", torch.float32, (experts,))
-    ids = torch.empty((m, top_k), dtype=torch.int32, device=dev) if ids is None else ids
-    weights = torch.empty((m, top_k), dtype=torch.float32, device=dev) if weights is None else weights
+    ids = torch.empty((m, top_k), dtype=torch.int32, device=logits.device) if ids is None else ids
+    weights = torch.empty((m, top_k), dtype=torch.float32, device=logits.device) if weights is None else weights
     _need(ids, "ids", torch.int32, (m, top_k))
     _need(weights, "weights", torch.float32, (m, top_k))
-    router = MoeRouter(MOE_SCORINGS[scoring], top_k, groups, top_groups, MOE_GROUP_SCORES[group_score],
-                       int(renormalize), scale)
-    _check("ffn_nvfp4_moe_route", lib.ffn_nvfp4_moe_route(
-        logits.data_ptr(), _LOGITS_TYPES[logits.dtype], m, experts, ld if m > 1 else max(ld, experts),
-        None if bias is None else bias.data_ptr(), ctypes.byref(router), ids.data_ptr(), weights.data_ptr(),
-        _stream(stream)))
+    _on_current_device(logits, bias, ids, weights)
+    st = lib.ffn_nvfp4_moe_route(
+        logits.data_ptr(), kind, m, experts, ld if m > 1 else max(ld, experts), None if bias is None else bias.data_ptr(),
+        _router(scoring, top_k, groups, top_groups, group_score, renormalize, scale), ids.data_ptr(), weights.data_ptr(),
+        _stream(stream))
+    if st:
+        _check("ffn_nvfp4_moe_route", st)
     return ids, weights
 
 
@@ -416,6 +445,7 @@ def ffn_nvfp4_experts_create(codes: torch.Tensor, block_scales: torch.Tensor, gl
     k = 2 * half_k
     _need(block_scales, "block_scales", torch.uint8, (e, n, k // 16))
     _need(global_scales, "global_scales", torch.float32)
+    _on_current_device(codes, block_scales, global_scales)
     if gate_up and tuple(global_scales.shape) != (e, 2) or not gate_up and global_scales.numel() != e:
         raise ValueError(f"global_scales must hold {'[E, 2]' if gate_up else 'E'} values for {e} experts, "
                          f"got shape {tuple(global_scales.shape)}")
@@ -457,9 +487,11 @@ def ffn_nvfp4_experts_linear(x: torch.Tensor, w: Experts, ids: torch.Tensor, y=N
         workspace = _workspace(ffn_nvfp4_experts_workspace_size(m, top_k, w.experts, w.n, k), x.device, None)
     else:
         _need(workspace, "workspace", torch.uint8)
-    _check("ffn_nvfp4_experts_linear", lib.ffn_nvfp4_experts_linear(
-        x.data_ptr(), m, w.handle, ids.data_ptr(), top_k, y.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        _stream(stream)))
+    _on_current_device(x, ids, y, workspace)
+    st = lib.ffn_nvfp4_experts_linear(x.data_ptr(), m, w.handle, ids.data_ptr(), top_k, y.data_ptr(),
+                                      workspace.data_ptr(), workspace.numel(), _stream(stream))
+    if st:
+        _check("ffn_nvfp4_experts_linear", st)
     return y
 
 
@@ -480,9 +512,12 @@ def ffn_nvfp4_moe_forward(x: torch.Tensor, gate_up: Experts, down: Experts, ids:
         workspace = _workspace(ffn_nvfp4_moe_workspace_size(m, top_k, down.experts, hidden, inter), x.device, None)
     else:
         _need(workspace, "workspace", torch.uint8)
-    _check("ffn_nvfp4_moe_forward", lib.ffn_nvfp4_moe_forward(
-        x.data_ptr(), m, hidden, inter, gate_up.handle, down.handle, ids.data_ptr(), weights.data_ptr(), top_k,
-        out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    _on_current_device(x, ids, weights, out, workspace)
+    st = lib.ffn_nvfp4_moe_forward(x.data_ptr(), m, hidden, inter, gate_up.handle, down.handle, ids.data_ptr(),
+                                   weights.data_ptr(), top_k, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                   _stream(stream))
+    if st:
+        _check("ffn_nvfp4_moe_forward", st)
     return out
 
 

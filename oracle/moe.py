@@ -17,7 +17,7 @@ def log_score(logits: np.ndarray, scoring: str) -> np.ndarray:
     if scoring == "softmax":
         top = l.max()
         with np.errstate(invalid="ignore"):
-            return l - (top + np.log(np.exp(l - top).sum()))
+            return (l - top) - np.log(np.exp(l - top).sum())  # (top + log would swallow the log of huge logits)
     with np.errstate(over="ignore"):
         return np.where(l < 0, l - np.log1p(np.exp(np.minimum(l, 0))), -np.log1p(np.exp(-np.maximum(l, 0))))
 
