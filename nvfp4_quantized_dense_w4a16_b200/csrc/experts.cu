@@ -49,6 +49,7 @@ bool valid_pairs(int64_t m, int top_k) { return m <= (int64_t)INT32_MAX / 2 / to
 struct Carve {
   size_t offsets = 0, order = 0, tiles = 0, arrived = 0, xs = 0, h = 0, y = 0, total = 0;
   bool tc = false;
+  int tile_rows = 0;
   int splits = 1;  // of the down products' K
 };
 
@@ -67,11 +68,12 @@ Carve carve(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter
   const int64_t pairs = m * top_k;
   if (pairs == 0) return c;
   c.tc = use_tc(pairs, experts);
+  c.tile_rows = c.tc ? ffn::kTcTile : ffn::rows_tile(pairs, experts);
   const int64_t padded = pairs + ffn::kTcTile;
   size_t off = 0;
   c.offsets = take(off, sizeof(int) * (experts + 1));
   c.order = take(off, sizeof(int) * pairs);
-  c.tiles = take(off, sizeof(int) * (1 + 3 * ffn::moe_max_tiles(pairs, experts, c.tc ? ffn::kTcTile : ffn::kRowsTile)));
+  c.tiles = take(off, sizeof(int) * (1 + 3 * ffn::moe_max_tiles(pairs, experts, c.tile_rows)));
   c.arrived = take(off, sizeof(int) * ((hidden + 127) / 128));
   if (inter > 0 && !c.tc) {
     ffn::ExpertsView down;
@@ -198,11 +200,10 @@ ffn_status ffn_nvfp4_experts_linear(const void* x, int64_t m, const ffn_nvfp4_ex
   const int64_t pairs = m * top_k;
   cudaError_t e = cudaSuccess;
   if (pairs > ffn::kFewPairs)
-    e = ffn::launch_moe_plan(ids, pairs, v.experts, c.tc ? ffn::kTcTile : ffn::kRowsTile, p, s);
+    e = ffn::launch_moe_plan(ids, pairs, v.experts, c.tile_rows, p, s);
   if (c.tc) {
-    if (e == cudaSuccess) e = ffn::launch_moe_gather(x, top_k, p, v.experts, pairs, v.k, ws + c.xs, s);
+    if (e == cudaSuccess) e = ffn::launch_moe_gather(x, top_k, p, v.experts, pairs, v.k, ws + c.xs, y, v.n, s);
     if (e == cudaSuccess) e = ffn::launch_experts_tc(ws + c.xs, v, p, pairs, ffn::ExpertsOut::kBf16, y, s);
-    if (e == cudaSuccess) e = ffn::launch_experts_zero(ids, pairs, v.experts, v.n, y, s);
   } else if (e == cudaSuccess) {
     e = ffn::launch_experts_rows(x, top_k, v, ids, p, pairs, top_k, ffn::ExpertsOut::kBf16, 1, y, nullptr, 0, nullptr, s);
   }
@@ -251,9 +252,9 @@ ffn_status ffn_nvfp4_moe_forward(const void* x, int64_t m, int64_t hidden, int64
     if (e == cudaSuccess) e = ffn::launch_experts_rows(ws + c.h, 1, dn, ids, p, pairs, top_k, kF32, c.splits, y, nullptr, 0, &sum, s);
     return ffn::moe_status(e);
   }
-  e = ffn::launch_moe_plan(ids, pairs, dn.experts, c.tc ? ffn::kTcTile : ffn::kRowsTile, p, s);
+  e = ffn::launch_moe_plan(ids, pairs, dn.experts, c.tile_rows, p, s);
   if (c.tc) {
-    if (e == cudaSuccess) e = ffn::launch_moe_gather(x, top_k, p, dn.experts, pairs, hidden, ws + c.xs, s);
+    if (e == cudaSuccess) e = ffn::launch_moe_gather(x, top_k, p, dn.experts, pairs, hidden, ws + c.xs, nullptr, 0, s);
     if (e == cudaSuccess) e = ffn::launch_experts_tc(ws + c.xs, gu, p, pairs, kSilu, ws + c.h, s);
     if (e == cudaSuccess) e = ffn::launch_experts_tc(ws + c.h, dn, p, pairs, kF32, y, s);
   } else {

@@ -1,6 +1,8 @@
 // Products of few rows with the NVFP4 weights of the experts picked for them
 // (decode), the plan that sorts the rows by expert, and the weighted sum of
 // the experts' outputs.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "launch.cuh"
 #include "moe.h"
@@ -17,51 +19,100 @@ using namespace sm100;
 // ---------------------------------------------------------------- the plan
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanEach = 4;  // ids a thread takes at a time
 
-// One CTA: a histogram of the ids, its prefix sums, and the scatter of the
-// pairs.  The order of an expert's rows follows the atomics; no result
-// depends on it, as every row is computed by itself.
+// One CTA, or a cluster of them that share the pairs: a histogram of the ids,
+// its prefix sums over the experts (and over the cluster's CTAs, read from
+// their shared memory), and the scatter of the pairs.  Pairs without an expert
+// form the bucket behind the last expert.  The order of an expert's rows
+// follows the atomics; no result depends on it, as every row is computed by
+// itself.
 __global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(const int32_t* __restrict__ ids, int pairs, int E,
                                                                int tile_rows, MoePlan p) {
+  namespace cg = cooperative_groups;
   extern __shared__ int plan_smem[];
-  int* count = plan_smem;       // [E]
-  int* start = plan_smem + E;   // [E]
-  int* tile0 = plan_smem + 2 * E;
+  int* count = plan_smem;              // [E + 1]
+  int* start = plan_smem + E + 1;      // [E + 1]
+  __shared__ int2 warp_sums[kPlanThreads / 32];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   griddep_wait();
   griddep_launch_dependents();
-  for (int e = threadIdx.x; e < E; e += blockDim.x) count[e] = 0;
+  for (int e = threadIdx.x; e <= E; e += kPlanThreads) count[e] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
-    const int e = ids[i];
-    if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+  const int each = (pairs + ctas - 1) / ctas, p0 = min(pairs, rank * each), p1 = min(pairs, p0 + each);
+  for (int i0 = p0 + threadIdx.x; i0 < p1; i0 += kPlanEach * kPlanThreads) {
+    int e[kPlanEach];
+#pragma unroll
+    for (int j = 0; j < kPlanEach; ++j) e[j] = i0 + j * kPlanThreads < p1 ? ids[i0 + j * kPlanThreads] : -1;
+#pragma unroll
+    for (int j = 0; j < kPlanEach; ++j)
+      if (i0 + j * kPlanThreads < p1) atomicAdd(&count[e[j] >= 0 && e[j] < E ? e[j] : E], 1);
   }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int at = 0, tiles = 0;
-    for (int e = 0; e < E; ++e) {
-      start[e] = at;
-      tile0[e] = tiles;
-      p.offsets[e] = at;
-      at += count[e];
-      tiles += (count[e] + tile_rows - 1) / tile_rows;
+  cluster.sync();
+  // thread e: its expert's rows in all CTAs, and in those before this one (E + 1 may exceed the block by one)
+  int at = 0, tiles = 0;  // of the chunks of experts before
+  for (int e0 = 0; e0 <= E; e0 += kPlanThreads) {
+    const int e = e0 + threadIdx.x;
+    int all = 0, before = 0;
+    if (e <= E)
+      for (int c = 0; c < ctas; ++c) {
+        const int n = ctas == 1 ? count[e] : *cluster.map_shared_rank(&count[e], c);
+        before += c < rank ? n : 0;
+        all += n;
+      }
+    const int mine = e < E ? (all + tile_rows - 1) / tile_rows : 0;
+    int2 sum = make_int2(all, mine);  // inclusive scan over the block
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sum.x, o), y = __shfl_up_sync(0xffffffffu, sum.y, o);
+      if ((threadIdx.x & 31) >= o) sum.x += x, sum.y += y;
     }
-    p.offsets[E] = at;
-    p.tiles[0] = tiles;
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    int* t = p.tiles + 1 + 3 * tile0[e];
-    for (int r = 0; r < count[e]; r += tile_rows, t += 3) {
-      t[0] = e;
-      t[1] = start[e] + r;
-      t[2] = min(tile_rows, count[e] - r);
+    if ((threadIdx.x & 31) == 31) warp_sums[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      int2 w = warp_sums[threadIdx.x];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, w.x, o), y = __shfl_up_sync(0xffffffffu, w.y, o);
+        if (threadIdx.x >= o) w.x += x, w.y += y;
+      }
+      warp_sums[threadIdx.x] = w;
     }
+    __syncthreads();
+    if (threadIdx.x >= 32) {
+      const int2 w = warp_sums[(threadIdx.x >> 5) - 1];
+      sum.x += w.x, sum.y += w.y;
+    }
+    if (e <= E) {
+      const int first = at + sum.x - all;
+      start[e] = first + before;
+      if (rank == 0) {
+        p.offsets[e] = first;
+        int* t = p.tiles + 1 + 3 * (tiles + sum.y - mine);
+        if (e < E)
+          for (int r = 0; r < all; r += tile_rows, t += 3) {
+            t[0] = e;
+            t[1] = first + r;
+            t[2] = min(tile_rows, all - r);
+          }
+      }
+    }
+    at += warp_sums[kPlanThreads / 32 - 1].x;
+    tiles += warp_sums[kPlanThreads / 32 - 1].y;
+    __syncthreads();
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
-    const int e = ids[i];
-    if (e >= 0 && e < E) p.order[atomicAdd(&start[e], 1)] = i;
+  if (rank == 0 && threadIdx.x == 0) p.tiles[0] = tiles;
+  for (int i0 = p0 + threadIdx.x; i0 < p1; i0 += kPlanEach * kPlanThreads) {
+    int e[kPlanEach];
+#pragma unroll
+    for (int j = 0; j < kPlanEach; ++j) e[j] = i0 + j * kPlanThreads < p1 ? ids[i0 + j * kPlanThreads] : -1;
+#pragma unroll
+    for (int j = 0; j < kPlanEach; ++j)
+      if (i0 + j * kPlanThreads < p1)
+        p.order[atomicAdd(&start[e[j] >= 0 && e[j] < E ? e[j] : E], 1)] = i0 + j * kPlanThreads;
   }
+  cluster.sync();  // the others may still read this CTA's counts
 }
 
 // ------------------------------------------------------ products, few rows
@@ -390,7 +441,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) experts_rows_kernel(const Row
   // offsets in a stage of this lane's codes (rows row0, row0 + 8), their scales and its elements of x
   const int at0 = cc * kChunkBytes + code_offset(row0, h, cc), at1 = cc * kChunkBytes + code_offset(row0 + 8, h, cc);
   const int at_sc = cc * kChunkBytes + scale_offset(row0, cc), at_x = 2 * kTileStep + g * kXRow + 64 * t;
-  const uint32_t pick = h ? 0x4432 : 0x4410;  // this half's two scales
+  const uint32_t pick0 = h ? 0x4242 : 0x4040, pick1 = pick0 + 0x0101;  // this half's two scales
   int n = 0, step0 = 0, slot = -1, buf = 0;  // the group's steps, the items' steps so far
   RowTile rt{0, 0, 0};
   float gs0 = 0.0f, gs1 = 0.0f;
@@ -411,14 +462,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1) experts_rows_kernel(const Row
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint8_t* st = ring + s * C::kStageBytes;
       uint4 cw[4];
-      uint32_t s01[4];
+      uint32_t sc[4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         cw[2 * j] = *reinterpret_cast<const uint4*>(st + j * kTileStep + at0);
         cw[2 * j + 1] = *reinterpret_cast<const uint4*>(st + j * kTileStep + at1);
-        const uint2 sc = *reinterpret_cast<const uint2*>(st + j * kTileStep + at_sc);
-        s01[2 * j] = __byte_perm(sc.x, 0, pick);
-        s01[2 * j + 1] = __byte_perm(sc.y, 0, pick);
+        const uint2 v = *reinterpret_cast<const uint2*>(st + j * kTileStep + at_sc);
+        sc[2 * j] = v.x;
+        sc[2 * j + 1] = v.y;
       }
       // Columns of the MMA are independent and those behind the last row are
       // not stored: their lanes read whatever the stage holds.
@@ -431,22 +482,24 @@ __global__ void __launch_bounds__(kRowsThreads, 1) experts_rows_kernel(const Row
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           cw[j] = make_uint4(0, 0, 0, 0);
-          s01[j] = 0;
+          sc[j] = 0;
 #pragma unroll
           for (int i = 0; i < NT; ++i) xv[i][j] = make_uint4(0, 0, 0, 0);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);  // the step is in registers
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s01[j] = scale_pair(s01[j]);
+      uint32_t s2[4];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         uint32_t d[4][4];
+        if (w == 0 || w == 2)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s2[j] = scale_twice(sc[j], w == 0 ? pick0 : pick1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t word = w == 0 ? cw[j].x : w == 1 ? cw[j].y : w == 2 ? cw[j].z : cw[j].w;
-          decode8(word, __byte_perm(s01[j], 0, w < 2 ? 0x1010 : 0x3232), d[j]);
+          decode8(word, s2[j], d[j]);
         }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -572,24 +625,28 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const float* __restric
                  (uint32_t)f32_to_bf16_bits(s.z) | ((uint32_t)f32_to_bf16_bits(s.w) << 16));
 }
 
-__global__ void __launch_bounds__(256) experts_zero_kernel(const int32_t* __restrict__ ids, int64_t pairs,
-                                                           int experts, int64_t n, uint16_t* __restrict__ y) {
-  griddep_wait();
-  griddep_launch_dependents();
-  for (int64_t p = blockIdx.x; p < pairs; p += gridDim.x) {
-    const int e = ids[p];
-    if (e >= 0 && e < experts) continue;
-    for (int64_t c = threadIdx.x; c < n; c += blockDim.x) y[p * n + c] = 0;
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_moe_plan(const int32_t* ids, int64_t pairs, int experts, int tile_rows, const MoePlan& p,
                             cudaStream_t s) {
   ProfScope prof(s, "moe_plan");
-  return launch_pdl(moe_plan_kernel, dim3(1), dim3(kPlanThreads), 3 * sizeof(int) * experts, s, ids, (int)pairs,
-                    experts, tile_rows, p);
+  // a CTA takes its ids in one go up to kPlanEach a thread; eight CTAs cut a
+  // prompt's 32768 pairs from 35 to 6 us, and a second one costs a small batch 1 us
+  const int ctas = pairs <= kPlanEach * kPlanThreads ? 1 : 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = 2 * sizeof(int) * (experts + 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = profiling() ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, moe_plan_kernel, ids, (int)pairs, experts, tile_rows, p);
 }
 
 namespace {
@@ -610,8 +667,10 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s) {
 // SUM: of few pairs; from a plan the sum is a launch of its own.
 template <int MODE, bool SUM>
 cudaError_t launch_rows_from(const RowsArgs& a, cudaStream_t s) {
-  constexpr int kNT = kRowsTile / 8;
-  if (a.pairs > kFewPairs) return launch_rows<MODE, kNT, kFromPlan, false>(a, s);
+  constexpr int kNT = 2;
+  if (a.pairs > kFewPairs)
+    return rows_tile(a.pairs, a.w.experts) == 8 ? launch_rows<MODE, 1, kFromPlan, false>(a, s)
+                                                : launch_rows<MODE, kNT, kFromPlan, false>(a, s);
   if (a.pairs == a.top_k) return launch_rows<MODE, 1, kFromOneRow, SUM>(a, s);
   // an expert has at most one row per row of x where a row's ids differ: so few
   // rows fill one tile
@@ -674,12 +733,6 @@ cudaError_t launch_moe_combine(const float* y, int splits, const int32_t* ids, c
   const int64_t blocks = (m * (hidden / 4) + 255) / 256;
   return launch_pdl(moe_combine_kernel, dim3((unsigned)blocks), dim3(256), 0, s, y, splits, ids, weights, m, top_k,
                     experts, hidden, static_cast<uint16_t*>(out));
-}
-
-cudaError_t launch_experts_zero(const int32_t* ids, int64_t pairs, int experts, int64_t n, void* y, cudaStream_t s) {
-  ProfScope prof(s, "experts_zero");
-  return launch_pdl(experts_zero_kernel, dim3((unsigned)(pairs < 65536 ? pairs : 65536)), dim3(256), 0, s, ids, pairs,
-                    experts, n, static_cast<uint16_t*>(y));
 }
 
 }  // namespace ffn

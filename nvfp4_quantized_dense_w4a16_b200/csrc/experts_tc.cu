@@ -251,13 +251,14 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
 #pragma unroll
         for (int j = 0; j < kUnit; ++j) {
           if (j >= nc) break;
-          const uint32_t s01 = scale_pair(sc[j] & 0xffffu), s23 = scale_pair(sc[j] >> 16);
+          const uint32_t s2[4] = {scale_twice(sc[j], 0x4040), scale_twice(sc[j], 0x4141), scale_twice(sc[j], 0x4242),
+                                  scale_twice(sc[j], 0x4343)};
           const uint32_t words[8] = {lo[j].x, lo[j].y, lo[j].z, lo[j].w, hi[j].x, hi[j].y, hi[j].z, hi[j].w};
           uint32_t v[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             uint32_t o[4];
-            decode8(words[i], __byte_perm(i < 4 ? s01 : s23, 0, (i & 2) ? 0x3232 : 0x1010), o);
+            decode8(words[i], s2[i >> 1], o);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[4 * i + k] = o[k];
           }
@@ -369,17 +370,24 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
   }
 }
 
-// xs[q, :] = x[order[q] / row_div, :] for the sorted positions q.
+// xs[q, :] = x[order[q] / row_div, :] for the sorted positions q, a warp each.
+// Behind the last expert's rows: zeros to the rows of y that have no expert.
 __global__ void __launch_bounds__(256) moe_gather_kernel(const uint4* __restrict__ x, int row_div, MoePlan p,
-                                                         int experts, int64_t pairs, int vecs,
-                                                         uint4* __restrict__ xs) {
+                                                         int experts, int64_t pairs, int vecs, uint4* __restrict__ xs,
+                                                         uint16_t* __restrict__ y, int64_t n) {
   griddep_wait();
   griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
   const int64_t q = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (q >= p.offsets[experts]) return;
-  const uint4* src = x + (int64_t)(p.order[q] / row_div) * vecs;
-  uint4* dst = xs + q * vecs;
-  for (int i = threadIdx.x & 31; i < vecs; i += 32) dst[i] = __ldg(src + i);
+  if (q >= pairs) return;
+  const int64_t pair = p.order[q];
+  if (q < p.offsets[experts]) {
+    const uint4* src = x + (pair / row_div) * vecs;
+    uint4* dst = xs + q * vecs;
+    for (int i = lane; i < vecs; i += 32) dst[i] = __ldg(src + i);
+  } else if (y) {
+    for (int64_t c = lane; c < n; c += 32) y[pair * n + c] = 0;
+  }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -407,10 +415,11 @@ cudaError_t launch_one(const CUtensorMap& map, const TcExpertsArgs& a, int grid,
 }  // namespace
 
 cudaError_t launch_moe_gather(const void* x, int row_div, const MoePlan& p, int experts, int64_t pairs, int64_t k,
-                              void* xs, cudaStream_t s) {
+                              void* xs, void* y, int64_t n, cudaStream_t s) {
   ProfScope prof(s, "moe_gather");
   return launch_pdl(moe_gather_kernel, dim3((unsigned)((pairs + 7) / 8)), dim3(256), 0, s,
-                    static_cast<const uint4*>(x), row_div, p, experts, pairs, (int)(k / 8), static_cast<uint4*>(xs));
+                    static_cast<const uint4*>(x), row_div, p, experts, pairs, (int)(k / 8), static_cast<uint4*>(xs),
+                    static_cast<uint16_t*>(y), n);
 }
 
 cudaError_t launch_experts_tc(const void* xs, const ExpertsView& w, const MoePlan& p, int64_t pairs, ExpertsOut mode,

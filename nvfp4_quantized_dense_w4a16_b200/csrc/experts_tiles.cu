@@ -9,9 +9,8 @@ namespace {
 
 using namespace moe;
 
-// One thread per row of a tile's chunk.  Scales lose the sign bit (they are
-// magnitudes); a block whose scale is zero gets zero codes; rows and K past
-// the weight are zero.
+// One thread per row of a tile's chunk.  A block whose scale is zero gets zero
+// codes; rows and K past the weight are zero.
 __global__ void __launch_bounds__(256) tile_experts_kernel(const uint8_t* __restrict__ codes,
                                                            const uint8_t* __restrict__ scales, int64_t weights,
                                                            int64_t rows, int64_t k, int tiles, int kc,
@@ -32,7 +31,7 @@ __global__ void __launch_bounds__(256) tile_experts_kernel(const uint8_t* __rest
       if (64 * (int64_t)c + 32 * h < k) {  // k is a multiple of 32
         const uint4 v = *reinterpret_cast<const uint4*>(crow + 16 * h);
         w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
-        sc |= (uint32_t)(srow[2 * h] & 0x7F) << (16 * h) | (uint32_t)(srow[2 * h + 1] & 0x7F) << (16 * h + 8);
+        sc |= scale_byte(srow[2 * h]) << (16 * h) | scale_byte(srow[2 * h + 1]) << (16 * h + 8);
       }
   }
 #pragma unroll

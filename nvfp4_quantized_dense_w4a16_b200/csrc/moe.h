@@ -47,7 +47,7 @@ struct ExpertsView {
 // in [0, E): device arrays in the caller's workspace.
 struct MoePlan {
   int* offsets;  // [E + 1]: expert e owns order[offsets[e] .. offsets[e + 1])
-  int* order;    // [pairs]: the pairs, expert by expert
+  int* order;    // [pairs]: the pairs, expert by expert, then those without one
   int* tiles;    // [0]: number of tiles; then per tile {expert, first, rows}
 };
 
@@ -68,7 +68,9 @@ enum class ExpertsOut : int {
 // Up to this many pairs the kernels for few rows read the ids themselves: no
 // plan is needed.
 constexpr int kFewPairs = 32;
-constexpr int kRowsTile = 16;  // rows of a plan's tiles for launch_experts_rows
+// Rows of a plan's tiles for launch_experts_rows: 8, where a tile of 16 would be
+// half empty on average.
+inline int rows_tile(int64_t pairs, int64_t experts) { return pairs <= 5 * experts ? 8 : 16; }
 
 // How many ranges of K the down products are cut into for `tiles` tiles of
 // rows, so that the items fill the SMs evenly; each range leaves its own sums.
@@ -95,18 +97,15 @@ cudaError_t launch_experts_rows(const void* x, int row_div, const ExpertsView& w
 // out[i, :] = bf16(sum_j weights[i, j] * y[i * top_k + j, :]), j ascending, y the sum of its splits.
 cudaError_t launch_moe_combine(const float* y, int splits, const int32_t* ids, const float* weights, int64_t m,
                                int top_k, int experts, int64_t hidden, void* out, cudaStream_t s);
-// Rows of y [pairs, n] bf16 whose id is outside [0, E): zeros.
-cudaError_t launch_experts_zero(const int32_t* ids, int64_t pairs, int experts, int64_t n, void* y, cudaStream_t s);
-
 // Many rows per expert, on the tensor cores (plan with kTcTile rows a tile).
 // xs holds the rows sorted by expert, and kTcTile more rows of any content;
 // kSiluMul writes h in the same order, the others write row p of the pair.
 constexpr int kTcTile = 128;
 cudaError_t launch_experts_tc(const void* xs, const ExpertsView& w, const MoePlan& p, int64_t pairs, ExpertsOut mode,
                               void* out, cudaStream_t s);
-// xs[q, :] = x[order[q] / row_div, :]
+// xs[q, :] = x[order[q] / row_div, :]; with y, zeros to its rows without an expert.
 cudaError_t launch_moe_gather(const void* x, int row_div, const MoePlan& p, int experts, int64_t pairs, int64_t k,
-                              void* xs, cudaStream_t s);
+                              void* xs, void* y, int64_t n, cudaStream_t s);
 // Error bits of these kernels' bounded waits, as read_device_error.
 cudaError_t read_moe_device_error(int* flags, bool clear);
 cudaError_t read_rows_device_error(int* flags, bool clear);

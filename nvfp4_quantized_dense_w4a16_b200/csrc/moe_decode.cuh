@@ -15,6 +15,9 @@
 // exponent bits and the top mantissa bit, subnormal for 0 and 0.5).  The block
 // scale is applied as the bf16 number s * 2^118, so an element is exactly
 // E2M1 * s * 2^-8 (at most 6 significant bits), and sums are scaled by 2^8.
+// Scales have no sign, so a byte holds five exponent bits and the mantissa's
+// three: E4M3's subnormal scales are normal there, and a scale becomes a bf16
+// number by one shift and one addition.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -65,14 +68,17 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
-// Two E4M3 scales (no sign) -> the bf16 numbers s * 2^118, low byte in the low
-// half.  The half-precision value is exact; three bits to the right its
-// exponent field is bf16's, re-biased.  (A zero scale gives 2^103; its block's
-// codes are zero.)
-__device__ __forceinline__ uint32_t scale_pair(uint32_t two) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(two));
-  return ((h >> 3) & 0x1FFF1FFFu) + 0x73007300u;
+// E4M3 byte (its sign ignored) -> scale byte: exponent + 10 above the mantissa.
+__host__ __device__ __forceinline__ uint32_t scale_byte(uint32_t e4m3) {
+  const uint32_t e = (e4m3 >> 3) & 15u, m = e4m3 & 7u;
+  if (e) return (e + 3) << 3 | m;
+  return m >= 4 ? 3u << 3 | (m & 3u) << 1 : m >= 2 ? 2u << 3 | (m & 1u) << 2 : m << 3;
+}
+
+// Scale `byte` of a word -> the bf16 number s * 2^118 in both halves; select:
+// 0x4040 + 0x0101 * byte.  (A zero byte gives 2^108; its block's codes are zero.)
+__device__ __forceinline__ uint32_t scale_twice(uint32_t word, uint32_t select) {
+  return __byte_perm(word, 0, select) * 16u + 0x75807580u;
 }
 
 // s2 holds the block's scale twice.
