@@ -53,8 +53,11 @@ struct Carve {
   int splits = 1;  // of the down products' K
 };
 
-// From how many rows an expert (on average) the tensor cores take over.
-bool use_tc(int64_t pairs, int64_t experts) { return pairs > ffn::kFewPairs && pairs > 16 * experts; }
+// From how many rows an expert (on average) the tensor cores take over: with 64
+// experts of 2048 x 1024 the few-row kernel takes 97 us at 8 rows an expert and
+// 151 at 16, the tensor cores 95 and 111; with 8 of 4096 x 6144 132 / 210 and
+// 136 / 147; with 20 of 1056 x 672 32 / 36 and 34 / 35.
+bool use_tc(int64_t pairs, int64_t experts) { return pairs > ffn::kFewPairs && pairs > 10 * experts; }
 
 size_t take(size_t& off, size_t bytes) {
   const size_t at = off;

@@ -62,6 +62,13 @@ constexpr int kSmemAlloc = kSmemBar + kNumBars * 8 + 16 + 1024;  // slack for 10
 static_assert(kSmemAlloc <= 232448, "shared memory budget");
 constexpr int kAColBase = 256;
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 struct TcExpertsArgs {
   ExpertsView w;
   MoePlan plan;
@@ -110,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* err = &g_moe_device_error;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kc = a.w.kc, units = (kc + kUnit - 1) / kUnit;
+  const int kc = a.w.kc;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kXStages; ++s) {
@@ -196,32 +203,40 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
     }
   } else if (warp < 4) {
     // ----------------------------------------------------------- MMA issuers
-    if (lane == 0) {
-      const int half = warp - 2;
-      const uint32_t idesc = idesc_bf16_f32(kOpRows, kTcTile), d = tmem + 128 * half;
-      int u = 0, i = 0;
-      bool ok = true;
-      for (int T = blockIdx.x; ok && T < total; T += gridDim.x, ++i) {
-        if (i > 0 && !mbar_wait(accempty, (i - 1) & 1, abort_flag, err, 2)) break;
-        for (int c = 0; c < kc; c += kUnit, ++u) {
-          const int sx = u % kXStages, sa = u % kASlots, nc = min(kUnit, kc - c);
-          // (the decode warps have waited for the rows as well)
-          if (!mbar_wait(&afull[half * kASlots + sa], (u / kASlots) & 1, abort_flag, err, 2)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          for (int j = 0; j < nc; ++j) {
-            const uint64_t b = smem_desc_sw128(smem_u32(xs + sx * kXStageBytes + j * kXChunkBytes));
-            const uint32_t aslot = tmem + kAColBase + 128 * sa + 64 * half + 32 * j;
+    // (the whole warp walks the loop and one elected lane issues: uniform
+    // control flow keeps the descriptors in uniform registers)
+    const int half = warp - 2;
+    const uint32_t d = tmem + 128 * half;
+    int u = 0, i = 0;
+    bool ok = true;
+    for (int T = blockIdx.x; ok && T < total; T += gridDim.x, ++i) {
+      if (i > 0) {
+        ok = mbar_wait(accempty, (i - 1) & 1, abort_flag, err, 2);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      }
+      // a tile with few rows needs few columns
+      const uint32_t idesc = idesc_bf16_f32(kOpRows, min(kTcTile, (tile_at(a, T).rows + 15) & ~15));
+      for (int c = 0; c < kc; c += kUnit, ++u) {
+        const int sx = u % kXStages, sa = u % kASlots;
+        // (the decode warps have waited for the rows as well)
+        ok = mbar_wait(&afull[half * kASlots + sa], (u / kASlots) & 1, abort_flag, err, 2);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        const uint64_t b = smem_desc_sw128(smem_u32(xs + sx * kXStageBytes));
+        const uint32_t aslot = tmem + kAColBase + 128 * sa + 64 * half;
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < kUnit; ++j) {
+            if (c + j >= kc) break;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ts(d, aslot + 8 * kk, b + 2 * kk, idesc, (c == 0 && j == 0 && kk == 0) ? 0u : 1u);
+              mma_bf16_ts(d, aslot + 32 * j + 8 * kk, b + j * (kXChunkBytes >> 4) + 2 * kk, idesc, (c | j | kk) ? 1u : 0u);
           }
           mma_commit(&aempty[half * kASlots + sa]);
           mma_commit(&xempty[sx]);
+          if (c + kUnit >= kc) mma_commit(accfull);
         }
-        if (ok) mma_commit(accfull);
+        __syncwarp();
       }
     }
   } else if (warp < 12) {
