@@ -263,9 +263,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = l[i];
   }
-  // An upper bound of a key's error: EPL + 5 additions of the sum and about ten
-  // steps of the exponential, the quotient and the bias.
-  const float err = (EPL + 16) * 1.1920929e-7f;
+  // An upper bound of a score's relative error: softmax has EPL + 5 additions
+  // and about ten steps of the exponentials and the quotient, sigmoid three;
+  // a key's adds a step of its size.
+  constexpr float kStep = 1.1920929e-7f;
+  const float err = (softmax ? EPL + 16 : 4) * kStep;
   bool close = false;
   if (a.groups > 1) {
     const float gap =
@@ -273,61 +275,128 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
     float most = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) most = fmaxf(most, key[i] > -INFINITY ? fabsf(key[i]) : 0.0f);
-    close = scored && gap <= 4.0f * err * (1.0f + redux_max(most));
+    close = scored && gap <= 4.0f * err + 8.0f * kStep * redux_max(most);  // (up to four scores, each at most one)
   }
 
-  // top_k rounds of a warp-wide maximum, and one for the runner-up; lane j
-  // keeps the j-th choice
+  // rounds of a warp-wide maximum; lane j keeps the j-th choice, and lane top_k
+  // the runner-up where its distance matters
   int my_id = -1;
-  float my_l = -INFINITY, my_c = -INFINITY, next_c = -INFINITY, next_l = 0.0f, next_b = 0.0f;
-  float best = -INFINITY, best_l = -INFINITY;
-  int at = 0;
-  auto rescan = [&] {
-    best = -INFINITY;
+  float my_l = -INFINITY, my_c = -INFINITY;
+  // each lane's keys in descending order (equal ones by id), so that a round
+  // only looks at their heads; up to eight: a longer list is scanned again
+  constexpr bool kSorted = EPL <= 8;
+  int at[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        best_l = l[i];
-        at = i;
-      }
+  for (int i = 0; i < EPL; ++i) at[i] = i;
+  auto swap_if = [&](int x, int y) {
+    const bool s = key[y] > key[x] || (key[y] == key[x] && at[y] < at[x]);
+    const float kx = key[x], lx = l[x];
+    const int ax = at[x];
+    key[x] = s ? key[y] : kx, key[y] = s ? kx : key[y];
+    l[x] = s ? l[y] : lx, l[y] = s ? lx : l[y];
+    at[x] = s ? at[y] : ax, at[y] = s ? ax : at[y];
   };
-  rescan();
-  const int rounds = a.top_k + scored;
-  for (int j = 0; j < rounds; ++j) {
-    const float c = redux_max(best);
-    if (c == -INFINITY) break;  // nothing is left
-    const int w = __ffs(__ballot_sync(0xffffffffu, best == c)) - 1;  // the lowest lane: the lowest id
-    const int id = __shfl_sync(0xffffffffu, lane * EPL + at, w);
-    const float wl = __shfl_sync(0xffffffffu, best_l, w);
-    if (j == a.top_k) {
-      next_c = c;
-      next_l = wl;
-      next_b = a.bias ? a.bias[id] : 0.0f;
-      break;
-    }
-    if (lane == j) {
-      my_id = id;
-      my_l = wl;
-      my_c = c;
-    }
-    if (lane == w) {
+  if (kSorted) {  // odd-even merges
 #pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (i == at) key[i] = -INFINITY;
-      rescan();
-    }
+    for (int p = 1; p < EPL; p *= 2)
+#pragma unroll
+      for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+        for (int j = k % p; j <= EPL - 1 - k; j += 2 * k)
+#pragma unroll
+          for (int i = 0; i <= (k - 1 < EPL - j - k - 1 ? k - 1 : EPL - j - k - 1); ++i)
+            if ((i + j) / (p * 2) == (i + j + k) / (p * 2)) swap_if(i + j, i + j + k);
   }
+  auto to_front = [&] {  // the best of the list to its head
+    if (kSorted) return;
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) swap_if(0, i);
+  };
+  to_front();
+  auto choose = [&](int from, int to) {  // the rounds from .. to - 1; how many choices there are
+    for (int j = from; j < to; ++j) {
+      const float c = redux_max(key[0]);
+      if (c == -INFINITY) return j;  // nothing is left
+      const int w = __ffs(__ballot_sync(0xffffffffu, key[0] == c)) - 1;  // the lowest lane: the lowest id
+      const int id = __shfl_sync(0xffffffffu, lane * EPL + at[0], w);
+      const float wl = __shfl_sync(0xffffffffu, l[0], w);
+      if (lane == j) {
+        my_id = id;
+        my_l = wl;
+        my_c = c;
+      }
+      if (lane == w) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          if (!kSorted && i > 0) break;
+          key[i] = kSorted && i + 1 < EPL ? key[i + 1] : -INFINITY;
+          if (kSorted && i + 1 < EPL) l[i] = l[i + 1], at[i] = at[i + 1];
+        }
+        to_front();
+      }
+    }
+    return to;
+  };
+  int found = choose(0, min(32, a.top_k + scored));
   if (scored) {
     // Is a choice nearer to the next one than their errors?  (Equal logits with
-    // equal biases have equal keys.)
+    // equal biases have equal keys.)  With all 32 lanes taken by choices there is
+    // no room for the runner-up: such rows are always computed in 64 bits.
     const float my_b = a.bias && my_id >= 0 ? a.bias[my_id] : 0.0f;
-    float c = __shfl_down_sync(0xffffffffu, my_c, 1), cl = __shfl_down_sync(0xffffffffu, my_l, 1),
-          cb = __shfl_down_sync(0xffffffffu, my_b, 1);
-    if (lane == a.top_k - 1) c = next_c, cl = next_l, cb = next_b;
-    close |= lane < a.top_k && c > -INFINITY && my_c - c <= 2.0f * err * (1.0f + fmaxf(fabsf(my_c), fabsf(c))) &&
-             !(cl == my_l && cb == my_b);
-    if (__any_sync(0xffffffffu, close)) {
+    auto tolerance = [&](float c, float cb, float o, float ob) {
+      const float scores = fabsf(c - cb) + fabsf(o - ob), keys = fabsf(c) + fabsf(o);
+      return err * scores + 2.0f * kStep * (keys + scores);
+    };
+    const float c = __shfl_down_sync(0xffffffffu, my_c, 1), cl = __shfl_down_sync(0xffffffffu, my_l, 1),
+                cb = __shfl_down_sync(0xffffffffu, my_b, 1);
+    const bool near = lane + 1 < found && my_c - c <= tolerance(my_c, my_b, c, cb) && !(cl == my_l && cb == my_b);
+    bool whole = __any_sync(0xffffffffu, close) || a.top_k == 32 || bad;
+    if (!whole && __any_sync(0xffffffffu, near)) {
+      // Three more candidates; where the last of them is clearly behind the
+      // choices, the candidates' keys in 64 bits settle the order.
+      const int most = min(32, a.top_k + 4);
+      const bool all = found < min(32, a.top_k + 1);  // nothing was left already
+      if (!all) found = choose(found, most);
+      const float ob = a.bias && my_id >= 0 ? a.bias[my_id] : 0.0f;
+      const int e0 = min(a.top_k, found) - 1, e1 = found - 1;
+      const float c0 = __shfl_sync(0xffffffffu, my_c, e0), b0 = __shfl_sync(0xffffffffu, ob, e0);
+      const float c1 = __shfl_sync(0xffffffffu, my_c, e1), b1 = __shfl_sync(0xffffffffu, ob, e1);
+      whole = !(all || found < most) && !(c0 - c1 > tolerance(c0, b0, c1, b1));
+      if (!whole) {
+        double k64 = -INFINITY;
+        if (softmax) {
+          float r[EPL];
+          load_logits<EPL, BF16, WIDE>(a, row, lane, r);
+          double total = 0.0;
+#pragma unroll
+          for (int i = 0; i < EPL; ++i)
+            if (r[i] > -INFINITY) total += exp((double)r[i] - (double)top);
+          total = warp_sum64(total);
+          k64 = exp((double)my_l - (double)top) / total;
+        } else {
+          k64 = 1.0 / (1.0 + exp(-(double)my_l));
+        }
+        k64 += (double)ob;
+        int rank = 0;
+        for (int i = 0; i < found; ++i) {
+          const double o = __shfl_sync(0xffffffffu, k64, i);
+          const int id = __shfl_sync(0xffffffffu, my_id, i);
+          rank += o > k64 || (o == k64 && id < my_id);
+        }
+        int src = lane;
+        for (int i = 0; i < found; ++i) {
+          const int at_rank = __ffs(__ballot_sync(0xffffffffu, lane < found && rank == i)) - 1;
+          if (lane == i) src = at_rank;
+        }
+        my_id = __shfl_sync(0xffffffffu, my_id, src);
+        my_l = __shfl_sync(0xffffffffu, my_l, src);
+      }
+    }
+    if (whole) {
+      load_logits<EPL, BF16, WIDE>(a, row, lane, l);  // (the rounds have moved them)
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (isnan(l[i])) l[i] = -INFINITY;
       my_id = choose_64<EPL>(a, l, lane, route_smem + (size_t)warp * a.experts);
       // the chosen logits, from the lanes that hold them
       my_l = -INFINITY;
@@ -337,6 +406,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
         if (my_id >= 0 && my_id % EPL == i) my_l = v;
       }
     }
+  }
+  if (lane >= a.top_k) {  // candidates that were not chosen
+    my_id = -1;
+    my_l = -INFINITY;
   }
 
   float w = 0.0f;

@@ -360,14 +360,16 @@ def ffn_nvfp4_linear(x: torch.Tensor, w: Weight, fmt="bf16", y=None, workspace=N
     return y
 
 
-def _on_current_device(first: torch.Tensor, *others):
-    """Refuse tensors of another device than the current one: their pointers would mean nothing there."""
-    dev = first.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    for t in others:
+def _launch_stream(stream, *tensors) -> int:
+    """The stream to launch on; refuses tensors of another device than the current one, where their
+    pointers would mean nothing."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors are on cuda:{dev} and cuda:{t.get_device()}")
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 @functools.lru_cache(maxsize=256)
@@ -398,11 +400,11 @@ def ffn_nvfp4_moe_route(logits: torch.Tensor, top_k: int, scoring="softmax", bia
     weights = torch.empty((m, top_k), dtype=torch.float32, device=logits.device) if weights is None else weights
     _need(ids, "ids", torch.int32, (m, top_k))
     _need(weights, "weights", torch.float32, (m, top_k))
-    _on_current_device(logits, bias, ids, weights)
+    launch = _launch_stream(stream, logits, bias, ids, weights)
     st = lib.ffn_nvfp4_moe_route(
         logits.data_ptr(), kind, m, experts, ld if m > 1 else max(ld, experts), None if bias is None else bias.data_ptr(),
         _router(scoring, top_k, groups, top_groups, group_score, renormalize, scale), ids.data_ptr(), weights.data_ptr(),
-        _stream(stream))
+        launch)
     if st:
         _check("ffn_nvfp4_moe_route", st)
     return ids, weights
@@ -445,14 +447,13 @@ def ffn_nvfp4_experts_create(codes: torch.Tensor, block_scales: torch.Tensor, gl
     k = 2 * half_k
     _need(block_scales, "block_scales", torch.uint8, (e, n, k // 16))
     _need(global_scales, "global_scales", torch.float32)
-    _on_current_device(codes, block_scales, global_scales)
     if gate_up and tuple(global_scales.shape) != (e, 2) or not gate_up and global_scales.numel() != e:
         raise ValueError(f"global_scales must hold {'[E, 2]' if gate_up else 'E'} values for {e} experts, "
                          f"got shape {tuple(global_scales.shape)}")
     h = ctypes.c_void_p()
     _check("ffn_nvfp4_experts_create", lib.ffn_nvfp4_experts_create(
-        _ptr(codes), _ptr(block_scales), _ptr(global_scales), e, n, k, int(gate_up), _stream(stream),
-        ctypes.byref(h)))
+        _ptr(codes), _ptr(block_scales), _ptr(global_scales), e, n, k, int(gate_up),
+        _launch_stream(stream, codes, block_scales, global_scales), ctypes.byref(h)))
     return Experts(h)
 
 
@@ -487,9 +488,9 @@ def ffn_nvfp4_experts_linear(x: torch.Tensor, w: Experts, ids: torch.Tensor, y=N
         workspace = _workspace(ffn_nvfp4_experts_workspace_size(m, top_k, w.experts, w.n, k), x.device, None)
     else:
         _need(workspace, "workspace", torch.uint8)
-    _on_current_device(x, ids, y, workspace)
     st = lib.ffn_nvfp4_experts_linear(x.data_ptr(), m, w.handle, ids.data_ptr(), top_k, y.data_ptr(),
-                                      workspace.data_ptr(), workspace.numel(), _stream(stream))
+                                      workspace.data_ptr(), workspace.numel(),
+                                      _launch_stream(stream, x, ids, y, workspace))
     if st:
         _check("ffn_nvfp4_experts_linear", st)
     return y
@@ -512,10 +513,9 @@ def ffn_nvfp4_moe_forward(x: torch.Tensor, gate_up: Experts, down: Experts, ids:
         workspace = _workspace(ffn_nvfp4_moe_workspace_size(m, top_k, down.experts, hidden, inter), x.device, None)
     else:
         _need(workspace, "workspace", torch.uint8)
-    _on_current_device(x, ids, weights, out, workspace)
     st = lib.ffn_nvfp4_moe_forward(x.data_ptr(), m, hidden, inter, gate_up.handle, down.handle, ids.data_ptr(),
                                    weights.data_ptr(), top_k, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                   _stream(stream))
+                                   _launch_stream(stream, x, ids, weights, out, workspace))
     if st:
         _check("ffn_nvfp4_moe_forward", st)
     return out
