@@ -265,17 +265,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
   }
   // An upper bound of a score's relative error: softmax has EPL + 5 additions
   // and about ten steps of the exponentials and the quotient, sigmoid three;
-  // a key's adds a step of its size.
-  constexpr float kStep = 1.1920929e-7f;
+  // a key's adds a step of its size.  Below the normal range errors are steps of
+  // 2^-149: keys that are all this small are always close.
+  constexpr float kStep = 1.1920929e-7f, kTiny = 1e-37f;
   const float err = (softmax ? EPL + 16 : 4) * kStep;
   bool close = false;
   if (a.groups > 1) {
-    const float gap =
-        keep_best_groups<EPL, float>(a, key, lane, reinterpret_cast<float*>(route_smem + (size_t)warp * a.experts));
-    float most = 0.0f;
+    float most = 0.0f;  // of the groups left out as well: two large keys may cancel in their sum
 #pragma unroll
     for (int i = 0; i < EPL; ++i) most = fmaxf(most, key[i] > -INFINITY ? fabsf(key[i]) : 0.0f);
-    close = scored && gap <= 4.0f * err + 8.0f * kStep * redux_max(most);  // (up to four scores, each at most one)
+    const float gap =
+        keep_best_groups<EPL, float>(a, key, lane, reinterpret_cast<float*>(route_smem + (size_t)warp * a.experts));
+    close = scored && gap <= 4.0f * err + 8.0f * kStep * redux_max(most) + kTiny;  // (up to four scores, each at most one)
   }
 
   // rounds of a warp-wide maximum; lane j keeps the j-th choice, and lane top_k
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
     const float my_b = a.bias && my_id >= 0 ? a.bias[my_id] : 0.0f;
     auto tolerance = [&](float c, float cb, float o, float ob) {
       const float scores = fabsf(c - cb) + fabsf(o - ob), keys = fabsf(c) + fabsf(o);
-      return err * scores + 2.0f * kStep * (keys + scores);
+      return err * scores + 2.0f * kStep * (keys + scores) + kTiny;
     };
     const float c = __shfl_down_sync(0xffffffffu, my_c, 1), cl = __shfl_down_sync(0xffffffffu, my_l, 1),
                 cb = __shfl_down_sync(0xffffffffu, my_b, 1);

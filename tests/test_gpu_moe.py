@@ -124,6 +124,53 @@ def test_route_masked_experts(native, scoring, groups):
     check_route(native, logits, None, renormalize=False, **kw)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_group_scores_that_cancel(native, scoring):
+    """Groups whose two best keys are large and of opposite sign: their sum keeps little of fp32."""
+    rng = np.random.default_rng(11)
+    experts, groups = 64, 8
+    size = experts // groups
+    logits = rng.standard_normal((200, experts)).astype(np.float32)
+    bias = np.full(experts, -np.inf, np.float32)
+    for g in range(groups):
+        big = 0.0 if g % 2 else 3.0e5 * (g + 1)
+        bias[g * size + g] = big + (0.0 if big else 0.25)
+        bias[g * size + (g + 3) % size] = -big + (0.0 if big else 0.25)
+    check_route(native, logits, bias, top_k=4, scoring=scoring, groups=groups, top_groups=2, group_score="top2")
+
+
+def test_route_scores_below_the_normal_range(native):
+    """Softmax scores around fp32's smallest numbers decide as 64-bit ones do.  A weight of theirs is off by some of
+    the smallest steps (2^-149): two of the exponential, one of its product, doubled by a sum of one half, one of the
+    quotient."""
+    rng = np.random.default_rng(12)
+    logits = rng.uniform(-104.0, -86.0, (100, 64)).astype(np.float32)
+    logits[:, 10] = 0.0
+    for bias, kw in ((None, dict(groups=4, top_groups=2, group_score="top2")), (np.zeros(64, np.float32), {}),
+                     (None, dict(scoring="sigmoid", groups=4, top_groups=2, group_score="top2"))):
+        ids, w = native.ffn_nvfp4_moe_route(torch.from_numpy(logits).cuda(), 8,
+                                            bias=None if bias is None else torch.from_numpy(bias).cuda(), **kw)
+        rid, rw = M.route(logits.astype(np.float64), bias, 8, **kw)
+        assert np.array_equal(ids.cpu().numpy(), rid)
+        assert np.all(np.abs(w.double().cpu().numpy() - rw) <= 15 * 2.0 ** -24 * rw + 8 * 2.0 ** -149)
+
+
+def test_route_infinite_keys(native):
+    """+inf biases tie by id; +inf logits under sigmoid score one; biases and logits of -inf close an expert."""
+    rng = np.random.default_rng(13)
+    logits = rng.standard_normal((20, 48)).astype(np.float32)
+    bias = (0.1 * rng.standard_normal(48)).astype(np.float32)
+    bias[[30, 7, 19]] = np.inf
+    bias[[3, 31]] = -np.inf
+    logits[5, 7] = -np.inf
+    check_route(native, logits, bias, top_k=5)
+    check_route(native, logits, bias, top_k=5, groups=6, top_groups=3, group_score="top2")
+    logits[2, [4, 40, 30]] = np.inf
+    check_route(native, logits, bias, top_k=5, scoring="sigmoid")
+    check_route(native, logits, None, top_k=5, scoring="sigmoid")
+    check_route(native, np.zeros((2, 32)), np.linspace(0, 1, 32), top_k=32, scoring="sigmoid")
+
+
 def test_route_non_finite_rows(native):
     logits = np.random.default_rng(10).standard_normal((6, 40)).astype(np.float32)
     logits[1, 3] = np.nan
@@ -156,6 +203,17 @@ def test_route_strided_rows_and_streams(native):
     assert np.array_equal(ids.cpu().numpy(), rid)
     empty = native.ffn_nvfp4_moe_route(part[:0], 8)
     assert empty[0].shape == (0, 8)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("experts,start,width", [(128, 1, 130), (256, 8, 264), (64, 2, 70), (512, 4, 520)])
+def test_route_rows_off_the_wide_boundaries(native, dtype, experts, start, width):
+    wide = torch.randn((33, width), generator=torch.Generator().manual_seed(experts)).to(dtype)
+    part = wide.cuda()[:, start:start + experts]
+    ids, w = native.ffn_nvfp4_moe_route(part, 8, groups=4, top_groups=2)
+    rid, rw = M.route(wide[:, start:start + experts].double().numpy(), None, 8, groups=4, top_groups=2)
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    assert np.allclose(w.double().cpu().numpy(), rw, rtol=(experts / 32 + 13) * 2.0 ** -24, atol=0)
 
 
 def test_route_refusals(native):
@@ -256,6 +314,66 @@ def test_linear_uneven_experts(native, m):
     assert int(torch.count_nonzero(y.view(torch.int16))) == 0
 
 
+@pytest.mark.parametrize("m,n,k,experts,top_k,padding", [
+    # a plan of few and of many pairs per expert, made by one CTA and by several
+    (32, 72, 96, 3, 1, 0.0), (33, 72, 96, 3, 1, 0.0), (35, 136, 64, 7, 1, 0.0), (36, 136, 64, 7, 1, 0.1),
+    (70, 136, 64, 7, 1, 0.0), (71, 136, 64, 7, 1, 0.1), (700, 64, 32, 1024, 6, 0.1), (2049, 72, 96, 17, 2, 0.1),
+    (4096, 40, 32, 2, 1, 0.0), (4097, 40, 32, 2, 1, 0.3),
+])
+def test_linear_at_the_kernels_boundaries(native, m, n, k, experts, top_k, padding):
+    rng = np.random.default_rng(2300 + m)
+    s = Stack(native, experts, n, k, 2400 + m)
+    x, x64 = rows(m, k, 2500 + m)
+    check_linear(native, s, x, x64, pick(rng, m, experts, top_k, padding))
+
+
+@pytest.mark.parametrize("m", [3, 64])
+def test_linear_every_code_and_scale(native, m):
+    """Rows with a single one in them read the weight itself: every code with every scale, subnormal ones included,
+    in every place of a chunk."""
+    n, k = 200, 224
+    rng = np.random.default_rng(43)
+    codes = rng.integers(0, 256, (2, n, k // 2), dtype=np.uint8)
+    scales = np.resize(np.arange(0x7F, dtype=np.uint8), 2 * n * (k // 16))
+    scales = rng.permutation(scales).reshape(2, n, k // 16)
+    gs = np.array([1.0, 0.5], np.float32)
+    w = M.experts_dequant(codes, scales, gs)
+    h = native.ffn_nvfp4_experts_create(*(torch.from_numpy(a).cuda() for a in (codes, scales, gs)))
+    ids = np.tile(np.array([[1, 0]], np.int32), (m, 1))
+    for k0 in range(0, k, m):
+        xi = np.zeros((m, k))
+        for i in range(m):
+            xi[i, (k0 + i) % k] = 1.0
+        y = native.ffn_nvfp4_experts_linear(torch.from_numpy(xi).to(torch.bfloat16).cuda(), h, torch.from_numpy(ids).cuda())
+        assert np.array_equal(bf16_to_f64(y), M.experts_linear(xi, w, ids))
+
+
+def test_linear_offsets_past_32_bits(native):
+    """Weights of more than 4 GB and outputs of more than 2^31 elements: the far ends are where they belong."""
+    experts, n, k = 600, 16384, 1024
+    gen = torch.Generator("cuda").manual_seed(44)
+    codes = torch.randint(0, 256, (experts, n, k // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    scales = torch.randint(0x30, 0x40, (experts, n, k // 16), dtype=torch.uint8, device="cuda", generator=gen)
+    gs = torch.full((experts,), 2.0 ** -6, device="cuda")
+    h = native.ffn_nvfp4_experts_create(codes, scales, gs)
+    w = {e: M.experts_dequant(codes[e:e + 1].cpu().numpy(), scales[e:e + 1].cpu().numpy(), gs[:1].cpu().numpy())[0]
+         for e in (599, 511)}
+    del codes, scales
+    m = 70000
+    x, x64 = rows(m, k, 45)
+    for count in (1, 40, m):
+        ids = torch.full((count, 2), -1, dtype=torch.int32)
+        ids[:, 0] = torch.arange(count) % 97
+        ids[0, 1], ids[count - 1, 0] = 511, 599
+        y = native.ffn_nvfp4_experts_linear(x[:count], h, ids.cuda())
+        for i, j, e in ((0, 1, 511), (count - 1, 0, 599)):
+            ref, mag = w[e] @ x64[i], np.abs(w[e]) @ np.abs(x64[i])
+            got = bf16_to_f64(y[i, j])
+            assert np.all(np.abs(got - ref) <= HALF * np.abs(ref) + (1 + HALF) * sum_error(k) * mag)
+        if count > 1:
+            assert int(torch.count_nonzero(y[count - 1, 1])) == 0
+
+
 def test_linear_exact_integers(native):
     """Small whole numbers: every product and sum is exact, so the bits are the oracle's."""
     rng = np.random.default_rng(41)
@@ -340,6 +458,106 @@ def test_layer_matches_oracle(native, m, experts, top_k, hidden, inter, padding)
     ids = pick(rng, m, experts, top_k, padding)
     weights = rng.uniform(0.0, 1.0, (m, top_k)).astype(np.float32)
     layer.check(layer.run(x, ids, weights), x64, ids, weights)
+
+
+@pytest.mark.parametrize("m,experts,top_k,hidden,inter", [
+    (1, 2, 1, 256, 2080, ), (3, 3, 2, 64, 4096), (16, 2, 2, 96, 1600), (33, 12, 1, 64, 2080), (32, 7, 1, 128, 64),
+    (33, 7, 1, 128, 64), (35, 7, 1, 128, 64), (36, 7, 1, 128, 64), (70, 7, 1, 128, 64), (71, 7, 1, 128, 64),
+    (2100, 17, 2, 96, 32), (1, 64, 32, 96, 64), (2, 40, 33, 96, 64),
+])
+def test_layer_at_the_kernels_boundaries(native, m, experts, top_k, hidden, inter):
+    """Long sums over few tiles (cut into ranges of K), and the numbers of pairs where other kernels take over."""
+    rng = np.random.default_rng(3300 + m)
+    layer = Layer(native, experts, hidden, inter, 3400 + m)
+    x, x64 = rows(m, hidden, 3500 + m)
+    ids = pick(rng, m, experts, top_k)
+    weights = rng.uniform(0.0, 1.0, (m, top_k)).astype(np.float32)
+    layer.check(layer.run(x, ids, weights), x64, ids, weights)
+
+
+@pytest.mark.parametrize("m", [1, 2, 4, 5, 8, 11, 60])
+def test_layer_the_same_expert_again(native, m):
+    """Equal ids in a row count each, with their own weights; all rows at one expert."""
+    layer = Layer(native, 3, 160, 96, 66)
+    x, x64 = rows(m, 160, 67)
+    rng = np.random.default_rng(68)
+    weights = rng.uniform(-1.0, 1.0, (m, 4)).astype(np.float32)
+    for ids in (np.full((m, 4), 2, np.int32), np.tile(np.array([[1, 0, 1, 5]], np.int32), (m, 1))):
+        layer.check(layer.run(x, ids, weights), x64, ids, weights)
+
+
+@pytest.mark.parametrize("m", [4, 20, 100])
+def test_layer_non_finite_rows_stay_their_own(native, m):
+    layer = Layer(native, 3, 128, 96, 74)
+    x, _ = rows(m, 128, 75)
+    rng = np.random.default_rng(76)
+    ids, w = pick(rng, m, 3, 2), rng.uniform(0, 1, (m, 2)).astype(np.float32)
+    clean = layer.run(x, ids, w)
+    x[2, 5] = float("inf")
+    x[3] = float("nan")
+    got = layer.run(x, ids, w)
+    rest = [i for i in range(m) if i not in (2, 3)]
+    assert torch.equal(got[rest], clean[rest]) and bool(torch.isnan(got[3]).all())
+
+
+def test_calls_on_two_streams_at_once(native):
+    """Layers and products of several sizes on two streams, each with its workspace: the bits of calls made alone."""
+    layer = Layer(native, 8, 512, 256, 77)
+    cases = []
+    for i, m in enumerate((1, 6, 40, 300)):
+        x, _ = rows(m, 512, 780 + i)
+        rng = np.random.default_rng(790 + i)
+        ids = torch.from_numpy(pick(rng, m, 8, 2)).cuda()
+        w = torch.from_numpy(rng.uniform(0, 1, (m, 2)).astype(np.float32)).cuda()
+        cases.append((x, ids, w))
+    run = lambda c, **kw: native.ffn_nvfp4_moe_forward(c[0], layer.gu.handle, layer.dn.handle, c[1], c[2], **kw)
+    alone = [run(c) for c in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            for c in (cases if i == 0 else reversed(cases)):
+                outs[i].append(run(c, stream=s))  # (its buffers belong to the stream)
+    torch.cuda.synchronize()
+    for i in range(2):
+        for j, o in enumerate(outs[i]):
+            assert torch.equal(o, alone[j % 4 if i == 0 else 3 - j % 4])
+
+
+def test_graphs_that_share_a_workspace(native):
+    """Two captured layers of different sizes over one workspace, replayed in turn, and an uncaptured call between."""
+    layer = Layer(native, 8, 256, 160, 84)
+    size = native.ffn_nvfp4_moe_workspace_size(600, 8, 8, 256, 160)
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    parts = []
+    for m, top_k in ((3, 2), (600, 8), (30, 2)):
+        x, _ = rows(m, 256, 85 + m)
+        rng = np.random.default_rng(86 + m)
+        ids = torch.from_numpy(pick(rng, m, 8, top_k)).cuda()
+        w = torch.from_numpy(rng.uniform(0, 1, (m, top_k)).astype(np.float32)).cuda()
+        out = torch.empty((m, 256), dtype=torch.bfloat16, device="cuda")
+        run = lambda x=x, ids=ids, w=w, out=out: native.ffn_nvfp4_moe_forward(
+            x, layer.gu.handle, layer.dn.handle, ids, w, out=out, workspace=ws)
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            want = run().clone()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                run()
+        parts.append((graph, run, out, want))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for a in parts:
+            for b in parts:
+                for p in (a, b):
+                    p[2].fill_(float("nan"))
+                a[0].replay()
+                b[1]()
+                b[0].replay()
+                s.synchronize()
+                assert torch.equal(a[2], a[3]) and torch.equal(b[2], b[3])
 
 
 @pytest.mark.parametrize("m", [1, 20, 150])
