@@ -333,7 +333,8 @@ ffn_status ffn_nvfp4_moe_route(const void* logits, ffn_logits_type type, int64_t
 typedef struct ffn_nvfp4_experts ffn_nvfp4_experts;
 
 /* Build a stack from NVFP4 tensors: codes uint8 [experts, n, k/2], block_scales
- * uint8 [experts, n, k/16] (layout and meaning as for a single weight),
+ * uint8 [experts, n, k/16] (layout and meaning as for a single weight; block
+ * scales are finite and not negative: a sign bit is ignored, 0x7F is no NaN),
  * global_scales fp32 [experts].  With gate_up = 1, n = 2 * inter: rows
  * [0, inter) of each expert are its gate and rows [inter, 2 * inter) its up
  * weight, and global_scales is [experts, 2] (gate, up).  Reads the caller's
@@ -362,7 +363,9 @@ ffn_status ffn_nvfp4_experts_info(const ffn_nvfp4_experts* w, int64_t* experts, 
  * same kernels run (they are chosen by m, top_k and the shapes).  m == 0 is a
  * no-op.  The workspace holds the rows sorted by expert; it may be shared by
  * calls on one stream.  Errors: FFN_ERR_UNSUPPORTED for a gate and up stack;
- * FFN_ERR_SHAPE when 2 * m * top_k exceeds 2^31 - 1. */
+ * FFN_ERR_SHAPE when 2 * m * top_k exceeds 2^31 - 1 or m * top_k rows of n or k
+ * columns are more than 2^40 elements (the sizes: FFN_ERR_UNSUPPORTED for
+ * experts > FFN_MOE_MAX_EXPERTS). */
 ffn_status ffn_nvfp4_experts_workspace_size(int64_t m, int top_k, int64_t experts, int64_t n, int64_t k,
                                             size_t* bytes);
 ffn_status ffn_nvfp4_experts_linear(const void* x, int64_t m, const ffn_nvfp4_experts* w, const int32_t* ids,
@@ -382,7 +385,8 @@ ffn_status ffn_nvfp4_experts_linear(const void* x, int64_t m, const ffn_nvfp4_ex
  * An id outside [0, experts) contributes weights[i, j] * 0, so padding rows
  * (all ids -1, weights 0) give zeros.  Deterministic: the same call gives the
  * same bits.  m == 0 is a no-op.  Allocates nothing and does not synchronise;
- * the workspace may be shared by calls on one stream. */
+ * the workspace may be shared by calls on one stream.  Errors as for
+ * ffn_nvfp4_experts_linear; FFN_ERR_SHAPE where the two stacks do not match. */
 ffn_status ffn_nvfp4_moe_workspace_size(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter,
                                         size_t* bytes);
 ffn_status ffn_nvfp4_moe_forward(const void* x, int64_t m, int64_t hidden, int64_t inter,

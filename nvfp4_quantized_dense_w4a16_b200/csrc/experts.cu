@@ -46,6 +46,12 @@ ffn_status check_device(const ffn_nvfp4_experts* w) {
 // m * top_k pairs must fit an int, and so must the rows of every product.
 bool valid_pairs(int64_t m, int top_k) { return m <= (int64_t)INT32_MAX / 2 / top_k; }
 
+// What a call touches fits 64 bits and the grids' 31 with room to spare: 2^40
+// elements of any one buffer are more than a GPU holds.
+bool valid_size(int64_t pairs, int64_t columns) {
+  return columns <= INT32_MAX / 2 && (pairs == 0 || columns <= ((int64_t)1 << 40) / pairs);
+}
+
 struct Carve {
   size_t offsets = 0, order = 0, tiles = 0, arrived = 0, xs = 0, h = 0, y = 0, total = 0;
   bool tc = false;
@@ -179,7 +185,8 @@ ffn_status ffn_nvfp4_experts_info(const ffn_nvfp4_experts* w, int64_t* experts, 
 ffn_status ffn_nvfp4_experts_workspace_size(int64_t m, int top_k, int64_t experts, int64_t n, int64_t k,
                                             size_t* bytes) {
   if (!bytes || m < 0 || top_k < 1 || experts < 1 || n < 1) return FFN_ERR_INVALID_ARG;
-  if (!valid_k(k) || !valid_pairs(m, top_k)) return FFN_ERR_SHAPE;
+  if (experts > FFN_MOE_MAX_EXPERTS) return FFN_ERR_UNSUPPORTED;
+  if (!valid_k(k) || !valid_pairs(m, top_k) || !valid_size(m * top_k, n) || !valid_size(m * top_k, k)) return FFN_ERR_SHAPE;
   *bytes = carve(m, top_k, experts, n, 0, k).total;
   return FFN_OK;
 }
@@ -188,7 +195,7 @@ ffn_status ffn_nvfp4_experts_linear(const void* x, int64_t m, const ffn_nvfp4_ex
                                     int top_k, void* y, void* workspace, size_t workspace_bytes, void* stream) {
   if (m < 0 || !w || top_k < 1) return FFN_ERR_INVALID_ARG;
   if (w->gate_up) return FFN_ERR_UNSUPPORTED;
-  if (!valid_pairs(m, top_k)) return FFN_ERR_SHAPE;
+  if (!valid_pairs(m, top_k) || !valid_size(m * top_k, w->n) || !valid_size(m * top_k, w->k)) return FFN_ERR_SHAPE;
   if (m == 0) return FFN_OK;
   if (!x || !ids || !y) return FFN_ERR_INVALID_ARG;
   if (ffn_status st = check_device(w)) return st;
@@ -216,7 +223,10 @@ ffn_status ffn_nvfp4_experts_linear(const void* x, int64_t m, const ffn_nvfp4_ex
 ffn_status ffn_nvfp4_moe_workspace_size(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter,
                                         size_t* bytes) {
   if (!bytes || m < 0 || top_k < 1 || experts < 1) return FFN_ERR_INVALID_ARG;
-  if (!valid_k(hidden) || !valid_k(inter) || !valid_pairs(m, top_k)) return FFN_ERR_SHAPE;
+  if (experts > FFN_MOE_MAX_EXPERTS) return FFN_ERR_UNSUPPORTED;
+  if (!valid_k(hidden) || !valid_k(inter) || !valid_pairs(m, top_k) || !valid_size(m * top_k, hidden) ||
+      !valid_size(m * top_k, inter))
+    return FFN_ERR_SHAPE;
   *bytes = carve(m, top_k, experts, hidden, inter, hidden).total;
   return FFN_OK;
 }
@@ -229,7 +239,8 @@ ffn_status ffn_nvfp4_moe_forward(const void* x, int64_t m, int64_t hidden, int64
   if (!valid_k(hidden) || !valid_k(inter)) return FFN_ERR_SHAPE;
   if (!gate_up->gate_up || down->gate_up) return FFN_ERR_INVALID_ARG;
   if (gate_up->n != 2 * inter || gate_up->k != hidden || down->n != hidden || down->k != inter ||
-      gate_up->experts != down->experts || !valid_pairs(m, top_k))
+      gate_up->experts != down->experts || !valid_pairs(m, top_k) || !valid_size(m * top_k, hidden) ||
+      !valid_size(m * top_k, inter))
     return FFN_ERR_SHAPE;
   if (m == 0) return FFN_OK;
   if (!x || !ids || !weights || !out) return FFN_ERR_INVALID_ARG;

@@ -85,3 +85,15 @@ def test_workspace_sizes(native):
     assert L.ffn_nvfp4_moe_workspace_size(4, 8, 64, 256, 512, None) == INVALID
     for args, status in (((-1, 8, 64, 256, 512), INVALID), ((4, 8, 64, 0, 512), INVALID), ((4, 8, 64, 256, 500), SHAPE)):
         assert L.ffn_nvfp4_experts_workspace_size(*args, ctypes.byref(out)) == status, args
+
+
+def test_sizes_that_overflow_are_refused(native):
+    L, out = native.lib, ctypes.c_size_t()
+    big = 1 << 40
+    for args in ((1 << 24, 8, 64, 1 << 29, 512), (1, 1, 1, big, 32), (1, 1, 1, 32, big), (1 << 20, 32, 64, 1 << 18, 32),
+                 (1, 1, 1, (1 << 63) - 32, 32)):
+        assert L.ffn_nvfp4_moe_workspace_size(*args, ctypes.byref(out)) == SHAPE, args
+        assert L.ffn_nvfp4_experts_workspace_size(*args, ctypes.byref(out)) == SHAPE, args
+    for experts in (1025, 1 << 62):
+        assert L.ffn_nvfp4_moe_workspace_size(1, 1, experts, 64, 64, ctypes.byref(out)) == UNSUPPORTED
+        assert L.ffn_nvfp4_experts_workspace_size(1, 1, experts, 64, 64, ctypes.byref(out)) == UNSUPPORTED
