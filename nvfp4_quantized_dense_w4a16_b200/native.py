@@ -372,6 +372,19 @@ def _launch_stream(stream, *tensors) -> int:
     return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output or a workspace for work on `stream` (None: the current one): allocated for that stream, so that no
+    pending work of another one still uses it, and kept until the current stream has read it as well."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if current != stream:
+        t.record_stream(current)
+    return t
+
+
 @functools.lru_cache(maxsize=256)
 def _router(scoring, top_k, groups, top_groups, group_score, renormalize, scale):
     return MoeRouter(MOE_SCORINGS[scoring], top_k, groups, top_groups, MOE_GROUP_SCORES[group_score],
@@ -396,8 +409,8 @@ def ffn_nvfp4_moe_route(logits: torch.Tensor, top_k: int, scoring="softmax", bia
         raise ValueError("logits must have contiguous, non-overlapping rows")
     if bias is not None:
         _need(bias, "bias", torch.float32, (experts,))
-    ids = torch.empty((m, top_k), dtype=torch.int32, device=logits.device) if ids is None else ids
-    weights = torch.empty((m, top_k), dtype=torch.float32, device=logits.device) if weights is None else weights
+    ids = _empty((m, top_k), torch.int32, logits.device, stream) if ids is None else ids
+    weights = _empty((m, top_k), torch.float32, logits.device, stream) if weights is None else weights
     _need(ids, "ids", torch.int32, (m, top_k))
     _need(weights, "weights", torch.float32, (m, top_k))
     launch = _launch_stream(stream, logits, bias, ids, weights)
@@ -482,10 +495,10 @@ def ffn_nvfp4_experts_linear(x: torch.Tensor, w: Experts, ids: torch.Tensor, y=N
     if ids.dim() != 2 or ids.shape[0] != m:
         raise ValueError(f"ids must have shape ({m}, top_k), got {tuple(ids.shape)}")
     top_k = ids.shape[1]
-    y = torch.empty((m, top_k, w.n), dtype=torch.bfloat16, device=x.device) if y is None else y
+    y = _empty((m, top_k, w.n), torch.bfloat16, x.device, stream) if y is None else y
     _need(y, "y", torch.bfloat16, (m, top_k, w.n))
     if workspace is None:
-        workspace = _workspace(ffn_nvfp4_experts_workspace_size(m, top_k, w.experts, w.n, k), x.device, None)
+        workspace = _empty(max(ffn_nvfp4_experts_workspace_size(m, top_k, w.experts, w.n, k), 16), torch.uint8, x.device, stream)
     else:
         _need(workspace, "workspace", torch.uint8)
     st = lib.ffn_nvfp4_experts_linear(x.data_ptr(), m, w.handle, ids.data_ptr(), top_k, y.data_ptr(),
@@ -506,11 +519,12 @@ def ffn_nvfp4_moe_forward(x: torch.Tensor, gate_up: Experts, down: Experts, ids:
         raise ValueError(f"ids must have shape ({m}, top_k), got {tuple(ids.shape)}")
     top_k = ids.shape[1]
     _need(weights, "weights", torch.float32, (m, top_k))
-    out = torch.empty((m, hidden), dtype=torch.bfloat16, device=x.device) if out is None else out
+    out = _empty((m, hidden), torch.bfloat16, x.device, stream) if out is None else out
     _need(out, "out", torch.bfloat16, (m, hidden))
     inter = down.k
     if workspace is None:
-        workspace = _workspace(ffn_nvfp4_moe_workspace_size(m, top_k, down.experts, hidden, inter), x.device, None)
+        workspace = _empty(max(ffn_nvfp4_moe_workspace_size(m, top_k, down.experts, hidden, inter), 16), torch.uint8,
+                           x.device, stream)
     else:
         _need(workspace, "workspace", torch.uint8)
     st = lib.ffn_nvfp4_moe_forward(x.data_ptr(), m, hidden, inter, gate_up.handle, down.handle, ids.data_ptr(),
