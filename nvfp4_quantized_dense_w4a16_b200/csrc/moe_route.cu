@@ -131,6 +131,20 @@ __device__ __forceinline__ Key keep_best_groups(const RouteArgs& a, Key (&key)[E
   return high > -INFINITY && low < INFINITY ? low - high : (Key)INFINITY;
 }
 
+// Odd-even merges of EPL registers: order(x, y) for x < y puts the better one at x.
+template <int EPL, typename Order>
+__device__ __forceinline__ void merge_sort(Order order) {
+#pragma unroll
+  for (int p = 1; p < EPL; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j <= EPL - 1 - k; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i <= (k - 1 < EPL - j - k - 1 ? k - 1 : EPL - j - k - 1); ++i)
+          if ((i + j) / (p * 2) == (i + j + k) / (p * 2)) order(i + j, i + j + k);
+}
+
 // The row's choice in 64 bits: lane j gets the j-th id (-1: none).
 template <int EPL>
 __device__ __noinline__ int choose_64(const RouteArgs& a, const float (&l)[EPL], int lane, double* smem) {
@@ -217,6 +231,53 @@ __device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t row, int
   }
 }
 
+// The choice by bf16 keys: a word holds a key, in an order that unsigned numbers
+// have, above the id's complement, so that one maximum over the warp gives the
+// best key and of equal ones the lowest id.  Lane j gets the j-th id (-1: none)
+// and its logit.
+template <int EPL>
+__device__ __forceinline__ void choose_words(const float (&key)[EPL], int lane, int top_k, int& my_id, float& my_l) {
+  uint32_t w[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const uint32_t b = __float_as_uint(key[i] + 0.0f);  // (one zero)
+    const uint32_t up = (b ^ ((uint32_t)((int)b >> 31) | 0x80000000u)) & 0xffff0000u;
+    w[i] = key[i] > -INFINITY ? up | (0xffffu - (lane * EPL + i)) : 0u;
+  }
+  constexpr bool kSorted = EPL <= 8;
+  auto order = [&](int x, int y) {
+    const uint32_t hi = max(w[x], w[y]), lo = min(w[x], w[y]);
+    w[x] = hi, w[y] = lo;
+  };
+  if (kSorted) merge_sort<EPL>(order);
+  uint32_t head = w[0];
+#pragma unroll
+  for (int i = 1; i < EPL; ++i)
+    if (!kSorted) head = max(head, w[i]);
+  uint32_t mine = 0;
+  for (int j = 0; j < top_k; ++j) {
+    const uint32_t best = __reduce_max_sync(0xffffffffu, head);
+    if (best == 0) break;  // nothing is left
+    if (lane == j) mine = best;
+    if (head == best) {
+      if (kSorted) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) w[i] = i + 1 < EPL ? w[i + 1] : 0u;
+        head = w[0];
+      } else {
+        head = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) head = max(head, w[i] < best ? w[i] : 0u);
+      }
+    }
+  }
+  if (mine) {
+    my_id = 0xffff - (int)(mine & 0xffffu);
+    const uint32_t b = mine & 0xffff0000u;
+    my_l = __uint_as_float(b & 0x80000000u ? b ^ 0x80000000u : ~b & 0xffff0000u);
+  }
+}
+
 template <int EPL, bool BF16, bool WIDE>
 __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteArgs a) {
   extern __shared__ double route_smem[];  // [warps][experts], only with groups that are not whole lanes
@@ -276,135 +337,131 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
     for (int i = 0; i < EPL; ++i) most = fmaxf(most, key[i] > -INFINITY ? fabsf(key[i]) : 0.0f);
     const float gap =
         keep_best_groups<EPL, float>(a, key, lane, reinterpret_cast<float*>(route_smem + (size_t)warp * a.experts));
-    close = scored && gap <= 4.0f * err + 8.0f * kStep * redux_max(most) + kTiny;  // (up to four scores, each at most one)
+    // (up to four scores, each at most one)
+    close = scored && gap <= 4.0f * err + 8.0f * kStep * redux_max(most) + kTiny;
   }
 
-  // rounds of a warp-wide maximum; lane j keeps the j-th choice, and lane top_k
-  // the runner-up where its distance matters
   int my_id = -1;
-  float my_l = -INFINITY, my_c = -INFINITY;
-  // each lane's keys in descending order (equal ones by id), so that a round
-  // only looks at their heads; up to eight: a longer list is scanned again
-  constexpr bool kSorted = EPL <= 8;
-  int at[EPL];
+  float my_l = -INFINITY;
+  if (BF16 && !scored) {
+    choose_words<EPL>(key, lane, a.top_k, my_id, my_l);
+  } else {
+    // rounds of a warp-wide maximum; lane j keeps the j-th choice, and lane top_k
+    // the runner-up where its distance matters
+    float my_c = -INFINITY;
+    // each lane's keys in descending order (equal ones by id), so that a round
+    // only looks at their heads; up to eight: a longer list is scanned again
+    constexpr bool kSorted = EPL <= 8;
+    int at[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) at[i] = i;
-  auto swap_if = [&](int x, int y) {
-    const bool s = key[y] > key[x] || (key[y] == key[x] && at[y] < at[x]);
-    const float kx = key[x], lx = l[x];
-    const int ax = at[x];
-    key[x] = s ? key[y] : kx, key[y] = s ? kx : key[y];
-    l[x] = s ? l[y] : lx, l[y] = s ? lx : l[y];
-    at[x] = s ? at[y] : ax, at[y] = s ? ax : at[y];
-  };
-  if (kSorted) {  // odd-even merges
+    for (int i = 0; i < EPL; ++i) at[i] = i;
+    auto swap_if = [&](int x, int y) {
+      const bool s = key[y] > key[x] || (key[y] == key[x] && at[y] < at[x]);
+      const float kx = key[x], lx = l[x];
+      const int ax = at[x];
+      key[x] = s ? key[y] : kx, key[y] = s ? kx : key[y];
+      l[x] = s ? l[y] : lx, l[y] = s ? lx : l[y];
+      at[x] = s ? at[y] : ax, at[y] = s ? ax : at[y];
+    };
+    if (kSorted) merge_sort<EPL>(swap_if);
+    auto to_front = [&] {  // the best of the list to its head
+      if (kSorted) return;
 #pragma unroll
-    for (int p = 1; p < EPL; p *= 2)
+      for (int i = 1; i < EPL; ++i) swap_if(0, i);
+    };
+    to_front();
+    auto choose = [&](int from, int to) {  // the rounds from .. to - 1; how many choices there are
+      for (int j = from; j < to; ++j) {
+        const float c = redux_max(key[0]);
+        if (c == -INFINITY) return j;  // nothing is left
+        const int w = __ffs(__ballot_sync(0xffffffffu, key[0] == c)) - 1;  // the lowest lane: the lowest id
+        const int id = __shfl_sync(0xffffffffu, lane * EPL + at[0], w);
+        const float wl = __shfl_sync(0xffffffffu, l[0], w);
+        if (lane == j) {
+          my_id = id;
+          my_l = wl;
+          my_c = c;
+        }
+        if (lane == w) {
 #pragma unroll
-      for (int k = p; k >= 1; k /= 2)
-#pragma unroll
-        for (int j = k % p; j <= EPL - 1 - k; j += 2 * k)
-#pragma unroll
-          for (int i = 0; i <= (k - 1 < EPL - j - k - 1 ? k - 1 : EPL - j - k - 1); ++i)
-            if ((i + j) / (p * 2) == (i + j + k) / (p * 2)) swap_if(i + j, i + j + k);
-  }
-  auto to_front = [&] {  // the best of the list to its head
-    if (kSorted) return;
-#pragma unroll
-    for (int i = 1; i < EPL; ++i) swap_if(0, i);
-  };
-  to_front();
-  auto choose = [&](int from, int to) {  // the rounds from .. to - 1; how many choices there are
-    for (int j = from; j < to; ++j) {
-      const float c = redux_max(key[0]);
-      if (c == -INFINITY) return j;  // nothing is left
-      const int w = __ffs(__ballot_sync(0xffffffffu, key[0] == c)) - 1;  // the lowest lane: the lowest id
-      const int id = __shfl_sync(0xffffffffu, lane * EPL + at[0], w);
-      const float wl = __shfl_sync(0xffffffffu, l[0], w);
-      if (lane == j) {
-        my_id = id;
-        my_l = wl;
-        my_c = c;
+          for (int i = 0; i < EPL; ++i) {
+            if (!kSorted && i > 0) break;
+            key[i] = kSorted && i + 1 < EPL ? key[i + 1] : -INFINITY;
+            if (kSorted && i + 1 < EPL) l[i] = l[i + 1], at[i] = at[i + 1];
+          }
+          to_front();
+        }
       }
-      if (lane == w) {
+      return to;
+    };
+    int found = choose(0, min(32, a.top_k + scored));
+    if (scored) {
+      // Is a choice nearer to the next one than their errors?  (Equal logits with
+      // equal biases have equal keys.)  With all 32 lanes taken by choices there is
+      // no room for the runner-up: such rows are always computed in 64 bits.
+      const float my_b = a.bias && my_id >= 0 ? a.bias[my_id] : 0.0f;
+      auto tolerance = [&](float c, float cb, float o, float ob) {
+        const float scores = fabsf(c - cb) + fabsf(o - ob), keys = fabsf(c) + fabsf(o);
+        return err * scores + 2.0f * kStep * (keys + scores) + kTiny;
+      };
+      const float c = __shfl_down_sync(0xffffffffu, my_c, 1), cl = __shfl_down_sync(0xffffffffu, my_l, 1),
+                  cb = __shfl_down_sync(0xffffffffu, my_b, 1);
+      const bool near = lane + 1 < found && my_c - c <= tolerance(my_c, my_b, c, cb) && !(cl == my_l && cb == my_b);
+      bool whole = __any_sync(0xffffffffu, close) || a.top_k == 32 || bad;
+      if (!whole && __any_sync(0xffffffffu, near)) {
+        // Three more candidates; where the last of them is clearly behind the
+        // choices, the candidates' keys in 64 bits settle the order.
+        const int most = min(32, a.top_k + 4);
+        const bool all = found < min(32, a.top_k + 1);  // nothing was left already
+        if (!all) found = choose(found, most);
+        const float ob = a.bias && my_id >= 0 ? a.bias[my_id] : 0.0f;
+        const int e0 = min(a.top_k, found) - 1, e1 = found - 1;
+        const float c0 = __shfl_sync(0xffffffffu, my_c, e0), b0 = __shfl_sync(0xffffffffu, ob, e0);
+        const float c1 = __shfl_sync(0xffffffffu, my_c, e1), b1 = __shfl_sync(0xffffffffu, ob, e1);
+        whole = !(all || found < most) && !(c0 - c1 > tolerance(c0, b0, c1, b1));
+        if (!whole) {
+          double k64 = -INFINITY;
+          if (softmax) {
+            float r[EPL];
+            load_logits<EPL, BF16, WIDE>(a, row, lane, r);
+            double total = 0.0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+              if (r[i] > -INFINITY) total += exp((double)r[i] - (double)top);
+            total = warp_sum64(total);
+            k64 = exp((double)my_l - (double)top) / total;
+          } else {
+            k64 = 1.0 / (1.0 + exp(-(double)my_l));
+          }
+          k64 += (double)ob;
+          int rank = 0;
+          for (int i = 0; i < found; ++i) {
+            const double o = __shfl_sync(0xffffffffu, k64, i);
+            const int id = __shfl_sync(0xffffffffu, my_id, i);
+            rank += o > k64 || (o == k64 && id < my_id);
+          }
+          int src = lane;
+          for (int i = 0; i < found; ++i) {
+            const int at_rank = __ffs(__ballot_sync(0xffffffffu, lane < found && rank == i)) - 1;
+            if (lane == i) src = at_rank;
+          }
+          my_id = __shfl_sync(0xffffffffu, my_id, src);
+          my_l = __shfl_sync(0xffffffffu, my_l, src);
+        }
+      }
+      if (whole) {
+        load_logits<EPL, BF16, WIDE>(a, row, lane, l);  // (the rounds have moved them)
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (isnan(l[i])) l[i] = -INFINITY;
+        my_id = choose_64<EPL>(a, l, lane, route_smem + (size_t)warp * a.experts);
+        // the chosen logits, from the lanes that hold them
+        my_l = -INFINITY;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-          if (!kSorted && i > 0) break;
-          key[i] = kSorted && i + 1 < EPL ? key[i + 1] : -INFINITY;
-          if (kSorted && i + 1 < EPL) l[i] = l[i + 1], at[i] = at[i + 1];
+          const float v = __shfl_sync(0xffffffffu, l[i], my_id >= 0 ? my_id / EPL : 0);
+          if (my_id >= 0 && my_id % EPL == i) my_l = v;
         }
-        to_front();
-      }
-    }
-    return to;
-  };
-  int found = choose(0, min(32, a.top_k + scored));
-  if (scored) {
-    // Is a choice nearer to the next one than their errors?  (Equal logits with
-    // equal biases have equal keys.)  With all 32 lanes taken by choices there is
-    // no room for the runner-up: such rows are always computed in 64 bits.
-    const float my_b = a.bias && my_id >= 0 ? a.bias[my_id] : 0.0f;
-    auto tolerance = [&](float c, float cb, float o, float ob) {
-      const float scores = fabsf(c - cb) + fabsf(o - ob), keys = fabsf(c) + fabsf(o);
-      return err * scores + 2.0f * kStep * (keys + scores) + kTiny;
-    };
-    const float c = __shfl_down_sync(0xffffffffu, my_c, 1), cl = __shfl_down_sync(0xffffffffu, my_l, 1),
-                cb = __shfl_down_sync(0xffffffffu, my_b, 1);
-    const bool near = lane + 1 < found && my_c - c <= tolerance(my_c, my_b, c, cb) && !(cl == my_l && cb == my_b);
-    bool whole = __any_sync(0xffffffffu, close) || a.top_k == 32 || bad;
-    if (!whole && __any_sync(0xffffffffu, near)) {
-      // Three more candidates; where the last of them is clearly behind the
-      // choices, the candidates' keys in 64 bits settle the order.
-      const int most = min(32, a.top_k + 4);
-      const bool all = found < min(32, a.top_k + 1);  // nothing was left already
-      if (!all) found = choose(found, most);
-      const float ob = a.bias && my_id >= 0 ? a.bias[my_id] : 0.0f;
-      const int e0 = min(a.top_k, found) - 1, e1 = found - 1;
-      const float c0 = __shfl_sync(0xffffffffu, my_c, e0), b0 = __shfl_sync(0xffffffffu, ob, e0);
-      const float c1 = __shfl_sync(0xffffffffu, my_c, e1), b1 = __shfl_sync(0xffffffffu, ob, e1);
-      whole = !(all || found < most) && !(c0 - c1 > tolerance(c0, b0, c1, b1));
-      if (!whole) {
-        double k64 = -INFINITY;
-        if (softmax) {
-          float r[EPL];
-          load_logits<EPL, BF16, WIDE>(a, row, lane, r);
-          double total = 0.0;
-#pragma unroll
-          for (int i = 0; i < EPL; ++i)
-            if (r[i] > -INFINITY) total += exp((double)r[i] - (double)top);
-          total = warp_sum64(total);
-          k64 = exp((double)my_l - (double)top) / total;
-        } else {
-          k64 = 1.0 / (1.0 + exp(-(double)my_l));
-        }
-        k64 += (double)ob;
-        int rank = 0;
-        for (int i = 0; i < found; ++i) {
-          const double o = __shfl_sync(0xffffffffu, k64, i);
-          const int id = __shfl_sync(0xffffffffu, my_id, i);
-          rank += o > k64 || (o == k64 && id < my_id);
-        }
-        int src = lane;
-        for (int i = 0; i < found; ++i) {
-          const int at_rank = __ffs(__ballot_sync(0xffffffffu, lane < found && rank == i)) - 1;
-          if (lane == i) src = at_rank;
-        }
-        my_id = __shfl_sync(0xffffffffu, my_id, src);
-        my_l = __shfl_sync(0xffffffffu, my_l, src);
-      }
-    }
-    if (whole) {
-      load_logits<EPL, BF16, WIDE>(a, row, lane, l);  // (the rounds have moved them)
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (isnan(l[i])) l[i] = -INFINITY;
-      my_id = choose_64<EPL>(a, l, lane, route_smem + (size_t)warp * a.experts);
-      // the chosen logits, from the lanes that hold them
-      my_l = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const float v = __shfl_sync(0xffffffffu, l[i], my_id >= 0 ? my_id / EPL : 0);
-        if (my_id >= 0 && my_id % EPL == i) my_l = v;
       }
     }
   }
