@@ -90,11 +90,13 @@ __global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(const int32_t* _
       if (rank == 0) {
         p.offsets[e] = first;
         int* t = p.tiles + 1 + 3 * (tiles + sum.y - mine);
+        // tiles of the tensor cores are of even sizes: one of few rows takes as long as one of many
+        const int step = tile_rows == kTcTile && mine > 0 ? ((all + mine - 1) / mine + 31) & ~31 : tile_rows;
         if (e < E)
-          for (int r = 0; r < all; r += tile_rows, t += 3) {
+          for (int r = 0; r < all; r += step, t += 3) {
             t[0] = e;
             t[1] = first + r;
-            t[2] = min(tile_rows, all - r);
+            t[2] = min(step, all - r);
           }
       }
     }

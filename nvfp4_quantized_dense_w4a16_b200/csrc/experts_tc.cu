@@ -2,26 +2,32 @@
 // one launch computes, for every expert, its rows (sorted by expert) times
 // its NVFP4 weight.
 //
-// A persistent CTA per SM walks the tiles (128 rows of one expert) x (a pair
-// of MMA operands of 128 weight rows: gate and up rows of the same columns, or
-// 256 consecutive rows of a plain weight).  Per unit of two 64-element K chunks:
-//   * one warp streams the weights' chunks (18432 B) by bulk copies
-//     and one the rows' chunks (2 x 128 x 128 B, 128-byte swizzle) by TMA;
-//   * two warpgroups, one per operand, decode the codes to bf16 and write
-//     them to tensor memory, where they are the MMA's A operand (M = 128);
-//   * two threads, one per operand, issue tcgen05.mma kind::f16 against
-//     the same rows in shared memory (N = 128), each into its own fp32
-//     accumulator.  A barrier wait, a fence and a commit cost an issuing thread
-//     about 0.1 us each while its MMAs of 64 cycles drain: one thread with
-//     one-chunk units kept the tensor pipe busy for half of the time;
-//   * two further warpgroups (64 rows each) read a finished tile's
-//     accumulators, one into registers and one into shared memory, hand them
-//     back and run the epilogue while the next tile's MMAs proceed.
-// The pair is what bounds the traffic: a row tile is read from L2 once per 256
-// weight rows, 50 KB per unit of 1024 MMA cycles (50 B/clk per SM).
-// Tensor memory: accumulators in columns 0..255, two A slots of a unit per
-// operand in columns 256..511.  Every wait is bounded; on expiry a device
-// error bit is raised and the CTA frees its tensor memory and exits.
+// A persistent cluster of two CTAs (a pair of SMs) walks the tiles: up to 256
+// rows of one expert x 256 weight rows, 128 per CTA (64 gate rows and the up
+// rows of the same columns, or 128 consecutive rows of a plain weight).  Per
+// unit of two 64-element K chunks, in each CTA:
+//   * one warp streams its weights' chunks (9216 B) by bulk copies, and one its
+//     half of the rows' chunks (2 x 128 x 128 B, 128-byte swizzle) by TMA;
+//   * two sets of four warps take the units in turn, decode the codes to bf16
+//     and write them to tensor memory, where they are the MMA's A operand;
+//   * one warp of CTA 0 issues tcgen05.mma cta_group::2 kind::f16 (M = 256, N =
+//     the tile's rows) for both CTAs: each multiplies its weight rows by both
+//     halves of the rows, into its own fp32 accumulator;
+//   * two warpgroups (128 rows each) take a finished tile's accumulators, half
+//     into shared memory and half into registers, hand them back and store the
+//     results while the next tile's MMAs proceed.
+// What bounds such a loop here is the decode, 670 cycles of the ALU pipe per 256
+// weight rows and unit whatever the number of rows, and the traffic from L2.  A
+// wide N spreads the decode over 256 rows (512 MMA cycles per 128 of them), and
+// the pair halves the rows' traffic: 41 KB per unit of 1024 MMA cycles and CTA.
+// One CTA by itself with 256 weight rows and N = 128 (50 KB per unit, the decode
+// used once per 128 rows) ran at 1640 cycles per unit: 32768 pairs of 2048 x 1024
+// took 478 us and take 433, 1024 pairs of 4096 x 12288 404 and 334.  Arrivals on
+// the other CTA's barriers carry no memory of other proxies and so no cluster
+// scope: with it each costs a fence of 1000 cycles (732 us).
+// Tensor memory: accumulators in columns 0..255, four A slots of a unit in
+// columns 256..511.  Every wait is bounded; on expiry a device error bit is
+// raised and the CTAs free their tensor memory and exit.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -47,17 +53,20 @@ __device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f 
 
 constexpr int kThreads = 640;
 constexpr int kUnit = 2;  // K chunks per unit
-constexpr int kXStages = 3, kWStages = 3, kASlots = 2;
-constexpr int kTiles = 4;  // weight tiles of 64 rows per CTA tile: two per MMA operand
+constexpr int kCtas = 2;  // of a cluster: they share a row tile, each holds half of it
+constexpr int kXStages = 3, kWStages = 6, kASlots = 4;
+constexpr int kSets = 2;                                // of four decode warps: they take the units in turn
+constexpr int kTiles = 2;                               // weight tiles of 64 rows per CTA tile
+constexpr int kOpRows = kTiles * kTileRows;             // weight rows of a CTA: M of its half of the MMA
 constexpr int kWStageBytes = kTiles * kUnit * kChunkBytes;  // [tile][chunk]
-constexpr int kXChunkBytes = kTcTile * 128, kXStageBytes = kUnit * kXChunkBytes;
+constexpr int kXChunkBytes = kTcTile / kCtas * 128, kXStageBytes = kUnit * kXChunkBytes;
 constexpr int kMine = kTcTile / 2;                      // rows of a tile per epilogue warpgroup
-constexpr int kOpRows = 2 * kTileRows;                  // weight rows of an MMA operand
-constexpr int kParkBytes = kMine * kOpRows * 4;       // one warpgroup's half of an accumulator
+constexpr int kHeld = kMine / 2;                        // of them in registers, and as many in shared memory
+constexpr int kParkBytes = kHeld * kOpRows * 4;
 constexpr int kSmemW = kXStages * kXStageBytes;
 constexpr int kSmemPark = kSmemW + kWStages * kWStageBytes;
 constexpr int kSmemBar = kSmemPark + 2 * kParkBytes;
-constexpr int kNumBars = 2 * kXStages + 2 * kWStages + 4 * kASlots + 2;
+constexpr int kNumBars = 2 * kXStages + 2 * kWStages + 2 * kASlots + 2;
 constexpr int kSmemAlloc = kSmemBar + kNumBars * 8 + 16 + 1024;  // slack for 1024-byte alignment
 static_assert(kSmemAlloc <= 232448, "shared memory budget");
 constexpr int kAColBase = 256;
@@ -69,22 +78,86 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// ------------------------------------------------- the pair of CTAs of a cluster
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Arrive on CTA 0's barrier that stands where `bar` does.
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
+// One MMA of both CTAs (256 weight rows): each gives its A, its half of the rows and its accumulator.
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrive on `bar` of both CTAs once this thread's MMAs so far have completed.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// Whether `ok` holds for all 128 threads that meet at barrier `id`.
+__device__ __forceinline__ bool all_of_group(int id, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
 struct TcExpertsArgs {
   ExpertsView w;
   MoePlan plan;
   void* out;
-  int pairs_n;  // CTA tiles (two MMA operands) along the weight of an expert
+  int wide_n;  // cluster tiles along the weight of an expert
 };
 
 struct TileInfo {
   int e, first, rows, wt;
 };
 
-__device__ __forceinline__ TileInfo tile_at(const TcExpertsArgs& a, int T) {
-  const int tt = T / a.pairs_n;
+__device__ __forceinline__ TileInfo tile_at(const TcExpertsArgs& a, int T, int rank) {
+  const int tt = T / a.wide_n;
   const int* p = a.plan.tiles + 1 + 3 * tt;
-  return TileInfo{__ldcg(p), __ldcg(p + 1), __ldcg(p + 2), T % a.pairs_n};
+  return TileInfo{__ldcg(p), __ldcg(p + 1), __ldcg(p + 2), kCtas * (T - tt * a.wide_n) + rank};
 }
+
+// Columns of the tile's MMA: a tile with few rows needs few.  Each CTA holds half of them.
+__device__ __forceinline__ int tile_columns(int rows) { return min(kTcTile, (rows + 31) & ~31); }
 
 // Wait that ignores the abort flag (in-flight copies must land before exit).
 __device__ __forceinline__ bool drain(uint64_t* bar, uint32_t parity) {
@@ -98,7 +171,7 @@ __device__ __forceinline__ bool drain(uint64_t* bar, uint32_t parity) {
 }
 
 template <int MODE>
-__global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_constant__ CUtensorMap xmap,
+__global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_constant__ CUtensorMap xmap,
                                                                 const TcExpertsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
@@ -109,41 +182,42 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
   uint64_t* xempty = xfull + kXStages;
   uint64_t* wfull = xempty + kXStages;
   uint64_t* wempty = wfull + kWStages;
-  uint64_t* afull = wempty + kWStages;     // [operand][slot]
-  uint64_t* aempty = afull + 2 * kASlots;  // likewise
-  uint64_t* accfull = aempty + 2 * kASlots;
+  uint64_t* afull = wempty + kWStages;
+  uint64_t* aempty = afull + kASlots;
+  uint64_t* accfull = aempty + kASlots;
   uint64_t* accempty = accfull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accempty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* err = &g_moe_device_error;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kc = a.w.kc;
+  const int kc = a.w.kc, rank = (int)cluster_rank();
+  const int first_tile = blockIdx.x / kCtas, tile_step = gridDim.x / kCtas;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kXStages; ++s) {
       mbar_init(&xfull[s], 1);
-      mbar_init(&xempty[s], 2);  // one commit per MMA thread
+      mbar_init(&xempty[s], 1);
     }
     for (int s = 0; s < kWStages; ++s) {
       mbar_init(&wfull[s], 1);
-      mbar_init(&wempty[s], 8);
+      mbar_init(&wempty[s], 4);
     }
-    for (int s = 0; s < 2 * kASlots; ++s) {
-      mbar_init(&afull[s], 4);
+    for (int s = 0; s < kASlots; ++s) {
+      mbar_init(&afull[s], 4 * kCtas);  // (CTA 0's)
       mbar_init(&aempty[s], 1);
     }
-    mbar_init(accfull, 2);
-    mbar_init(accempty, 8);
+    mbar_init(accfull, 1);
+    mbar_init(accempty, 8 * kCtas);  // (CTA 0's)
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 2) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(tmem_slot, 512);
   }
   if (warp == 1 && lane == 0) tma_prefetch_desc(&xmap);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // The kernel before this one (the sorting of the rows, or the gate and up
@@ -151,23 +225,23 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
   // plan is in L2.  So only the warp that reads that kernel's rows waits for it,
   // the weights are streamed and decoded ahead (20 experts of 1056 x 672, 111
   // rows: 36.0 -> 33.4 us), and all that is written follows from those rows.
-  const int total = __ldcg(a.plan.tiles) * a.pairs_n;
+  const int total = __ldcg(a.plan.tiles) * a.wide_n;
 
   if (warp == 0) {
     // ------------------------------------------------------ weight producer
     if (lane == 0) {
       int u = 0;
       bool ok = true;
-      for (int T = blockIdx.x; ok && T < total; T += gridDim.x) {
-        const TileInfo ti = tile_at(a, T);
+      for (int T = first_tile; ok && T < total; T += tile_step) {
+        const TileInfo ti = tile_at(a, T, rank);
         const size_t tile_bytes = (size_t)kc * kChunkBytes;
         // Past the last tile, that tile stands in: its sums are not stored.
         const uint8_t* w[kTiles];
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
-          const bool silu = MODE == (int)ExpertsOut::kSiluMul;
-          const int tile = min(silu ? 2 * ti.wt + (i & 1) : kTiles * ti.wt + i, a.w.wtiles - 1);
-          w[i] = a.w.tiles + ((size_t)(silu ? 2 * ti.e + (i >> 1) : ti.e) * a.w.wtiles + tile) * tile_bytes;
+          const bool silu = MODE == (int)ExpertsOut::kSiluMul;  // gate and up rows of the same 64 columns
+          const int tile = min(silu ? ti.wt : kTiles * ti.wt + i, a.w.wtiles - 1);
+          w[i] = a.w.tiles + ((size_t)(silu ? 2 * ti.e + i : ti.e) * a.w.wtiles + tile) * tile_bytes;
         }
         for (int c = 0; c < kc; c += kUnit, ++u) {
           const int s = u % kWStages;
@@ -191,8 +265,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
     if (lane == 0) {
       int u = 0;
       bool ok = true;
-      for (int T = blockIdx.x; ok && T < total; T += gridDim.x) {
-        const TileInfo ti = tile_at(a, T);
+      for (int T = first_tile; ok && T < total; T += tile_step) {
+        const TileInfo ti = tile_at(a, T, rank);
+        const int row = ti.first + rank * (tile_columns(ti.rows) / kCtas);
         for (int c = 0; c < kc; c += kUnit, ++u) {
           const int s = u % kXStages, nc = min(kUnit, kc - c);
           if (u >= kXStages && !mbar_wait(&xempty[s], ((u / kXStages) - 1) & 1, abort_flag, err, 1)) {
@@ -201,65 +276,63 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
           }
           mbar_arrive_expect_tx(&xfull[s], nc * kXChunkBytes);
           for (int j = 0; j < nc; ++j)
-            tma_load_2d(xs + s * kXStageBytes + j * kXChunkBytes, &xmap, (c + j) * kChunkK, ti.first, &xfull[s]);
+            tma_load_2d(xs + s * kXStageBytes + j * kXChunkBytes, &xmap, (c + j) * kChunkK, row, &xfull[s]);
         }
       }
       for (int r = max(0, u - kXStages); r < u; ++r) drain(&xfull[r % kXStages], (r / kXStages) & 1);
     }
-  } else if (warp < 4) {
-    // ----------------------------------------------------------- MMA issuers
-    // (the whole warp walks the loop and one elected lane issues: uniform
-    // control flow keeps the descriptors in uniform registers)
-    const int half = warp - 2;
-    const uint32_t d = tmem + 128 * half;
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ MMA issuer
+    // (CTA 0's, for both; the whole warp walks the loop and one elected lane
+    // issues: uniform control flow keeps the descriptors in uniform registers)
     int u = 0, i = 0;
     bool ok = true;
-    for (int T = blockIdx.x; ok && T < total; T += gridDim.x, ++i) {
+    for (int T = first_tile; rank == 0 && ok && T < total; T += tile_step, ++i) {
+      const uint32_t idesc = idesc_bf16_f32(kCtas * kOpRows, tile_columns(tile_at(a, T, rank).rows));
       if (i > 0) {
         ok = mbar_wait(accempty, (i - 1) & 1, abort_flag, err, 2);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
       }
-      // a tile with few rows needs few columns
-      const uint32_t idesc = idesc_bf16_f32(kOpRows, min(kTcTile, (tile_at(a, T).rows + 15) & ~15));
       for (int c = 0; c < kc; c += kUnit, ++u) {
         const int sx = u % kXStages, sa = u % kASlots;
         // (the decode warps have waited for the rows as well)
-        ok = mbar_wait(&afull[half * kASlots + sa], (u / kASlots) & 1, abort_flag, err, 2);
+        ok = mbar_wait(&afull[sa], (u / kASlots) & 1, abort_flag, err, 2);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         const uint64_t b = smem_desc_sw128(smem_u32(xs + sx * kXStageBytes));
-        const uint32_t aslot = tmem + kAColBase + 128 * sa + 64 * half;
+        const uint32_t aslot = tmem + kAColBase + 32 * kUnit * sa;
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < kUnit; ++j) {
             if (c + j >= kc) break;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ts(d, aslot + 32 * j + 8 * kk, b + j * (kXChunkBytes >> 4) + 2 * kk, idesc, (c | j | kk) ? 1u : 0u);
+              mma_pair(tmem, aslot + 32 * j + 8 * kk, b + j * (kXChunkBytes >> 4) + 2 * kk, idesc, (c | j | kk) ? 1u : 0u);
           }
-          mma_commit(&aempty[half * kASlots + sa]);
-          mma_commit(&xempty[sx]);
-          if (c + kUnit >= kc) mma_commit(accfull);
+          commit_pair(&aempty[sa]);
+          commit_pair(&xempty[sx]);
+          if (c + kUnit >= kc) commit_pair(accfull);
         }
         __syncwarp();
       }
     }
-  } else if (warp < 12) {
+  } else if (warp >= 4 && warp < 4 + 4 * kSets) {
     // --------------------------------------------------------------- decode
-    const int half = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane;
-    const uint32_t col = tmem + ((uint32_t)(32 * q) << 16) + kAColBase + 64 * half;
-    int u = 0;
+    const int set = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane, r = row & 63;
+    const uint32_t col = tmem + ((uint32_t)(32 * q) << 16) + kAColBase;
+    const uint8_t* mine = wsm + (row >> 6) * kUnit * kChunkBytes;
+    const int units = (kc + kUnit - 1) / kUnit;
+    int base = 0;  // units of the tiles before
     bool ok = true;
-    for (int T = blockIdx.x; ok && T < total; T += gridDim.x) {
-      for (int c = 0; c < kc; c += kUnit, ++u) {
-        const int sw = u % kWStages, sa = u % kASlots, nc = min(kUnit, kc - c);
+    for (int T = first_tile; ok && T < total; T += tile_step, base += units) {
+      for (int i = (set - base) & (kSets - 1); i < units; i += kSets) {
+        const int u = base + i, sw = u % kWStages, sa = u % kASlots, nc = min(kUnit, kc - kUnit * i);
         ok = mbar_wait(&wfull[sw], (u / kWStages) & 1, abort_flag, err, 4);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         uint4 lo[kUnit], hi[kUnit];
         uint32_t sc[kUnit];
-        const uint8_t* w = wsm + sw * kWStageBytes + (2 * half + (row >> 6)) * kUnit * kChunkBytes;
-        const int r = row & 63;
+        const uint8_t* w = mine + sw * kWStageBytes;
 #pragma unroll
         for (int j = 0; j < kUnit; ++j) {  // (a missing second chunk reads what the stage held before)
           lo[j] = *reinterpret_cast<const uint4*>(w + j * kChunkBytes + code_offset(r, 0, j));
@@ -276,19 +349,19 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
           const uint32_t words[8] = {lo[j].x, lo[j].y, lo[j].z, lo[j].w, hi[j].x, hi[j].y, hi[j].z, hi[j].w};
           uint32_t v[32];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int k = 0; k < 8; ++k) {
             uint32_t o[4];
-            decode8(words[i], s2[i >> 1], o);
+            decode8(words[k], s2[k >> 1], o);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[4 * i + k] = o[k];
+            for (int z = 0; z < 4; ++z) v[4 * k + z] = o[z];
           }
-          if (j == 0 && u >= kASlots) {  // the MMAs that read this slot two units ago are done
-            ok = mbar_wait(&aempty[half * kASlots + sa], ((u / kASlots) - 1) & 1, abort_flag, err, 4);
+          if (j == 0 && u >= kASlots) {  // the MMAs that read this slot before are done
+            ok = mbar_wait(&aempty[sa], ((u / kASlots) - 1) & 1, abort_flag, err, 4);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
           }
-          tmem_st32(col + 128 * sa + 32 * j, v);
+          tmem_st32(col + 32 * (kUnit * sa + j), v);
         }
         if (!ok) break;
         // the unit's rows, on the MMA thread's behalf
@@ -298,95 +371,109 @@ __global__ void __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_co
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&afull[half * kASlots + sa]);
+        if (lane == 0) arrive_first(&afull[sa]);
       }
     }
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------- epilogue
-    const int g = (warp - 12) >> 2, q = warp & 3, row = 32 * q + lane;
-    const int et = threadIdx.x - 384 - 128 * g;  // 0..127 within this warpgroup
-    float* park = reinterpret_cast<float*>(smem + kSmemPark + g * kParkBytes);  // [kMine][128]
+    const int g = (warp - 4 - 4 * kSets) >> 2, q = warp & 3, row = 32 * q + lane;
+    float* park = reinterpret_cast<float*>(smem + kSmemPark + g * kParkBytes);  // [kHeld][128]
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + kMine * g;
     int i = 0;
-    for (int T = blockIdx.x; T < total; T += gridDim.x, ++i) {
-      const TileInfo ti = tile_at(a, T);
+    for (int T = first_tile; T < total; T += tile_step, ++i) {
+      const TileInfo ti = tile_at(a, T, rank);
       const int first = ti.first + kMine * g, mine = min(kMine, ti.rows - kMine * g);  // may be <= 0
       const bool silu = MODE == (int)ExpertsOut::kSiluMul;
       const float gs0 = a.w.gs[silu ? 2 * ti.e : ti.e] * kUnscale;
       const float gs1 = silu ? a.w.gs[2 * ti.e + 1] * kUnscale : gs0;
-      int pr[2] = {0, 0};  // the rows' pairs
+      int pr[kMine / 32] = {};  // the rows' pairs
       if (!silu)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kMine / 32; ++h)
           if (32 * h + lane < mine) pr[h] = __ldcg(a.plan.order + first + 32 * h + lane);
       bool ok = mbar_wait(accfull, i & 1, abort_flag, err, 8);
       ok = __all_sync(0xffffffffu, ok);
+      ok = all_of_group(1 + g, ok);  // (the group's warps pass the same barriers)
       if (!ok) break;
       tc_fence_after();
-      float v[kMine];
+      float v[kHeld];  // rows kHeld .. kMine - 1
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t t[32];
-        tmem_ld32(lane_addr + 128 + 32 * h, t);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) park[(32 * h + j) * kOpRows + row] = gs1 * __uint_as_float(t[j]);
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kHeld / 32; ++h) {
         uint32_t t[32];
         tmem_ld32(lane_addr + 32 * h, t);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[32 * h + j] = gs0 * __uint_as_float(t[j]);
+        for (int j = 0; j < 32; ++j) park[(32 * h + j) * kOpRows + row] = __uint_as_float(t[j]);
+      }
+#pragma unroll
+      for (int h = 0; h < kHeld / 32; ++h) {
+        uint32_t t[32];
+        tmem_ld32(lane_addr + kHeld + 32 * h, t);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[32 * h + j] = __uint_as_float(t[j]);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(accempty);
-      if (silu) {
-        // h = silu(g) * u, left as bf16 in the low half of u's own word
+      if (lane == 0) arrive_first(accempty);
+      // Half of the rows at a time meet in shared memory, so that a warp stores
+      // whole rows of the tile's columns (and the gate products of lanes 0..63
+      // find the up products of the others).
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-          float* u = park + j * kOpRows + row;
-          *reinterpret_cast<uint32_t*>(u) = f32_to_bf16_bits(silu_fast(v[j]) * *u);
-        }
-        // rows in sorted order, 16 bytes at a time (inter is a multiple of 32)
-        named_bar_sync(1 + g, 128);
-        const int64_t inter = a.w.n / 2, c0 = kOpRows * (int64_t)ti.wt;
-        uint16_t* h = static_cast<uint16_t*>(a.out) + first * inter + c0;
-        for (int idx = et; idx < mine * 16; idx += 128) {
-          const int j = idx >> 4, ch = idx & 15;
-          if (c0 + 8 * ch >= inter) continue;
-          const uint4 p0 = *reinterpret_cast<const uint4*>(park + j * kOpRows + 8 * ch);
-          const uint4 p1 = *reinterpret_cast<const uint4*>(park + j * kOpRows + 8 * ch + 4);
-          *reinterpret_cast<uint4*>(h + j * inter + 8 * ch) =
-              make_uint4(p0.x | (p0.y << 16), p0.z | (p0.w << 16), p1.x | (p1.y << 16), p1.z | (p1.w << 16));
-        }
-        named_bar_sync(1 + g, 128);
-      } else {
-        const int64_t c0 = 2 * kOpRows * (int64_t)ti.wt + row, c1 = c0 + kOpRows, n = a.w.n;
+      for (int part = 0; part < 2; ++part) {
+        if (part == 1)
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-          if (j >= mine) break;
-          const int64_t at = (int64_t)__shfl_sync(0xffffffffu, pr[j >> 5], j & 31) * n;
-          if (MODE == (int)ExpertsOut::kF32) {
-            float* y = static_cast<float*>(a.out) + at;
-            if (c0 < n) y[c0] = v[j];
-            if (c1 < n) y[c1] = park[j * kOpRows + row];
-          } else {
-            uint16_t* y = static_cast<uint16_t*>(a.out) + at;
-            if (c0 < n) y[c0] = f32_to_bf16_bits(v[j]);
-            if (c1 < n) y[c1] = f32_to_bf16_bits(park[j * kOpRows + row]);
+          for (int j = 0; j < kHeld; ++j) park[j * kOpRows + row] = v[j];
+        named_bar_sync(1 + g, 128);
+        const int left = mine - kHeld * part;
+        if (silu) {
+          const int64_t inter = a.w.n / 2, col = kTileRows * (int64_t)ti.wt + 2 * lane;  // (inter is a multiple of 32)
+          uint16_t* h = static_cast<uint16_t*>(a.out) + (first + kHeld * part) * inter + col;
+          const int n = col < inter ? min(kHeld, left) : 0;
+#pragma unroll 4
+          for (int j = q; j < n; j += 4) {
+            const float2 z = *reinterpret_cast<const float2*>(park + j * kOpRows + 2 * lane);
+            const float2 u = *reinterpret_cast<const float2*>(park + j * kOpRows + kTileRows + 2 * lane);
+            const uint32_t h0 = f32_to_bf16_bits(silu_fast(gs0 * z.x) * (gs1 * u.x)),
+                           h1 = f32_to_bf16_bits(silu_fast(gs0 * z.y) * (gs1 * u.y));
+            *reinterpret_cast<uint32_t*>(h + j * inter) = h0 | (h1 << 16);
+          }
+        } else {
+          const int64_t col = kOpRows * (int64_t)ti.wt + 4 * lane, n = a.w.n;
+#pragma unroll
+          for (int t = 0; t < kHeld / 4; ++t) {
+            const int j = 4 * t + q;
+            if (4 * t >= left) break;
+            const int64_t at = (int64_t)__shfl_sync(0xffffffffu, pr[2 * part + (t >> 3)], j & 31) * n + col;
+            float4 z = *reinterpret_cast<const float4*>(park + j * kOpRows + 4 * lane);
+            z.x *= gs0, z.y *= gs0, z.z *= gs0, z.w *= gs0;
+            if (j >= left || col >= n) continue;
+            if (MODE == (int)ExpertsOut::kF32) {  // (n is a multiple of 32)
+              *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = z;
+            } else {
+              uint16_t* y = static_cast<uint16_t*>(a.out) + at;
+              const uint16_t b[4] = {f32_to_bf16_bits(z.x), f32_to_bf16_bits(z.y), f32_to_bf16_bits(z.z),
+                                     f32_to_bf16_bits(z.w)};
+              if ((n & 3) == 0) {
+                *reinterpret_cast<uint2*>(y) = make_uint2(b[0] | ((uint32_t)b[1] << 16), b[2] | ((uint32_t)b[3] << 16));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (col + i < n) y[i] = b[i];
+              }
+            }
           }
         }
+        named_bar_sync(1 + g, 128);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may arrive on its barriers or read its rows
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -450,7 +537,7 @@ cudaError_t launch_experts_tc(const void* xs, const ExpertsView& w, const MoePla
   // kTcTile rows behind the last pair belong to the buffer: no box leaves it
   cuuint64_t dims[2] = {(cuuint64_t)w.k, (cuuint64_t)(pairs + kTcTile)};
   cuuint64_t strides[1] = {(cuuint64_t)w.k * 2};
-  cuuint32_t box[2] = {(cuuint32_t)kChunkK, (cuuint32_t)kTcTile};
+  cuuint32_t box[2] = {(cuuint32_t)kChunkK, (cuuint32_t)(kTcTile / kCtas)};
   cuuint32_t estr[2] = {1, 1};
   if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(xs), dims, strides, box, estr,
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -460,10 +547,11 @@ cudaError_t launch_experts_tc(const void* xs, const ExpertsView& w, const MoePla
   a.w = w;
   a.plan = p;
   a.out = out;
-  a.pairs_n = mode == ExpertsOut::kSiluMul ? (w.wtiles + 1) / 2 : (w.wtiles + kTiles - 1) / kTiles;
-  const int64_t most = moe_max_tiles(pairs, w.experts, kTcTile) * a.pairs_n;
-  const int sms = device_sms();
-  const int grid = (int)(most < sms ? most : sms);
+  const int tiles = kCtas * (mode == ExpertsOut::kSiluMul ? 1 : kTiles);  // of 64 columns, a cluster
+  a.wide_n = (w.wtiles + tiles - 1) / tiles;
+  const int64_t most = moe_max_tiles(pairs, w.experts, kTcTile) * a.wide_n;
+  const int clusters = device_sms() / kCtas;
+  const int grid = kCtas * (int)(most < clusters ? most : clusters);
   ProfScope prof(s, mode == ExpertsOut::kSiluMul ? "experts_tc_silu" : "experts_tc");
   switch (mode) {
     case ExpertsOut::kSiluMul: return launch_one<(int)ExpertsOut::kSiluMul>(map, a, grid, s);

@@ -100,7 +100,7 @@ cudaError_t launch_moe_combine(const float* y, int splits, const int32_t* ids, c
 // Many rows per expert, on the tensor cores (plan with kTcTile rows a tile).
 // xs holds the rows sorted by expert, and kTcTile more rows of any content;
 // kSiluMul writes h in the same order, the others write row p of the pair.
-constexpr int kTcTile = 128;
+constexpr int kTcTile = 256;
 cudaError_t launch_experts_tc(const void* xs, const ExpertsView& w, const MoePlan& p, int64_t pairs, ExpertsOut mode,
                               void* out, cudaStream_t s);
 // xs[q, :] = x[order[q] / row_div, :]; with y, zeros to its rows without an expert.
