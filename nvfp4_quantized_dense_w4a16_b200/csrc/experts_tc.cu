@@ -22,9 +22,10 @@
 // the pair halves the rows' traffic: 41 KB per unit of 1024 MMA cycles and CTA.
 // One CTA by itself with 256 weight rows and N = 128 (50 KB per unit, the decode
 // used once per 128 rows) ran at 1640 cycles per unit: 32768 pairs of 2048 x 1024
-// took 478 us and take 433, 1024 pairs of 4096 x 12288 404 and 334.  Arrivals on
-// the other CTA's barriers carry no memory of other proxies and so no cluster
-// scope: with it each costs a fence of 1000 cycles (732 us).
+// took 478 us and take 433, 1024 pairs of 4096 x 12288 404 and 334.  What an
+// arrival on the other CTA's barrier announces (rows, tensor memory) has been
+// waited for before it, so it has no cluster scope, whose fences cost some 1000
+// cycles a unit (732 us).
 // Tensor memory: accumulators in columns 0..255, four A slots of a unit in
 // columns 256..511.  Every wait is bounded; on expiry a device error bit is
 // raised and the CTAs free their tensor memory and exit.
@@ -56,6 +57,9 @@ constexpr int kUnit = 2;  // K chunks per unit
 constexpr int kCtas = 2;  // of a cluster: they share a row tile, each holds half of it
 constexpr int kXStages = 3, kWStages = 6, kASlots = 4;
 constexpr int kSets = 2;                                // of four decode warps: they take the units in turn
+// A wait tells a phase of its barrier from the next one only, so a set has to wait
+// for every phase of the barriers that it waits on: a slot belongs to one set.
+static_assert(kWStages % kSets == 0 && kASlots % kSets == 0, "stages and slots are the sets' own");
 constexpr int kTiles = 2;                               // weight tiles of 64 rows per CTA tile
 constexpr int kOpRows = kTiles * kTileRows;             // weight rows of a CTA: M of its half of the MMA
 constexpr int kWStageBytes = kTiles * kUnit * kChunkBytes;  // [tile][chunk]
@@ -203,7 +207,7 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_t
       mbar_init(&wempty[s], 4);
     }
     for (int s = 0; s < kASlots; ++s) {
-      mbar_init(&afull[s], 4 * kCtas);  // (CTA 0's)
+      mbar_init(&afull[s], (4 + 1) * kCtas);  // (CTA 0's) decoded weights, and rows
       mbar_init(&aempty[s], 1);
     }
     mbar_init(accfull, 1);
@@ -295,7 +299,6 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_t
       }
       for (int c = 0; c < kc; c += kUnit, ++u) {
         const int sx = u % kXStages, sa = u % kASlots;
-        // (the decode warps have waited for the rows as well)
         ok = mbar_wait(&afull[sa], (u / kASlots) & 1, abort_flag, err, 2);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
@@ -315,6 +318,20 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_t
         }
         __syncwarp();
       }
+    }
+  } else if (warp == 3) {
+    // ---------------------------------------- both CTAs' rows, for the issuer
+    // (not ahead of its barrier's phase: rows of the unit kASlots later are only
+    // fetched once this unit's MMAs are done)
+    static_assert(kXStages <= kASlots, "rows are counted in the phase of their unit");
+    if (lane == 0) {
+      int u = 0;
+      bool ok = true;
+      for (int T = first_tile; ok && T < total; T += tile_step)
+        for (int c = 0; ok && c < kc; c += kUnit, ++u) {
+          ok = mbar_wait(&xfull[u % kXStages], (u / kXStages) & 1, abort_flag, err, 4);
+          if (ok) arrive_first(&afull[u % kASlots]);
+        }
     }
   } else if (warp >= 4 && warp < 4 + 4 * kSets) {
     // --------------------------------------------------------------- decode
@@ -363,10 +380,6 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_t
           }
           tmem_st32(col + 32 * (kUnit * sa + j), v);
         }
-        if (!ok) break;
-        // the unit's rows, on the MMA thread's behalf
-        ok = mbar_wait(&xfull[u % kXStages], (u / kXStages) & 1, abort_flag, err, 4);
-        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tmem_st_wait();
         tc_fence_before();
