@@ -59,11 +59,12 @@ struct Carve {
   int splits = 1;  // of the down products' K
 };
 
-// From how many rows an expert (on average) the tensor cores take over: with 64
-// experts of 2048 x 1024 the few-row kernel takes 97 us at 8 rows an expert and
-// 151 at 16, the tensor cores 95 and 111; with 8 of 4096 x 6144 132 / 210 and
-// 136 / 147; with 20 of 1056 x 672 32 / 36 and 34 / 35.
-bool use_tc(int64_t pairs, int64_t experts) { return pairs > ffn::kFewPairs && pairs > 10 * experts; }
+// From how many rows an expert (on average) the tensor cores take over.  The
+// layer with the few-row kernel and with the tensor cores, in us: 64 experts of
+// 2048 x 1024 at 6, 8, 12 rows an expert 90, 96, 112 and 90, 94, 101; 8 of
+// 4096 x 6144 at 8, 12, 16 rows 121, 140, 170 and 134, 139, 145; 20 of
+// 1056 x 672 at 7, 10, 14 rows 32.2, 32.6, 35.5 and 31.2, 31.7, 32.6.
+bool use_tc(int64_t pairs, int64_t experts) { return pairs > ffn::kFewPairs && pairs > 8 * experts; }
 
 size_t take(size_t& off, size_t bytes) {
   const size_t at = off;

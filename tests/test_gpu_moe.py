@@ -317,7 +317,7 @@ def test_linear_uneven_experts(native, m):
 @pytest.mark.parametrize("m,n,k,experts,top_k,padding", [
     # a plan of few and of many pairs per expert, made by one CTA and by several
     (32, 72, 96, 3, 1, 0.0), (33, 72, 96, 3, 1, 0.0), (35, 136, 64, 7, 1, 0.0), (36, 136, 64, 7, 1, 0.1),
-    (70, 136, 64, 7, 1, 0.0), (71, 136, 64, 7, 1, 0.1), (700, 64, 32, 1024, 6, 0.1), (2049, 72, 96, 17, 2, 0.1),
+    (56, 136, 64, 7, 1, 0.0), (57, 136, 64, 7, 1, 0.1), (70, 136, 64, 7, 1, 0.0), (71, 136, 64, 7, 1, 0.1), (700, 64, 32, 1024, 6, 0.1), (2049, 72, 96, 17, 2, 0.1),
     (4096, 40, 32, 2, 1, 0.0), (4097, 40, 32, 2, 1, 0.3),
 ])
 def test_linear_at_the_kernels_boundaries(native, m, n, k, experts, top_k, padding):
@@ -325,6 +325,20 @@ def test_linear_at_the_kernels_boundaries(native, m, n, k, experts, top_k, paddi
     s = Stack(native, experts, n, k, 2400 + m)
     x, x64 = rows(m, k, 2500 + m)
     check_linear(native, s, x, x64, pick(rng, m, experts, top_k, padding))
+
+
+@pytest.mark.parametrize("k", [32, 64, 96, 128, 544])
+@pytest.mark.parametrize("n", [1, 63, 130, 260])
+def test_linear_many_rows_any_depth(native, n, k):
+    """Row tiles of even sizes around the largest, odd numbers of K chunks, and as many tiles as keep every stage of
+    the pipeline in turn; columns that no vector store fits."""
+    rng = np.random.default_rng(2600 + n + k)
+    s = Stack(native, 2, n, k, 2700 + n + k)
+    m = 1100
+    x, x64 = rows(m, k, 2800 + k)
+    ids = np.zeros((m, 1), np.int32)
+    ids[rng.permutation(m)[:300]] = 1
+    check_linear(native, s, x, x64, ids)
 
 
 @pytest.mark.parametrize("m", [3, 64])
@@ -462,7 +476,9 @@ def test_layer_matches_oracle(native, m, experts, top_k, hidden, inter, padding)
 
 @pytest.mark.parametrize("m,experts,top_k,hidden,inter", [
     (1, 2, 1, 256, 2080, ), (3, 3, 2, 64, 4096), (16, 2, 2, 96, 1600), (33, 12, 1, 64, 2080), (32, 7, 1, 128, 64),
-    (33, 7, 1, 128, 64), (35, 7, 1, 128, 64), (36, 7, 1, 128, 64), (70, 7, 1, 128, 64), (71, 7, 1, 128, 64),
+    (33, 7, 1, 128, 64), (35, 7, 1, 128, 64), (36, 7, 1, 128, 64), (56, 7, 1, 128, 64), (57, 7, 1, 128, 64),
+    (70, 7, 1, 128, 64), (71, 7, 1, 128, 64), (255, 1, 1, 64, 64), (256, 1, 1, 128, 96), (257, 1, 1, 96, 32),
+    (513, 2, 1, 160, 64), (640, 3, 2, 64, 128),
     (2100, 17, 2, 96, 32), (1, 64, 32, 96, 64), (2, 40, 33, 96, 64),
 ])
 def test_layer_at_the_kernels_boundaries(native, m, experts, top_k, hidden, inter):
