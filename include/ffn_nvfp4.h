@@ -361,9 +361,9 @@ ffn_status ffn_nvfp4_experts_info(const ffn_nvfp4_experts* w, int64_t* experts, 
  * zeros; equal ids in a row are computed each.  fp32 accumulation; a row's
  * result does not depend on which other rows share its expert as long as the
  * same kernels run (they are chosen by m, top_k and the shapes).  m == 0 is a
- * no-op.  The workspace holds the rows sorted by expert; it may be shared by
- * calls on one stream.  Errors: FFN_ERR_UNSUPPORTED for a gate and up stack;
- * FFN_ERR_SHAPE when 2 * m * top_k exceeds 2^31 - 1 or m * top_k rows of n or k
+ * no-op.  The workspace holds the rows' places by expert and, for many rows,
+ * their copies in that order; it may be shared by calls on one stream.
+ * Errors: FFN_ERR_UNSUPPORTED for a gate and up stack; FFN_ERR_SHAPE when 2 * m * top_k exceeds 2^31 - 1 or m * top_k rows of n or k
  * columns are more than 2^40 elements (the sizes: FFN_ERR_UNSUPPORTED for
  * experts > FFN_MOE_MAX_EXPERTS). */
 ffn_status ffn_nvfp4_experts_workspace_size(int64_t m, int top_k, int64_t experts, int64_t n, int64_t k,
