@@ -63,6 +63,11 @@ static_assert(kWStages % kSets == 0 && kASlots % kSets == 0, "stages and slots a
 constexpr int kTiles = 2;                               // weight tiles of 64 rows per CTA tile
 constexpr int kOpRows = kTiles * kTileRows;             // weight rows of a CTA: M of its half of the MMA
 constexpr int kWStageBytes = kTiles * kUnit * kChunkBytes;  // [tile][chunk]
+// Rows of a copy come in steps, each with its tensor map: a tile of few rows reads
+// few (512 rows over 8 large experts: 342 -> 329 us).  Copies of 32 rows issued
+// one after the other cost their issuing thread more than they save (433 us).
+constexpr int kBoxStep = 32;
+constexpr int kBoxes = kTcTile / kCtas / kBoxStep;
 constexpr int kXChunkBytes = kTcTile / kCtas * 128, kXStageBytes = kUnit * kXChunkBytes;
 constexpr int kMine = kTcTile / 2;                      // rows of a tile per epilogue warpgroup
 constexpr int kHeld = kMine / 2;                        // of them in registers, and as many in shared memory
@@ -150,6 +155,10 @@ struct TcExpertsArgs {
   int wide_n;  // cluster tiles along the weight of an expert
 };
 
+struct RowMaps {
+  CUtensorMap box[kBoxes];  // of kBoxStep, 2 kBoxStep, ... rows
+};
+
 struct TileInfo {
   int e, first, rows, wt;
 };
@@ -175,7 +184,7 @@ __device__ __forceinline__ bool drain(uint64_t* bar, uint32_t parity) {
 }
 
 template <int MODE>
-__global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_constant__ CUtensorMap xmap,
+__global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_constant__ RowMaps maps,
                                                                 const TcExpertsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
@@ -218,7 +227,7 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_t
   if (warp == 2) {
     tmem_alloc_pair(tmem_slot, 512);
   }
-  if (warp == 1 && lane == 0) tma_prefetch_desc(&xmap);
+  if (warp == 1 && lane < kBoxes) tma_prefetch_desc(&maps.box[lane]);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -271,16 +280,17 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_t
       bool ok = true;
       for (int T = first_tile; ok && T < total; T += tile_step) {
         const TileInfo ti = tile_at(a, T, rank);
-        const int row = ti.first + rank * (tile_columns(ti.rows) / kCtas);
+        const int half = tile_columns(ti.rows) / kCtas, row = ti.first + rank * half;
+        const int box = (half + kBoxStep - 1) / kBoxStep;  // in steps
         for (int c = 0; c < kc; c += kUnit, ++u) {
           const int s = u % kXStages, nc = min(kUnit, kc - c);
           if (u >= kXStages && !mbar_wait(&xempty[s], ((u / kXStages) - 1) & 1, abort_flag, err, 1)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&xfull[s], nc * kXChunkBytes);
+          mbar_arrive_expect_tx(&xfull[s], nc * box * kBoxStep * 128);
           for (int j = 0; j < nc; ++j)
-            tma_load_2d(xs + s * kXStageBytes + j * kXChunkBytes, &xmap, (c + j) * kChunkK, row, &xfull[s]);
+            tma_load_2d(xs + s * kXStageBytes + j * kXChunkBytes, &maps.box[box - 1], (c + j) * kChunkK, row, &xfull[s]);
         }
       }
       for (int r = max(0, u - kXStages); r < u; ++r) drain(&xfull[r % kXStages], (r / kXStages) & 1);
@@ -524,12 +534,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 template <int MODE>
-cudaError_t launch_one(const CUtensorMap& map, const TcExpertsArgs& a, int grid, cudaStream_t s) {
+cudaError_t launch_one(const RowMaps& maps, const TcExpertsArgs& a, int grid, cudaStream_t s) {
   auto kern = experts_tc_kernel<MODE>;
   // set on every launch: the attribute belongs to the current device's context
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), kSmemAlloc, s, map, a);
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), kSmemAlloc, s, maps, a);
 }
 
 }  // namespace
@@ -546,16 +556,18 @@ cudaError_t launch_experts_tc(const void* xs, const ExpertsView& w, const MoePla
                               void* out, cudaStream_t s) {
   auto enc = encode_fn();
   if (!enc) return cudaErrorInvalidValue;
-  CUtensorMap map;
+  RowMaps maps;
   // kTcTile rows behind the last pair belong to the buffer: no box leaves it
   cuuint64_t dims[2] = {(cuuint64_t)w.k, (cuuint64_t)(pairs + kTcTile)};
   cuuint64_t strides[1] = {(cuuint64_t)w.k * 2};
-  cuuint32_t box[2] = {(cuuint32_t)kChunkK, (cuuint32_t)(kTcTile / kCtas)};
   cuuint32_t estr[2] = {1, 1};
-  if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(xs), dims, strides, box, estr,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
+  for (int i = 0; i < kBoxes; ++i) {
+    cuuint32_t box[2] = {(cuuint32_t)kChunkK, (cuuint32_t)(kBoxStep * (i + 1))};
+    if (enc(&maps.box[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(xs), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
   TcExpertsArgs a;
   a.w = w;
   a.plan = p;
@@ -567,9 +579,9 @@ cudaError_t launch_experts_tc(const void* xs, const ExpertsView& w, const MoePla
   const int grid = kCtas * (int)(most < clusters ? most : clusters);
   ProfScope prof(s, mode == ExpertsOut::kSiluMul ? "experts_tc_silu" : "experts_tc");
   switch (mode) {
-    case ExpertsOut::kSiluMul: return launch_one<(int)ExpertsOut::kSiluMul>(map, a, grid, s);
-    case ExpertsOut::kF32: return launch_one<(int)ExpertsOut::kF32>(map, a, grid, s);
-    default: return launch_one<(int)ExpertsOut::kBf16>(map, a, grid, s);
+    case ExpertsOut::kSiluMul: return launch_one<(int)ExpertsOut::kSiluMul>(maps, a, grid, s);
+    case ExpertsOut::kF32: return launch_one<(int)ExpertsOut::kF32>(maps, a, grid, s);
+    default: return launch_one<(int)ExpertsOut::kBf16>(maps, a, grid, s);
   }
 }
 
