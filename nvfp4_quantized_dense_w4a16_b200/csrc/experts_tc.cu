@@ -7,7 +7,8 @@
 // rows of the same columns, or 128 consecutive rows of a plain weight).  Per
 // unit of two 64-element K chunks, in each CTA:
 //   * one warp streams its weights' chunks (9216 B) by bulk copies, and one its
-//     half of the rows' chunks (2 x 128 x 128 B, 128-byte swizzle) by TMA;
+//     half of the rows' chunks (2 x 128 x 128 B, 128-byte swizzle) by TMA, which
+//     counts on a barrier of CTA 0 for both;
 //   * two sets of four warps take the units in turn, decode the codes to bf16
 //     and write them to tensor memory, where they are the MMA's A operand;
 //   * one warp of CTA 0 issues tcgen05.mma cta_group::2 kind::f16 (M = 256, N =
@@ -136,6 +137,22 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// The address of CTA 0's barrier that stands where `bar` does.
+__device__ __forceinline__ uint32_t in_first(uint64_t* bar) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+  return a;
+}
+
+// A copy into this CTA's shared memory that counts on a barrier of either CTA.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
 // Whether `ok` holds for all 128 threads that meet at barrier `id`.
 __device__ __forceinline__ bool all_of_group(int id, bool ok) {
   uint32_t r;
@@ -208,7 +225,7 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_t
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kXStages; ++s) {
-      mbar_init(&xfull[s], 1);
+      mbar_init(&xfull[s], 1);  // (CTA 0's)
       mbar_init(&xempty[s], 1);
     }
     for (int s = 0; s < kWStages; ++s) {
@@ -216,7 +233,7 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_t
       mbar_init(&wempty[s], 4);
     }
     for (int s = 0; s < kASlots; ++s) {
-      mbar_init(&afull[s], (4 + 1) * kCtas);  // (CTA 0's) decoded weights, and rows
+      mbar_init(&afull[s], 4 * kCtas);  // (CTA 0's)
       mbar_init(&aempty[s], 1);
     }
     mbar_init(accfull, 1);
@@ -288,12 +305,14 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_t
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&xfull[s], nc * box * kBoxStep * 128);
+          if (rank == 0) mbar_arrive_expect_tx(&xfull[s], kCtas * nc * box * kBoxStep * 128);  // both CTAs' copies
           for (int j = 0; j < nc; ++j)
-            tma_load_2d(xs + s * kXStageBytes + j * kXChunkBytes, &maps.box[box - 1], (c + j) * kChunkK, row, &xfull[s]);
+            tma_load_pair(xs + s * kXStageBytes + j * kXChunkBytes, &maps.box[box - 1], (c + j) * kChunkK, row,
+                          in_first(&xfull[s]));
         }
       }
-      for (int r = max(0, u - kXStages); r < u; ++r) drain(&xfull[r % kXStages], (r / kXStages) & 1);
+      if (rank == 0)  // (CTA 1 leaves after this one)
+        for (int r = max(0, u - kXStages); r < u; ++r) drain(&xfull[r % kXStages], (r / kXStages) & 1);
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ MMA issuer
@@ -309,7 +328,8 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_t
       }
       for (int c = 0; c < kc; c += kUnit, ++u) {
         const int sx = u % kXStages, sa = u % kASlots;
-        ok = mbar_wait(&afull[sa], (u / kASlots) & 1, abort_flag, err, 2);
+        ok = mbar_wait(&xfull[sx], (u / kXStages) & 1, abort_flag, err, 2) &&
+             mbar_wait(&afull[sa], (u / kASlots) & 1, abort_flag, err, 2);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         const uint64_t b = smem_desc_sw128(smem_u32(xs + sx * kXStageBytes));
@@ -328,20 +348,6 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_t
         }
         __syncwarp();
       }
-    }
-  } else if (warp == 3) {
-    // ---------------------------------------- both CTAs' rows, for the issuer
-    // (not ahead of its barrier's phase: rows of the unit kASlots later are only
-    // fetched once this unit's MMAs are done)
-    static_assert(kXStages <= kASlots, "rows are counted in the phase of their unit");
-    if (lane == 0) {
-      int u = 0;
-      bool ok = true;
-      for (int T = first_tile; ok && T < total; T += tile_step)
-        for (int c = 0; ok && c < kc; c += kUnit, ++u) {
-          ok = mbar_wait(&xfull[u % kXStages], (u / kXStages) & 1, abort_flag, err, 4);
-          if (ok) arrive_first(&afull[u % kASlots]);
-        }
     }
   } else if (warp >= 4 && warp < 4 + 4 * kSets) {
     // --------------------------------------------------------------- decode
