@@ -23,7 +23,10 @@
 // the pair halves the rows' traffic: 41 KB per unit of 1024 MMA cycles and CTA.
 // One CTA by itself with 256 weight rows and N = 128 (50 KB per unit, the decode
 // used once per 128 rows) ran at 1640 cycles per unit: 32768 pairs of 2048 x 1024
-// took 478 us and take 433, 1024 pairs of 4096 x 12288 404 and 334.  What an
+// took 478 us and take 433, 1024 pairs of 4096 x 12288 404 and 324 (tensor pipe
+// 72% busy).  What is left is the way of a stage of rows: its MMAs' commit, the
+// copy, the wait for it, three stages in all.  Four sets of decode warps change
+// nothing (346 against 343 us).  What an
 // arrival on the other CTA's barrier announces (rows, tensor memory) has been
 // waited for before it, so it has no cluster scope, whose fences cost some 1000
 // cycles a unit (732 us).
@@ -201,8 +204,8 @@ __device__ __forceinline__ bool drain(uint64_t* bar, uint32_t parity) {
 }
 
 template <int MODE>
-__global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_tc_kernel(const __grid_constant__ RowMaps maps,
-                                                                const TcExpertsArgs a) {
+__global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1)
+    experts_tc_kernel(const __grid_constant__ RowMaps maps, const TcExpertsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -253,7 +256,7 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads, 1) experts_t
   // The kernel before this one (the sorting of the rows, or the gate and up
   // products) lets it start once it has itself waited for the ones before: the
   // plan is in L2.  So only the warp that reads that kernel's rows waits for it,
-  // the weights are streamed and decoded ahead (20 experts of 1056 x 672, 111
+  // the weights are streamed and decoded ahead (20 experts of 1056 x 672, 203
   // rows: 36.0 -> 33.4 us), and all that is written follows from those rows.
   const int total = __ldcg(a.plan.tiles) * a.wide_n;
 
