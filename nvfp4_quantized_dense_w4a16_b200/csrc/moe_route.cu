@@ -9,8 +9,11 @@
 // registers.  Without a bias (and with group scores that are maxima) the keys
 // are monotone in the logits, which are compared as they are: exact.  Else the
 // keys are computed in fp32, and the row is computed again in 64 bits where two
-// keys whose order matters are closer than their error: the choice is always
-// that of 64-bit arithmetic, and few rows in a thousand pay for it.
+// keys whose order matters are closer than their errors: the choice is always
+// that of 64-bit arithmetic, and few rows in a thousand pay for it.  A key's
+// error goes by its score, which its bias may cancel: a key that seems to stand
+// far behind may belong in front.  So distances are held against the largest
+// error of the row first, and where that is too much against each key's own.
 //
 // Bound by instructions: the logits and results of 16384 rows of 128 experts are
 // 0.8 us of memory traffic, and 8 choices of each take 10.3 us at 520 instructions
@@ -281,8 +284,10 @@ __device__ __forceinline__ void choose_words(const float (&key)[EPL], int lane, 
   }
 }
 
+// Ten CTAs an SM for up to 128 experts: 48 registers (16384 x 128: 10.2 us, 10.4
+// with the 52 to 56 that the compiler takes by itself).
 template <int EPL, bool BF16, bool WIDE>
-__global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 4 ? 10 : 0) moe_route_kernel(const RouteArgs a) {
   extern __shared__ double route_smem[];  // [warps][experts], only with groups that are not whole lanes
   griddep_wait();
   griddep_launch_dependents();
@@ -315,33 +320,35 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
     }
     sum = warp_sum(sum);
   }
-  if (scored) {
-    const float inv = summed ? 1.0f / sum : 0.0f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      float c = softmax ? key[i] * inv : sigmoid_f32(l[i]);
-      if (a.bias && l[i] > -INFINITY) c += a.bias[lane * EPL + i];
-      key[i] = l[i] > -INFINITY && c > -INFINITY ? c : -INFINITY;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = l[i];
-  }
   // An upper bound of a score's relative error: softmax has EPL + 5 additions
   // and about ten steps of the exponentials and the quotient, sigmoid three;
   // a key's adds a step of its size.  Below the normal range errors are steps of
   // 2^-149: keys that are all this small are always close.
   constexpr float kStep = 1.1920929e-7f, kTiny = 1e-37f;
   const float err = (softmax ? EPL + 16 : 4) * kStep;
+  auto key_error = [&](float score, float c) { return err * score + 2.0f * kStep * (fabsf(c) + score) + kTiny; };
+  float most = 0.0f;  // the largest score or key of the row, those of groups that get closed as well
+  if (scored) {
+    const float inv = summed ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float score = softmax ? key[i] * inv : sigmoid_f32(l[i]);
+      float c = score;
+      if (a.bias && l[i] > -INFINITY) c += a.bias[lane * EPL + i];
+      key[i] = l[i] > -INFINITY && c > -INFINITY ? c : -INFINITY;
+      if (key[i] > -INFINITY) most = fmaxf(most, fmaxf(score, fabsf(c)));
+    }
+    most = redux_max(most);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = l[i];
+  }
   bool close = false;
   if (a.groups > 1) {
-    float most = 0.0f;  // of the groups left out as well: two large keys may cancel in their sum
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) most = fmaxf(most, key[i] > -INFINITY ? fabsf(key[i]) : 0.0f);
     const float gap =
         keep_best_groups<EPL, float>(a, key, lane, reinterpret_cast<float*>(route_smem + (size_t)warp * a.experts));
-    // (up to four scores, each at most one)
-    close = scored && gap <= 4.0f * err + 8.0f * kStep * redux_max(most) + kTiny;
+    // (up to four scores, each at most one; two large keys may cancel in their sum)
+    close = scored && gap <= 4.0f * err + 8.0f * kStep * most + kTiny;
   }
 
   int my_id = -1;
@@ -399,30 +406,53 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
     };
     int found = choose(0, min(32, a.top_k + scored));
     if (scored) {
-      // Is a choice nearer to the next one than their errors?  (Equal logits with
-      // equal biases have equal keys.)  With all 32 lanes taken by choices there is
-      // no room for the runner-up: such rows are always computed in 64 bits.
-      const float my_b = a.bias && my_id >= 0 ? a.bias[my_id] : 0.0f;
-      auto tolerance = [&](float c, float cb, float o, float ob) {
-        const float scores = fabsf(c - cb) + fabsf(o - ob), keys = fabsf(c) + fabsf(o);
-        return err * scores + 2.0f * kStep * (keys + scores) + kTiny;
-      };
-      const float c = __shfl_down_sync(0xffffffffu, my_c, 1), cl = __shfl_down_sync(0xffffffffu, my_l, 1),
-                  cb = __shfl_down_sync(0xffffffffu, my_b, 1);
-      const bool near = lane + 1 < found && my_c - c <= tolerance(my_c, my_b, c, cb) && !(cl == my_l && cb == my_b);
-      bool whole = __any_sync(0xffffffffu, close) || a.top_k == 32 || bad;
+      // Is a choice nearer to the next one than the largest errors of the row?  With all
+      // 32 lanes taken by choices there is no room for the runner-up: such rows
+      // are always computed in 64 bits.
+      const float next = __shfl_down_sync(0xffffffffu, my_c, 1);
+      const bool near = lane + 1 < found && !(my_c - next > 2.0f * key_error(most, most));
+      bool whole = __any_sync(0xffffffffu, close) || a.top_k == 32 || bad || !(most < INFINITY);
       if (!whole && __any_sync(0xffffffffu, near)) {
-        // Three more candidates; where the last of them is clearly behind the
-        // choices, the candidates' keys in 64 bits settle the order.
-        const int most = min(32, a.top_k + 4);
-        const bool all = found < min(32, a.top_k + 1);  // nothing was left already
-        if (!all) found = choose(found, most);
-        const float ob = a.bias && my_id >= 0 ? a.bias[my_id] : 0.0f;
-        const int e0 = min(a.top_k, found) - 1, e1 = found - 1;
-        const float c0 = __shfl_sync(0xffffffffu, my_c, e0), b0 = __shfl_sync(0xffffffffu, ob, e0);
-        const float c1 = __shfl_sync(0xffffffffu, my_c, e1), b1 = __shfl_sync(0xffffffffu, ob, e1);
-        whole = !(all || found < most) && !(c0 - c1 > tolerance(c0, b0, c1, b1));
-        if (!whole) {
+        // Each key's own error, |c - b| in place of its score.
+        auto bias_of = [&](int id) { return a.bias ? a.bias[id] : 0.0f; };
+        auto top_of = [&](float c, float b) { return c + key_error(fabsf(c - b), c); };
+        // How high a key that was not chosen may be, but for those of logit tl and
+        // bias tb: they equal a choice, and stand behind it by their ids.
+        auto left_over = [&](float tl, float tb) {
+          float high = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < EPL; ++i)
+            if (key[i] > -INFINITY) {
+              const float b = bias_of(lane * EPL + at[i]);
+              if (l[i] != tl || b != tb) high = fmaxf(high, top_of(key[i], b));
+            }
+          return redux_max(high);
+        };
+        int cut = min(a.top_k, found) - 1;  // the last choice
+        float my_b = my_id >= 0 ? bias_of(my_id) : 0.0f;
+        const float high = lane < found ? top_of(my_c, my_b) : -INFINITY;
+        const float low = my_c - key_error(fabsf(my_c - my_b), my_c);
+        // Of neighbours of equal logits and biases the last one stands for all, and
+        // if the runner-up equals the last choice, it does.
+        const float nl = __shfl_down_sync(0xffffffffu, my_l, 1), nb = __shfl_down_sync(0xffffffffu, my_b, 1);
+        const bool same = lane + 1 < found && nl == my_l && nb == my_b;
+        float behind = __shfl_down_sync(0xffffffffu, high, 1);
+        bool unsure = lane + 1 < found && !same && !(low > behind);
+        if (!__any_sync(0xffffffffu, unsure)) {  // no two neighbours are near by their own errors: is any other key?
+          const bool cut_same = __shfl_sync(0xffffffffu, same, cut);
+          const float rest = left_over(__shfl_sync(0xffffffffu, my_l, cut), __shfl_sync(0xffffffffu, my_b, cut));
+          behind = high;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) behind = fmaxf(behind, __shfl_down_sync(0xffffffffu, behind, o));
+          behind = fmaxf(__shfl_down_sync(0xffffffffu, behind, 1), rest);
+          unsure = lane <= cut + cut_same && !same && !(low > (lane + 1 < found ? behind : rest));
+        }
+        if (__any_sync(0xffffffffu, unsure)) {
+          // Three more candidates, whose order keys in 64 bits settle; where another
+          // one may stand before the last choice among them, the row is computed.
+          found = choose(found, min(32, a.top_k + 4));
+          my_b = my_id >= 0 ? bias_of(my_id) : 0.0f;
+          const float end = __shfl_sync(0xffffffffu, my_c, found - 1);
           double k64 = -INFINITY;
           if (softmax) {
             float r[EPL];
@@ -436,7 +466,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
           } else {
             k64 = 1.0 / (1.0 + exp(-(double)my_l));
           }
-          k64 += (double)ob;
+          k64 += (double)my_b;
           int rank = 0;
           for (int i = 0; i < found; ++i) {
             const double o = __shfl_sync(0xffffffffu, k64, i);
@@ -450,6 +480,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
           }
           my_id = __shfl_sync(0xffffffffu, my_id, src);
           my_l = __shfl_sync(0xffffffffu, my_l, src);
+          my_b = __shfl_sync(0xffffffffu, my_b, src);
+          k64 = __shfl_sync(0xffffffffu, k64, src);
+          cut = min(a.top_k, found) - 1;
+          const double last = __shfl_sync(0xffffffffu, k64, cut);
+          // (nothing is left above the last candidate; the same in all lanes)
+          whole = !((double)(end + key_error(most, most)) < last) &&
+                  !((double)left_over(__shfl_sync(0xffffffffu, my_l, cut), __shfl_sync(0xffffffffu, my_b, cut)) < last);
         }
       }
       if (whole) {

@@ -155,6 +155,57 @@ def test_route_scores_below_the_normal_range(native):
         assert np.all(np.abs(w.double().cpu().numpy() - rw) <= 15 * 2.0 ** -24 * rw + 8 * 2.0 ** -149)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,big,top_k", [(8, 1, 1), (40, 2, 4), (64, 1, 8), (128, 3, 31), (200, 2, 8), (700, 3, 6)])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_route_large_errors_behind_the_choice(native, scoring, experts, big, top_k, groups):
+    """A score near one that its bias cancels has an error far beyond that of the tiny keys it stands among: however far
+    behind them it seems to stand, it may belong in front."""
+    rng = np.random.default_rng(21 + experts)
+    rows = 60
+    logits = rng.uniform(-10.0, -9.9, (rows, experts)).astype(np.float32)
+    where = rng.permutation(experts)[:big]
+    logits[:, where] = rng.uniform(1.0, 3.0, big)
+    logits[rows // 2:, :] = logits[0]  # half of them but for the cancelled experts the same
+    logits[rows // 2:, where] += rng.uniform(-1e-7, 1e-7, (rows - rows // 2, big))
+    score = np.exp(M.log_score(logits[0].astype(np.float64), scoring))
+    bias = (1e-4 + 6e-8 * rng.uniform(-1.0, 1.0, experts) - score).astype(np.float32)
+    kw = dict(top_k=top_k, scoring=scoring, groups=groups, top_groups=max(1, groups - 1), group_score="max")
+    check_route(native, logits, bias, **kw)
+    # equal tiny keys, so that the choice ends among equal ones
+    bias[:] = 1e-4
+    logits[:] = -10.0
+    logits[:, where] = rng.uniform(1.0, 3.0, big)
+    score = np.exp(M.log_score(logits[0].astype(np.float64), scoring))
+    rest = np.setdiff1d(np.arange(experts), where)
+    bias[where] = bias[rest[0]] + score[rest[0]] - score[where] + 3e-8 * rng.uniform(-1.0, 1.0, big)
+    check_route(native, logits, bias, **kw)
+
+
+def test_route_large_errors_by_hand(native):
+    """Rows whose last key in fp32 is the first one in fact."""
+    for logits, bias, best in (
+            ([2.15468, -9.210265, -9.210468], [-0.8960053, 0.0, 0.0], 0),
+            ([-30.0, -30.0, 6.491729259490967], [0.009999999776482582, 0.009999992325901985, -0.9884862899780273], 2)):
+        ids, _ = check_route(native, [logits], bias, top_k=1, scoring="sigmoid")
+        assert ids.tolist() == [[best]]
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_peaked_and_equal_rows(native, scoring):
+    """One score near one beside many small and close ones, rows of one logit, few distinct logits."""
+    rng = np.random.default_rng(22)
+    logits = rng.uniform(-9.0, -8.9, (64, 160)).astype(np.float32)
+    logits[:, 77] = 8.0
+    logits[::2, 20:] = logits[::2, :1]
+    logits[5] = 0.25
+    bias = (1e-4 * rng.standard_normal(160)).astype(np.float32)
+    for b in (bias, np.zeros(160, np.float32), np.full(160, 1e6, np.float32)):
+        check_route(native, logits, b, top_k=8, scoring=scoring)
+        check_route(native, logits, b, dtype=torch.bfloat16, top_k=13, scoring=scoring)
+        check_route(native, logits, b, top_k=8, scoring=scoring, groups=8, top_groups=3, group_score="top2")
+
+
 def test_route_infinite_keys(native):
     """+inf biases tie by id; +inf logits under sigmoid score one; biases and logits of -inf close an expert."""
     rng = np.random.default_rng(13)
