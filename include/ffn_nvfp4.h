@@ -362,7 +362,8 @@ ffn_status ffn_nvfp4_experts_info(const ffn_nvfp4_experts* w, int64_t* experts, 
  * result does not depend on which other rows share its expert as long as the
  * same kernels run (they are chosen by m, top_k and the shapes).  m == 0 is a
  * no-op.  The workspace holds the rows' places by expert and, for many rows,
- * their copies in that order; it may be shared by calls on one stream.
+ * their copies in that order; it may be shared by calls on one stream, and the
+ * size for m rows serves every smaller m (of the same other arguments) too.
  * Errors: FFN_ERR_UNSUPPORTED for a gate and up stack; FFN_ERR_SHAPE when 2 * m * top_k exceeds 2^31 - 1 or m * top_k rows of n or k
  * columns are more than 2^40 elements (the sizes: FFN_ERR_UNSUPPORTED for
  * experts > FFN_MOE_MAX_EXPERTS). */
@@ -385,7 +386,8 @@ ffn_status ffn_nvfp4_experts_linear(const void* x, int64_t m, const ffn_nvfp4_ex
  * An id outside [0, experts) contributes weights[i, j] * 0, so padding rows
  * (all ids -1, weights 0) give zeros.  Deterministic: the same call gives the
  * same bits.  m == 0 is a no-op.  Allocates nothing and does not synchronise;
- * the workspace may be shared by calls on one stream.  Errors as for
+ * the workspace may be shared by calls on one stream and serves smaller m, as
+ * above.  Errors as for
  * ffn_nvfp4_experts_linear; FFN_ERR_SHAPE where the two stacks do not match. */
 ffn_status ffn_nvfp4_moe_workspace_size(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter,
                                         size_t* bytes);

@@ -1,6 +1,7 @@
 // Mixture-of-experts part of the C ABI: the handle of stacked NVFP4 experts,
 // argument checks, workspace carving and dispatch of ffn_nvfp4_experts_linear
 // and ffn_nvfp4_moe_forward.
+#include <algorithm>
 #include <new>
 
 #include "ffn_nvfp4.h"
@@ -64,7 +65,8 @@ struct Carve {
 // 2048 x 1024 at 6, 8, 12 rows an expert 90, 96, 112 and 90, 94, 101; 8 of
 // 4096 x 6144 at 8, 12, 16 rows 121, 140, 170 and 134, 139, 145; 20 of
 // 1056 x 672 at 7, 10, 14 rows 32.2, 32.6, 35.5 and 31.2, 31.7, 32.6.
-bool use_tc(int64_t pairs, int64_t experts) { return pairs > ffn::kFewPairs && pairs > 8 * experts; }
+int64_t last_rows_pairs(int64_t experts) { return std::max((int64_t)ffn::kFewPairs, 8 * experts); }
+bool use_tc(int64_t pairs, int64_t experts) { return pairs > last_rows_pairs(experts); }
 
 size_t take(size_t& off, size_t bytes) {
   const size_t at = off;
@@ -73,7 +75,7 @@ size_t take(size_t& off, size_t bytes) {
 }
 
 // inter = 0: one projection of `hidden` columns and k, whose output is the caller's.
-Carve carve(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter, int64_t k) {
+Carve carve(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter, int64_t k, int sms) {
   Carve c;
   const int64_t pairs = m * top_k;
   if (pairs == 0) return c;
@@ -90,7 +92,7 @@ Carve carve(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter
     down.wtiles = ffn::experts_tiles(hidden);
     down.kc = (int)((inter + 63) / 64);
     // every pair has an expert of its own with few pairs of one row; a batch spreads over all experts
-    c.splits = ffn::rows_splits(down, pairs < experts ? pairs : experts);
+    c.splits = ffn::rows_splits(down, pairs < experts ? pairs : experts, sms);
   }
   // the sorted rows are read before the down products are written: one buffer
   const size_t xs = c.tc ? (size_t)padded * k * 2 : 0, y = inter > 0 ? (size_t)c.splits * pairs * hidden * 4 : 0;
@@ -98,6 +100,22 @@ Carve carve(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter
   if (inter > 0) c.h = take(off, (size_t)padded * inter * 2);
   c.total = off;
   return c;
+}
+
+// A workspace's size serves every smaller batch as well, though a smaller one may
+// need more: its K is cut into more ranges, its tiles have fewer rows, or other
+// kernels compute it.  Between such changes the need grows with m: the last
+// batches before the changes, and those of fewer pairs than experts, by which K
+// is cut, hold the most.
+size_t workspace_bytes(int64_t m, int top_k, int64_t experts, int64_t hidden, int64_t inter, int64_t k) {
+  const int sms = ffn::device_sms();
+  auto need = [&](int64_t rows) { return carve(rows, top_k, experts, hidden, inter, k, sms).total; };
+  size_t most = need(m);
+  for (const int64_t pairs : {ffn::last_narrow_pairs(experts), last_rows_pairs(experts)})
+    if (pairs / top_k < m) most = std::max(most, need(pairs / top_k));
+  if (inter > 0 && m * top_k < ffn::kMaxSplits * experts)  // (from there one sum a pair is more)
+    for (int64_t rows = std::min(m, experts / top_k); rows > 0; --rows) most = std::max(most, need(rows));
+  return most;
 }
 
 ffn::MoePlan plan_at(uint8_t* ws, const Carve& c) {
@@ -188,7 +206,7 @@ ffn_status ffn_nvfp4_experts_workspace_size(int64_t m, int top_k, int64_t expert
   if (!bytes || m < 0 || top_k < 1 || experts < 1 || n < 1) return FFN_ERR_INVALID_ARG;
   if (experts > FFN_MOE_MAX_EXPERTS) return FFN_ERR_UNSUPPORTED;
   if (!valid_k(k) || !valid_pairs(m, top_k) || !valid_size(m * top_k, n) || !valid_size(m * top_k, k)) return FFN_ERR_SHAPE;
-  *bytes = carve(m, top_k, experts, n, 0, k).total;
+  *bytes = workspace_bytes(m, top_k, experts, n, 0, k);
   return FFN_OK;
 }
 
@@ -200,7 +218,7 @@ ffn_status ffn_nvfp4_experts_linear(const void* x, int64_t m, const ffn_nvfp4_ex
   if (m == 0) return FFN_OK;
   if (!x || !ids || !y) return FFN_ERR_INVALID_ARG;
   if (ffn_status st = check_device(w)) return st;
-  const Carve c = carve(m, top_k, w->experts, w->n, 0, w->k);
+  const Carve c = carve(m, top_k, w->experts, w->n, 0, w->k, ffn::device_sms());
   if (!workspace || workspace_bytes < c.total) return FFN_ERR_WORKSPACE;
   if (!aligned16(x) || !aligned16(y) || !aligned16(workspace) || !aligned4(ids)) return FFN_ERR_ALIGNMENT;
   if (ffn_status st = ffn::moe_precheck()) return st;
@@ -228,7 +246,7 @@ ffn_status ffn_nvfp4_moe_workspace_size(int64_t m, int top_k, int64_t experts, i
   if (!valid_k(hidden) || !valid_k(inter) || !valid_pairs(m, top_k) || !valid_size(m * top_k, hidden) ||
       !valid_size(m * top_k, inter))
     return FFN_ERR_SHAPE;
-  *bytes = carve(m, top_k, experts, hidden, inter, hidden).total;
+  *bytes = workspace_bytes(m, top_k, experts, hidden, inter, hidden);
   return FFN_OK;
 }
 
@@ -247,7 +265,7 @@ ffn_status ffn_nvfp4_moe_forward(const void* x, int64_t m, int64_t hidden, int64
   if (!x || !ids || !weights || !out) return FFN_ERR_INVALID_ARG;
   if (ffn_status st = check_device(gate_up)) return st;
   if (ffn_status st = check_device(down)) return st;
-  const Carve c = carve(m, top_k, down->experts, hidden, inter, hidden);
+  const Carve c = carve(m, top_k, down->experts, hidden, inter, hidden, ffn::device_sms());
   if (!workspace || workspace_bytes < c.total) return FFN_ERR_WORKSPACE;
   if (!aligned16(x) || !aligned16(out) || !aligned16(workspace) || !aligned4(ids) || !aligned4(weights))
     return FFN_ERR_ALIGNMENT;

@@ -689,10 +689,10 @@ cudaError_t launch_rows_from(const RowsArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int rows_splits(const ExpertsView& w, int64_t tiles) {
+int rows_splits(const ExpertsView& w, int64_t tiles, int sms) {
   // rounds of items over the SMs times the steps of an item, and about four
   // steps' time for an item's sums
-  const int64_t sms = device_sms(), steps = (w.kc + kStepChunks - 1) / kStepChunks, items = tiles * rows_units(w);
+  const int64_t steps = (w.kc + kStepChunks - 1) / kStepChunks, items = tiles * rows_units(w);
   int64_t best = 0, least = INT64_MAX;
   for (int64_t s = 1; s <= kMaxSplits && s <= steps; ++s) {
     const int64_t cost = ((items * s + sms - 1) / sms) * ((steps + s - 1) / s + 4);

@@ -70,12 +70,13 @@ enum class ExpertsOut : int {
 constexpr int kFewPairs = 32;
 // Rows of a plan's tiles for launch_experts_rows: 8, where a tile of 16 would be
 // half empty on average.
-inline int rows_tile(int64_t pairs, int64_t experts) { return pairs <= 5 * experts ? 8 : 16; }
+inline int64_t last_narrow_pairs(int64_t experts) { return 5 * experts; }
+inline int rows_tile(int64_t pairs, int64_t experts) { return pairs <= last_narrow_pairs(experts) ? 8 : 16; }
 
 // How many ranges of K the down products are cut into for `tiles` tiles of
 // rows, so that the items fill the SMs evenly; each range leaves its own sums.
 constexpr int kMaxSplits = 8;
-int rows_splits(const ExpertsView& w, int64_t tiles);
+int rows_splits(const ExpertsView& w, int64_t tiles, int sms);
 
 // The weighted sum over a row's experts, made by the down products themselves
 // (kF32, at most kFewPairs pairs): out = bf16(sum_j weights[j] * y[j]).

@@ -627,6 +627,29 @@ def test_graphs_that_share_a_workspace(native):
                 assert torch.equal(a[2], a[3]) and torch.equal(b[2], b[3])
 
 
+@pytest.mark.parametrize("most,experts,top_k,hidden,inter", [(33, 8, 2, 256, 4096), (20, 4, 2, 256, 2048), (70, 7, 1, 128, 2080)])
+def test_one_workspace_for_every_smaller_batch(native, most, experts, top_k, hidden, inter):
+    """A buffer of the largest batch's size, as a server keeps it, at every batch up to that one."""
+    layer = Layer(native, experts, hidden, inter, 1001)
+    x, _ = rows(most, hidden, 1002)
+    rng = np.random.default_rng(1003)
+    ids = torch.from_numpy(pick(rng, most, experts, top_k)).cuda()
+    w = torch.from_numpy(rng.uniform(0, 1, (most, top_k)).astype(np.float32)).cuda()
+    size = native.ffn_nvfp4_moe_workspace_size(most, top_k, experts, hidden, inter)
+    ws = torch.full((size + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    y = torch.empty((most, top_k, hidden), dtype=torch.bfloat16, device="cuda")
+    linear = native.ffn_nvfp4_experts_workspace_size(most, top_k, experts, hidden, hidden)
+    plain = Stack(native, experts, hidden, hidden, 1004)
+    for m in range(1, most + 1):
+        args = (x[:m], layer.gu.handle, layer.dn.handle, ids[:m], w[:m])
+        out = native.ffn_nvfp4_moe_forward(*args, workspace=ws[:size])
+        assert torch.equal(out, native.ffn_nvfp4_moe_forward(*args))
+        native.ffn_nvfp4_experts_linear(x[:m], plain.handle, ids[:m], y=y[:m], workspace=ws[:linear])
+        assert torch.equal(y[:m], native.ffn_nvfp4_experts_linear(x[:m], plain.handle, ids[:m]))
+    torch.cuda.synchronize()
+    assert bool((ws[size:] == 0xA5).all())
+
+
 @pytest.mark.parametrize("m", [1, 20, 150])
 def test_layer_padding_rows_and_canaries(native, m):
     """Rows without an expert are zeros; nothing behind row m is written; the workspace's size is enough."""

@@ -97,3 +97,18 @@ def test_sizes_that_overflow_are_refused(native):
     for experts in (1025, 1 << 62):
         assert L.ffn_nvfp4_moe_workspace_size(1, 1, experts, 64, 64, ctypes.byref(out)) == UNSUPPORTED
         assert L.ffn_nvfp4_experts_workspace_size(1, 1, experts, 64, 64, ctypes.byref(out)) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("experts,top_k,hidden,inter", [
+    (8, 2, 4096, 12288), (64, 8, 2048, 1024), (20, 3, 1056, 672), (1, 1, 32, 32), (3, 1, 256, 4096), (1024, 1, 64, 4096),
+    (256, 8, 7168, 2048), (40, 33, 96, 1600), (2, 5, 128, 64),
+])
+def test_a_workspace_serves_every_smaller_batch(native, experts, top_k, hidden, inter):
+    """A size never falls as m grows, where other kernels take over (32 pairs, 5 and 8 pairs an expert) or K is cut
+    into fewer ranges as well."""
+    last = 9 * max(32, 8 * experts) // top_k // 8 + 8
+    layer = [native.ffn_nvfp4_moe_workspace_size(m, top_k, experts, hidden, inter) for m in range(last)]
+    linear = [native.ffn_nvfp4_experts_workspace_size(m, top_k, experts, hidden, inter) for m in range(last)]
+    for sizes in (layer, linear):
+        falls = [(m, a, b) for m, (a, b) in enumerate(zip(sizes, sizes[1:])) if b < a]
+        assert not falls, falls[:4]
