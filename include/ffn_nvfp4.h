@@ -312,10 +312,14 @@ typedef struct ffn_moe_router {
  * With s = softmax(logits) or sigmoid(logits) of a row, the choice goes by the
  * keys s + bias: with groups > 1 the top_groups groups of the highest score
  * stay open; ids are the top_k open experts of the highest keys, in descending
- * order, equal keys by the lower id (groups likewise).  weights = scale * s of
- * the chosen experts, or scale * s / (sum of s over the chosen ones).
- * The choice is the one that 64-bit arithmetic makes; weights are accurate to
- * a few fp32 steps.
+ * order.  weights = scale * s of the chosen experts, or scale * s / (sum of s
+ * over the chosen ones).
+ * The choice is the one that 64-bit arithmetic makes.  Keys that it does not
+ * tell apart (scores that saturate or underflow) go by the larger logit, then
+ * by the lower id, infinite ones by the id alone: without a bias, as with one
+ * that is the same for all experts, the logits' order decides.  Groups of equal
+ * score go by their best experts in this order (FFN_MOE_GROUP_MAX) or by the
+ * lower group (FFN_MOE_GROUP_TOP2).  Weights are accurate to a few fp32 steps.
  * An expert whose logit is -inf or NaN, or whose key is, is never chosen; where
  * fewer than top_k are left, the remaining ids are -1 with weight 0 (a row
  * without any open expert: all of them).  A group's score counts only such

@@ -6,8 +6,10 @@
 // the weights by s alone, renormalised over the chosen experts on request.
 //
 // One warp owns one row; lane l holds experts l * EPL .. l * EPL + EPL - 1 in
-// registers.  Without a bias (and with group scores that are maxima) the keys
-// are monotone in the logits, which are compared as they are: exact.  Else the
+// registers.  Finite keys that 64 bits do not tell apart (scores that saturate or
+// underflow) go by their logits, so that of experts of equal biases the logits
+// alone decide.  Without a bias (and with group scores that are maxima) they are
+// compared as they are: exact, and the order that a bias of zeros gives.  Else the
 // keys are computed in fp32, and the row is computed again in 64 bits where two
 // keys whose order matters are closer than their errors: the choice is always
 // that of 64-bit arithmetic, and few rows in a thousand pay for it.  A key's
@@ -84,9 +86,12 @@ __device__ __forceinline__ float sigmoid_f32(float l) {
 
 // The experts of the row that may be chosen after the groups: keys of the
 // others become -inf.  Key is float or double.  Returns how near the worst
-// group kept and the best one left out are (infinity: no matter).
+// group kept and the best one left out are (infinity: no matter).  Equal finite
+// maxima go by the logits l of the experts that they belong to (double: fp32 is
+// never left to decide between near scores).
 template <int EPL, typename Key>
-__device__ __forceinline__ Key keep_best_groups(const RouteArgs& a, Key (&key)[EPL], int lane, Key* smem) {
+__device__ __forceinline__ Key keep_best_groups(const RouteArgs& a, Key (&key)[EPL], const float (&l)[EPL], int lane,
+                                                Key* smem) {
   const int size = a.experts / a.groups;
   const bool top2 = a.group_score == FFN_MOE_GROUP_TOP2;
   Key best = -INFINITY, second = -INFINITY;  // of group `lane` (or of the lane's group)
@@ -113,13 +118,37 @@ __device__ __forceinline__ Key keep_best_groups(const RouteArgs& a, Key (&key)[E
       for (int i = 0; i < size; ++i) take(smem[lane * size + i]);
     __syncwarp();
   }
+  constexpr bool kTies = sizeof(Key) == 8;
+  float tie = 0.0f;
+  if (kTies && !top2) {
+    tie = -INFINITY;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (key[i] == best) tie = fmaxf(tie, l[i]);
+      for (int o = 1; o < span; o <<= 1) tie = fmaxf(tie, __shfl_xor_sync(0xffffffffu, tie, o));
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane * EPL + i;
+        const Key its = __shfl_sync(0xffffffffu, best, min(e / size, 31));
+        if (e < a.experts) smem[e] = key[i] == its ? (Key)l[i] : (Key)-INFINITY;
+      }
+      __syncwarp();
+      if (lane < a.groups)
+        for (int i = 0; i < size; ++i) tie = fmaxf(tie, (float)smem[lane * size + i]);
+      __syncwarp();
+    }
+    if (!(best < INFINITY)) tie = 0.0f;
+  }
   if (top2 && second > -INFINITY) best += second;
   // rank among the groups: ties to the lower one
   const int step = whole ? span : 1, mine = whole ? lane / span : lane;
   int rank = 0;
   for (int g = 0; g < a.groups; ++g) {
     const Key o = __shfl_sync(0xffffffffu, best, g * step);
-    rank += o > best || (o == best && g < mine);
+    const float ot = kTies ? __shfl_sync(0xffffffffu, tie, g * step) : 0.0f;
+    rank += o > best || (o == best && (ot > tie || (ot == tie && g < mine)));
   }
   const bool in = mine < a.groups, kept = in && rank < a.top_groups;
   Key low = kept ? best : (Key)INFINITY, high = in && !kept ? best : (Key)-INFINITY;
@@ -156,6 +185,7 @@ template <int EPL>
 __device__ __noinline__ int choose_64(const RouteArgs& a, const float (&l)[EPL], int lane, double* smem) {
   const bool softmax = a.scoring == FFN_MOE_SOFTMAX;
   double key[EPL];
+  float tie[EPL];
   double top = -INFINITY, sum = 0.0;
   if (softmax) {
 #pragma unroll
@@ -175,26 +205,30 @@ __device__ __noinline__ int choose_64(const RouteArgs& a, const float (&l)[EPL],
       if (a.bias) c += (double)a.bias[lane * EPL + i];
       if (c > -INFINITY) key[i] = c;
     }
+    tie[i] = key[i] < INFINITY ? l[i] : 0.0f;  // what equal keys go by, before the id
   }
-  if (a.groups > 1) keep_best_groups<EPL, double>(a, key, lane, smem);
+  if (a.groups > 1) keep_best_groups<EPL, double>(a, key, l, lane, smem);
   int mine = -1;
   for (int j = 0; j < a.top_k; ++j) {
     double best = -INFINITY;
+    float best_tie = -INFINITY;
     int at = 0x7fffffff;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = lane * EPL + i;
-      }
+    for (int i = 0; i < EPL; ++i) {
+      const bool take = (key[i] > best) | ((key[i] == best) & (key[i] > -INFINITY) & (tie[i] > best_tie));
+      best = take ? key[i] : best;
+      best_tie = take ? tie[i] : best_tie;
+      at = take ? lane * EPL + i : at;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const double ob = __shfl_xor_sync(0xffffffffu, best, o);
+      const float ot = __shfl_xor_sync(0xffffffffu, best_tie, o);
       const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-      if (ob > best || (ob == best && oa < at)) {
-        best = ob;
-        at = oa;
-      }
+      const bool take = (ob > best) | ((ob == best) & ((ot > best_tie) | ((ot == best_tie) & (oa < at))));
+      best = take ? ob : best;
+      best_tie = take ? ot : best_tie;
+      at = take ? oa : at;
     }
     if (best == -INFINITY) break;  // nothing is left
     if (lane == j) mine = at;
@@ -346,12 +380,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 4 ? 10 : 0) moe_route
   bool close = false;
   if (a.groups > 1) {
     const float gap =
-        keep_best_groups<EPL, float>(a, key, lane, reinterpret_cast<float*>(route_smem + (size_t)warp * a.experts));
+        keep_best_groups<EPL, float>(a, key, l, lane, reinterpret_cast<float*>(route_smem + (size_t)warp * a.experts));
     // (up to four scores, each at most one; two large keys may cancel in their sum)
     close = scored && gap <= 4.0f * err + 8.0f * kStep * most + kTiny;
   }
 
-  int my_id = -1;
+  int my_id = -1, slot = lane;  // a choice, and which one it is
   float my_l = -INFINITY;
   if (BF16 && !scored) {
     choose_words<EPL>(key, lane, a.top_k, my_id, my_l);
@@ -412,19 +446,20 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 4 ? 10 : 0) moe_route
       const float next = __shfl_down_sync(0xffffffffu, my_c, 1);
       const bool near = lane + 1 < found && !(my_c - next > 2.0f * key_error(most, most));
       bool whole = __any_sync(0xffffffffu, close) || a.top_k == 32 || bad || !(most < INFINITY);
-      if (!whole && __any_sync(0xffffffffu, near)) {
+      const uint32_t nears = __ballot_sync(0xffffffffu, near);
+      if (!whole && nears) {
         // Each key's own error, |c - b| in place of its score.
         auto bias_of = [&](int id) { return a.bias ? a.bias[id] : 0.0f; };
         auto top_of = [&](float c, float b) { return c + key_error(fabsf(c - b), c); };
-        // How high a key that was not chosen may be, but for those of logit tl and
-        // bias tb: they equal a choice, and stand behind it by their ids.
+        // How high a key that was not chosen may be, but for those of bias tb and a
+        // logit of at most tl: of equal biases the logits decide, then the ids.
         auto left_over = [&](float tl, float tb) {
           float high = -INFINITY;
 #pragma unroll
           for (int i = 0; i < EPL; ++i)
             if (key[i] > -INFINITY) {
               const float b = bias_of(lane * EPL + at[i]);
-              if (l[i] != tl || b != tb) high = fmaxf(high, top_of(key[i], b));
+              if (l[i] > tl || b != tb) high = fmaxf(high, top_of(key[i], b));
             }
           return redux_max(high);
         };
@@ -432,10 +467,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 4 ? 10 : 0) moe_route
         float my_b = my_id >= 0 ? bias_of(my_id) : 0.0f;
         const float high = lane < found ? top_of(my_c, my_b) : -INFINITY;
         const float low = my_c - key_error(fabsf(my_c - my_b), my_c);
-        // Of neighbours of equal logits and biases the last one stands for all, and
-        // if the runner-up equals the last choice, it does.
+        // Of neighbours of equal biases and falling logits the last one stands for
+        // all, and if the runner-up is such a neighbour of the last choice, it does.
         const float nl = __shfl_down_sync(0xffffffffu, my_l, 1), nb = __shfl_down_sync(0xffffffffu, my_b, 1);
-        const bool same = lane + 1 < found && nl == my_l && nb == my_b;
+        const bool same = lane + 1 < found && nl <= my_l && nb == my_b;
         float behind = __shfl_down_sync(0xffffffffu, high, 1);
         bool unsure = lane + 1 < found && !same && !(low > behind);
         if (!__any_sync(0xffffffffu, unsure)) {  // no two neighbours are near by their own errors: is any other key?
@@ -448,9 +483,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 4 ? 10 : 0) moe_route
           unsure = lane <= cut + cut_same && !same && !(low > (lane + 1 < found ? behind : rest));
         }
         if (__any_sync(0xffffffffu, unsure)) {
-          // Three more candidates, whose order keys in 64 bits settle; where another
-          // one may stand before the last choice among them, the row is computed.
-          found = choose(found, min(32, a.top_k + 4));
+          // Keys in 64 bits settle the order of the choices, and of three more
+          // candidates where the runner-up is near the last choice; where another one
+          // may stand before the last choice among them, the row is computed.
+          if ((nears >> cut) & 1) found = choose(found, min(32, a.top_k + 4));
           my_b = my_id >= 0 ? bias_of(my_id) : 0.0f;
           const float end = __shfl_sync(0xffffffffu, my_c, found - 1);
           double k64 = -INFINITY;
@@ -467,22 +503,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 4 ? 10 : 0) moe_route
             k64 = 1.0 / (1.0 + exp(-(double)my_l));
           }
           k64 += (double)my_b;
-          int rank = 0;
+          int rank = 0;  // (candidates of equal scores and keys stand in the order of their ids)
           for (int i = 0; i < found; ++i) {
             const double o = __shfl_sync(0xffffffffu, k64, i);
-            const int id = __shfl_sync(0xffffffffu, my_id, i);
-            rank += o > k64 || (o == k64 && id < my_id);
+            const float ol = __shfl_sync(0xffffffffu, my_l, i);
+            rank += (o > k64) | ((o == k64) & ((ol > my_l) | ((ol == my_l) & (i < lane))));
           }
-          int src = lane;
-          for (int i = 0; i < found; ++i) {
-            const int at_rank = __ffs(__ballot_sync(0xffffffffu, lane < found && rank == i)) - 1;
-            if (lane == i) src = at_rank;
-          }
-          my_id = __shfl_sync(0xffffffffu, my_id, src);
-          my_l = __shfl_sync(0xffffffffu, my_l, src);
-          my_b = __shfl_sync(0xffffffffu, my_b, src);
-          k64 = __shfl_sync(0xffffffffu, k64, src);
-          cut = min(a.top_k, found) - 1;
+          if (lane < found) slot = rank;
+          cut = __ffs(__ballot_sync(0xffffffffu, slot == min(a.top_k, found) - 1)) - 1;
           const double last = __shfl_sync(0xffffffffu, k64, cut);
           // (nothing is left above the last candidate; the same in all lanes)
           whole = !((double)(end + key_error(most, most)) < last) &&
@@ -490,6 +518,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 4 ? 10 : 0) moe_route
         }
       }
       if (whole) {
+        slot = lane;
         load_logits<EPL, BF16, WIDE>(a, row, lane, l);  // (the rounds have moved them)
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
@@ -505,7 +534,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 4 ? 10 : 0) moe_route
       }
     }
   }
-  if (lane >= a.top_k) {  // candidates that were not chosen
+  if (slot >= a.top_k) {  // candidates that were not chosen
     my_id = -1;
     my_l = -INFINITY;
   }
@@ -521,9 +550,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 4 ? 10 : 0) moe_route
   } else if (my_id >= 0) {
     w = softmax ? exp_diff(my_l, top) / sum : sigmoid_f32(my_l);
   }
-  if (lane < a.top_k) {
-    a.ids[row * a.top_k + lane] = my_id;
-    a.weights[row * a.top_k + lane] = bad ? NAN : w * a.scale;
+  if (slot < a.top_k) {
+    a.ids[row * a.top_k + slot] = my_id;
+    a.weights[row * a.top_k + slot] = bad ? NAN : w * a.scale;
   }
 }
 

@@ -30,16 +30,24 @@ def route_row(logits, bias, top_k, scoring="softmax", groups=1, top_groups=1, gr
     ls = log_score(l, scoring) if np.any(l > -np.inf) else np.full(n, -np.inf)
     key = np.exp(ls) + (0.0 if bias is None else np.asarray(bias, dtype=np.float64))
     key = np.where((l > -np.inf) & (key > -np.inf), key, -np.inf)
+
+    def place(e):  # the experts' order: key, logit (where the key is finite), id
+        return -key[e], -l[e] if np.isfinite(key[e]) else 0.0, e
+
     if groups > 1:
         size = n // groups
         scores = []
         for g in range(groups):
-            best = sorted((c for c in key[g * size:(g + 1) * size] if c > -np.inf), reverse=True)
-            best = best[:2 if group_score == "top2" else 1]
-            scores.append(sum(best) if best else -np.inf)
-        open_ = sorted(range(groups), key=lambda g: (-scores[g], g))[:top_groups]
+            best = sorted((e for e in range(g * size, (g + 1) * size) if key[e] > -np.inf), key=place)
+            if not best:
+                scores.append((np.inf, 0.0, g))
+            elif group_score == "top2":
+                scores.append((-key[best[:2]].sum(), 0.0, g))
+            else:
+                scores.append(place(best[0]))
+        open_ = sorted(range(groups), key=lambda g: scores[g])[:top_groups]
         key = np.where(np.isin(np.arange(n) // size, open_), key, -np.inf)
-    order = sorted((e for e in range(n) if key[e] > -np.inf), key=lambda e: (-key[e], e))[:top_k]
+    order = sorted((e for e in range(n) if key[e] > -np.inf), key=place)[:top_k]
     ids = np.full(top_k, -1, dtype=np.int32)
     w = np.zeros(top_k)
     ids[:len(order)] = order

@@ -206,6 +206,37 @@ def test_route_peaked_and_equal_rows(native, scoring):
         check_route(native, logits, b, top_k=8, scoring=scoring, groups=8, top_groups=3, group_score="top2")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scoring,low,high", [("sigmoid", 30.0, 60.0), ("sigmoid", -900.0, -700.0), ("sigmoid", -1e-8, 1e-8),
+                                              ("softmax", -900.0, -700.0), ("softmax", -1e-17, 1e-17)])
+def test_route_scores_that_64_bits_do_not_tell_apart(native, dtype, scoring, low, high):
+    """Scores that saturate, underflow or round to one number: the logits' order decides, with no bias as with one that
+    is the same for all experts, in the groups' scores as well; of equal logits the lower id."""
+    rng = np.random.default_rng(23)
+    logits = rng.uniform(low, high, (40, 96)).astype(np.float32)
+    logits[20:] = rng.choice(logits[0, :7], (20, 96))
+    if scoring == "softmax":
+        logits[:, 50] = 1.0
+    for kw in (dict(top_k=9), dict(top_k=32), dict(top_k=6, groups=8, top_groups=3, group_score="max"),
+               dict(top_k=6, groups=6, top_groups=2, group_score="max"), dict(top_k=6, groups=3, top_groups=2, group_score="max")):
+        rid, _ = M.route(torch.from_numpy(logits).to(dtype).double().numpy(), None, scoring=scoring, **kw)
+        for bias in (None, np.zeros(96), np.full(96, 0.25), np.full(96, -3.0)):
+            b = None if bias is None else torch.from_numpy(bias.astype(np.float32)).cuda()
+            ids, _ = native.ffn_nvfp4_moe_route(torch.from_numpy(logits).to(dtype).cuda(), bias=b, scoring=scoring, **kw)
+            assert np.array_equal(ids.cpu().numpy(), rid), (kw, bias is None)
+
+
+def test_route_equal_keys_by_hand(native):
+    for scoring, logits, top_k, want in (("sigmoid", [38.0, 40.0], 1, [1]), ("sigmoid", [40.0, 50.0, 50.0], 2, [1, 2]),
+                                         ("softmax", [-800.0, -790.0, 0.0], 2, [2, 1]), ("softmax", [0.0, -800.0, -790.0], 2, [0, 2])):
+        for bias in (None, np.zeros(len(logits))):
+            ids, _ = check_route(native, [logits], bias, top_k=top_k, scoring=scoring)
+            assert ids.tolist() == [want]
+    # equal infinite keys by the id
+    ids, _ = check_route(native, [[1.0, 2.0, 3.0]], [np.inf, 0.0, np.inf], top_k=2, scoring="sigmoid")
+    assert ids.tolist() == [[0, 2]]
+
+
 def test_route_infinite_keys(native):
     """+inf biases tie by id; +inf logits under sigmoid score one; biases and logits of -inf close an expert."""
     rng = np.random.default_rng(13)

@@ -71,3 +71,14 @@ def test_layer_of_one_expert_is_the_dense_layer():
     # two picks of the same expert add their weights
     two = M.moe_forward(x, wgu, wd, np.zeros((3, 2), np.int32), np.full((3, 2), 0.5))
     assert np.allclose(two, out, rtol=1e-12)
+
+
+def test_route_orders_equal_scores_by_their_logits():
+    """Scores that 64 bits do not tell apart, with no bias and with one for all; infinite keys by the id."""
+    for bias in (None, np.zeros(3), np.full(3, 0.5)):
+        assert M.route([[38.0, 40.0, 40.0]], bias, 2, scoring="sigmoid")[0].tolist() == [[1, 2]]
+        assert M.route([[-800.0, -790.0, 0.0]], bias, 2)[0].tolist() == [[2, 1]]
+    for bias in (None, np.zeros(4)):
+        ids, _ = M.route([[40.0, 30.0, 50.0, 41.0]], bias, 2, scoring="sigmoid", groups=2, top_groups=1, group_score="max")
+        assert ids.tolist() == [[2, 3]]
+    assert M.route([[1.0, 2.0, 3.0]], [np.inf, 0.0, np.inf], 2, scoring="sigmoid")[0].tolist() == [[0, 2]]
