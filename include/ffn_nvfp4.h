@@ -319,7 +319,9 @@ typedef struct ffn_moe_router {
  * by the lower id, infinite ones by the id alone: without a bias, as with one
  * that is the same for all experts, the logits' order decides.  Groups of equal
  * score go by their best experts in this order (FFN_MOE_GROUP_MAX) or by the
- * lower group (FFN_MOE_GROUP_TOP2).  Weights are accurate to a few fp32 steps.
+ * lower group (FFN_MOE_GROUP_TOP2).  Weights are accurate to a few fp32 steps;
+ * one below fp32's normal range, or a score there that is not renormalised, to
+ * a few of the smallest steps (2^-149).
  * An expert whose logit is -inf or NaN, or whose key is, is never chosen; where
  * fewer than top_k are left, the remaining ids are -1 with weight 0 (a row
  * without any open expert: all of them).  A group's score counts only such

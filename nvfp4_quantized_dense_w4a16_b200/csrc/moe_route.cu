@@ -541,10 +541,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 4 ? 10 : 0) moe_route
 
   float w = 0.0f;
   if (a.renormalize) {
-    // Ratios of exponentials where the scores are so (softmax; sigmoids of
-    // logits below -60, to e^-60): scores that underflow keep their ratio.
-    const float high = redux_max(my_l);
-    if (my_id >= 0) w = softmax || high < -60.0f ? exp_diff(my_l, high) : sigmoid_f32(my_l);
+    // Scores by the best one's exponential (of a logit of at most zero, under
+    // sigmoid: e^l / (1 + e^l)), so that scores that underflow keep their ratio.
+    const float high = redux_max(my_l), base = softmax ? high : fminf(high, 0.0f);
+    if (my_id >= 0)
+      w = softmax ? exp_diff(my_l, base) : my_l < 0.0f ? exp_diff(my_l, base) / (1.0f + expf(my_l)) : sigmoid_f32(my_l);
     const float total = warp_sum(w);
     if (my_id >= 0) w /= total;
   } else if (my_id >= 0) {

@@ -237,6 +237,22 @@ def test_route_equal_keys_by_hand(native):
     assert ids.tolist() == [[0, 2]]
 
 
+@pytest.mark.parametrize("top", [-90.0, -60.5, -59.5, -40.0, -25.0])
+def test_route_sigmoids_below_the_normal_range_keep_their_ratio(native, top):
+    """Renormalised sigmoids of logits so low that fp32 holds their scores in few bits, or not at all, beside a better
+    one: the weights are ratios and far from that."""
+    rng = np.random.default_rng(24)
+    logits = rng.uniform(top - 80.0, top, (50, 40))
+    logits[:, 11] = top
+    check_route(native, logits, None, top_k=12, scoring="sigmoid")
+    check_route(native, logits, np.zeros(40), top_k=12, scoring="sigmoid", scale=2.5)
+    logits[:, 30] = 4.0  # from here on to the smallest numbers
+    ids, w = native.ffn_nvfp4_moe_route(torch.from_numpy(logits.astype(np.float32)).cuda(), 12, scoring="sigmoid")
+    rid, rw = M.route(logits.astype(np.float32).astype(np.float64), None, 12, scoring="sigmoid")
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    assert np.all(np.abs(w.double().cpu().numpy() - rw) <= 15 * 2.0 ** -24 * rw + 4 * 2.0 ** -149)
+
+
 def test_route_infinite_keys(native):
     """+inf biases tie by id; +inf logits under sigmoid score one; biases and logits of -inf close an expert."""
     rng = np.random.default_rng(13)
