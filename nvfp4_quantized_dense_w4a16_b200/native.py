@@ -387,6 +387,9 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
 
 @functools.lru_cache(maxsize=256)
 def _router(scoring, top_k, groups, top_groups, group_score, renormalize, scale):
+    for name, value, known in (("scoring", scoring, MOE_SCORINGS), ("group_score", group_score, MOE_GROUP_SCORES)):
+        if value not in known:
+            raise ValueError(f"{name} must be one of {', '.join(map(repr, known))}, got {value!r}")
     return MoeRouter(MOE_SCORINGS[scoring], top_k, groups, top_groups, MOE_GROUP_SCORES[group_score],
                      int(renormalize), scale)
 
@@ -396,6 +399,7 @@ def ffn_nvfp4_moe_route(logits: torch.Tensor, top_k: int, scoring="softmax", bia
                         ids=None, weights=None, stream=None):
     """[m, experts] float32 or bfloat16 logits -> (ids int32 [m, top_k], weights float32 [m, top_k]).
     The rows may be strided (a slice of wider rows), each row contiguous."""
+    router = _router(scoring, top_k, groups, top_groups, group_score, renormalize, scale)
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits must be a torch.Tensor")
     if not logits.is_cuda:
@@ -416,8 +420,7 @@ def ffn_nvfp4_moe_route(logits: torch.Tensor, top_k: int, scoring="softmax", bia
     launch = _launch_stream(stream, logits, bias, ids, weights)
     st = lib.ffn_nvfp4_moe_route(
         logits.data_ptr(), kind, m, experts, ld if m > 1 else max(ld, experts), None if bias is None else bias.data_ptr(),
-        _router(scoring, top_k, groups, top_groups, group_score, renormalize, scale), ids.data_ptr(), weights.data_ptr(),
-        launch)
+        router, ids.data_ptr(), weights.data_ptr(), launch)
     if st:
         _check("ffn_nvfp4_moe_route", st)
     return ids, weights

@@ -112,3 +112,11 @@ def test_a_workspace_serves_every_smaller_batch(native, experts, top_k, hidden, 
     for sizes in (layer, linear):
         falls = [(m, a, b) for m, (a, b) in enumerate(zip(sizes, sizes[1:])) if b < a]
         assert not falls, falls[:4]
+
+
+@pytest.mark.parametrize("kw,name", [(dict(scoring="soft"), "scoring"), (dict(scoring=None), "scoring"),
+                                     (dict(group_score="top3"), "group_score"), (dict(group_score=0), "group_score")])
+def test_unknown_router_names_are_refused_by_name(native, kw, name):
+    import torch
+    with pytest.raises(ValueError, match=f"^{name} must be one of"):
+        native.ffn_nvfp4_moe_route(torch.zeros((4, 32)), 4, **kw)
