@@ -589,6 +589,47 @@ def test_layer_at_the_kernels_boundaries(native, m, experts, top_k, hidden, inte
     layer.check(layer.run(x, ids, weights), x64, ids, weights)
 
 
+@pytest.mark.parametrize("m,experts,top_k,hidden,inter", [
+    (1, 4, 2, 64, 96), (1, 8, 8, 96, 544), (1, 1, 1, 128, 64), (2, 4, 2, 64, 96), (4, 6, 3, 160, 256),
+    (4, 3, 8, 64, 544), (5, 6, 3, 96, 96), (8, 7, 4, 128, 160), (16, 5, 2, 64, 320), (32, 9, 1, 96, 64),
+])
+def test_layer_of_few_pairs_keeps_16_bits_of_the_hidden_rows(native, m, experts, top_k, hidden, inter):
+    """Up to 32 pairs h goes to the down products as two bf16 parts, off by 2^-16 of it (half a step of the second part,
+    which is at most half a step of the first).
+
+    Whole x and gate and up weights of small whole numbers make the products exact; silu and its product cost 16 half
+    steps of fp32 as above, the down sums theirs.  The bound is far below half a step of bf16 of the terms, so that an
+    oracle without the second part leaves it."""
+    rng = np.random.default_rng(3800 + m + inter)
+    codes = rng.integers(0, 256, (experts, 2 * inter, hidden // 2), dtype=np.uint8)
+    scales = np.full((experts, 2 * inter, hidden // 16), 0x38, np.uint8)  # 1.0
+    gs = np.full((experts, 2), 2.0 ** -6, np.float32)
+    w_gu = M.experts_dequant(codes, scales, gs)
+    gu = native.ffn_nvfp4_experts_create(*(torch.from_numpy(a).cuda() for a in (codes, scales, gs)), gate_up=True)
+    dn = Stack(native, experts, hidden, inter, 3900 + m)
+    x64 = rng.integers(-2, 3, (m, hidden)).astype(np.float64)
+    ids = np.resize(pick(rng, m, experts, min(top_k, experts)).T, (top_k, m)).T  # (some experts twice in a row)
+    weights = rng.uniform(0.25, 1.0, (m, top_k)).astype(np.float32)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    out = native.ffn_nvfp4_moe_forward(dev(x64).to(torch.bfloat16), gu, dn.handle, dev(ids), dev(weights))
+    g, u, rounded = M.moe_hidden(x64, w_gu, ids)
+    h = g / (1.0 + np.exp(-g)) * u
+    dh = (2.0 ** -16 + 16 * 2.0 ** -24) * np.abs(h)
+    ref, bound, without = np.zeros((3, m, hidden))
+    for i in range(m):
+        for j, e in enumerate(ids[i]):
+            w, a = dn.w[e], float(weights[i, j])
+            ref[i] += a * (w @ h[i, j])
+            without[i] += a * (w @ rounded[i, j])
+            terms = np.abs(w) @ (np.abs(h[i, j]) + dh[i, j])
+            bound[i] += a * (np.abs(w) @ dh[i, j] + (sum_error(inter) + (top_k + 1) * 2.0 ** -24) * terms)
+    bound = (1 + HALF) * bound + HALF * np.abs(ref)
+    err = np.abs(bf16_to_f64(out) - ref)
+    assert np.all(err <= bound), float((err / bound).max())
+    lost = np.abs(O.round_to_bf16(without) - ref)
+    assert np.any(lost > bound), "the bound would not see the second part missing"
+
+
 @pytest.mark.parametrize("m", [1, 2, 4, 5, 8, 11, 60])
 def test_layer_the_same_expert_again(native, m):
     """Equal ids in a row count each, with their own weights; all rows at one expert."""
