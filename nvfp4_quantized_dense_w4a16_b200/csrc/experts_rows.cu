@@ -315,7 +315,9 @@ struct Item {
 // Bound by the decode: 500 cycles a step and quarter of an SM, of which the ALU
 // pipe is busy for 370 (the MMAs for 160).  One row through 2 of 8 experts of
 // 4096 x 12288 takes 49 us (170 MB of weights, 26 us at the copy rate), through 8
-// of 64 of 2048 x 1024 15.5 us (28 MB, 4.3), 256 pairs of those 71 us (34).
+// of 64 of 2048 x 1024 15.9 us (28 MB, 4.3), 256 pairs of those 71 us (34).
+// Tiles of 16 rows (NT = 2) do not fit the 96 registers a thread and spill 28 to
+// 68 bytes; those of 8 do.
 template <int MODE, int NT, int FROM, bool SUM>
 __global__ void __launch_bounds__(kRowsThreads, 1) experts_rows_kernel(const RowsArgs a) {
   using C = RowsCfg<NT>;
@@ -690,8 +692,10 @@ cudaError_t launch_rows_from(const RowsArgs& a, cudaStream_t s) {
 }  // namespace
 
 int rows_splits(const ExpertsView& w, int64_t tiles, int sms) {
-  // rounds of items over the SMs times the steps of an item, and about four
-  // steps' time for an item's sums
+  // Rounds of items over the SMs times the steps of an item, and about four
+  // steps' time for an item's sums.  One row through 2 of 8 experts of
+  // 4096 x 12288 takes 48.9 us with the two ranges that this gives and 61.5 with one,
+  // through 2 of 8 of 1056 x 672 11.5 with six and 12.0 with one.
   const int64_t steps = (w.kc + kStepChunks - 1) / kStepChunks, items = tiles * rows_units(w);
   int64_t best = 0, least = INT64_MAX;
   for (int64_t s = 1; s <= kMaxSplits && s <= steps; ++s) {

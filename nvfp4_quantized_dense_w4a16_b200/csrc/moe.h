@@ -65,11 +65,19 @@ enum class ExpertsOut : int {
   kF32 = 2       // y[p, :] = gs * acc, fp32
 };
 
-// Up to this many pairs the kernels for few rows read the ids themselves: no
-// plan is needed.
+// Up to this many pairs the kernels for few rows read the ids themselves, a lane
+// per pair: no plan is needed, and the down products make the sum.  The layer so
+// and with a plan, in us: 8 of 64 experts of 2048 x 1024, 1, 2 and 4 rows 15.9,
+// 26.9 and 37.9 against 23.0, 32.0 and 40.7; 2 of 8 of 4096 x 12288, 1 row 48.9
+// against 56.4.  From about 8 rows the two bf16 parts of h, for which a tile holds
+// half the rows, cost more than the plan: 8 and 16 rows of those 168 and 218
+// against 150 and 167, 32 rows of one pick each of the small ones 51 against 39.
+// The parts are what the layer documents for so few pairs.
 constexpr int kFewPairs = 32;
-// Rows of a plan's tiles for launch_experts_rows: 8, where a tile of 16 would be
-// half empty on average.
+// Rows of a plan's tiles for launch_experts_rows: 8 or 16.  The layer of 64 experts
+// of 2048 x 1024 with tiles of 8 and of 16 at 2, 4, 5, 6, 7 and 8 rows an expert,
+// in us: 65, 71, 77, 80, 87, 95.5 and 80, 86, 87, 89, 90, 90; 8 of 4096 x 6144 at 4,
+// 5, 6, 7, 8: 96, 97, 108, 120, 132 and 117, 117, 118, 119, 119.
 inline int64_t last_narrow_pairs(int64_t experts) { return 5 * experts; }
 inline int rows_tile(int64_t pairs, int64_t experts) { return pairs <= last_narrow_pairs(experts) ? 8 : 16; }
 

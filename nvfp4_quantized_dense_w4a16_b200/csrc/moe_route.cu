@@ -166,7 +166,8 @@ __device__ __forceinline__ Key keep_best_groups(const RouteArgs& a, Key (&key)[E
   return high > -INFINITY && low < INFINITY ? low - high : (Key)INFINITY;
 }
 
-// Odd-even merges of EPL registers: order(x, y) for x < y puts the better one at x.
+// Batcher's odd-even merge sort of EPL registers: order(x, y) for x < y puts the
+// better one at x.
 template <int EPL, typename Order>
 __device__ __forceinline__ void merge_sort(Order order) {
 #pragma unroll
