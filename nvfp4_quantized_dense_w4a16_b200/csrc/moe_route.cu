@@ -18,12 +18,13 @@
 // error of the row first, and where that is too much against each key's own.
 //
 // Bound by instructions: the logits and results of 16384 rows of 128 experts are
-// 0.8 us of memory traffic, and 8 choices of each take 10.3 us at 520 instructions
+// 0.8 us of memory traffic, and 8 choices of each take 10.2 us at 520 instructions
 // a row (67% of the issue slots): half of them the rounds of a warp-wide maximum,
 // whose lanes hold their keys sorted, half the softmax.  fp32 keys need a vote and
 // two shuffles a round to find the winner; bf16 keys carry their id in the word
 // (12.9 -> 10.7 us).  509 rows of 256 with groups and a bias, one row a warp and
-// four warps an SM, take 7.3 us: the latency of one row.
+// four warps an SM, take 6.1 us: the latency of one row, of one that 64 bits settle
+// (5.5 without such rows).
 #include <math.h>
 
 #include "common.cuh"
@@ -147,8 +148,12 @@ __device__ __forceinline__ Key keep_best_groups(const RouteArgs& a, Key (&key)[E
   int rank = 0;
   for (int g = 0; g < a.groups; ++g) {
     const Key o = __shfl_sync(0xffffffffu, best, g * step);
-    const float ot = kTies ? __shfl_sync(0xffffffffu, tie, g * step) : 0.0f;
-    rank += o > best || (o == best && (ot > tie || (ot == tie && g < mine)));
+    bool first = g < mine;
+    if constexpr (kTies) {
+      const float ot = __shfl_sync(0xffffffffu, tie, g * step);
+      first = (ot > tie) | ((ot == tie) & first);
+    }
+    rank += o > best || (o == best && first);
   }
   const bool in = mine < a.groups, kept = in && rank < a.top_groups;
   Key low = kept ? best : (Key)INFINITY, high = in && !kept ? best : (Key)-INFINITY;
@@ -221,16 +226,20 @@ __device__ __noinline__ int choose_64(const RouteArgs& a, const float (&l)[EPL],
       best_tie = take ? tie[i] : best_tie;
       at = take ? lane * EPL + i : at;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const double ob = __shfl_xor_sync(0xffffffffu, best, o);
-      const float ot = __shfl_xor_sync(0xffffffffu, best_tie, o);
-      const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-      const bool take = (ob > best) | ((ob == best) & ((ot > best_tie) | ((ot == best_tie) & (oa < at))));
-      best = take ? ob : best;
-      best_tie = take ? ot : best_tie;
-      at = take ? oa : at;
-    }
+    // the warp's best by maxima of words in the numbers' order: the key's two
+    // halves, the logit; of equal ones the lowest lane
+    const long long bits = __double_as_longlong(best + 0.0);  // (one zero)
+    const unsigned long long up = bits ^ ((bits >> 63) | (long long)0x8000000000000000ull);
+    const uint32_t hi = (uint32_t)(up >> 32), lo = (uint32_t)up;
+    const int tbits = __float_as_int(best_tie + 0.0f);
+    const uint32_t top_hi = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t top_lo = __reduce_max_sync(0xffffffffu, hi == top_hi ? lo : 0u);
+    const bool equal = hi == top_hi && lo == top_lo;
+    const uint32_t order = equal ? tbits ^ ((tbits >> 31) | 0x80000000u) : 0u;
+    const uint32_t top_order = __reduce_max_sync(0xffffffffu, order);
+    const int w = __ffs(__ballot_sync(0xffffffffu, equal && order == top_order)) - 1;
+    best = __shfl_sync(0xffffffffu, best, w);
+    at = __shfl_sync(0xffffffffu, at, w);
     if (best == -INFINITY) break;  // nothing is left
     if (lane == j) mine = at;
 #pragma unroll
@@ -520,16 +529,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 4 ? 10 : 0) moe_route
       }
       if (whole) {
         slot = lane;
-        load_logits<EPL, BF16, WIDE>(a, row, lane, l);  // (the rounds have moved them)
+        float r[EPL];  // (the rounds have moved l, and a call's argument stands in memory)
+        load_logits<EPL, BF16, WIDE>(a, row, lane, r);
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-          if (isnan(l[i])) l[i] = -INFINITY;
-        my_id = choose_64<EPL>(a, l, lane, route_smem + (size_t)warp * a.experts);
+          if (isnan(r[i])) r[i] = -INFINITY;
+        my_id = choose_64<EPL>(a, r, lane, route_smem + (size_t)warp * a.experts);
         // the chosen logits, from the lanes that hold them
         my_l = -INFINITY;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-          const float v = __shfl_sync(0xffffffffu, l[i], my_id >= 0 ? my_id / EPL : 0);
+          const float v = __shfl_sync(0xffffffffu, r[i], my_id >= 0 ? my_id / EPL : 0);
           if (my_id >= 0 && my_id % EPL == i) my_l = v;
         }
       }
@@ -544,9 +554,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 4 ? 10 : 0) moe_route
   if (a.renormalize) {
     // Scores by the best one's exponential (of a logit of at most zero, under
     // sigmoid: e^l / (1 + e^l)), so that scores that underflow keep their ratio.
-    const float high = redux_max(my_l), base = softmax ? high : fminf(high, 0.0f);
-    if (my_id >= 0)
-      w = softmax ? exp_diff(my_l, base) : my_l < 0.0f ? exp_diff(my_l, base) / (1.0f + expf(my_l)) : sigmoid_f32(my_l);
+    const float high = redux_max(my_l);
+    if (my_id >= 0) {
+      w = softmax || high < 0.0f ? exp_diff(my_l, high) : sigmoid_f32(my_l);
+      if (!softmax && high < 0.0f) w /= 1.0f + expf(my_l);
+    }
     const float total = warp_sum(w);
     if (my_id >= 0) w /= total;
   } else if (my_id >= 0) {
