@@ -317,11 +317,13 @@ typedef struct ffn_moe_router {
  * The choice is the one that 64-bit arithmetic makes.  Keys that it does not
  * tell apart (scores that saturate or underflow) go by the larger logit, then
  * by the lower id, infinite ones by the id alone: without a bias, as with one
- * that is the same for all experts, the logits' order decides.  Groups of equal
- * score go by their best experts in this order (FFN_MOE_GROUP_MAX) or by the
- * lower group (FFN_MOE_GROUP_TOP2).  Weights are accurate to a few fp32 steps;
- * one below fp32's normal range, or a score there that is not renormalised, to
- * a few of the smallest steps (2^-149).
+ * that is the same for all experts, the logits' order decides.  (Keys of
+ * different biases, or sums of two, that differ by rounding in 64 bits alone may
+ * go either way, the same way in every call.)  Groups of equal score go by their
+ * best experts in this order (FFN_MOE_GROUP_MAX) or by the lower group
+ * (FFN_MOE_GROUP_TOP2).  Weights are accurate to a few fp32 steps; one below
+ * fp32's normal range, or a score there that is not renormalised, to a few of
+ * the smallest steps (2^-149).
  * An expert whose logit is -inf or NaN, or whose key is, is never chosen; where
  * fewer than top_k are left, the remaining ids are -1 with weight 0 (a row
  * without any open expert: all of them).  A group's score counts only such
@@ -370,9 +372,10 @@ ffn_status ffn_nvfp4_experts_info(const ffn_nvfp4_experts* w, int64_t* experts, 
  * no-op.  The workspace holds the rows' places by expert and, for many rows,
  * their copies in that order; it may be shared by calls on one stream, and the
  * size for m rows serves every smaller m (of the same other arguments) too.
- * Errors: FFN_ERR_UNSUPPORTED for a gate and up stack; FFN_ERR_SHAPE when 2 * m * top_k exceeds 2^31 - 1 or m * top_k rows of n or k
- * columns are more than 2^40 elements (the sizes: FFN_ERR_UNSUPPORTED for
- * experts > FFN_MOE_MAX_EXPERTS). */
+ * Errors: FFN_ERR_UNSUPPORTED for a gate and up stack; FFN_ERR_SHAPE when
+ * 2 * m * top_k exceeds 2^31 - 1 or m * top_k rows of n or k columns are more
+ * than 2^40 elements; the size: FFN_ERR_UNSUPPORTED for experts >
+ * FFN_MOE_MAX_EXPERTS. */
 ffn_status ffn_nvfp4_experts_workspace_size(int64_t m, int top_k, int64_t experts, int64_t n, int64_t k,
                                             size_t* bytes);
 ffn_status ffn_nvfp4_experts_linear(const void* x, int64_t m, const ffn_nvfp4_experts* w, const int32_t* ids,
