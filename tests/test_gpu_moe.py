@@ -630,6 +630,43 @@ def test_layer_of_few_pairs_keeps_16_bits_of_the_hidden_rows(native, m, experts,
     assert np.any(lost > bound), "the bound would not see the second part missing"
 
 
+@pytest.mark.parametrize("m,experts,top_k,hidden,inter", [
+    (40, 12, 1, 96, 160), (60, 9, 1, 64, 544), (100, 4, 2, 128, 96), (300, 3, 2, 64, 320),
+])
+def test_layer_of_many_pairs_rounds_the_hidden_rows_once(native, m, experts, top_k, hidden, inter):
+    """Beyond 32 pairs h is rounded to bf16, once: where no midpoint between two bf16 numbers is within silu's error of
+    it, to the oracle's number.  The products are exact, as above.  silu's exponential is off by 2 + 1.2 |g| steps of
+    fp32 (CUDA's bound for the fast one), the sum, the quotient and the products by 5 more."""
+    rng = np.random.default_rng(4000 + m)
+    codes = rng.integers(0, 256, (experts, 2 * inter, hidden // 2), dtype=np.uint8)
+    scales = np.full((experts, 2 * inter, hidden // 16), 0x38, np.uint8)  # 1.0
+    gs = np.full((experts, 2), 2.0 ** -6, np.float32)
+    w_gu = M.experts_dequant(codes, scales, gs)
+    gu = native.ffn_nvfp4_experts_create(*(torch.from_numpy(a).cuda() for a in (codes, scales, gs)), gate_up=True)
+    dn = Stack(native, experts, hidden, inter, 4100 + m)
+    x64 = rng.integers(-2, 3, (m, hidden)).astype(np.float64)
+    ids = pick(rng, m, experts, top_k)
+    weights = rng.uniform(0.25, 1.0, (m, top_k)).astype(np.float32)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    out = native.ffn_nvfp4_moe_forward(dev(x64).to(torch.bfloat16), gu, dn.handle, dev(ids), dev(weights))
+    g, u, h = M.moe_hidden(x64, w_gu, ids)
+    exact = g / (1.0 + np.exp(-g)) * u
+    off = (7.0 + 1.2 * np.abs(g)) * 2.0 ** -23 * np.abs(exact)
+    near = O.round_to_bf16(exact - off) != O.round_to_bf16(exact + off)
+    assert near.mean() < 0.05
+    dh = np.where(near, np.abs(O.round_to_bf16(exact + off).astype(np.float64) - O.round_to_bf16(exact - off)), 0.0)
+    ref, bound = np.zeros((2, m, hidden))
+    for i in range(m):
+        for j, e in enumerate(ids[i]):
+            w, a = dn.w[e], float(weights[i, j])
+            ref[i] += a * (w @ h[i, j])
+            terms = np.abs(w) @ (np.abs(h[i, j]) + dh[i, j])
+            bound[i] += a * (np.abs(w) @ dh[i, j] + (sum_error(inter) + (top_k + 1) * 2.0 ** -24) * terms)
+    bound = (1 + HALF) * bound + HALF * np.abs(ref)
+    err = np.abs(bf16_to_f64(out) - ref)
+    assert np.all(err <= bound), float((err / bound).max())
+
+
 @pytest.mark.parametrize("m", [1, 2, 4, 5, 8, 11, 60])
 def test_layer_the_same_expert_again(native, m):
     """Equal ids in a row count each, with their own weights; all rows at one expert."""
