@@ -18,7 +18,7 @@
 // error of the row first, and where that is too much against each key's own.
 //
 // Bound by instructions: the logits and results of 16384 rows of 128 experts are
-// 0.8 us of memory traffic, and 8 choices of each take 10.2 us at 520 instructions
+// 0.8 us of memory traffic, and 8 choices of each take 10.3 us at 520 instructions
 // a row (67% of the issue slots): half of them the rounds of a warp-wide maximum,
 // whose lanes hold their keys sorted, half the softmax.  fp32 keys need a vote and
 // two shuffles a round to find the winner; bf16 keys carry their id in the word
@@ -328,7 +328,7 @@ __device__ __forceinline__ void choose_words(const float (&key)[EPL], int lane, 
   }
 }
 
-// Ten CTAs an SM for up to 128 experts: 48 registers (16384 x 128: 10.2 us, 10.4
+// Ten CTAs an SM for up to 128 experts: 48 registers (16384 x 128: 10.3 us, 10.4
 // with the 52 to 56 that the compiler takes by itself).
 template <int EPL, bool BF16, bool WIDE>
 __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 4 ? 10 : 0) moe_route_kernel(const RouteArgs a) {
