@@ -405,6 +405,139 @@ ffn_status ffn_nvfp4_moe_forward(const void* x, int64_t m, int64_t hidden, int64
                                  const int32_t* ids, const float* weights, int top_k, void* out, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit integers: the layer's products over int8 weights and int8 activations,
+ * with one fp32 scale for each output channel and each row (token).  A second
+ * fixed activation format beside FFN_ACT_NVFP4_FIXED, for weights that are kept
+ * in 8 bits; the weights are plain tensors, no handle.  ("metrale_model_layers/
+ * layers/dense_ffn_fixed.rs", forward_fixed, has such an 8-bit arm, of FP8
+ * rows; this integer format and its definitions are this library's.)
+ * The sums are exact in 32-bit integers and what follows them is the same in
+ * every kernel: each output row is bit-identical whatever m is.
+ * ------------------------------------------------------------------------- */
+#define FFN_INT8_MAX_K 131040 /* sums of k products of magnitude 128^2 fit 32 bits */
+
+/* Quantise bf16 rows to int8: scales[i] = a / 127 with a = max_k |x[i, k]|, and
+ * codes[i, k] = x[i, k] * (127 / a), rounded to the nearest integer, ties to
+ * even (fp32 arithmetic, each operation rounded once; where 127 / a would be
+ * infinite, both factors are scaled by 2^64 and 2^-64).  The rows of
+ * activations, or of a weight [n, k] (its output channels).  A row of zeros has
+ * the scale 0; a row with a NaN or an infinity has the scale NaN and codes 0,
+ * so that everything computed from it is NaN.
+ *   x       [m, k] bf16, row i at i * row_stride elements (row_stride >= k, a
+ *           multiple of 8)
+ *   codes   int8 [m, k] (output);  scales fp32 [m] (output)
+ * m == 0 is a no-op.  Errors: FFN_ERR_SHAPE unless k is a positive multiple of 32,
+ * or where m rows are more than 2^40 elements. */
+ffn_status ffn_int8_quantize(const void* x_bf16, int64_t m, int64_t k, int64_t row_stride, int8_t* codes,
+                             float* scales, void* stream);
+
+/* One projection of int8 weights:
+ *   y[i, j] = bf16(((float)sum_k xq[i, k] * w[j, k]) * xs[i] * w_scales[j] + bias[j])
+ *   x        with x_scales: int8 codes [m, k] and their scales fp32 [m]
+ *            (any codes, -128 included); with x_scales NULL: bf16 [m, k],
+ *            quantised first as ffn_int8_quantize does
+ *   w        int8 [n, k];  w_scales fp32 [n];  bias bf16 [n] or NULL
+ *   y        [m, n] bf16; only rows 0..m-1 are written; may not overlap an input
+ * The sum is exact; the factors, the bias and the last rounding follow in this
+ * order, each rounded once to fp32.  m == 0 is a no-op.  Allocates nothing and
+ * does not synchronise.  The workspace (ffn_int8_linear_workspace_size bytes;
+ * not needed with x_scales) may be shared by calls on one stream, and its size
+ * serves every smaller m.  Launched with programmatic stream serialisation:
+ * weights and their scales may be read while the kernel before in the stream is
+ * finishing, all else after it has completed.
+ * Errors: FFN_ERR_SHAPE unless k is a positive multiple of 32 and n > 0, or for
+ * buffers of more than 2^40 elements; FFN_ERR_UNSUPPORTED for k > FFN_INT8_MAX_K. */
+ffn_status ffn_int8_linear_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
+ffn_status ffn_int8_linear(const void* x, const float* x_scales, int64_t m, const int8_t* w, const float* w_scales,
+                           const void* bias, int64_t n, int64_t k, void* y, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* The FFN layer over int8 weights: out = down(silu(gate(x)) * up(x)).
+ *   x        as for ffn_int8_linear, [m, hidden]
+ *   gate_up  int8 [2 * inter, hidden], gate rows first, then up rows, with
+ *            scales fp32 [2 * inter];  down int8 [hidden, inter], scales [hidden]
+ *   out      [m, hidden] bf16; only rows 0..m-1 are written; may be x (bf16)
+ * Numerics: gate and up stay fp32 (their exact sums times the two scales);
+ * h = silu(gate) * up is rounded to bf16 and quantised as ffn_int8_quantize
+ * does; the down projection is ffn_int8_linear's.  Everything else (workspace,
+ * launch order, m == 0, errors) as for ffn_int8_linear, with
+ * ffn_int8_workspace_size bytes, which are always needed. */
+ffn_status ffn_int8_workspace_size(int64_t m, int64_t hidden, int64_t inter, size_t* bytes);
+ffn_status ffn_int8_forward(const void* x, const float* x_scales, int64_t m, int64_t hidden, int64_t inter,
+                            const int8_t* gate_up, const float* gate_up_scales, const int8_t* down,
+                            const float* down_scales, void* out, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* ---------------------------------------------------------------------------
+ * What stands between two layers: the norm after a layer, its gate, the
+ * residual, and the norm before the next layer, in one pass over the rows.
+ * (The pages' layers are called between such norms by their drivers, which are
+ * not on the pages; the definition is this library's.)
+ * ------------------------------------------------------------------------- */
+#define FFN_NORM_MAX_HIDDEN 32768
+
+typedef enum ffn_value_type { FFN_VALUE_F32 = 0, FFN_VALUE_BF16 = 1 } ffn_value_type;
+typedef enum ffn_norm_kind {
+  FFN_NORM_RMS = 0,   /* v / sqrt(mean(v^2) + eps)                            */
+  FFN_NORM_LAYER = 1  /* the same of v - mean(v)                              */
+} ffn_norm_kind;
+typedef enum ffn_gate_activation { FFN_GATE_NONE = 0, FFN_GATE_SIGMOID = 1, FFN_GATE_TANH = 2 } ffn_gate_activation;
+
+/* norm(v) = v normalised by its kind, * (offset + weight) + bias; eps > 0. */
+typedef struct ffn_norm {
+  int kind;           /* ffn_norm_kind                                        */
+  int type;           /* ffn_value_type of weight and bias                    */
+  const void* weight; /* [hidden], or NULL: factor 1 (offset is not used)     */
+  const void* bias;   /* [hidden], or NULL: none                              */
+  float eps, offset;
+} ffn_norm;
+
+/* For each of m rows of `hidden` values:
+ *   z    = post norm of y, or y without one
+ *   r'   = residual_scale * residual + branch_scale * act(gate) * z,
+ *          rounded to the residual's type                  -> residual_out
+ *   x'   = pre norm of r' (as rounded), in bf16            -> out
+ * with out_scales: x' is quantised as ffn_int8_quantize does -> out (int8 codes)
+ * and out_scales.  Without y (the first layer) r' is the residual itself: there
+ * is no gate and no residual_out, and the scales are 1.  Statistics are fp32.
+ * Rows are strided: row i of a tensor starts at i * stride elements. */
+typedef struct ffn_block_norm_args {
+  const void* y;            /* bf16 [m, hidden], or NULL                      */
+  int64_t y_stride;
+  const ffn_norm* post;     /* norm of y, or NULL                             */
+  const void* gate;         /* or NULL: 1; element (i, j) at i * gate_row_stride +
+                               j * gate_col_stride                            */
+  int gate_type;            /* ffn_value_type                                 */
+  int gate_activation;      /* ffn_gate_activation                            */
+  int64_t gate_row_stride;  /* 0: one gate for all rows                       */
+  int64_t gate_col_stride;  /* 0: one gate for a row; or 1                    */
+  const void* residual;     /* [m, hidden] of residual_type                   */
+  int residual_type;        /* ffn_value_type                                 */
+  int64_t residual_stride;
+  void* residual_out;       /* of residual_type, or NULL: not stored; may be the
+                               residual itself (same stride)                  */
+  int64_t residual_out_stride;
+  float residual_scale, branch_scale;
+  const ffn_norm* pre;      /* norm of r', or NULL: no out                    */
+  void* out;                /* bf16 [m, hidden], or int8 with out_scales; a bf16
+                               out may be y itself (same stride)              */
+  int64_t out_stride;
+  float* out_scales;        /* fp32 [m], or NULL                              */
+} ffn_block_norm_args;
+
+/* One launch; m == 0 is a no-op; allocates nothing and does not synchronise.
+ * Outputs may not overlap inputs but as said above.  Any hidden from 1 on, at
+ * any stride >= hidden; tensors are aligned to their elements (rows of whole 16
+ * bytes take a faster path).  A row with a NaN, or an infinity in what a norm
+ * reads, has NaN for x' (codes 0, scale NaN).  Errors: FFN_ERR_INVALID_ARG for
+ * a missing tensor, an unknown enum value, a stride below hidden, scales that
+ * are not finite or an eps that is not finite and positive;
+ * FFN_ERR_UNSUPPORTED for hidden > FFN_NORM_MAX_HIDDEN; FFN_ERR_SHAPE for m rows
+ * of a stride of more than 2^40 elements; with out_scales hidden is a multiple of
+ * 32 (FFN_ERR_SHAPE) and out_stride equals hidden. */
+ffn_status ffn_block_norm(const ffn_block_norm_args* args, int64_t m, int64_t hidden, void* stream);
+
 /* Kernel configuration a projection of m rows would use (the m-dispatch),
  * without launching anything; callable without a GPU (the SM count of the
  * current device is used when there is one, else 148).  Lets callers and

@@ -1,0 +1,28 @@
+// Host-side declarations of the 8-bit integer layers.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace ffn {
+
+// codes and scales of bf16 rows of k columns (a multiple of 8), row i at i * stride.
+cudaError_t launch_int8_quantize(const void* x, int64_t m, int64_t k, int64_t stride, int8_t* codes, float* scales,
+                                 cudaStream_t s);
+
+// One projection of int8 rows.  Plain: y bf16 [m, n].  With silu_mul the weight
+// holds n / 2 gate rows, then n / 2 up rows, and y is h bf16 [m, n / 2].
+struct Int8Product {
+  const int8_t* x;
+  const float* xs;
+  int64_t m;
+  const int8_t* w;
+  const float* ws;
+  const uint16_t* bias;  // bf16 [n] or null
+  int64_t n, k;
+  uint16_t* y;
+  bool silu_mul;
+};
+cudaError_t launch_int8_product(const Int8Product& p, cudaStream_t s);
+
+}  // namespace ffn

@@ -12,6 +12,7 @@ import ctypes
 import functools
 import os
 import re
+import struct
 
 import torch
 
@@ -99,6 +100,12 @@ def _load() -> ctypes.CDLL:
         "ffn_nvfp4_experts_linear": (ctypes.c_int, [vp, i64, vp, vp, ctypes.c_int, vp, vp, sz, vp]),
         "ffn_nvfp4_moe_workspace_size": (ctypes.c_int, [i64, ctypes.c_int, i64, i64, i64, P(sz)]),
         "ffn_nvfp4_moe_forward": (ctypes.c_int, [vp, i64, i64, i64, vp, vp, vp, vp, ctypes.c_int, vp, vp, sz, vp]),
+        "ffn_int8_quantize": (ctypes.c_int, [vp, i64, i64, i64, vp, vp, vp]),
+        "ffn_int8_linear_workspace_size": (ctypes.c_int, [i64, i64, i64, P(sz)]),
+        "ffn_int8_linear": (ctypes.c_int, [vp, vp, i64, vp, vp, vp, i64, i64, vp, vp, sz, vp]),
+        "ffn_int8_workspace_size": (ctypes.c_int, [i64, i64, i64, P(sz)]),
+        "ffn_int8_forward": (ctypes.c_int, [vp, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "ffn_block_norm": (ctypes.c_int, [vp, i64, i64, vp]),
         "ffn_nvfp4_profile_begin": (ctypes.c_int, []),
         "ffn_nvfp4_device_error": (ctypes.c_int, [P(ctypes.c_int), ctypes.c_int]),
         "ffn_nvfp4_profile_end": (ctypes.c_int, [P(KernelTime), ctypes.c_int, P(ctypes.c_int)]),
@@ -536,6 +543,247 @@ def ffn_nvfp4_moe_forward(x: torch.Tensor, gate_up: Experts, down: Experts, ids:
     if st:
         _check("ffn_nvfp4_moe_forward", st)
     return out
+
+
+def _row_stride(t: torch.Tensor, name: str, dtypes, m: int, cols: int) -> int:
+    """Elements between the rows of a [m, cols] CUDA tensor whose rows are contiguous (a slice of wider rows, say)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != m or t.shape[1] != cols:
+        raise ValueError(f"{name} must have shape ({m}, {cols}), got {tuple(t.shape)}")
+    ld, step = t.stride()
+    if m > 0 and (cols > 1 and step != 1 or m > 1 and ld < cols):
+        raise ValueError(f"{name} must have contiguous, non-overlapping rows")
+    return ld if m > 1 else cols  # (of one row the stride means nothing)
+
+
+_BF16 = (torch.bfloat16,)
+_VALUE_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+_VALUES = tuple(_VALUE_TYPES)
+
+
+def ffn_int8_quantize(x: torch.Tensor, codes=None, scales=None, stream=None):
+    """bf16 [m, k] (rows may be strided) -> (codes int8 [m, k], scales float32 [m]): activations by row, or a weight
+    [n, k] by output channel."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dim() != 2:
+        raise ValueError(f"x must have shape (m, k), got {tuple(x.shape)}")
+    m, k = x.shape
+    ld = _row_stride(x, "x", _BF16, m, k)
+    codes = _empty((m, k), torch.int8, x.device, stream) if codes is None else codes
+    scales = _empty((m,), torch.float32, x.device, stream) if scales is None else scales
+    _need(codes, "codes", torch.int8, (m, k))
+    _need(scales, "scales", torch.float32, (m,))
+    _check("ffn_int8_quantize", lib.ffn_int8_quantize(
+        x.data_ptr(), m, k, ld, codes.data_ptr(), scales.data_ptr(), _launch_stream(stream, x, codes, scales)))
+    return codes, scales
+
+
+def ffn_int8_linear_workspace_size(m: int, n: int, k: int) -> int:
+    out = ctypes.c_size_t()
+    _check("ffn_int8_linear_workspace_size", lib.ffn_int8_linear_workspace_size(m, n, k, ctypes.byref(out)))
+    return out.value
+
+
+def ffn_int8_workspace_size(m: int, hidden: int, inter: int) -> int:
+    out = ctypes.c_size_t()
+    _check("ffn_int8_workspace_size", lib.ffn_int8_workspace_size(m, hidden, inter, ctypes.byref(out)))
+    return out.value
+
+
+def _int8_rows(x, x_scales):
+    """m and k of bf16 rows, or of int8 codes with their scales."""
+    _need(x, "x", torch.bfloat16 if x_scales is None else torch.int8)
+    if x.dim() != 2:
+        raise ValueError(f"x must have shape (m, k), got {tuple(x.shape)}")
+    m, k = x.shape
+    if x_scales is not None:
+        _need(x_scales, "x_scales", torch.float32, (m,))
+    return m, k
+
+
+def _int8_weight(w, scales, name, n, k):
+    _need(w, name, torch.int8, None if n is None else (n, k))
+    if w.dim() != 2 or w.shape[1] != k:
+        raise ValueError(f"{name} must have shape (n, {k}), got {tuple(w.shape)}")
+    n = w.shape[0]
+    _need(scales, name + "_scales", torch.float32, (n,))
+    return n
+
+
+def ffn_int8_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, x_scales=None, bias=None, y=None,
+                    workspace=None, stream=None) -> torch.Tensor:
+    """y[m, n] = bf16((x @ w^T) * x_scales * w_scales + bias): x int8 codes with their x_scales float32 [m], or bf16
+    rows, quantised first; w int8 [n, k] with w_scales float32 [n]; bias bf16 [n] or None."""
+    m, k = _int8_rows(x, x_scales)
+    n = _int8_weight(w, w_scales, "w", None, k)
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, (n,))
+    y = _empty((m, n), torch.bfloat16, x.device, stream) if y is None else y
+    _need(y, "y", torch.bfloat16, (m, n))
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8)
+    elif x_scales is None:
+        workspace = _empty(max(ffn_int8_linear_workspace_size(m, n, k), 16), torch.uint8, x.device, stream)
+    st = lib.ffn_int8_linear(
+        x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), m, w.data_ptr(), w_scales.data_ptr(),
+        None if bias is None else bias.data_ptr(), n, k, y.data_ptr(), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel(), _launch_stream(stream, x, x_scales, w, w_scales, bias, y, workspace))
+    if st:
+        _check("ffn_int8_linear", st)
+    return y
+
+
+def ffn_int8_forward(x: torch.Tensor, gate_up: torch.Tensor, gate_up_scales: torch.Tensor, down: torch.Tensor,
+                     down_scales: torch.Tensor, x_scales=None, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """out[m, hidden] = down(silu(gate(x)) * up(x)) over int8 weights (gate_up [2 * inter, hidden], gate rows first; down
+    [hidden, inter]; scales float32 by row); x as for ffn_int8_linear."""
+    m, hidden = _int8_rows(x, x_scales)
+    n = _int8_weight(gate_up, gate_up_scales, "gate_up", None, hidden)
+    if n % 2:
+        raise ValueError(f"gate_up must have 2 * inter rows, got {n}")
+    inter = n // 2
+    _int8_weight(down, down_scales, "down", hidden, inter)
+    out = _empty((m, hidden), torch.bfloat16, x.device, stream) if out is None else out
+    _need(out, "out", torch.bfloat16, (m, hidden))
+    if workspace is None:
+        workspace = _empty(max(ffn_int8_workspace_size(m, hidden, inter), 16), torch.uint8, x.device, stream)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    st = lib.ffn_int8_forward(
+        x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), m, hidden, inter, gate_up.data_ptr(),
+        gate_up_scales.data_ptr(), down.data_ptr(), down_scales.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _launch_stream(stream, x, x_scales, gate_up, gate_up_scales, down, down_scales, out, workspace))
+    if st:
+        _check("ffn_int8_forward", st)
+    return out
+
+
+class _NormStruct(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("type", ctypes.c_int), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("offset", ctypes.c_float)]
+
+
+NORM_KINDS = {"rms": 0, "layer": 1}
+GATE_ACTIVATIONS = {"none": 0, "sigmoid": 1, "tanh": 2}
+
+
+class Norm:
+    """norm(v) = v / sqrt(mean(v^2) + eps) * (offset + weight) + bias; kind "layer": of v - mean(v).  weight and bias:
+    float32 or bfloat16 [hidden] of one type, or None.  Holds the tensors; their values are read by each call."""
+
+    def __init__(self, weight=None, bias=None, kind="rms", eps: float = 1e-6, offset: float = 0.0):
+        if kind not in NORM_KINDS:
+            raise ValueError(f"kind must be one of {', '.join(map(repr, NORM_KINDS))}, got {kind!r}")
+        given = [t for t in (weight, bias) if t is not None]
+        for name, t in (("weight", weight), ("bias", bias)):
+            if t is not None:
+                _need(t, name, t.dtype if isinstance(t, torch.Tensor) and t.dtype in _VALUE_TYPES else torch.bfloat16)
+                if t.dim() != 1 or t.shape != given[0].shape or t.dtype != given[0].dtype or t.device != given[0].device:
+                    raise ValueError("weight and bias must be vectors of one length, type and device")
+        self.weight, self.bias, self.kind, self.eps, self.offset = weight, bias, kind, eps, offset
+        self.hidden = given[0].numel() if given else None
+        self.device_index = given[0].get_device() if given else None
+        self._struct = _NormStruct(NORM_KINDS[kind], _VALUE_TYPES[given[0].dtype] if given else 0,
+                                   None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
+                                   eps, offset)
+        self._address = ctypes.addressof(self._struct)
+
+
+# struct ffn_block_norm_args
+_BLOCK_NORM = struct.Struct("@PqPPiiqqPiqPqffPPqP")
+
+
+def _norm_address(norm, name, hidden):
+    if norm is None:
+        return 0
+    if not isinstance(norm, Norm):
+        raise TypeError(f"{name} must be a Norm")
+    if norm.hidden is not None:
+        if norm.hidden != hidden:
+            raise ValueError(f"{name} has {norm.hidden} weights, the rows {hidden} values")
+        if norm.device_index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on cuda:{norm.device_index}, the current device is cuda:{torch.cuda.current_device()}")
+    return norm._address
+
+
+def ffn_block_norm(residual: torch.Tensor, y=None, post: Norm | None = None, gate=None, gate_activation="none",
+                   residual_scale: float = 1.0, branch_scale: float = 1.0, pre: Norm | None = None, quantize: bool = False,
+                   residual_out=None, store_residual: bool = True, out=None, out_scales=None, stream=None):
+    """What stands between two layers: r = residual_scale * residual + branch_scale * act(gate) * post(y), rounded to the
+    residual's type, and x = pre(r).  Returns (r, x), or with quantize (r, codes, scales) of x as ffn_int8_quantize.
+
+    residual: float32 or bfloat16 [m, hidden]; y: a layer's output, bfloat16 [m, hidden], or None (then r is the residual
+    itself); gate: float32 or bfloat16, [hidden], [m, hidden], [1, hidden], [m, 1] or [1, 1]; without `pre` x is None.
+    residual_out may be the residual, a bf16 out may be y; store_residual=False leaves r out (None) where only x is
+    wanted.  Rows of all of them may be strided."""
+    if not isinstance(residual, torch.Tensor):
+        raise TypeError("residual must be a torch.Tensor")
+    if residual.dim() != 2:
+        raise ValueError(f"residual must have shape (m, hidden), got {tuple(residual.shape)}")
+    m, hidden = residual.shape
+    r_ld = _row_stride(residual, "residual", _VALUES, m, hidden)
+    y_ld = ro_ld = out_ld = gate_row = gate_col = 0
+    if y is not None:
+        y_ld = _row_stride(y, "y", _BF16, m, hidden)
+        if residual_out is not None:
+            if not store_residual:
+                raise ValueError("residual_out is given, but store_residual is False")
+        elif store_residual:
+            residual_out = _empty((m, hidden), residual.dtype, residual.device, stream)
+        if residual_out is not None:
+            ro_ld = _row_stride(residual_out, "residual_out", (residual.dtype,), m, hidden)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs y: without it the residual does not change")
+    if gate_activation not in GATE_ACTIVATIONS:
+        raise ValueError(f"gate_activation must be one of {', '.join(map(repr, GATE_ACTIVATIONS))}, got {gate_activation!r}")
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor):
+            raise TypeError("gate must be a torch.Tensor")
+        if not gate.is_cuda:
+            raise ValueError("gate must be a CUDA tensor (the library has no CPU path)")
+        if gate.dtype not in _VALUE_TYPES:
+            raise TypeError(f"gate must be torch.float32 or torch.bfloat16, got {gate.dtype}")
+        if gate.dim() == 1:
+            gate = gate[None]
+        if gate.dim() != 2 or gate.shape[0] not in (1, m) or gate.shape[1] not in (1, hidden):
+            raise ValueError(f"gate must have shape ({m} or 1, {hidden} or 1), got {tuple(gate.shape)}")
+        gate_row = 0 if gate.shape[0] == 1 else gate.stride(0)
+        gate_col = 0 if gate.shape[1] == 1 else gate.stride(1)
+        if gate_col not in (0, 1) or gate_col and gate_row and gate_row < hidden:
+            raise ValueError("gate must have contiguous, non-overlapping rows")
+    if pre is None:
+        if quantize or out is not None or out_scales is not None:
+            raise ValueError("an output needs the norm `pre`")
+    else:
+        out = _empty((m, hidden), torch.int8 if quantize else torch.bfloat16, residual.device, stream) if out is None else out
+        if quantize:
+            out_scales = _empty((m,), torch.float32, residual.device, stream) if out_scales is None else out_scales
+            _need(out, "out", torch.int8, (m, hidden))
+            _need(out_scales, "out_scales", torch.float32, (m,))
+            out_ld = hidden
+        else:
+            if out_scales is not None:
+                raise ValueError("out_scales needs quantize")
+            out_ld = _row_stride(out, "out", _BF16, m, hidden)
+    launch = _launch_stream(stream, residual, y, gate, residual_out, out, out_scales)
+    args = _BLOCK_NORM.pack(
+        0 if y is None else y.data_ptr(), y_ld, _norm_address(post, "post", hidden), 0 if gate is None else gate.data_ptr(),
+        0 if gate is None else _VALUE_TYPES[gate.dtype], GATE_ACTIVATIONS[gate_activation], gate_row, gate_col,
+        residual.data_ptr(), _VALUE_TYPES[residual.dtype], r_ld, 0 if residual_out is None else residual_out.data_ptr(), ro_ld,
+        residual_scale, branch_scale, _norm_address(pre, "pre", hidden), 0 if out is None else out.data_ptr(), out_ld,
+        0 if out_scales is None else out_scales.data_ptr())
+    st = lib.ffn_block_norm(args, m, hidden, launch)
+    if st:
+        _check("ffn_block_norm", st)
+    if y is None:
+        residual_out = residual
+    return (residual_out, out, out_scales) if quantize else (residual_out, out)
 
 
 def ffn_nvfp4_profile_begin():
