@@ -443,9 +443,11 @@ ffn_status ffn_int8_quantize(const void* x_bf16, int64_t m, int64_t k, int64_t r
  * order, each rounded once to fp32.  m == 0 is a no-op.  Allocates nothing and
  * does not synchronise.  The workspace (ffn_int8_linear_workspace_size bytes;
  * not needed with x_scales) may be shared by calls on one stream, and its size
- * serves every smaller m.  Launched with programmatic stream serialisation:
- * weights and their scales may be read while the kernel before in the stream is
- * finishing, all else after it has completed.
+ * serves every smaller m.  Launched with programmatic stream serialisation: the
+ * weights may be read while the kernel before in the stream is finishing, all
+ * else after it has completed.  So a weight must not come from a kernel that
+ * lets the next one start early (those of this library that write weights,
+ * ffn_int8_quantize among them, do not).
  * Errors: FFN_ERR_SHAPE unless k is a positive multiple of 32 and n > 0, or for
  * buffers of more than 2^40 elements; FFN_ERR_UNSUPPORTED for k > FFN_INT8_MAX_K. */
 ffn_status ffn_int8_linear_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);

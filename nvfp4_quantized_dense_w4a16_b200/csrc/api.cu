@@ -6,6 +6,7 @@
 #include <new>
 
 #include "ffn_nvfp4.h"
+#include "int8.h"
 #include "internal.h"
 #include "moe.h"
 
@@ -665,11 +666,12 @@ ffn_status ffn_nvfp4_device_error(int* flags, int clear) {
     cudaGetLastError();
     return FFN_ERR_CUDA;
   }
-  int moe = 0, rows = 0;
+  int moe = 0, rows = 0, int8 = 0;
   cudaError_t e = ffn::read_device_error(flags, clear != 0);
   if (e == cudaSuccess) e = ffn::read_moe_device_error(&moe, clear != 0);
   if (e == cudaSuccess) e = ffn::read_rows_device_error(&rows, clear != 0);
-  *flags |= moe | rows;
+  if (e == cudaSuccess) e = ffn::read_int8_device_error(&int8, clear != 0);
+  *flags |= moe | rows | int8;
   return cuda_status(e);
 }
 

@@ -69,7 +69,7 @@ ffn_status ffn_int8_quantize(const void* x_bf16, int64_t m, int64_t k, int64_t r
   if (!aligned16(x_bf16) || row_stride % 8 || !aligned16(codes) || !aligned(scales, 4)) return FFN_ERR_ALIGNMENT;
   if (ffn_status st = ffn::moe_precheck()) return st;
   return ffn::moe_status(
-      ffn::launch_int8_quantize(x_bf16, m, k, row_stride, codes, scales, reinterpret_cast<cudaStream_t>(stream)));
+      ffn::launch_int8_quantize(x_bf16, m, k, row_stride, codes, scales, false, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 ffn_status ffn_int8_linear_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
@@ -97,7 +97,7 @@ ffn_status ffn_int8_linear(const void* x, const float* x_scales, int64_t m, cons
   if (!x_scales) {
     int8_t* xq = reinterpret_cast<int8_t*>(ws + c.xq);
     float* xs = reinterpret_cast<float*>(ws + c.xs);
-    e = ffn::launch_int8_quantize(x, m, k, k, xq, xs, s);
+    e = ffn::launch_int8_quantize(x, m, k, k, xq, xs, true, s);
     x = xq;
     x_scales = xs;
   }
@@ -136,7 +136,7 @@ ffn_status ffn_int8_forward(const void* x, const float* x_scales, int64_t m, int
   uint16_t* h = reinterpret_cast<uint16_t*>(ws + c.h);
   cudaError_t e = cudaSuccess;
   if (!x_scales) {
-    e = ffn::launch_int8_quantize(x, m, hidden, hidden, xq, xs, s);
+    e = ffn::launch_int8_quantize(x, m, hidden, hidden, xq, xs, true, s);
     x = xq;
     x_scales = xs;
   }
@@ -144,7 +144,7 @@ ffn_status ffn_int8_forward(const void* x, const float* x_scales, int64_t m, int
     e = ffn::launch_int8_product(ffn::Int8Product{static_cast<const int8_t*>(x), x_scales, m, gate_up, gate_up_scales,
                                                   nullptr, 2 * inter, hidden, h, true},
                                  s);
-  if (e == cudaSuccess) e = ffn::launch_int8_quantize(h, m, inter, inter, hq, hs, s);
+  if (e == cudaSuccess) e = ffn::launch_int8_quantize(h, m, inter, inter, hq, hs, true, s);
   if (e == cudaSuccess)
     e = ffn::launch_int8_product(ffn::Int8Product{hq, hs, m, down, down_scales, nullptr, hidden, inter,
                                                   static_cast<uint16_t*>(out), false},

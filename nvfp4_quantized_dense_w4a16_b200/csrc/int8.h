@@ -7,8 +7,9 @@
 namespace ffn {
 
 // codes and scales of bf16 rows of k columns (a multiple of 8), row i at i * stride.
+// chained: the next launch is a product of these rows.
 cudaError_t launch_int8_quantize(const void* x, int64_t m, int64_t k, int64_t stride, int8_t* codes, float* scales,
-                                 cudaStream_t s);
+                                 bool chained, cudaStream_t s);
 
 // One projection of int8 rows.  Plain: y bf16 [m, n].  With silu_mul the weight
 // holds n / 2 gate rows, then n / 2 up rows, and y is h bf16 [m, n / 2].
@@ -24,5 +25,7 @@ struct Int8Product {
   bool silu_mul;
 };
 cudaError_t launch_int8_product(const Int8Product& p, cudaStream_t s);
+// Error bits of these kernels' bounded waits, as read_device_error.
+cudaError_t read_int8_device_error(int* flags, bool clear);
 
 }  // namespace ffn

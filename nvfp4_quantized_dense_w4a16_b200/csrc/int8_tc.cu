@@ -1,0 +1,652 @@
+// Products of the 8-bit integer layers on the tensor cores (tcgen05 kind::i8,
+// 32-bit sums in tensor memory, operands streamed by TMA as rows of 128 codes).
+//
+// Many rows: a persistent pair of CTAs (cta_group::2) computes tiles of 256 rows
+// of x by up to 256 weight rows.  Per 128 codes of K each CTA loads its 128 rows
+// of x and half of the tile's weight rows (with silu_mul: CTA 0 the gate rows,
+// CTA 1 the up rows of the same columns), and one warp of CTA 0 issues the MMAs
+// of both.  Two accumulators: eight warps scale and store a tile while the next
+// one's MMAs run.
+//
+// Few rows: the weight rows are the MMA's M (a tile of 128; with silu_mul 64 gate
+// rows and the 64 up rows of the same columns), x is its N.  Bound by the stream
+// of the weights, which all SMs have to share: a cluster of CTAs cuts the K of a
+// tile into ranges, and each CTA adds a share of the others' sums, read from their
+// shared memory.  Sums are whole numbers: the cut does not change a bit.
+//
+// Weights are loaded before the kernel ahead in the stream has completed, rows
+// after it.  Every wait is bounded; on expiry a device error bit is raised, the
+// CTAs free their tensor memory and exit.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "int8.cuh"
+#include "int8.h"
+#include "launch.cuh"
+#include "moe.h"
+#include "profile.h"
+#include "sm100.cuh"
+
+namespace ffn {
+namespace {
+
+using namespace sm100;
+
+__device__ int g_int8_device_error = 0;
+
+constexpr int kChunkK = 128;  // codes of K in a stage: one 128-byte swizzled row
+
+// Instruction descriptor of kind::i8: signed 8-bit A and B (both K-major), 32-bit sums.
+__host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
+  return (2u << 4)                      // D format: s32
+         | (1u << 7)                    // A format: signed
+         | (1u << 10)                   // B format: signed
+         | ((uint32_t)(N >> 3) << 17)   // N / 8
+         | ((uint32_t)(M >> 4) << 24);  // M / 16
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The shared address of `p` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+
+__device__ __forceinline__ int4 load_cluster(uint32_t a) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+
+// Wait that ignores the abort flag (in-flight copies must land before exit).
+__device__ __forceinline__ bool drain(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > kWaitLimitCycles) {
+      atomicOr(&g_int8_device_error, 16);
+      return false;
+    }
+  return true;
+}
+
+// ------------------------------------------------------------- many rows
+
+__device__ __forceinline__ void mma_pair_s8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrive on `bar` of both CTAs once this thread's MMAs so far have completed.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// A copy into this CTA's shared memory that counts on a barrier of either CTA.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+struct PairArgs {
+  const float *xs, *ws;
+  const uint16_t* bias;
+  uint16_t* y;
+  int64_t m, cols;  // rows and columns of y
+  int kc;           // chunks of K
+  int tile_n;       // weight rows of a tile: a multiple of 32 up to 256
+  int m_tiles, n_tiles;
+};
+
+constexpr int kPairRows = 256;
+constexpr int kPairThreads = 384;
+constexpr int kPairStages = 6;
+constexpr int kPairOperand = 128 * kChunkK;              // 128 rows of x, or up to 128 weight rows
+constexpr int kPairStageBytes = 2 * kPairOperand;
+constexpr int kPairOut = kPairStages * kPairStageBytes;  // 32 rows x 32 columns of bf16 per epilogue warp
+constexpr int kPairScales = kPairOut + 8 * 2048;         // [group][tile parity][scales, biases][256]
+constexpr int kPairBar = kPairScales + 2 * 2 * 2 * 256 * 4;
+constexpr int kPairSmem = kPairBar + (2 * kPairStages + 4) * 8 + 16 + 1024;  // slack for 1024-byte alignment
+static_assert(kPairSmem <= 232448, "shared memory budget");
+
+// Tiles go by groups of this many row tiles, so that those which run at a time
+// share rows of x and of the weight in L2.
+constexpr int kPairGroup = 8;
+
+__device__ __forceinline__ void tile_place(const PairArgs& a, int t, int* mt, int* nt) {
+  const int group = t / (kPairGroup * a.n_tiles), first = group * kPairGroup;
+  const int rows = min(kPairGroup, a.m_tiles - first), in = t - first * a.n_tiles;
+  *mt = first + in % rows;
+  *nt = in / rows;
+}
+
+template <bool SILU>
+__global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
+    int8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const PairArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairBar);
+  uint64_t* empty = full + kPairStages;
+  uint64_t* accfull = empty + kPairStages;
+  uint64_t* accempty = accfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accempty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* err = &g_int8_device_error;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int first = blockIdx.x / 2, step = gridDim.x / 2, total = a.m_tiles * a.n_tiles;
+  const int half = a.tile_n / 2;  // weight rows of a CTA
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&full[s], 1);  // (CTA 0's)
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accfull[b], 1);
+      mbar_init(&accempty[b], 2 * 8);  // (CTA 0's)
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&xmap);
+    tma_prefetch_desc(&wmap);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ----------------------------------------------------------- producer
+    if (lane == 0) {
+      const int units = first < total ? (total - first + step - 1) / step * a.kc : 0;
+      const uint32_t bytes = 2 * (kPairOperand + half * kChunkK);  // of both CTAs
+      auto load = [&](int u, bool weights) {
+        const int s = u % kPairStages, c = u % a.kc;
+        int mt, nt;
+        tile_place(a, first + u / a.kc * step, &mt, &nt);
+        uint8_t* at = smem + s * kPairStageBytes;
+        const uint32_t bar = in_cta(&full[s], 0);
+        if (weights) {
+          const int64_t row = (int64_t)nt * (SILU ? half : a.tile_n) + (SILU ? rank * a.cols : rank * half);
+          tma_load_pair(at + kPairOperand, &wmap, c * kChunkK, (int)row, bar);
+        } else {
+          tma_load_pair(at, &xmap, c * kChunkK, mt * kPairRows + rank * 128, bar);
+        }
+      };
+      const int ahead = min(units, kPairStages);
+      for (int u = 0; u < ahead; ++u) {
+        if (rank == 0) mbar_arrive_expect_tx(&full[u], bytes);
+        load(u, true);
+      }
+      griddep_wait();
+      griddep_launch_dependents();
+      for (int u = 0; u < ahead; ++u) load(u, false);
+      int u = ahead;
+      for (; u < units; ++u) {
+        const int s = u % kPairStages;
+        if (!mbar_wait(&empty[s], ((u / kPairStages) - 1) & 1, abort_flag, err, 1)) break;
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+        load(u, true);
+        load(u, false);
+      }
+      if (rank == 0)  // (CTA 1 leaves after this one)
+        for (int r = max(0, u - kPairStages); r < u; ++r) drain(&full[r % kPairStages], (r / kPairStages) & 1);
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------- MMAs, CTA 0's for both
+    const uint32_t idesc = idesc_s8_s32(kPairRows, a.tile_n);
+    int u = 0, i = 0;
+    bool ok = true;
+    for (int t = first; rank == 0 && ok && t < total; t += step, ++i) {
+      const int buf = i & 1;
+      if (i >= 2) {
+        ok = mbar_wait(&accempty[buf], ((i >> 1) - 1) & 1, abort_flag, err, 2);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+      }
+      for (int c = 0; c < a.kc; ++c, ++u) {
+        const int s = u % kPairStages;
+        ok = mbar_wait(&full[s], (u / kPairStages) & 1, abort_flag, err, 2);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        const uint64_t xd = smem_desc_sw128(smem_u32(smem + s * kPairStageBytes));
+        const uint64_t wd = smem_desc_sw128(smem_u32(smem + s * kPairStageBytes + kPairOperand));
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_pair_s8(tmem + 256 * buf, xd + 2 * kk, wd + 2 * kk, idesc, (c | kk) ? 1u : 0u);
+          commit_pair(&empty[s]);
+          if (c + 1 == a.kc) commit_pair(&accfull[buf]);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp >= 4) {
+    // ----------------------------------------------------------- epilogue
+    const int g = (warp - 4) >> 2, q = warp & 3, tid = threadIdx.x & 127;
+    uint8_t* out = smem + kPairOut + (warp - 4) * 2048;
+    // 16 columns at a time; the two groups share them
+    const int outs = SILU ? half : a.tile_n, parts = outs / 16;
+    const int part0 = g ? (parts + 1) / 2 : 0, part1 = g ? parts : (parts + 1) / 2;
+    const bool wide = a.cols % 8 == 0;
+    griddep_wait();
+    int i = 0;
+    for (int t = first; t < total; t += step, ++i) {
+      int mt, nt;
+      tile_place(a, t, &mt, &nt);
+      const int buf = i & 1;
+      const int64_t row0 = (int64_t)mt * kPairRows + rank * 128 + 32 * q, col0 = (int64_t)nt * outs;
+      const float xs = row0 + lane < a.m ? a.xs[row0 + lane] : 0.0f;
+      float* sc = reinterpret_cast<float*>(smem + kPairScales) + (2 * g + buf) * 512;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = tid + 128 * h;
+        if (SILU) {
+          const int64_t col = col0 + tid;  // gate scales, then up scales
+          if (tid < half) sc[h * 256 + tid] = col < a.cols ? a.ws[h * a.cols + col] : 0.0f;
+        } else if (j < outs) {
+          const bool in = col0 + j < a.cols;
+          sc[j] = in ? a.ws[col0 + j] : 0.0f;
+          sc[256 + j] = in && a.bias ? bf16_bits_to_float(a.bias[col0 + j]) : 0.0f;
+        }
+      }
+      named_bar_sync(1 + g, 128);
+      bool ok = mbar_wait(&accfull[buf], (i >> 1) & 1, abort_flag, err, 8);
+      ok = __all_sync(0xffffffffu, ok);
+      uint32_t any;  // (the group's warps pass the same barriers)
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(any)
+          : "r"((uint32_t)ok), "r"(1 + g)
+          : "memory");
+      if (!any) break;
+      tc_fence_after();
+      const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + 256 * buf;
+      for (int p = part0; p < part1; p += 2) {
+        const int width = min(2, part1 - p) * 16;  // columns of this step
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (16 * h >= width) break;
+          const int c = 16 * (p + h);
+          uint32_t v[16], w[16];
+          tmem_ld16(lane_addr + c, v);
+          if (SILU) tmem_ld16(lane_addr + half + c, w);
+          tmem_ld_wait();
+          uint32_t o[8];
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            float r[2];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              r[z] = int8_scaled((int)v[j + z], xs, sc[c + j + z]);
+              if (SILU)
+                r[z] = int8_silu_mul(r[z], int8_scaled((int)w[j + z], xs, sc[256 + c + j + z]));
+              else if (a.bias)
+                r[z] = __fadd_rn(r[z], sc[256 + c + j + z]);
+            }
+            o[j / 2] = f32_to_bf16_bits(r[0]) | ((uint32_t)f32_to_bf16_bits(r[1]) << 16);
+          }
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+            *reinterpret_cast<uint4*>(out + lane * 64 + 16 * ((2 * h + z) ^ ((lane >> 1) & 3))) =
+                make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+        }
+        __syncwarp();
+        // four lanes store 64 bytes of a row
+        const int64_t col = col0 + 16 * p + 8 * (lane & 3);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const int r = 8 * z + (lane >> 2);
+          if (row0 + r >= a.m || 8 * (lane & 3) >= width || col >= a.cols) continue;
+          const uint4 v = *reinterpret_cast<const uint4*>(out + r * 64 + 16 * ((lane & 3) ^ ((r >> 1) & 3)));
+          uint16_t* y = a.y + (row0 + r) * a.cols + col;
+          if (wide) {
+            *reinterpret_cast<uint4*>(y) = v;
+          } else {
+            const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (col + j < a.cols) y[j] = (uint16_t)(e[j >> 1] >> (16 * (j & 1)));
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_cta(&accempty[buf], 0)) : "memory");
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may arrive on its barriers or read its rows
+  if (warp == 2) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// -------------------------------------------------------------- few rows
+
+__device__ __forceinline__ void mma_s8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+struct FewArgs {
+  const float *xs, *ws;
+  const uint16_t* bias;
+  uint16_t* y;
+  int64_t cols;
+  int m, kc;
+  int n;       // the MMA's N: rows of x, a multiple of 16
+  int stages;  // of the ring
+};
+
+constexpr int kFewThreads = 192;  // a producer, an issuer, four warps for the sums
+constexpr int kFewWeights = 128 * kChunkK;
+constexpr int kFewMaxStages = 8;
+constexpr int kFewRing = 100 * 1024;  // two CTAs an SM
+constexpr int kFewBar = 0;            // the barriers stand in front of the ring
+constexpr int kFewSmem = 1024 + kFewRing + 1024;
+
+template <bool SILU>
+__global__ void __launch_bounds__(kFewThreads)
+    int8_few_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const FewArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kFewBar);
+  uint64_t* empty = full + kFewMaxStages;
+  uint64_t* done = empty + kFewMaxStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint8_t* ring = smem + 1024;
+  int* err = &g_int8_device_error;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t splits;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(splits));
+  const int rank = (int)cluster_rank();
+  const int64_t tile = blockIdx.x / splits;
+  const int c0 = (int)((int64_t)a.kc * rank / splits), c1 = (int)((int64_t)a.kc * (rank + 1) / splits), units = c1 - c0;
+  const int stage_bytes = kFewWeights + a.n * kChunkK;
+  const uint32_t columns = a.n <= 32 ? 32 : a.n <= 64 ? 64 : 128;  // of tensor memory
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, columns);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      auto load_weights = [&](int u) {
+        const int s = u % a.stages, k = (c0 + u) * kChunkK;
+        uint8_t* at = ring + s * stage_bytes;
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        if (SILU) {
+          tma_load_2d(at, &wmap, k, (int)(tile * 64), &full[s]);
+          tma_load_2d(at + kFewWeights / 2, &wmap, k, (int)(a.cols + tile * 64), &full[s]);
+        } else {
+          tma_load_2d(at, &wmap, k, (int)(tile * 128), &full[s]);
+        }
+      };
+      auto load_rows = [&](int u) {
+        const int s = u % a.stages;
+        tma_load_2d(ring + s * stage_bytes + kFewWeights, &xmap, (c0 + u) * kChunkK, 0, &full[s]);
+      };
+      const int ahead = min(units, a.stages);
+      for (int u = 0; u < ahead; ++u) load_weights(u);
+      griddep_wait();
+      griddep_launch_dependents();
+      for (int u = 0; u < ahead; ++u) load_rows(u);
+      int u = ahead;
+      for (; u < units; ++u) {
+        if (!mbar_wait(&empty[u % a.stages], ((u / a.stages) - 1) & 1, abort_flag, err, 1)) break;
+        load_weights(u);
+        load_rows(u);
+      }
+      for (int r = max(0, u - a.stages); r < u; ++r) drain(&full[r % a.stages], (r / a.stages) & 1);
+    }
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_s8_s32(128, a.n);
+    for (int u = 0; u < units; ++u) {
+      const int s = u % a.stages;
+      ok = mbar_wait(&full[s], (u / a.stages) & 1, abort_flag, err, 2);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      tc_fence_after();
+      const uint64_t wd = smem_desc_sw128(smem_u32(ring + s * stage_bytes));
+      const uint64_t xd = smem_desc_sw128(smem_u32(ring + s * stage_bytes + kFewWeights));
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) mma_s8(tmem, wd + 2 * kk, xd + 2 * kk, idesc, (u | kk) ? 1u : 0u);
+        mma_commit(&empty[s]);
+        if (u + 1 == units) mma_commit(done);
+      }
+      __syncwarp();
+    }
+  } else {
+    griddep_wait();
+    ok = mbar_wait(done, 0, abort_flag, err, 8);
+    ok = __all_sync(0xffffffffu, ok);
+  }
+  // From here on no copy and no MMA is in flight: the ring holds the sums, [row of x][128].
+  __syncwarp();
+  ok = __syncthreads_and(ok) != 0;
+  int* sums = reinterpret_cast<int*>(ring);
+  if (ok && warp >= 2) {
+    tc_fence_after();
+    const int q = warp & 3;
+    for (int c = 0; c < a.n; c += 16) {
+      uint32_t v[16];
+      tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sums[(c + j) * 128 + 32 * q + lane] = (int)v[j];
+    }
+    tc_fence_before();
+  }
+  // A CTA whose wait expired has no sums: nobody of its cluster stores.
+  if (threadIdx.x == 0) *abort_flag = ok ? 0 : 1;
+  __syncthreads();
+  cluster_sync();
+  bool all = true;
+  for (uint32_t r = 0; r < splits; ++r) {
+    int bad;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(bad) : "r"(in_cta(const_cast<int*>(abort_flag), r)));
+    all = all && bad == 0;
+  }
+  if (all && warp >= 2) {
+    // Rows of x by CTA; a warp has 128 sums of a row, four a lane.
+    const int wq = warp - 2;
+    const int64_t col = tile * (SILU ? 64 : 128) + 4 * (SILU ? lane & 15 : lane);
+    float s0[4], s1[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool in = col + j < a.cols;
+      s0[j] = in ? a.ws[col + j] : 0.0f;
+      s1[j] = !in ? 0.0f : SILU ? a.ws[a.cols + col + j] : a.bias ? bf16_bits_to_float(a.bias[col + j]) : 0.0f;
+    }
+    const int per = SILU ? 2 : 1;  // rows of a warp at a time
+    for (int i = (rank * 4 + wq) * per + (SILU ? lane >> 4 : 0); i < a.m; i += (int)splits * 4 * per) {
+      int4 g = make_int4(0, 0, 0, 0), u = g;
+      const int at = i * 128 + 4 * (SILU ? lane & 15 : lane);
+      for (uint32_t r = 0; r < splits; ++r) {
+        const uint32_t from = in_cta(sums + at, r);
+        const int4 p = load_cluster(from);
+        g.x += p.x, g.y += p.y, g.z += p.z, g.w += p.w;
+        if (SILU) {
+          const int4 p2 = load_cluster(from + 64 * 4);
+          u.x += p2.x, u.y += p2.y, u.z += p2.z, u.w += p2.w;
+        }
+      }
+      const float xs = a.xs[i];
+      const int gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
+      uint16_t b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v = int8_scaled(gs[j], xs, s0[j]);
+        if (SILU)
+          v = int8_silu_mul(v, int8_scaled(us[j], xs, s1[j]));
+        else if (a.bias)
+          v = __fadd_rn(v, s1[j]);
+        b[j] = f32_to_bf16_bits(v);
+      }
+      uint16_t* y = a.y + (int64_t)i * a.cols + col;
+      if (a.cols % 4 == 0) {
+        if (col < a.cols)
+          *reinterpret_cast<uint2*>(y) = make_uint2(b[0] | ((uint32_t)b[1] << 16), b[2] | ((uint32_t)b[3] << 16));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (col + j < a.cols) y[j] = b[j];
+      }
+    }
+  }
+  cluster_sync();  // no CTA leaves while another reads its sums
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, columns);
+  }
+}
+
+// ----------------------------------------------------------------- host
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// Rows of k codes, 128 codes of box_rows rows at a time.
+bool encode_rows(CUtensorMap* map, const void* p, int64_t rows, int64_t k, int box_rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)k};
+  cuuint32_t box[2] = {kChunkK, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <bool SILU>
+cudaError_t launch_pair(const Int8Product& p, cudaStream_t s) {
+  const int64_t cols = SILU ? p.n / 2 : p.n;
+  const int clusters = device_sms() / 2;
+  PairArgs a{p.xs, p.ws, p.bias, p.y, p.m, cols, (int)ceil_div(p.k, kChunkK), 256, (int)ceil_div(p.m, kPairRows), 0};
+  // The widest tile, or one of fewer columns that leaves fewer pairs of SMs idle.
+  int64_t best = INT64_MAX;
+  for (int n = 256; n >= 64; n -= 32) {
+    const int64_t waves = ceil_div(a.m_tiles * ceil_div(cols, SILU ? n / 2 : n), clusters);
+    const int64_t cost = waves * (a.kc * std::max(2 * n, 220 + n) + 1500);
+    if (cost < best) best = cost, a.tile_n = n;
+  }
+  a.n_tiles = (int)ceil_div(cols, SILU ? a.tile_n / 2 : a.tile_n);
+  CUtensorMap xmap, wmap;
+  if (!encode_rows(&xmap, p.x, p.m, p.k, 128) || !encode_rows(&wmap, p.w, p.n, p.k, a.tile_n / 2)) return cudaErrorInvalidValue;
+  auto kern = int8_pair_kernel<SILU>;
+  // set on every launch: the attribute belongs to the current device's context
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+  return launch_pdl(kern, dim3((unsigned)(2 * (tiles < clusters ? tiles : clusters))), dim3(kPairThreads), kPairSmem, s, xmap,
+                    wmap, a);
+}
+
+template <bool SILU>
+cudaError_t launch_few(const Int8Product& p, cudaStream_t s) {
+  const int64_t cols = SILU ? p.n / 2 : p.n, tiles = ceil_div(cols, SILU ? 64 : 128);
+  FewArgs a{p.xs, p.ws, p.bias, p.y, cols, (int)p.m, (int)ceil_div(p.k, kChunkK), (int)ceil_div(p.m, 16) * 16, 0};
+  a.stages = std::min(kFewMaxStages, kFewRing / (kFewWeights + a.n * kChunkK));
+  // as many CTAs as are resident at a time, two an SM
+  const int64_t want = 2 * device_sms() / tiles, most = a.kc < 8 ? a.kc : 8;
+  const unsigned splits = (unsigned)(want < 1 ? 1 : want < most ? want : most);
+  CUtensorMap xmap, wmap;
+  if (!encode_rows(&xmap, p.x, p.m, p.k, a.n) || !encode_rows(&wmap, p.w, p.n, p.k, SILU ? 64 : 128)) return cudaErrorInvalidValue;
+  auto kern = int8_few_kernel<SILU>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl_clusters(kern, dim3((unsigned)(tiles * splits)), splits, dim3(kFewThreads), kFewSmem, s, xmap, wmap, a);
+}
+
+constexpr int64_t kFewRows = 128;
+
+}  // namespace
+
+cudaError_t launch_int8_product(const Int8Product& p, cudaStream_t s) {
+  ProfScope prof(s, p.silu_mul ? "int8_gate_up" : "int8_product");
+  if (p.m <= kFewRows) return p.silu_mul ? launch_few<true>(p, s) : launch_few<false>(p, s);
+  return p.silu_mul ? launch_pair<true>(p, s) : launch_pair<false>(p, s);
+}
+
+cudaError_t read_int8_device_error(int* flags, bool clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(flags, g_int8_device_error, sizeof(int));
+  const int zero = 0;
+  if (e == cudaSuccess && clear) e = cudaMemcpyToSymbol(g_int8_device_error, &zero, sizeof(int));
+  return e;
+}
+
+}  // namespace ffn
