@@ -195,36 +195,50 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
   if (warp == 0) {
     // ----------------------------------------------------------- producer
     if (lane == 0) {
-      const int units = first < total ? (total - first + step - 1) / step * a.kc : 0;
+      // What to load goes by two cursors, of the weights and of the rows; places of
+      // tiles cost divisions, which a cursor pays once a tile (each unit's own took
+      // 850 cycles of the 512 that its MMAs take).
       const uint32_t bytes = 2 * (kPairOperand + half * kChunkK);  // of both CTAs
-      auto load = [&](int u, bool weights) {
-        const int s = u % kPairStages, c = u % a.kc;
-        int mt, nt;
-        tile_place(a, first + u / a.kc * step, &mt, &nt);
-        uint8_t* at = smem + s * kPairStageBytes;
-        const uint32_t bar = in_cta(&full[s], 0);
-        if (weights) {
-          const int64_t row = (int64_t)nt * (SILU ? half : a.tile_n) + (SILU ? rank * a.cols : rank * half);
-          tma_load_pair(at + kPairOperand, &wmap, c * kChunkK, (int)row, bar);
-        } else {
-          tma_load_pair(at, &xmap, c * kChunkK, mt * kPairRows + rank * 128, bar);
+      const uint32_t bars = in_cta(full, 0);
+      struct Cursor {
+        int t, c = 0, s = 0, row = 0;
+        bool weights;
+        __device__ __forceinline__ void place(const PairArgs& a, int half, int rank) {
+          int mt, nt;
+          tile_place(a, t, &mt, &nt);
+          row = !weights ? mt * kPairRows + rank * 128 : SILU ? (int)(nt * half + rank * a.cols) : nt * a.tile_n + rank * half;
+        }
+        __device__ __forceinline__ void next(const PairArgs& a, int step, int total, int half, int rank) {
+          if (++s == kPairStages) s = 0;
+          if (++c < a.kc) return;
+          c = 0;
+          t += step;
+          if (t < total) place(a, half, rank);
         }
       };
-      const int ahead = min(units, kPairStages);
-      for (int u = 0; u < ahead; ++u) {
-        if (rank == 0) mbar_arrive_expect_tx(&full[u], bytes);
-        load(u, true);
-      }
+      Cursor w{first}, x{first};
+      w.weights = true, x.weights = false;
+      if (first < total) w.place(a, half, rank), x.place(a, half, rank);
+      auto load_weights = [&] {
+        if (rank == 0) mbar_arrive_expect_tx(&full[w.s], bytes);
+        tma_load_pair(smem + w.s * kPairStageBytes + kPairOperand, &wmap, w.c * kChunkK, w.row, bars + 8 * w.s);
+        w.next(a, step, total, half, rank);
+      };
+      auto load_rows = [&] {
+        tma_load_pair(smem + x.s * kPairStageBytes, &xmap, x.c * kChunkK, x.row, bars + 8 * x.s);
+        x.next(a, step, total, half, rank);
+      };
+      int ahead = 0, u = 0;
+      for (; ahead < kPairStages && w.t < total; ++ahead) load_weights();
       griddep_wait();
       griddep_launch_dependents();
-      for (int u = 0; u < ahead; ++u) load(u, false);
-      int u = ahead;
-      for (; u < units; ++u) {
-        const int s = u % kPairStages;
-        if (!mbar_wait(&empty[s], ((u / kPairStages) - 1) & 1, abort_flag, err, 1)) break;
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-        load(u, true);
-        load(u, false);
+      for (; u < ahead; ++u) load_rows();
+      uint32_t parity = 0;  // of the stage's last use
+      for (; w.t < total; ++u) {
+        if (!mbar_wait(&empty[w.s], parity, abort_flag, err, 1)) break;
+        if (w.s == kPairStages - 1) parity ^= 1;
+        load_weights();
+        load_rows();
       }
       if (rank == 0)  // (CTA 1 leaves after this one)
         for (int r = max(0, u - kPairStages); r < u; ++r) drain(&full[r % kPairStages], (r / kPairStages) & 1);
@@ -232,7 +246,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     // --------------------------------------------- MMAs, CTA 0's for both
     const uint32_t idesc = idesc_s8_s32(kPairRows, a.tile_n);
-    int u = 0, i = 0;
+    int s = 0, i = 0;
+    uint32_t parity = 0;
     bool ok = true;
     for (int t = first; rank == 0 && ok && t < total; t += step, ++i) {
       const int buf = i & 1;
@@ -241,9 +256,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
       }
-      for (int c = 0; c < a.kc; ++c, ++u) {
-        const int s = u % kPairStages;
-        ok = mbar_wait(&full[s], (u / kPairStages) & 1, abort_flag, err, 2);
+      for (int c = 0; c < a.kc; ++c) {
+        ok = mbar_wait(&full[s], parity, abort_flag, err, 2);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         const uint64_t xd = smem_desc_sw128(smem_u32(smem + s * kPairStageBytes));
@@ -255,6 +269,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
           if (c + 1 == a.kc) commit_pair(&accfull[buf]);
         }
         __syncwarp();
+        if (++s == kPairStages) s = 0, parity ^= 1;
       }
     }
   } else if (warp >= 4) {
