@@ -2,12 +2,23 @@
 // layer, gate and residual, the norm before the next layer and, if asked, its
 // quantisation to int8 (ffn_block_norm).
 //
-// A row stays in registers from its loads to its stores: a warp holds a short
-// row, a CTA a longer one.  Each norm is then one sum over the row (two for a
-// layer norm: the mean, and the squares of what differs from it).  It is bound by
-// its memory traffic.
+// A row stays in registers from its first norm to its stores: a warp holds a short
+// row, a CTA a longer one, some warps of a CTA one of many.  Each norm is then one
+// sum over the row (two for a layer norm: the mean, and the squares of what differs
+// from it).
+//
+// Few rows are a matter of latency: all loads of a row are under way before its first
+// sum (one row of 4096, both norms: 5.2 -> 3.8 us in a graph).  Many are bound by their
+// memory traffic if the instructions allow: 4096 rows of 5120, fp32 residual, both
+// norms, a gate for each channel (252 MB) take 47 us, 5.3 TB/s, 81% of the measured copy
+// rate; 16384 rows of 2048 with tanh gates of their own (336 MB) 69 us, 74%.  With a CTA
+// a row and plain loads those took 142 and 177 us (one or two rows under way in an SM,
+// 88 instructions a value); rows prefetched into a ring 93 and 139; 32 values a thread
+// and packed fp32 arithmetic 59 and 79; groups of one CTA that share the columns'
+// coefficients 47 and 77; the hardware's exponential and quotient in tanh 69.
 #include "ffn_nvfp4.h"
 #include "int8.cuh"
+#include "int8.h"
 #include "launch.cuh"
 #include "moe.h"
 #include "profile.h"
@@ -17,6 +28,8 @@ namespace ffn {
 namespace {
 
 using namespace sm100;
+
+__device__ int g_norm_device_error = 0;
 
 struct NormArgs {
   const void *weight, *bias;
@@ -75,6 +88,37 @@ __device__ __forceinline__ void load_any(const void* p, bool bf16, int64_t at, f
     load_f32<V>(static_cast<const float*>(p) + at, o);
 }
 
+// The same in two steps, so that a load can stand far before its use: the words as
+// they are, and their values.  WIDE: they may be fp32, else they are bf16.
+template <int V, bool WIDE>
+struct Raw {
+  static constexpr int kWords = V == 1 ? 1 : WIDE ? V : V / 2;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void* p, bool bf16, int64_t at) {
+    if (V == 1) {
+      w[0] = !WIDE || bf16 ? static_cast<const uint16_t*>(p)[at] : static_cast<const uint32_t*>(p)[at];
+    } else if (!WIDE || bf16) {
+      const uint4 t = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+      w[0] = t.x, w[1 % kWords] = t.y, w[2 % kWords] = t.z, w[3 % kWords] = t.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const uint4 t = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at)[i];
+        w[(4 * i) % kWords] = t.x, w[(4 * i + 1) % kWords] = t.y, w[(4 * i + 2) % kWords] = t.z, w[(4 * i + 3) % kWords] = t.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void get(bool bf16, float (&o)[V]) const {
+    if (WIDE && !bf16) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = __uint_as_float(w[i % kWords]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = __uint_as_float(V == 1 || i % 2 == 0 ? w[i / 2] << 16 : w[i / 2] & 0xffff0000u);
+    }
+  }
+};
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
 }
@@ -88,9 +132,14 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, const float (&v)[V]) {
     *p = f32_to_bf16_bits(v[0]);
 }
 
+__device__ __forceinline__ float from_bits(uint32_t w, float) { return __uint_as_float(w); }
+__device__ __forceinline__ uint32_t from_bits(uint32_t w, uint32_t) { return w; }
+__device__ __forceinline__ uint32_t to_bits(float v) { return __float_as_uint(v); }
+__device__ __forceinline__ uint32_t to_bits(uint32_t v) { return v; }
+
 // Sums and maxima over the threads that hold a row: a warp, or the CTA, whose
-// warps leave their parts in one of two sets of words in turn, so that one
-// barrier is enough.
+// warps leave their parts in one of two sets of 32 words in turn, so that one
+// barrier is enough.  Words behind the last warp's are zeros.
 template <bool WARP>
 struct Row {
   uint32_t* parts;
@@ -100,12 +149,15 @@ struct Row {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
     if (WARP) return v;
-    T* p = reinterpret_cast<T*>(parts + 32 * turn);
+    uint32_t* p = parts + 32 * turn;
     turn ^= 1;
-    if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = v;
+    if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = to_bits(v);
     __syncthreads();
-    v = p[0];
-    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) v = f(v, p[w]);
+    v = T(0);
+    for (int w = 0; w < (int)(blockDim.x >> 5); w += 4) {
+      const uint4 t = *reinterpret_cast<const uint4*>(p + w);
+      v = f(v, f(f(from_bits(t.x, v), from_bits(t.y, v)), f(from_bits(t.z, v), from_bits(t.w, v))));
+    }
     return v;
   }
   __device__ __forceinline__ float sum(float v) {
@@ -116,143 +168,647 @@ struct Row {
   }
 };
 
-// v = norm(v) of a row's N sets of V values, set i of this thread at column at(i).
-// The squares of values beyond 2^64 would pass fp32's range: such a row is
-// scaled by 2^-75 and gone over once more.
+// A norm of a row's N sets of V values, set i of this thread at column at(i), is
+// v * factor + shift before its weight and bias.
+struct NormFactors {
+  float factor, shift;
+};
+
 template <bool WARP, int V, int N, typename At>
-__device__ __forceinline__ void norm_row(Row<WARP>& row, const NormArgs& a, int hidden, float (&v)[N][V], At at) {
-  const float share = 1.0f / (float)hidden;
-  float c = 1.0f, mean, squares;
-  for (;;) {
-    mean = 0.0f;
-    if (a.layer) {
-      float s = 0.0f;
+__device__ __forceinline__ float row_squares(Row<WARP>& row, bool layer, int hidden, const float (&v)[N][V], At at, float* mean) {
+  *mean = 0.0f;
+  float s = 0.0f;
+  if (layer) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (at(i) < hidden)
+    for (int i = 0; i < N; ++i)
+      if (at(i) < hidden)
 #pragma unroll
-          for (int j = 0; j < V; ++j) s = fmaf(v[i][j], c, s);
-      mean = row.sum(s) * share;
-    }
-    float s = 0.0f;
+        for (int j = 0; j < V; ++j) s += v[i][j];
+    *mean = row.sum(s) * (1.0f / (float)hidden);
+    s = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (at(i) < hidden)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float d = fmaf(v[i][j], c, -mean);
+          const float d = v[i][j] - *mean;
           s = fmaf(d, d, s);
         }
-    squares = row.sum(s);
-    if (squares < __uint_as_float(0x7f800000u) || c != 1.0f) break;
-    c = 2.6469780e-23f;  // 2^-75
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (at(i) < hidden)
+#pragma unroll
+        for (int j = 0; j < V; ++j) s = fmaf(v[i][j], v[i][j], s);
   }
-  const float inv = rsqrtf(fmaf(squares, share, a.eps * (c * c)));
+  return row.sum(s);
+}
+
+// The squares of values beyond 2^64 would pass fp32's range: such a row is scaled
+// by 2^-75 and summed once more.
+template <bool WARP, int V, int N, typename At>
+__device__ __forceinline__ NormFactors norm_factors(Row<WARP>& row, const NormArgs& a, int hidden, float (&v)[N][V], At at) {
+  const float share = 1.0f / (float)hidden;
+  float mean, eps = a.eps;
+  float squares = row_squares<WARP, V, N>(row, a.layer, hidden, v, at, &mean);
+  if (!(squares < __uint_as_float(0x7f800000u))) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[i][j] *= 2.6469780e-23f;  // 2^-75
+    eps = 0.0f;  // (nothing beside the squares)
+    squares = row_squares<WARP, V, N>(row, a.layer, hidden, v, at, &mean);
+  }
+  const float factor = rsqrtf(fmaf(squares, share, eps));
+  return NormFactors{factor, -mean * factor};
+}
+
+// A norm's weights (and biases) at this thread's columns, loaded before the sums that they follow.
+template <int V, int N, bool WIDE>
+struct Weights {
+  Raw<V, WIDE> weight[N], bias[N];
+  template <typename At>
+  __device__ __forceinline__ void load(const NormArgs& a, int hidden, At at) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (at(i) < hidden) {
+        if (a.weight) weight[i].load(a.weight, a.bf16, at(i));
+        if (a.bias) bias[i].load(a.bias, a.bf16, at(i));
+      }
+  }
+  __device__ __forceinline__ void apply(const NormArgs& a, const NormFactors& f, int i, float (&v)[V]) const {
+    float t[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = fmaf(v[j], f.factor, f.shift);
+    if (a.weight) {
+      weight[i].get(a.bf16, t);
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] *= a.offset + t[j];
+    }
+    if (a.bias) {
+      bias[i].get(a.bf16, t);
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] += t[j];
+    }
+  }
+};
+
+// tanh by its power series up to 1/2 (the first term left out is below 2^-26 of it) and by
+// 1 - 2 / (exp(2 |g|) + 1) from there, where little cancels.
+__device__ __forceinline__ float tanh_fast(float g) {
+  const float a = fabsf(g), x = g * g;
+  float s = fmaf(x, -929569.0f / 638512875.0f, 21844.0f / 6081075.0f);
+  s = fmaf(x, s, -1382.0f / 155925.0f);
+  s = fmaf(x, s, 62.0f / 2835.0f);
+  s = fmaf(x, s, -17.0f / 315.0f);
+  s = fmaf(x, s, 2.0f / 15.0f);
+  s = fmaf(x, s, -1.0f / 3.0f);
+  const float small = fmaf(g * x, s, g);
+  const float large = copysignf(fmaf(-2.0f, rcp_approx(exp_approx(2.0f * a) + 1.0f), 1.0f), g);
+  return a < 0.5f ? small : large;
+}
+
+__device__ __forceinline__ float gate_value(float g, int activation) {
+  if (activation == FFN_GATE_SIGMOID) return rcp_approx(1.0f + expf(-g));
+  if (activation == FFN_GATE_TANH) return tanh_fast(g);
+  return g;
+}
+
+// The new residual of row r from v, the values of y, stored and left in v: each N sets of
+// V values at columns at(i), the residual's and (with gate_cols) the gates' by load_res and load_gate.
+template <bool R, bool WARP, int V, int N, bool WIDE, typename LoadRes, typename LoadGate, typename At>
+__device__ __forceinline__ void residual_row(Row<WARP>& row, const BlockArgs& a, int64_t r, float (&v)[N][V], LoadRes load_res,
+                                             LoadGate load_gate, At at) {
+  if (!a.y) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (at(i) < a.hidden) load_res(i, v[i]);
+    return;
+  }
+  NormFactors f = {};
+  Weights<V, N, WIDE> w;
+  if (a.post.on) {
+    w.load(a.post, a.hidden, at);
+    f = norm_factors<WARP, V, N>(row, a.post, a.hidden, v, at);
+  }
+  float scale = a.branch_scale;
+  if (a.gate && !a.gate_cols) {
+    float t[1];
+    load_any<1>(a.gate, a.gate_bf16, r * a.gate_row_stride, t);
+    scale *= gate_value(t[0], a.gate_activation);
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    if (at(i) < hidden) {
-      float w[V], b[V];
-      if (a.weight) load_any<V>(a.weight, a.bf16, at(i), w);
-      if (a.bias) load_any<V>(a.bias, a.bf16, at(i), b);
+    if (at(i) < a.hidden) {
+      float t[V];
+      if (a.post.on) w.apply(a.post, f, i, v[i]);
+      if (a.gate && a.gate_cols) {
+        load_gate(i, t);
+        if (a.gate_activation != FFN_GATE_NONE)
+#pragma unroll
+          for (int j = 0; j < V; ++j) t[j] = gate_value(t[j], a.gate_activation);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] *= t[j];
+      }
+      load_res(i, t);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        float t = fmaf(v[i][j], c, -mean) * inv;
-        if (a.weight) t *= a.offset + w[j];
-        if (a.bias) t += b[j];
-        v[i][j] = t;
+        const float x = fmaf(a.residual_scale, t[j], scale * v[i][j]);
+        v[i][j] = R ? bf16_round(x) : x;
+      }
+      if (a.residual_out) {
+        if (R) {
+          store_bf16<V>(static_cast<uint16_t*>(a.residual_out) + r * a.residual_out_stride + at(i), v[i]);
+        } else {
+          float* o = static_cast<float*>(a.residual_out) + r * a.residual_out_stride + at(i);
+          if (V == 8) {
+#pragma unroll
+            for (int q = 0; q < V / 4; ++q)
+              reinterpret_cast<float4*>(o)[q] =
+                  make_float4(v[i][(4 * q) % V], v[i][(4 * q + 1) % V], v[i][(4 * q + 2) % V], v[i][(4 * q + 3) % V]);
+          } else {
+            *o = v[i][0];
+          }
+        }
       }
     }
 }
 
-__device__ __forceinline__ float gate_value(float g, int activation) {
-  if (activation == FFN_GATE_SIGMOID) return 1.0f / (1.0f + expf(-g));
-  if (activation == FFN_GATE_TANH) return tanhf(g);
-  return g;
+// The norm of the new residual, and its stores.
+template <bool WARP, int V, int N, bool WIDE, typename At>
+__device__ __forceinline__ void output_row(Row<WARP>& row, const BlockArgs& a, int64_t r, int mine, float (&res)[N][V], At at) {
+  if (!a.pre.on) return;
+  Weights<V, N, WIDE> w;
+  w.load(a.pre, a.hidden, at);
+  const NormFactors f = norm_factors<WARP, V, N>(row, a.pre, a.hidden, res, at);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (at(i) < a.hidden) w.apply(a.pre, f, i, res[i]);
+  if (!a.out_scales) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (at(i) < a.hidden) store_bf16<V>(static_cast<uint16_t*>(a.out) + r * a.out_stride + at(i), res[i]);
+    return;
+  }
+  // The codes are those of the row as it would be stored in bf16.
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (at(i) < a.hidden)
+#pragma unroll
+      for (int j = 0; j < V; ++j) top = max(top, (uint32_t)(f32_to_bf16_bits(res[i][j]) & 0x7fffu));
+  const Int8Row q(row.max(top));
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (at(i) < a.hidden) {
+      int8_t* o = static_cast<int8_t*>(a.out) + r * a.out_stride + at(i);
+      if (V == 8)
+        *reinterpret_cast<uint2*>(o) =
+            int8_encode8(q, make_uint4(pack_bf16(res[i][0], res[i][1 % V]), pack_bf16(res[i][2 % V], res[i][3 % V]),
+                                       pack_bf16(res[i][4 % V], res[i][5 % V]), pack_bf16(res[i][6 % V], res[i][7 % V])));
+      else
+        *o = (int8_t)q.code(bf16_round(res[i][0]));
+    }
+  if (mine == 0) a.out_scales[r] = q.scale;
 }
 
 // R: the residual is bf16; WARP: a warp for each row, else the CTA; V: values of an
 // access (8, or 1 where a tensor's rows are not whole 16 bytes); N: accesses a thread.
 template <bool R, bool WARP, int V, int N, int THREADS>
-__global__ void __launch_bounds__(THREADS) block_norm_kernel(const BlockArgs a) {
-  __shared__ uint32_t parts[64];
+__global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const BlockArgs a) {
+  __shared__ __align__(16) uint32_t parts[64];
   Row<WARP> row{parts};
   const int threads = WARP ? 32 : blockDim.x, mine = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int per_cta = WARP ? blockDim.x >> 5 : 1;
   auto at = [&](int i) { return V * (mine + i * threads); };
+  if (!WARP) {
+    if (threadIdx.x < 64) parts[threadIdx.x] = 0;
+    if (blockDim.x < 64 && threadIdx.x < 32) parts[threadIdx.x + 32] = 0;
+    __syncthreads();
+  }
   griddep_wait();
   griddep_launch_dependents();
   for (int64_t r = blockIdx.x * (int64_t)per_cta + (WARP ? threadIdx.x >> 5 : 0); r < a.m;
        r += (int64_t)gridDim.x * per_cta) {
-    float res[N][V], z[N][V];
+    // all loads first: a row's latency counts here
+    float v[N][V];
+    Raw<V, !R> res[N];
+    Raw<V, true> g[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (at(i) < a.hidden) {
-        if (a.y) load_bf16<V>(a.y + r * a.y_stride + at(i), z[i]);
-        load_any<V>(a.residual, R, r * a.residual_stride + at(i), res[i]);
+        if (a.y) load_bf16<V>(a.y + r * a.y_stride + at(i), v[i]);
+        res[i].load(a.residual, R, r * a.residual_stride + at(i));
+        if (a.gate && a.gate_cols) g[i].load(a.gate, a.gate_bf16, r * a.gate_row_stride + at(i));
       }
+    residual_row<R, WARP, V, N, true>(
+        row, a, r, v, [&](int i, float(&t)[V]) { res[i].get(R, t); }, [&](int i, float(&t)[V]) { g[i].get(a.gate_bf16, t); }, at);
+    output_row<WARP, V, N, true>(row, a, r, mine, v, at);
+  }
+}
+
+// ------------------------------------------------- many rows of whole 16 bytes
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float2 v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 of_pair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_of(a)), "l"(pair_of(b)), "l"(pair_of(c)));
+  return of_pair(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_of(a)), "l"(pair_of(b)));
+  return of_pair(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_of(a)), "l"(pair_of(b)));
+  return of_pair(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// U (8 or 4) consecutive values in pairs.
+template <int U>
+__device__ __forceinline__ void load_u(const void* p, bool bf16, int64_t at, float2 (&o)[U / 2]) {
+  if (bf16) {
+    uint32_t w[U / 2];
+    if (U == 8) {
+      const uint4 t = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+      w[0] = t.x, w[1] = t.y, w[2 % (U / 2)] = t.z, w[3 % (U / 2)] = t.w;
+    } else {
+      const uint2 t = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+      w[0] = t.x, w[1] = t.y;
+    }
+#pragma unroll
+    for (int j = 0; j < U / 2; ++j) o[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+  } else {
+#pragma unroll
+    for (int j = 0; j < U / 4; ++j) {
+      const float4 t = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at)[j];
+      o[2 * j] = make_float2(t.x, t.y), o[2 * j + 1] = make_float2(t.z, t.w);
+    }
+  }
+}
+template <int U>
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[U / 2]) {
+  if (U == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2 % (U / 2)], w[3 % (U / 2)]);
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+// tanh_fast of two values.
+__device__ __forceinline__ float2 tanh2(float2 g) {
+  const float2 x = mul2(g, g);
+  float2 s = fma2(x, both(-929569.0f / 638512875.0f), both(21844.0f / 6081075.0f));
+  s = fma2(x, s, both(-1382.0f / 155925.0f));
+  s = fma2(x, s, both(62.0f / 2835.0f));
+  s = fma2(x, s, both(-17.0f / 315.0f));
+  s = fma2(x, s, both(2.0f / 15.0f));
+  s = fma2(x, s, both(-1.0f / 3.0f));
+  const float2 small = fma2(mul2(g, x), s, g);
+  const float2 e = add2(make_float2(exp_approx(2.0f * fabsf(g.x)), exp_approx(2.0f * fabsf(g.y))), both(1.0f));
+  const float2 large = fma2(both(-2.0f), make_float2(rcp_approx(e.x), rcp_approx(e.y)), both(1.0f));
+  return make_float2(fabsf(g.x) < 0.5f ? small.x : copysignf(large.x, g.x), fabsf(g.y) < 0.5f ? small.y : copysignf(large.y, g.y));
+}
+template <int U>
+__device__ __forceinline__ void gate_values(float2 (&g)[U / 2], int activation) {
+  if (activation == FFN_GATE_TANH) {
+#pragma unroll
+    for (int j = 0; j < U / 2; ++j) g[j] = tanh2(g[j]);
+  } else if (activation == FFN_GATE_SIGMOID) {
+#pragma unroll
+    for (int j = 0; j < U / 2; ++j) g[j] = make_float2(gate_value(g[j].x, FFN_GATE_SIGMOID), gate_value(g[j].y, FFN_GATE_SIGMOID));
+  }
+}
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// The threads of a CTA that hold a row: some of its warps, with a named barrier.
+struct Group {
+  uint32_t* parts;  // two sets of 16 words, zeros behind the last warp's
+  int id, threads, warp;
+  int turn = 0;
+  __device__ __forceinline__ float sum(float v) {
+    v = warp_sum(v);
+    uint32_t* p = parts + 16 * turn;
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) p[warp] = __float_as_uint(v);
+    named_bar_sync(id, threads);
+    float s[4] = {};
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      if (4 * w < threads / 32) {
+        const float4 t = *reinterpret_cast<const float4*>(p + 4 * w);
+        s[w] = (t.x + t.y) + (t.z + t.w);
+      }
+    return (s[0] + s[1]) + (s[2] + s[3]);
+  }
+  __device__ __forceinline__ uint32_t max(uint32_t v) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    uint32_t* p = parts + 16 * turn;
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) p[warp] = v;
+    named_bar_sync(id, threads);
+    v = 0;
+    for (int w = 0; w < threads / 32; ++w) v = ::max(v, p[w]);
+    return v;
+  }
+  __device__ __forceinline__ bool all(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)ok), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+  }
+};
+
+// The factors of a norm for N sets of U values; columns behind the row are zeros.
+template <int U, int N>
+__device__ __forceinline__ NormFactors norm_factors2(Group& row, const NormArgs& a, float share, float2 (&v)[N][U / 2],
+                                                     const bool (&in)[N]) {
+  float mean = 0.0f, eps = a.eps, squares;
+  for (bool again = false;; again = true) {
+    float2 s[2] = {both(0.0f), both(0.0f)};
+    if (a.layer) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < U / 2; ++j) s[j & 1] = add2(s[j & 1], v[i][j]);
+      s[0] = add2(s[0], s[1]);
+      mean = row.sum(s[0].x + s[0].y) * share;
+      s[0] = s[1] = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (in[i])
+#pragma unroll
+          for (int j = 0; j < U / 2; ++j) {
+            const float2 d = add2(v[i][j], both(-mean));
+            s[j & 1] = fma2(d, d, s[j & 1]);
+          }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < U / 2; ++j) s[j & 1] = fma2(v[i][j], v[i][j], s[j & 1]);
+    }
+    s[0] = add2(s[0], s[1]);
+    squares = row.sum(s[0].x + s[0].y);
+    if (again || squares < __uint_as_float(0x7f800000u)) break;
+    eps = 0.0f;  // (nothing beside the squares of such a row)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < U / 2; ++j) v[i][j] = mul2(v[i][j], both(2.6469780e-23f));  // 2^-75
+  }
+  const float factor = rsqrtf(fmaf(squares, share, eps));
+  return NormFactors{factor, -mean * factor};
+}
+
+// Coefficients of the columns in shared memory, fp32: 16 bytes at a time, those of a set of 8 in two planes.
+template <int U>
+__device__ __forceinline__ void load_plane(const float4* c, int vecs, int vec, float2 (&o)[U / 2]) {
+#pragma unroll
+  for (int j = 0; j < U / 4; ++j) {
+    const float4 t = c[j * vecs + vec];
+    o[2 * j] = make_float2(t.x, t.y), o[2 * j + 1] = make_float2(t.z, t.w);
+  }
+}
+template <int U>
+__device__ __forceinline__ void store_plane(float4* c, int vecs, int vec, const float2 (&v)[U / 2]) {
+#pragma unroll
+  for (int j = 0; j < U / 4; ++j) c[j * vecs + vec] = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
+}
+
+struct StreamPlan {
+  int threads, groups, slots;  // threads of a group; groups of a CTA, one CTA an SM; slots of a group
+  int slot_bytes;
+  bool shift;                  // the norms may have a mean or a bias
+};
+
+constexpr int kStreamValues = 32;    // of a thread
+constexpr int kStreamThreads = 768;  // of a CTA, at most
+
+// One persistent CTA an SM, groups of whose warps work on a row each: as many rows
+// are under way as their inputs find room for in shared memory (bulk copies, the next
+// row's as soon as all have read the last one's).  What belongs to the columns for all
+// rows is made once, in shared memory: the norms' weights, with a gate of the channels
+// and the branch's scale in the first.  A thread has N sets of U values, 32 in all: what a row
+// costs apart from its values (two sums over the group) is shared by as many.  U: 8, or 4
+// where the residual is fp32, so that neighbouring lanes access neighbouring 16 bytes.
+template <bool R>
+__global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(const BlockArgs a, const StreamPlan p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) uint32_t parts[15][32];
+  __shared__ uint64_t full[32];
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  const int g = threadIdx.x / p.threads, mine = threadIdx.x - g * p.threads;
+  Group row{parts[g], 1 + g, p.threads, mine >> 5};
+  constexpr int U = R ? 8 : 4, N = kStreamValues / U;
+  const int vecs = a.hidden / U;
+  auto vec = [&](int i) { return mine + i * p.threads; };
+  bool in[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) in[i] = vec(i) < vecs;
+  float4* w1 = reinterpret_cast<float4*>(smem);
+  float4* w2 = w1 + a.hidden / 4;
+  float4* b1 = w2 + a.hidden / 4;  // (with shift)
+  float4* b2 = b1 + a.hidden / 4;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(p.shift ? b2 + a.hidden / 4 : b1) + g * p.slots * p.slot_bytes;
+  uint64_t* bar = full + g * p.slots;
+  // A slot: y, the residual, the gates if each row has its own.
+  const bool own_gates = a.gate && a.gate_cols && a.gate_row_stride != 0, channel_gates = a.gate && a.gate_cols && !own_gates;
+  const int y_bytes = a.y ? 2 * a.hidden : 0, r_bytes = (R ? 2 : 4) * a.hidden;
+  const int g_bytes = own_gates ? (a.gate_bf16 ? 2 : 4) * a.hidden : 0;
+  for (int i = threadIdx.x; i < 15 * 32; i += blockDim.x) (&parts[0][0])[i] = 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.groups * p.slots; ++s) mbar_init(&full[s], 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  auto copy = [&](int64_t r, int s) {
+    uint8_t* to = ring + s * p.slot_bytes;
+    mbar_arrive_expect_tx(&bar[s], y_bytes + r_bytes + g_bytes);
+    if (y_bytes) bulk_load(to, a.y + r * a.y_stride, y_bytes, &bar[s]);
+    bulk_load(to + y_bytes, static_cast<const uint8_t*>(a.residual) + r * a.residual_stride * (R ? 2 : 4), r_bytes, &bar[s]);
+    if (g_bytes)
+      bulk_load(to + y_bytes + r_bytes, static_cast<const uint8_t*>(a.gate) + r * a.gate_row_stride * (a.gate_bf16 ? 2 : 4),
+                g_bytes, &bar[s]);
+  };
+  const int64_t first = blockIdx.x + (int64_t)g * gridDim.x, step = (int64_t)gridDim.x * p.groups;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (mine == 0)
+    for (int s = 0; s < p.slots && first + s * step < a.m; ++s) copy(first + s * step, s);
+  for (int i = threadIdx.x; i < vecs; i += blockDim.x) {
+    float2 w[U / 2], t[U / 2];
+    for (int j = 0; j < U / 2; ++j) w[j] = both(a.branch_scale);
+    if (channel_gates) {
+      load_u<U>(a.gate, a.gate_bf16, U * i, t);
+      gate_values<U>(t, a.gate_activation);
+      for (int j = 0; j < U / 2; ++j)
+        w[j] = mul2(w[j], t[j]);
+    }
+    if (p.shift) {
+      for (int j = 0; j < U / 2; ++j) t[j] = both(0.0f);
+      if (a.post.bias) load_u<U>(a.post.bias, a.post.bf16, U * i, t);
+      for (int j = 0; j < U / 2; ++j) t[j] = mul2(t[j], w[j]);
+      store_plane<U>(b1, vecs, i, t);
+    }
+    if (a.post.weight) {
+      load_u<U>(a.post.weight, a.post.bf16, U * i, t);
+      for (int j = 0; j < U / 2; ++j) w[j] = mul2(add2(t[j], both(a.post.offset)), w[j]);
+    }
+    store_plane<U>(w1, vecs, i, w);
+    for (int j = 0; j < U / 2; ++j) w[j] = both(1.0f), t[j] = both(0.0f);
+    if (p.shift) {
+      if (a.pre.bias) load_u<U>(a.pre.bias, a.pre.bf16, U * i, t);
+      store_plane<U>(b2, vecs, i, t);
+    }
+    if (a.pre.weight) {
+      load_u<U>(a.pre.weight, a.pre.bf16, U * i, t);
+      for (int j = 0; j < U / 2; ++j) w[j] = add2(t[j], both(a.pre.offset));
+    }
+    store_plane<U>(w2, vecs, i, w);
+  }
+  __syncthreads();
+  const float share = 1.0f / (float)a.hidden;
+  int s = 0;
+  uint32_t parity = 0;
+  for (int64_t r = first; r < a.m; r += step) {
+    float g1 = 1.0f;  // the row's gate
+    if (a.gate && !a.gate_cols) {
+      float t[1];
+      load_any<1>(a.gate, a.gate_bf16, r * a.gate_row_stride, t);
+      g1 = gate_value(t[0], a.gate_activation);
+    }
+    bool ok = mbar_wait(&bar[s], parity, abort_flag, &g_norm_device_error, 1);
+    const uint8_t* from = ring + s * p.slot_bytes;
+    float2 v[N][U / 2];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+      for (int j = 0; j < U / 2; ++j) v[i][j] = both(0.0f);
+      if (in[i]) load_u<U>(a.y ? from : from + y_bytes, a.y ? true : R, U * vec(i), v[i]);
+    }
     if (a.y) {
-      if (a.post.on) norm_row<WARP, V, N>(row, a.post, a.hidden, z, at);
-      float g1[1] = {1.0f};
-      if (a.gate && !a.gate_cols) {
-        load_any<1>(a.gate, a.gate_bf16, r * a.gate_row_stride, g1);
-        g1[0] = gate_value(g1[0], a.gate_activation);
+      NormFactors f{1.0f, 0.0f};
+      if (a.post.on) f = norm_factors2<U, N>(row, a.post, share, v, in);
+      f.factor *= g1, f.shift *= g1;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (!in[i]) continue;
+        float2 t[U / 2];
+        if (p.shift) {
+#pragma unroll
+          for (int j = 0; j < U / 2; ++j) v[i][j] = fma2(v[i][j], both(f.factor), both(f.shift));
+        } else {
+#pragma unroll
+          for (int j = 0; j < U / 2; ++j) v[i][j] = mul2(v[i][j], both(f.factor));
+        }
+        load_plane<U>(w1, vecs, vec(i), t);
+#pragma unroll
+        for (int j = 0; j < U / 2; ++j) v[i][j] = mul2(v[i][j], t[j]);
+        if (p.shift) {
+          load_plane<U>(b1, vecs, vec(i), t);
+#pragma unroll
+          for (int j = 0; j < U / 2; ++j) v[i][j] = fma2(both(g1), t[j], v[i][j]);
+        }
+        if (own_gates) {
+          load_u<U>(from + y_bytes + r_bytes, a.gate_bf16, U * vec(i), t);
+          gate_values<U>(t, a.gate_activation);
+#pragma unroll
+          for (int j = 0; j < U / 2; ++j) v[i][j] = mul2(v[i][j], t[j]);
+        }
+        load_u<U>(from + y_bytes, R, U * vec(i), t);
+#pragma unroll
+        for (int j = 0; j < U / 2; ++j) v[i][j] = fma2(both(a.residual_scale), t[j], v[i][j]);
+        if (R) {
+          uint32_t q[U / 2];
+#pragma unroll
+          for (int j = 0; j < U / 2; ++j) q[j] = pack2(v[i][j]), v[i][j] = unpack2(q[j]);
+          if (a.residual_out)
+            store_words<U>(static_cast<uint16_t*>(a.residual_out) + r * a.residual_out_stride + U * vec(i), q);
+        } else if (a.residual_out) {
+          float* o = static_cast<float*>(a.residual_out) + r * a.residual_out_stride + U * vec(i);
+#pragma unroll
+          for (int j = 0; j < U / 4; ++j)
+            reinterpret_cast<float4*>(o)[j] = make_float4(v[i][2 * j].x, v[i][2 * j].y, v[i][2 * j + 1].x, v[i][2 * j + 1].y);
+        }
+      }
+    }
+    ok = row.all(ok);  // and all have read the slot
+    const int64_t next = r + p.slots * step;
+    if (!ok) {  // (the copies in flight land before the CTA leaves)
+      if (mine == 0)
+        for (int64_t q = r; q < a.m && q < next; q += step) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait(&bar[s], parity) && clock64() - t0 < kWaitLimitCycles) {
+          }
+          if (++s == p.slots) s = 0, parity ^= 1;
+        }
+      return;
+    }
+    if (mine == 0 && next < a.m) copy(next, s);
+    if (++s == p.slots) s = 0, parity ^= 1;
+    if (!a.pre.on) continue;
+    const NormFactors f = norm_factors2<U, N>(row, a.pre, share, v, in);
+    uint32_t q[N][U / 2];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (!in[i]) continue;
+      float2 t[U / 2];
+      load_plane<U>(w2, vecs, vec(i), t);
+      if (p.shift) {
+        float2 u[U / 2];
+        load_plane<U>(b2, vecs, vec(i), u);
+#pragma unroll
+        for (int j = 0; j < U / 2; ++j) v[i][j] = fma2(fma2(v[i][j], both(f.factor), both(f.shift)), t[j], u[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < U / 2; ++j) v[i][j] = mul2(mul2(v[i][j], both(f.factor)), t[j]);
       }
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (at(i) < a.hidden) {
-          float g[V];
-          if (a.gate && a.gate_cols) load_any<V>(a.gate, a.gate_bf16, r * a.gate_row_stride + at(i), g);
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float gate = a.gate && a.gate_cols ? gate_value(g[j], a.gate_activation) : g1[0];
-            const float s = fmaf(a.residual_scale, res[i][j], a.branch_scale * (gate * z[i][j]));
-            res[i][j] = R ? bf16_round(s) : s;
-          }
-          if (a.residual_out) {
-            if (R) {
-              store_bf16<V>(static_cast<uint16_t*>(a.residual_out) + r * a.residual_out_stride + at(i), res[i]);
-            } else {
-              float* o = static_cast<float*>(a.residual_out) + r * a.residual_out_stride + at(i);
-              if (V == 8) {
-#pragma unroll
-                for (int q = 0; q < V / 4; ++q)
-                  reinterpret_cast<float4*>(o)[q] =
-                      make_float4(res[i][(4 * q) % V], res[i][(4 * q + 1) % V], res[i][(4 * q + 2) % V], res[i][(4 * q + 3) % V]);
-              } else {
-                *o = res[i][0];
-              }
-            }
-          }
-        }
+      for (int j = 0; j < U / 2; ++j) q[i][j] = pack2(v[i][j]);
+      if (!a.out_scales) store_words<U>(static_cast<uint16_t*>(a.out) + r * a.out_stride + U * vec(i), q[i]);
     }
-    if (!a.pre.on) continue;
-    norm_row<WARP, V, N>(row, a.pre, a.hidden, res, at);
-    if (!a.out_scales) {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (at(i) < a.hidden) store_bf16<V>(static_cast<uint16_t*>(a.out) + r * a.out_stride + at(i), res[i]);
-      continue;
-    }
-    // The codes are those of the row as it would be stored in bf16.
+    if (!a.out_scales) continue;
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (at(i) < a.hidden)
+      if (in[i])
 #pragma unroll
-        for (int j = 0; j < V; ++j) top = max(top, (uint32_t)(f32_to_bf16_bits(res[i][j]) & 0x7fffu));
-    const Int8Row q(row.max(top));
+        for (int j = 0; j < U / 2; ++j) top = amax_bf16x2(top, q[i][j]);
+    const Int8Row codes(row.max(amax_of_pair(top)));
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (at(i) < a.hidden) {
-        int8_t* o = static_cast<int8_t*>(a.out) + r * a.out_stride + at(i);
-        if (V == 8)
-          *reinterpret_cast<uint2*>(o) =
-              int8_encode8(q, make_uint4(pack_bf16(res[i][0], res[i][1 % V]), pack_bf16(res[i][2 % V], res[i][3 % V]),
-                                         pack_bf16(res[i][4 % V], res[i][5 % V]), pack_bf16(res[i][6 % V], res[i][7 % V])));
+      if (in[i]) {
+        int8_t* o = static_cast<int8_t*>(a.out) + r * a.out_stride + U * vec(i);
+        const uint2 c = int8_encode8(codes, make_uint4(q[i][0], q[i][1], U == 8 ? q[i][2 % (U / 2)] : 0u, U == 8 ? q[i][3 % (U / 2)] : 0u));
+        if (U == 8)
+          *reinterpret_cast<uint2*>(o) = c;
         else
-          *o = (int8_t)q.code(bf16_round(res[i][0]));
+          *reinterpret_cast<uint32_t*>(o) = c.x;
       }
-    if (mine == 0) a.out_scales[r] = q.scale;
+    if (mine == 0) a.out_scales[r] = codes.scale;
   }
 }
 
@@ -267,6 +823,25 @@ cudaError_t launch_one(const BlockArgs& a, int threads, cudaStream_t s) {
 
 int round_up_32(int v) { return (v + 31) / 32 * 32; }
 
+constexpr int kStreamBytes = 224 * 1024;  // of shared memory
+
+int stream_coefs(const BlockArgs& a, bool shift) { return (shift ? 4 : 2) * 4 * a.hidden; }
+
+// As many groups as fit (15 named barriers, 1024 threads), and a second slot for each where there is room;
+// no groups where even two rows do not fit.
+StreamPlan plan_stream(const BlockArgs& a, bool bf16) {
+  StreamPlan p = {};
+  const int own_gate = a.gate && a.gate_cols && a.gate_row_stride != 0 ? (a.gate_bf16 ? 2 : 4) : 0;
+  p.shift = a.post.layer || a.post.bias || a.pre.layer || a.pre.bias;
+  p.threads = round_up_32((a.hidden + kStreamValues - 1) / kStreamValues);
+  p.slot_bytes = a.hidden * ((a.y ? 2 : 0) + (bf16 ? 2 : 4) + own_gate);
+  const int slots = (kStreamBytes - stream_coefs(a, p.shift)) / p.slot_bytes, most = kStreamThreads / p.threads < 15 ? kStreamThreads / p.threads : 15;
+  if (slots < 2 || p.threads > 512) return p;
+  p.groups = slots < most ? slots : most;
+  p.slots = slots >= 2 * p.groups ? 2 : 1;
+  return p;
+}
+
 // Threads and accesses for a row: as few accesses as keep a CTA to 512 threads.
 template <bool R>
 cudaError_t launch_rows(const BlockArgs& a, bool vec, cudaStream_t s) {
@@ -275,6 +850,22 @@ cudaError_t launch_rows(const BlockArgs& a, bool vec, cudaStream_t s) {
     if (h <= 256) return launch_one<R, true, 1, 8, 256>(a, 256, s);
     if (h <= 4096) return launch_one<R, false, 1, 8, 512>(a, round_up_32((h + 7) / 8), s);
     return launch_one<R, false, 1, 32, 1024>(a, round_up_32((h + 31) / 32), s);
+  }
+  // The streaming kernel, from where its start (one CTA an SM, the columns' coefficients) is made up for: bf16
+  // residual, both norms, streaming and by rows, in us: 600 rows of 384, 1024, 2048, 4096 4.6, 5.3, 5.6, 6.5 and 3.6,
+  // 5.9, 6.9, 10.5; 2400 rows of 384, 768, 1536, 4096 6.9, 7.7, 10.0, 19.8 and 8.3, 12.0, 14.7, 37.6; of 256 (a warp a
+  // row, 8 values a lane) 6.3 and 4.3, 32000 rows 33 and 28.
+  if (h > 256 && a.m >= 2 * device_sms() && a.m * h >= 800000) {
+    const StreamPlan p = plan_stream(a, R);
+    if (p.groups > 0) {
+      auto kern = block_norm_stream_kernel<R>;
+      const int bytes = stream_coefs(a, p.shift) + p.groups * p.slots * p.slot_bytes;
+      // set on every launch: the attribute belongs to the current device's context
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (e != cudaSuccess) return e;
+      ProfScope prof(s, "block_norm");
+      return launch_pdl(kern, dim3(device_sms()), dim3(p.threads * p.groups), bytes, s, a, p);
+    }
   }
   if (h <= 256) return launch_one<R, true, 8, 1, 256>(a, 256, s);
   if (h <= 512) return launch_one<R, true, 8, 2, 256>(a, 256, s);
@@ -314,6 +905,13 @@ NormArgs norm_args(const ffn_norm* n) {
 bool whole(const void* p, int64_t stride) { return !p || (aligned(p, 16) && stride % 8 == 0); }
 
 }  // namespace
+cudaError_t read_norm_device_error(int* flags, bool clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(flags, g_norm_device_error, sizeof(int));
+  const int zero = 0;
+  if (e == cudaSuccess && clear) e = cudaMemcpyToSymbol(g_norm_device_error, &zero, sizeof(int));
+  return e;
+}
+
 }  // namespace ffn
 
 extern "C" ffn_status ffn_block_norm(const ffn_block_norm_args* b, int64_t m, int64_t hidden, void* stream) {

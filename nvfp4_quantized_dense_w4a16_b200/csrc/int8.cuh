@@ -11,10 +11,22 @@ __device__ __forceinline__ float int8_scaled(int sum, float xs, float ws) {
   return __fmul_rn(__fmul_rn(__int2float_rn(sum), xs), ws);
 }
 
-// h before its rounding to bf16.  The fast exponential and quotient are a few
-// steps of fp32 off, and 16 bits of the product are dropped right after.
+// exp(v) and 1 / v by the hardware's approximations, two steps of fp32 off (exp one
+// more for each unit of |v|).  Results below fp32's normal range are zeros.
+__device__ __forceinline__ float exp_approx(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fmul_rn(v, 1.44269504f)));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// h before its rounding to bf16, which drops 16 bits right after.
 __device__ __forceinline__ float int8_silu_mul(float gate, float up) {
-  return __fmul_rn(__fdividef(gate, __fadd_rn(1.0f, __expf(-gate))), up);
+  return __fmul_rn(__fmul_rn(gate, rcp_approx(__fadd_rn(1.0f, exp_approx(-gate)))), up);
 }
 
 // Quantisation of a row by the largest magnitude among its bf16 bits.  Factors

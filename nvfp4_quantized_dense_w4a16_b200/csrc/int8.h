@@ -27,5 +27,6 @@ struct Int8Product {
 cudaError_t launch_int8_product(const Int8Product& p, cudaStream_t s);
 // Error bits of these kernels' bounded waits, as read_device_error.
 cudaError_t read_int8_device_error(int* flags, bool clear);
+cudaError_t read_norm_device_error(int* flags, bool clear);
 
 }  // namespace ffn

@@ -118,6 +118,46 @@ def test_rows(native, m, hidden):
     check(native, m, hidden, torch.float32, branch=False, seed=m)
 
 
+@pytest.mark.parametrize("m,hidden", [(3000, 288), (2100, 384), (1500, 1000), (700, 2048), (601, 2056), (450, 5120), (400, 8192), (310, 12288), (300, 16384)])
+@pytest.mark.parametrize("residual", [torch.bfloat16, torch.float32])
+def test_many_rows(native, m, hidden, residual):
+    """The streaming kernel: rows that fill its groups unevenly, every kind of gate, biases, quantised outputs."""
+    check(native, m, hidden, residual, gate="channel", offset=1.0, a=0.9, b=0.5, seed=m)
+    check(native, m, hidden, residual, torch.float32, "layer", gate="full", activation="tanh", seed=m, spread=10.0)
+    check(native, m, hidden, residual, gate="full", gate_dtype=torch.float32, activation="sigmoid", pre=False, seed=m)
+    check(native, m, hidden, residual, gate="row", post=False, kind="layer", seed=m)
+    check(native, m, hidden, residual, branch=False, seed=m)
+    if hidden % 32 == 0:
+        r, y = rows(m, hidden, 4).to(residual).cuda(), rows(m, hidden, 5).cuda()
+        post, pre = make_norm(native, hidden, seed=1)[0], make_norm(native, hidden, "layer", seed=2)[0]
+        res, x = native.ffn_block_norm(r, y=y, post=post, pre=pre)
+        res2, c, s = native.ffn_block_norm(r, y=y, post=post, pre=pre, quantize=True, residual_out=r)
+        rc, rs = native.ffn_int8_quantize(x)
+        assert same_bits(res, res2) and torch.equal(c, rc) and torch.equal(s, rs)
+
+
+def test_many_rows_of_extreme_values(native):
+    m, hidden = 1500, 640
+    r = torch.randn((m, hidden), generator=torch.Generator().manual_seed(1), dtype=torch.float64)
+    r[::5] *= 1e37
+    r[1::5] *= 0.0
+    r[2::5] *= 1e-30
+    r[3::5] *= 1e19
+    for kind in ("rms", "layer"):
+        check(native, m, hidden, torch.float32, kind=kind, branch=False, r=r.float())
+        check(native, m, hidden, torch.float32, kind=kind, y=r.to(torch.bfloat16), r=rows(m, hidden, 1).float())
+    y, r = rows(m, hidden, 2).cuda(), rows(m, hidden, 3).cuda()
+    pre, post = make_norm(native, hidden, seed=1)[0], make_norm(native, hidden, seed=2)[0]
+    good = native.ffn_block_norm(r, y=y, post=post, pre=pre)
+    y[7, 3], r[8, 5], y[1499, 639] = float("nan"), float("nan"), float("inf")
+    _, c, s = native.ffn_block_norm(r, y=y, post=post, pre=pre, quantize=True)
+    res, x = native.ffn_block_norm(r, y=y, post=post, pre=pre, residual_out=r, out=y)
+    bad = torch.zeros(m, dtype=torch.bool, device="cuda")
+    bad[[7, 8, 1499]] = True
+    assert torch.all(torch.isnan(x[bad])) and torch.equal(torch.isnan(s), bad) and torch.all(c[bad] == 0)
+    assert same_bits(x[~bad], good[1][~bad]) and same_bits(res[~bad], good[0][~bad])
+
+
 def test_norms_without_weights(native):
     r = rows(4, 320, 3)
     for kind in ("rms", "layer"):
