@@ -40,6 +40,20 @@ Carve carve(int64_t m, int64_t k, int64_t inter) {
   return c;
 }
 
+// A product whose rows are quantised first, into `codes` and `scales`, if they have no scales.
+cudaError_t product(ffn::Int8Product p, uint8_t* codes, uint8_t* scales, cudaStream_t s) {
+  if (ffn::int8_gemv_serves(p.m, p.k)) return ffn::launch_int8_gemv(p, s);
+  if (!p.xs) {
+    int8_t* xq = reinterpret_cast<int8_t*>(codes);
+    float* xs = reinterpret_cast<float*>(scales);
+    const cudaError_t e = ffn::launch_int8_quantize(p.x, p.m, p.k, p.k, xq, xs, true, s);
+    if (e != cudaSuccess) return e;
+    p.x = xq;
+    p.xs = xs;
+  }
+  return ffn::launch_int8_product(p, s);
+}
+
 ffn_status check_linear(int64_t m, int64_t n, int64_t k) {
   if (m < 0) return FFN_ERR_INVALID_ARG;
   if (n <= 0 || !valid_k(k)) return FFN_ERR_SHAPE;
@@ -93,20 +107,8 @@ ffn_status ffn_int8_linear(const void* x, const float* x_scales, int64_t m, cons
   if (ffn_status st = ffn::moe_precheck()) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  cudaError_t e = cudaSuccess;
-  if (!x_scales) {
-    int8_t* xq = reinterpret_cast<int8_t*>(ws + c.xq);
-    float* xs = reinterpret_cast<float*>(ws + c.xs);
-    e = ffn::launch_int8_quantize(x, m, k, k, xq, xs, true, s);
-    x = xq;
-    x_scales = xs;
-  }
-  if (e == cudaSuccess)
-    e = ffn::launch_int8_product(ffn::Int8Product{static_cast<const int8_t*>(x), x_scales, m, w, w_scales,
-                                                  static_cast<const uint16_t*>(bias), n, k, static_cast<uint16_t*>(y),
-                                                  false},
-                                 s);
-  return ffn::moe_status(e);
+  const ffn::Int8Product p{x, x_scales, m, w, w_scales, static_cast<const uint16_t*>(bias), n, k, static_cast<uint16_t*>(y), false};
+  return ffn::moe_status(product(p, ws + c.xq, ws + c.xs, s));
 }
 
 ffn_status ffn_int8_workspace_size(int64_t m, int64_t hidden, int64_t inter, size_t* bytes) {
@@ -131,24 +133,12 @@ ffn_status ffn_int8_forward(const void* x, const float* x_scales, int64_t m, int
   if (ffn_status st = ffn::moe_precheck()) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  int8_t *xq = reinterpret_cast<int8_t*>(ws + c.xq), *hq = reinterpret_cast<int8_t*>(ws + c.hq);
-  float *xs = reinterpret_cast<float*>(ws + c.xs), *hs = reinterpret_cast<float*>(ws + c.hs);
   uint16_t* h = reinterpret_cast<uint16_t*>(ws + c.h);
-  cudaError_t e = cudaSuccess;
-  if (!x_scales) {
-    e = ffn::launch_int8_quantize(x, m, hidden, hidden, xq, xs, true, s);
-    x = xq;
-    x_scales = xs;
-  }
+  cudaError_t e = product(ffn::Int8Product{x, x_scales, m, gate_up, gate_up_scales, nullptr, 2 * inter, hidden, h, true},
+                          ws + c.xq, ws + c.xs, s);
   if (e == cudaSuccess)
-    e = ffn::launch_int8_product(ffn::Int8Product{static_cast<const int8_t*>(x), x_scales, m, gate_up, gate_up_scales,
-                                                  nullptr, 2 * inter, hidden, h, true},
-                                 s);
-  if (e == cudaSuccess) e = ffn::launch_int8_quantize(h, m, inter, inter, hq, hs, true, s);
-  if (e == cudaSuccess)
-    e = ffn::launch_int8_product(ffn::Int8Product{hq, hs, m, down, down_scales, nullptr, hidden, inter,
-                                                  static_cast<uint16_t*>(out), false},
-                                 s);
+    e = product(ffn::Int8Product{h, nullptr, m, down, down_scales, nullptr, hidden, inter, static_cast<uint16_t*>(out), false},
+                ws + c.hq, ws + c.hs, s);
   return ffn::moe_status(e);
 }
 

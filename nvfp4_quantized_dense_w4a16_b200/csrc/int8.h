@@ -14,7 +14,7 @@ cudaError_t launch_int8_quantize(const void* x, int64_t m, int64_t k, int64_t st
 // One projection of int8 rows.  Plain: y bf16 [m, n].  With silu_mul the weight
 // holds n / 2 gate rows, then n / 2 up rows, and y is h bf16 [m, n / 2].
 struct Int8Product {
-  const int8_t* x;
+  const void* x;  // int8 codes with their scales xs; for launch_int8_gemv also bf16, without
   const float* xs;
   int64_t m;
   const int8_t* w;
@@ -25,6 +25,9 @@ struct Int8Product {
   bool silu_mul;
 };
 cudaError_t launch_int8_product(const Int8Product& p, cudaStream_t s);
+// The same for one row, bf16 as well, whose quantisation is part of it.
+bool int8_gemv_serves(int64_t m, int64_t k);
+cudaError_t launch_int8_gemv(const Int8Product& p, cudaStream_t s);
 // Error bits of these kernels' bounded waits, as read_device_error.
 cudaError_t read_int8_device_error(int* flags, bool clear);
 cudaError_t read_norm_device_error(int* flags, bool clear);

@@ -72,7 +72,10 @@ __device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
 
 __device__ __forceinline__ int4 load_cluster(uint32_t a) {
   int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
   return v;
 }
 
@@ -401,7 +404,7 @@ struct FewArgs {
 
 constexpr int kFewThreads = 192;  // a producer, an issuer, four warps for the sums
 constexpr int kFewWeights = 128 * kChunkK;
-constexpr int kFewMaxStages = 8;
+constexpr int kFewMaxStages = 8, kFewMaxSplits = 8;
 constexpr int kFewRing = 100 * 1024;  // two CTAs an SM
 constexpr int kFewBar = 0;            // the barriers stand in front of the ring
 constexpr int kFewSmem = 1024 + kFewRing + 1024;
@@ -446,6 +449,8 @@ __global__ void __launch_bounds__(kFewThreads)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
+  const int64_t col = tile * (SILU ? 64 : 128) + 4 * (SILU ? lane & 15 : lane);  // of y, the first of a lane's four
+  float s0[4], s1[4];
 
   if (warp == 0) {
     if (lane == 0) {
@@ -496,6 +501,12 @@ __global__ void __launch_bounds__(kFewThreads)
     }
   } else {
     griddep_wait();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool in = col + j < a.cols;
+      s0[j] = in ? a.ws[col + j] : 0.0f;
+      s1[j] = !in ? 0.0f : SILU ? a.ws[a.cols + col + j] : a.bias ? bf16_bits_to_float(a.bias[col + j]) : 0.0f;
+    }
     ok = mbar_wait(done, 0, abort_flag, err, 8);
     ok = __all_sync(0xffffffffu, ok);
   }
@@ -519,28 +530,20 @@ __global__ void __launch_bounds__(kFewThreads)
   if (threadIdx.x == 0) *abort_flag = ok ? 0 : 1;
   __syncthreads();
   cluster_sync();
-  bool all = true;
-  for (uint32_t r = 0; r < splits; ++r) {
-    int bad;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(bad) : "r"(in_cta(const_cast<int*>(abort_flag), r)));
-    all = all && bad == 0;
-  }
-  if (all && warp >= 2) {
+  int bad = 0;
+  if (lane < (int)splits)
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(bad) : "r"(in_cta(const_cast<int*>(abort_flag), lane)));
+  if (warp >= 2) {
     // Rows of x by CTA; a warp has 128 sums of a row, four a lane.
-    const int wq = warp - 2;
-    const int64_t col = tile * (SILU ? 64 : 128) + 4 * (SILU ? lane & 15 : lane);
-    float s0[4], s1[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool in = col + j < a.cols;
-      s0[j] = in ? a.ws[col + j] : 0.0f;
-      s1[j] = !in ? 0.0f : SILU ? a.ws[a.cols + col + j] : a.bias ? bf16_bits_to_float(a.bias[col + j]) : 0.0f;
-    }
-    const int per = SILU ? 2 : 1;  // rows of a warp at a time
-    for (int i = (rank * 4 + wq) * per + (SILU ? lane >> 4 : 0); i < a.m; i += (int)splits * 4 * per) {
+    const int wq = warp - 2, per = SILU ? 2 : 1;  // rows of a warp at a time
+    ok = __all_sync(0xffffffffu, bad == 0);
+    for (int i = (rank * 4 + wq) * per + (SILU ? lane >> 4 : 0); ok && i < a.m; i += (int)splits * 4 * per) {
+      const float xs = a.xs[i];
       int4 g = make_int4(0, 0, 0, 0), u = g;
       const int at = i * 128 + 4 * (SILU ? lane & 15 : lane);
-      for (uint32_t r = 0; r < splits; ++r) {
+#pragma unroll
+      for (uint32_t r = 0; r < kFewMaxSplits; ++r) {
+        if (r >= splits) break;
         const uint32_t from = in_cta(sums + at, r);
         const int4 p = load_cluster(from);
         g.x += p.x, g.y += p.y, g.z += p.z, g.w += p.w;
@@ -549,7 +552,6 @@ __global__ void __launch_bounds__(kFewThreads)
           u.x += p2.x, u.y += p2.y, u.z += p2.z, u.w += p2.w;
         }
       }
-      const float xs = a.xs[i];
       const int gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
       uint16_t b[4];
 #pragma unroll
@@ -636,9 +638,17 @@ cudaError_t launch_few(const Int8Product& p, cudaStream_t s) {
   const int64_t cols = SILU ? p.n / 2 : p.n, tiles = ceil_div(cols, SILU ? 64 : 128);
   FewArgs a{p.xs, p.ws, p.bias, p.y, cols, (int)p.m, (int)ceil_div(p.k, kChunkK), (int)ceil_div(p.m, 16) * 16, 0};
   a.stages = std::min(kFewMaxStages, kFewRing / (kFewWeights + a.n * kChunkK));
-  // as many CTAs as are resident at a time, two an SM
-  const int64_t want = 2 * device_sms() / tiles, most = a.kc < 8 ? a.kc : 8;
-  const unsigned splits = (unsigned)(want < 1 ? 1 : want < most ? want : most);
+  // Clusters of 1, 2, ... CTAs that are resident at a time, an SM each or two an SM (measured; a cluster stays
+  // within a part of the GPU).  The most CTAs that start at once: with one more wave of clusters 5120 x 17408 takes
+  // 24 us, cut into 8, and 18.0, cut into 6.  Short ranges of K do better with one CTA an SM, beside which the next
+  // kernel's can start: 4096 x 4096 cut into 4 and 8 6.5 and 7.2 us, 4096 x 12288 13.7 and 12.0.
+  constexpr int kOneAnSm[] = {148, 74, 45, 33, 26, 22, 15, 15}, kTwoAnSm[] = {296, 148, 90, 68, 54, 45, 36, 33};
+  int one = 1, two = 1;
+  for (int c = 2; c <= kFewMaxSplits && c <= a.kc; ++c) {
+    if (tiles <= kOneAnSm[c - 1]) one = c;
+    if (tiles <= kTwoAnSm[c - 1]) two = c;
+  }
+  const unsigned splits = (unsigned)(ceil_div(a.kc, one) <= 12 ? one : two);
   CUtensorMap xmap, wmap;
   if (!encode_rows(&xmap, p.x, p.m, p.k, a.n) || !encode_rows(&wmap, p.w, p.n, p.k, SILU ? 64 : 128)) return cudaErrorInvalidValue;
   auto kern = int8_few_kernel<SILU>;
