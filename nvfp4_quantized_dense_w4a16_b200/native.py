@@ -596,23 +596,57 @@ def ffn_int8_workspace_size(m: int, hidden: int, inter: int) -> int:
     return out.value
 
 
-def _int8_rows(x, x_scales):
+_Tensor = torch.Tensor
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _get_device() -> int:
+    """The current device, or a number that no tensor is on where there is none."""
+    try:
+        return _raw_device()
+    except RuntimeError:
+        return -2
+
+
+def _good(t, dtype, shape, dev) -> bool:
+    """Whether `t` is what a call wants: the checks of a call that passes them all.  One that does not is gone over
+    again by those that say why."""
+    return type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _demand(t, name, dtype, shape, dev):
+    if not _good(t, dtype, shape, dev):
+        _need(t, name, dtype, shape)
+        _launch_stream(None, t)
+
+
+def _stream_of(stream, dev) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _int8_rows(x, x_scales, dev):
     """m and k of bf16 rows, or of int8 codes with their scales."""
-    _need(x, "x", torch.bfloat16 if x_scales is None else torch.int8)
-    if x.dim() != 2:
-        raise ValueError(f"x must have shape (m, k), got {tuple(x.shape)}")
-    m, k = x.shape
+    dtype = torch.bfloat16 if x_scales is None else torch.int8
+    shape = x.shape if isinstance(x, _Tensor) else None
+    _demand(x, "x", dtype, shape, dev)
+    if len(shape) != 2:
+        raise ValueError(f"x must have shape (m, k), got {tuple(shape)}")
+    m, k = shape
     if x_scales is not None:
-        _need(x_scales, "x_scales", torch.float32, (m,))
+        _demand(x_scales, "x_scales", torch.float32, (m,), dev)
     return m, k
 
 
-def _int8_weight(w, scales, name, n, k):
-    _need(w, name, torch.int8, None if n is None else (n, k))
-    if w.dim() != 2 or w.shape[1] != k:
-        raise ValueError(f"{name} must have shape (n, {k}), got {tuple(w.shape)}")
-    n = w.shape[0]
-    _need(scales, name + "_scales", torch.float32, (n,))
+def _int8_weight(w, scales, name, n, k, dev):
+    shape = w.shape if isinstance(w, _Tensor) else None
+    _demand(w, name, torch.int8, shape, dev)
+    if len(shape) != 2 or shape[1] != k or n is not None and shape[0] != n:
+        raise ValueError(f"{name} must have shape ({'n' if n is None else n}, {k}), got {tuple(shape)}")
+    n = shape[0]
+    if not _good(scales, torch.float32, (n,), dev):
+        _demand(scales, name + "_scales", torch.float32, (n,), dev)
     return n
 
 
@@ -620,20 +654,23 @@ def ffn_int8_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, x_
                     workspace=None, stream=None) -> torch.Tensor:
     """y[m, n] = bf16((x @ w^T) * x_scales * w_scales + bias): x int8 codes with their x_scales float32 [m], or bf16
     rows, quantised first; w int8 [n, k] with w_scales float32 [n]; bias bf16 [n] or None."""
-    m, k = _int8_rows(x, x_scales)
-    n = _int8_weight(w, w_scales, "w", None, k)
+    dev = _get_device()
+    m, k = _int8_rows(x, x_scales, dev)
+    n = _int8_weight(w, w_scales, "w", None, k, dev)
     if bias is not None:
-        _need(bias, "bias", torch.bfloat16, (n,))
-    y = _empty((m, n), torch.bfloat16, x.device, stream) if y is None else y
-    _need(y, "y", torch.bfloat16, (m, n))
+        _demand(bias, "bias", torch.bfloat16, (n,), dev)
+    if y is None:
+        y = _empty((m, n), torch.bfloat16, x.device, stream)
+    else:
+        _demand(y, "y", torch.bfloat16, (m, n), dev)
     if workspace is not None:
-        _need(workspace, "workspace", torch.uint8)
+        _demand(workspace, "workspace", torch.uint8, workspace.shape if isinstance(workspace, _Tensor) else None, dev)
     elif x_scales is None:
         workspace = _empty(max(ffn_int8_linear_workspace_size(m, n, k), 16), torch.uint8, x.device, stream)
     st = lib.ffn_int8_linear(
         x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), m, w.data_ptr(), w_scales.data_ptr(),
         None if bias is None else bias.data_ptr(), n, k, y.data_ptr(), None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel(), _launch_stream(stream, x, x_scales, w, w_scales, bias, y, workspace))
+        0 if workspace is None else workspace.numel(), _stream_of(stream, dev))
     if st:
         _check("ffn_int8_linear", st)
     return y
@@ -643,22 +680,25 @@ def ffn_int8_forward(x: torch.Tensor, gate_up: torch.Tensor, gate_up_scales: tor
                      down_scales: torch.Tensor, x_scales=None, out=None, workspace=None, stream=None) -> torch.Tensor:
     """out[m, hidden] = down(silu(gate(x)) * up(x)) over int8 weights (gate_up [2 * inter, hidden], gate rows first; down
     [hidden, inter]; scales float32 by row); x as for ffn_int8_linear."""
-    m, hidden = _int8_rows(x, x_scales)
-    n = _int8_weight(gate_up, gate_up_scales, "gate_up", None, hidden)
+    dev = _get_device()
+    m, hidden = _int8_rows(x, x_scales, dev)
+    n = _int8_weight(gate_up, gate_up_scales, "gate_up", None, hidden, dev)
     if n % 2:
         raise ValueError(f"gate_up must have 2 * inter rows, got {n}")
     inter = n // 2
-    _int8_weight(down, down_scales, "down", hidden, inter)
-    out = _empty((m, hidden), torch.bfloat16, x.device, stream) if out is None else out
-    _need(out, "out", torch.bfloat16, (m, hidden))
+    _int8_weight(down, down_scales, "down", hidden, inter, dev)
+    if out is None:
+        out = _empty((m, hidden), torch.bfloat16, x.device, stream)
+    else:
+        _demand(out, "out", torch.bfloat16, (m, hidden), dev)
     if workspace is None:
         workspace = _empty(max(ffn_int8_workspace_size(m, hidden, inter), 16), torch.uint8, x.device, stream)
     else:
-        _need(workspace, "workspace", torch.uint8)
+        _demand(workspace, "workspace", torch.uint8, workspace.shape if isinstance(workspace, _Tensor) else None, dev)
     st = lib.ffn_int8_forward(
         x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), m, hidden, inter, gate_up.data_ptr(),
         gate_up_scales.data_ptr(), down.data_ptr(), down_scales.data_ptr(), out.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), _launch_stream(stream, x, x_scales, gate_up, gate_up_scales, down, down_scales, out, workspace))
+        workspace.numel(), _stream_of(stream, dev))
     if st:
         _check("ffn_int8_forward", st)
     return out
@@ -699,17 +739,25 @@ class Norm:
 _BLOCK_NORM = struct.Struct("@PqPPiiqqPiqPqffPPqP")
 
 
-def _norm_address(norm, name, hidden):
+def _norm_address(norm, name, hidden, dev):
     if norm is None:
         return 0
     if not isinstance(norm, Norm):
         raise TypeError(f"{name} must be a Norm")
-    if norm.hidden is not None:
+    if norm.hidden is not None and (norm.hidden != hidden or norm.device_index != dev):
         if norm.hidden != hidden:
             raise ValueError(f"{name} has {norm.hidden} weights, the rows {hidden} values")
-        if norm.device_index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on cuda:{norm.device_index}, the current device is cuda:{torch.cuda.current_device()}")
+        raise ValueError(f"{name} is on cuda:{norm.device_index}, the current device is cuda:{dev}")
     return norm._address
+
+
+def _rows_of(t, name, dtypes, shape, dev) -> int:
+    """Elements between the rows of a tensor of rows on the current device."""
+    if type(t) is _Tensor and t.shape == shape and t.dtype in dtypes and t.get_device() == dev and t.is_contiguous():
+        return shape[1]
+    ld = _row_stride(t, name, dtypes, *shape)
+    _launch_stream(None, t)
+    return ld
 
 
 def ffn_block_norm(residual: torch.Tensor, y=None, post: Norm | None = None, gate=None, gate_activation="none",
@@ -722,22 +770,25 @@ def ffn_block_norm(residual: torch.Tensor, y=None, post: Norm | None = None, gat
     itself); gate: float32 or bfloat16, [hidden], [m, hidden], [1, hidden], [m, 1] or [1, 1]; without `pre` x is None.
     residual_out may be the residual, a bf16 out may be y; store_residual=False leaves r out (None) where only x is
     wanted.  Rows of all of them may be strided."""
-    if not isinstance(residual, torch.Tensor):
+    if not isinstance(residual, _Tensor):
         raise TypeError("residual must be a torch.Tensor")
-    if residual.dim() != 2:
-        raise ValueError(f"residual must have shape (m, hidden), got {tuple(residual.shape)}")
-    m, hidden = residual.shape
-    r_ld = _row_stride(residual, "residual", _VALUES, m, hidden)
+    shape = residual.shape
+    if len(shape) != 2:
+        raise ValueError(f"residual must have shape (m, hidden), got {tuple(shape)}")
+    dev = _get_device()
+    m, hidden = shape
+    dtype = residual.dtype
+    r_ld = _rows_of(residual, "residual", _VALUES, shape, dev)
     y_ld = ro_ld = out_ld = gate_row = gate_col = 0
     if y is not None:
-        y_ld = _row_stride(y, "y", _BF16, m, hidden)
+        y_ld = _rows_of(y, "y", _BF16, shape, dev)
         if residual_out is not None:
             if not store_residual:
                 raise ValueError("residual_out is given, but store_residual is False")
+            ro_ld = _rows_of(residual_out, "residual_out", (dtype,), shape, dev)
         elif store_residual:
-            residual_out = _empty((m, hidden), residual.dtype, residual.device, stream)
-        if residual_out is not None:
-            ro_ld = _row_stride(residual_out, "residual_out", (residual.dtype,), m, hidden)
+            residual_out = _empty((m, hidden), dtype, residual.device, stream)
+            ro_ld = hidden
     elif residual_out is not None:
         raise ValueError("residual_out needs y: without it the residual does not change")
     if gate_activation not in GATE_ACTIVATIONS:
@@ -757,28 +808,34 @@ def ffn_block_norm(residual: torch.Tensor, y=None, post: Norm | None = None, gat
         gate_col = 0 if gate.shape[1] == 1 else gate.stride(1)
         if gate_col not in (0, 1) or gate_col and gate_row and gate_row < hidden:
             raise ValueError("gate must have contiguous, non-overlapping rows")
+        if gate.get_device() != dev:
+            _launch_stream(None, gate)
     if pre is None:
         if quantize or out is not None or out_scales is not None:
             raise ValueError("an output needs the norm `pre`")
     else:
-        out = _empty((m, hidden), torch.int8 if quantize else torch.bfloat16, residual.device, stream) if out is None else out
-        if quantize:
-            out_scales = _empty((m,), torch.float32, residual.device, stream) if out_scales is None else out_scales
-            _need(out, "out", torch.int8, (m, hidden))
-            _need(out_scales, "out_scales", torch.float32, (m,))
+        if out is None:
+            out = _empty((m, hidden), torch.int8 if quantize else torch.bfloat16, residual.device, stream)
+            out_ld = hidden
+        elif quantize:
+            _demand(out, "out", torch.int8, shape, dev)
             out_ld = hidden
         else:
-            if out_scales is not None:
-                raise ValueError("out_scales needs quantize")
-            out_ld = _row_stride(out, "out", _BF16, m, hidden)
-    launch = _launch_stream(stream, residual, y, gate, residual_out, out, out_scales)
+            out_ld = _rows_of(out, "out", _BF16, shape, dev)
+        if quantize:
+            if out_scales is None:
+                out_scales = _empty((m,), torch.float32, residual.device, stream)
+            else:
+                _demand(out_scales, "out_scales", torch.float32, (m,), dev)
+        elif out_scales is not None:
+            raise ValueError("out_scales needs quantize")
     args = _BLOCK_NORM.pack(
-        0 if y is None else y.data_ptr(), y_ld, _norm_address(post, "post", hidden), 0 if gate is None else gate.data_ptr(),
+        0 if y is None else y.data_ptr(), y_ld, _norm_address(post, "post", hidden, dev), 0 if gate is None else gate.data_ptr(),
         0 if gate is None else _VALUE_TYPES[gate.dtype], GATE_ACTIVATIONS[gate_activation], gate_row, gate_col,
-        residual.data_ptr(), _VALUE_TYPES[residual.dtype], r_ld, 0 if residual_out is None else residual_out.data_ptr(), ro_ld,
-        residual_scale, branch_scale, _norm_address(pre, "pre", hidden), 0 if out is None else out.data_ptr(), out_ld,
+        residual.data_ptr(), _VALUE_TYPES[dtype], r_ld, 0 if residual_out is None else residual_out.data_ptr(), ro_ld,
+        residual_scale, branch_scale, _norm_address(pre, "pre", hidden, dev), 0 if out is None else out.data_ptr(), out_ld,
         0 if out_scales is None else out_scales.data_ptr())
-    st = lib.ffn_block_norm(args, m, hidden, launch)
+    st = lib.ffn_block_norm(args, m, hidden, _stream_of(stream, dev))
     if st:
         _check("ffn_block_norm", st)
     if y is None:
