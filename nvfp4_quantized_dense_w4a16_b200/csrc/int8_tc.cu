@@ -127,17 +127,18 @@ struct PairArgs {
   int kc;           // chunks of K
   int tile_n;       // weight rows of a tile: a multiple of 32 up to 256
   int m_tiles, n_tiles;
+  int stages;       // of the ring
 };
 
 constexpr int kPairRows = 256;
 constexpr int kPairThreads = 384;
-constexpr int kPairStages = 6;
-constexpr int kPairOperand = 128 * kChunkK;              // 128 rows of x, or up to 128 weight rows
-constexpr int kPairStageBytes = 2 * kPairOperand;
-constexpr int kPairOut = kPairStages * kPairStageBytes;  // 32 rows x 32 columns of bf16 per epilogue warp
+constexpr int kPairMaxStages = 10;
+constexpr int kPairOperand = 128 * kChunkK;  // 128 rows of x, or up to 128 weight rows
+constexpr int kPairRing = 6 * 2 * kPairOperand;
+constexpr int kPairOut = kPairRing;          // 32 rows x 32 columns of bf16 per epilogue warp
 constexpr int kPairScales = kPairOut + 8 * 2048;         // [group][tile parity][scales, biases][256]
 constexpr int kPairBar = kPairScales + 2 * 2 * 2 * 256 * 4;
-constexpr int kPairSmem = kPairBar + (2 * kPairStages + 4) * 8 + 16 + 1024;  // slack for 1024-byte alignment
+constexpr int kPairSmem = kPairBar + (2 * kPairMaxStages + 4) * 8 + 16 + 1024;  // slack for 1024-byte alignment
 static_assert(kPairSmem <= 232448, "shared memory budget");
 
 // Tiles go by groups of this many row tiles, so that those which run at a time
@@ -158,8 +159,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairBar);
-  uint64_t* empty = full + kPairStages;
-  uint64_t* accfull = empty + kPairStages;
+  uint64_t* empty = full + kPairMaxStages;
+  uint64_t* accfull = empty + kPairMaxStages;
   uint64_t* accempty = accfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accempty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -168,9 +169,10 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
   const int rank = (int)cluster_rank();
   const int first = blockIdx.x / 2, step = gridDim.x / 2, total = a.m_tiles * a.n_tiles;
   const int half = a.tile_n / 2;  // weight rows of a CTA
+  const int stages = a.stages, stage_bytes = kPairOperand + half * kChunkK;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);  // (CTA 0's)
       mbar_init(&empty[s], 1);
     }
@@ -212,7 +214,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
           row = !weights ? mt * kPairRows + rank * 128 : SILU ? (int)(nt * half + rank * a.cols) : nt * a.tile_n + rank * half;
         }
         __device__ __forceinline__ void next(const PairArgs& a, int step, int total, int half, int rank) {
-          if (++s == kPairStages) s = 0;
+          if (++s == a.stages) s = 0;
           if (++c < a.kc) return;
           c = 0;
           t += step;
@@ -224,27 +226,27 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
       if (first < total) w.place(a, half, rank), x.place(a, half, rank);
       auto load_weights = [&] {
         if (rank == 0) mbar_arrive_expect_tx(&full[w.s], bytes);
-        tma_load_pair(smem + w.s * kPairStageBytes + kPairOperand, &wmap, w.c * kChunkK, w.row, bars + 8 * w.s);
+        tma_load_pair(smem + w.s * stage_bytes + kPairOperand, &wmap, w.c * kChunkK, w.row, bars + 8 * w.s);
         w.next(a, step, total, half, rank);
       };
       auto load_rows = [&] {
-        tma_load_pair(smem + x.s * kPairStageBytes, &xmap, x.c * kChunkK, x.row, bars + 8 * x.s);
+        tma_load_pair(smem + x.s * stage_bytes, &xmap, x.c * kChunkK, x.row, bars + 8 * x.s);
         x.next(a, step, total, half, rank);
       };
       int ahead = 0, u = 0;
-      for (; ahead < kPairStages && w.t < total; ++ahead) load_weights();
+      for (; ahead < stages && w.t < total; ++ahead) load_weights();
       griddep_wait();
       griddep_launch_dependents();
       for (; u < ahead; ++u) load_rows();
       uint32_t parity = 0;  // of the stage's last use
       for (; w.t < total; ++u) {
         if (!mbar_wait(&empty[w.s], parity, abort_flag, err, 1)) break;
-        if (w.s == kPairStages - 1) parity ^= 1;
+        if (w.s == stages - 1) parity ^= 1;
         load_weights();
         load_rows();
       }
       if (rank == 0)  // (CTA 1 leaves after this one)
-        for (int r = max(0, u - kPairStages); r < u; ++r) drain(&full[r % kPairStages], (r / kPairStages) & 1);
+        for (int r = max(0, u - stages); r < u; ++r) drain(&full[r % stages], (r / stages) & 1);
     }
   } else if (warp == 1) {
     // --------------------------------------------- MMAs, CTA 0's for both
@@ -263,8 +265,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
         ok = mbar_wait(&full[s], parity, abort_flag, err, 2);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
-        const uint64_t xd = smem_desc_sw128(smem_u32(smem + s * kPairStageBytes));
-        const uint64_t wd = smem_desc_sw128(smem_u32(smem + s * kPairStageBytes + kPairOperand));
+        const uint64_t xd = smem_desc_sw128(smem_u32(smem + s * stage_bytes));
+        const uint64_t wd = smem_desc_sw128(smem_u32(smem + s * stage_bytes + kPairOperand));
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_pair_s8(tmem + 256 * buf, xd + 2 * kk, wd + 2 * kk, idesc, (c | kk) ? 1u : 0u);
@@ -272,7 +274,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
           if (c + 1 == a.kc) commit_pair(&accfull[buf]);
         }
         __syncwarp();
-        if (++s == kPairStages) s = 0, parity ^= 1;
+        if (++s == stages) s = 0, parity ^= 1;
       }
     }
   } else if (warp >= 4) {
@@ -454,8 +456,7 @@ __global__ void __launch_bounds__(kFewThreads)
 
   if (warp == 0) {
     if (lane == 0) {
-      auto load_weights = [&](int u) {
-        const int s = u % a.stages, k = (c0 + u) * kChunkK;
+      auto load_weights = [&](int s, int k) {
         uint8_t* at = ring + s * stage_bytes;
         mbar_arrive_expect_tx(&full[s], stage_bytes);
         if (SILU) {
@@ -465,28 +466,28 @@ __global__ void __launch_bounds__(kFewThreads)
           tma_load_2d(at, &wmap, k, (int)(tile * 128), &full[s]);
         }
       };
-      auto load_rows = [&](int u) {
-        const int s = u % a.stages;
-        tma_load_2d(ring + s * stage_bytes + kFewWeights, &xmap, (c0 + u) * kChunkK, 0, &full[s]);
-      };
+      auto load_rows = [&](int s, int k) { tma_load_2d(ring + s * stage_bytes + kFewWeights, &xmap, k, 0, &full[s]); };
       const int ahead = min(units, a.stages);
-      for (int u = 0; u < ahead; ++u) load_weights(u);
+      for (int u = 0; u < ahead; ++u) load_weights(u, (c0 + u) * kChunkK);
       griddep_wait();
       griddep_launch_dependents();
-      for (int u = 0; u < ahead; ++u) load_rows(u);
-      int u = ahead;
+      for (int u = 0; u < ahead; ++u) load_rows(u, (c0 + u) * kChunkK);
+      int u = ahead, s = 0;
+      uint32_t parity = 0;
       for (; u < units; ++u) {
-        if (!mbar_wait(&empty[u % a.stages], ((u / a.stages) - 1) & 1, abort_flag, err, 1)) break;
-        load_weights(u);
-        load_rows(u);
+        if (!mbar_wait(&empty[s], parity, abort_flag, err, 1)) break;
+        load_weights(s, (c0 + u) * kChunkK);
+        load_rows(s, (c0 + u) * kChunkK);
+        if (++s == a.stages) s = 0, parity ^= 1;
       }
       for (int r = max(0, u - a.stages); r < u; ++r) drain(&full[r % a.stages], (r / a.stages) & 1);
     }
   } else if (warp == 1) {
     const uint32_t idesc = idesc_s8_s32(128, a.n);
+    int s = 0;
+    uint32_t parity = 0;
     for (int u = 0; u < units; ++u) {
-      const int s = u % a.stages;
-      ok = mbar_wait(&full[s], (u / a.stages) & 1, abort_flag, err, 2);
+      ok = mbar_wait(&full[s], parity, abort_flag, err, 2);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc_fence_after();
       const uint64_t wd = smem_desc_sw128(smem_u32(ring + s * stage_bytes));
@@ -498,6 +499,7 @@ __global__ void __launch_bounds__(kFewThreads)
         if (u + 1 == units) mma_commit(done);
       }
       __syncwarp();
+      if (++s == a.stages) s = 0, parity ^= 1;
     }
   } else {
     griddep_wait();
@@ -613,7 +615,7 @@ template <bool SILU>
 cudaError_t launch_pair(const Int8Product& p, cudaStream_t s) {
   const int64_t cols = SILU ? p.n / 2 : p.n;
   const int clusters = device_sms() / 2;
-  PairArgs a{p.xs, p.ws, p.bias, p.y, p.m, cols, (int)ceil_div(p.k, kChunkK), 256, (int)ceil_div(p.m, kPairRows), 0};
+  PairArgs a{p.xs, p.ws, p.bias, p.y, p.m, cols, (int)ceil_div(p.k, kChunkK), 256, (int)ceil_div(p.m, kPairRows), 0, 0};
   // The widest tile, or one of fewer columns that leaves fewer pairs of SMs idle.
   int64_t best = INT64_MAX;
   for (int n = 256; n >= 64; n -= 32) {
@@ -622,6 +624,7 @@ cudaError_t launch_pair(const Int8Product& p, cudaStream_t s) {
     if (cost < best) best = cost, a.tile_n = n;
   }
   a.n_tiles = (int)ceil_div(cols, SILU ? a.tile_n / 2 : a.tile_n);
+  a.stages = std::min(kPairMaxStages, kPairRing / (kPairOperand + a.tile_n / 2 * kChunkK));
   CUtensorMap xmap, wmap;
   if (!encode_rows(&xmap, p.x, p.m, p.k, 128) || !encode_rows(&wmap, p.w, p.n, p.k, a.tile_n / 2)) return cudaErrorInvalidValue;
   auto kern = int8_pair_kernel<SILU>;
