@@ -132,7 +132,8 @@ struct PairArgs {
 
 constexpr int kPairRows = 256;
 constexpr int kPairThreads = 384;
-constexpr int kPairMaxStages = 10;
+constexpr int kPairUnit = 2;  // chunks of K in a stage
+constexpr int kPairMaxStages = 5;
 constexpr int kPairOperand = 128 * kChunkK;  // 128 rows of x, or up to 128 weight rows
 constexpr int kPairRing = 6 * 2 * kPairOperand;
 constexpr int kPairOut = kPairRing;          // 32 rows x 32 columns of bf16 per epilogue warp
@@ -169,7 +170,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
   const int rank = (int)cluster_rank();
   const int first = blockIdx.x / 2, step = gridDim.x / 2, total = a.m_tiles * a.n_tiles;
   const int half = a.tile_n / 2;  // weight rows of a CTA
-  const int stages = a.stages, stage_bytes = kPairOperand + half * kChunkK;
+  const int stages = a.stages, chunk_bytes = kPairOperand + half * kChunkK, stage_bytes = kPairUnit * chunk_bytes;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -203,7 +204,6 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
       // What to load goes by two cursors, of the weights and of the rows; places of
       // tiles cost divisions, which a cursor pays once a tile (each unit's own took
       // 850 cycles of the 512 that its MMAs take).
-      const uint32_t bytes = 2 * (kPairOperand + half * kChunkK);  // of both CTAs
       const uint32_t bars = in_cta(full, 0);
       struct Cursor {
         int t, c = 0, s = 0, row = 0;
@@ -215,7 +215,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
         }
         __device__ __forceinline__ void next(const PairArgs& a, int step, int total, int half, int rank) {
           if (++s == a.stages) s = 0;
-          if (++c < a.kc) return;
+          c += kPairUnit;
+          if (c < a.kc) return;
           c = 0;
           t += step;
           if (t < total) place(a, half, rank);
@@ -225,12 +226,16 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
       w.weights = true, x.weights = false;
       if (first < total) w.place(a, half, rank), x.place(a, half, rank);
       auto load_weights = [&] {
-        if (rank == 0) mbar_arrive_expect_tx(&full[w.s], bytes);
-        tma_load_pair(smem + w.s * stage_bytes + kPairOperand, &wmap, w.c * kChunkK, w.row, bars + 8 * w.s);
+        const int n = min(kPairUnit, a.kc - w.c);
+        if (rank == 0) mbar_arrive_expect_tx(&full[w.s], 2 * n * chunk_bytes);  // of both CTAs
+        for (int j = 0; j < n; ++j)
+          tma_load_pair(smem + w.s * stage_bytes + j * chunk_bytes + kPairOperand, &wmap, (w.c + j) * kChunkK, w.row, bars + 8 * w.s);
         w.next(a, step, total, half, rank);
       };
       auto load_rows = [&] {
-        tma_load_pair(smem + x.s * stage_bytes, &xmap, x.c * kChunkK, x.row, bars + 8 * x.s);
+        const int n = min(kPairUnit, a.kc - x.c);
+        for (int j = 0; j < n; ++j)
+          tma_load_pair(smem + x.s * stage_bytes + j * chunk_bytes, &xmap, (x.c + j) * kChunkK, x.row, bars + 8 * x.s);
         x.next(a, step, total, half, rank);
       };
       int ahead = 0, u = 0;
@@ -261,17 +266,22 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
       }
-      for (int c = 0; c < a.kc; ++c) {
+      for (int c = 0; c < a.kc; c += kPairUnit) {
         ok = mbar_wait(&full[s], parity, abort_flag, err, 2);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
-        const uint64_t xd = smem_desc_sw128(smem_u32(smem + s * stage_bytes));
-        const uint64_t wd = smem_desc_sw128(smem_u32(smem + s * stage_bytes + kPairOperand));
+        const uint32_t at = smem_u32(smem + s * stage_bytes);
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_pair_s8(tmem + 256 * buf, xd + 2 * kk, wd + 2 * kk, idesc, (c | kk) ? 1u : 0u);
+          for (int j = 0; j < kPairUnit; ++j) {
+            if (c + j >= a.kc) break;
+            const uint64_t xd = smem_desc_sw128(at + j * chunk_bytes), wd = smem_desc_sw128(at + j * chunk_bytes + kPairOperand);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_pair_s8(tmem + 256 * buf, xd + 2 * kk, wd + 2 * kk, idesc, (c | j | kk) ? 1u : 0u);
+          }
           commit_pair(&empty[s]);
-          if (c + 1 == a.kc) commit_pair(&accfull[buf]);
+          if (c + kPairUnit >= a.kc) commit_pair(&accfull[buf]);
         }
         __syncwarp();
         if (++s == stages) s = 0, parity ^= 1;
@@ -536,43 +546,55 @@ __global__ void __launch_bounds__(kFewThreads)
   if (lane < (int)splits)
     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(bad) : "r"(in_cta(const_cast<int*>(abort_flag), lane)));
   if (warp >= 2) {
-    // Rows of x by CTA; a warp has 128 sums of a row, four a lane.
-    const int wq = warp - 2, per = SILU ? 2 : 1;  // rows of a warp at a time
+    // Rows of x by CTA; a warp has 128 sums of a row, four a lane, and kAtOnce such rows under way.
+    constexpr int kAtOnce = 2, kPer = SILU ? 2 : 1;  // (with silu_mul half a warp has a row: gate and up sums)
+    const int wq = warp - 2, mine = 4 * (SILU ? lane & 15 : lane);
+    const int first = (rank * 4 + wq) * kPer + (SILU ? lane >> 4 : 0), step = (int)splits * 4 * kPer;
     ok = __all_sync(0xffffffffu, bad == 0);
-    for (int i = (rank * 4 + wq) * per + (SILU ? lane >> 4 : 0); ok && i < a.m; i += (int)splits * 4 * per) {
-      const float xs = a.xs[i];
-      int4 g = make_int4(0, 0, 0, 0), u = g;
-      const int at = i * 128 + 4 * (SILU ? lane & 15 : lane);
+    for (int i0 = first; ok && i0 < a.m; i0 += kAtOnce * step) {
+      int4 g[kAtOnce], u[kAtOnce];
 #pragma unroll
-      for (uint32_t r = 0; r < kFewMaxSplits; ++r) {
-        if (r >= splits) break;
-        const uint32_t from = in_cta(sums + at, r);
-        const int4 p = load_cluster(from);
-        g.x += p.x, g.y += p.y, g.z += p.z, g.w += p.w;
-        if (SILU) {
-          const int4 p2 = load_cluster(from + 64 * 4);
-          u.x += p2.x, u.y += p2.y, u.z += p2.z, u.w += p2.w;
+      for (int z = 0; z < kAtOnce; ++z) g[z] = u[z] = make_int4(0, 0, 0, 0);
+      for (uint32_t r = 0; r < splits; ++r) {
+        const uint32_t from = in_cta(sums + mine, r);
+        int4 p[kAtOnce], q[kAtOnce];
+#pragma unroll
+        for (int z = 0; z < kAtOnce; ++z) {
+          const int i = min(i0 + z * step, a.n - 1);  // (a row that is not there is read from the last)
+          p[z] = load_cluster(from + i * 512);
+          if (SILU) q[z] = load_cluster(from + i * 512 + 64 * 4);
+        }
+#pragma unroll
+        for (int z = 0; z < kAtOnce; ++z) {
+          g[z].x += p[z].x, g[z].y += p[z].y, g[z].z += p[z].z, g[z].w += p[z].w;
+          if (SILU) u[z].x += q[z].x, u[z].y += q[z].y, u[z].z += q[z].z, u[z].w += q[z].w;
         }
       }
-      const int gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
-      uint16_t b[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float v = int8_scaled(gs[j], xs, s0[j]);
-        if (SILU)
-          v = int8_silu_mul(v, int8_scaled(us[j], xs, s1[j]));
-        else if (a.bias)
-          v = __fadd_rn(v, s1[j]);
-        b[j] = f32_to_bf16_bits(v);
-      }
-      uint16_t* y = a.y + (int64_t)i * a.cols + col;
-      if (a.cols % 4 == 0) {
-        if (col < a.cols)
-          *reinterpret_cast<uint2*>(y) = make_uint2(b[0] | ((uint32_t)b[1] << 16), b[2] | ((uint32_t)b[3] << 16));
-      } else {
+      for (int z = 0; z < kAtOnce; ++z) {
+        const int i = i0 + z * step;
+        if (i >= a.m) break;
+        const float xs = a.xs[i];
+        const int gs[4] = {g[z].x, g[z].y, g[z].z, g[z].w}, us[4] = {u[z].x, u[z].y, u[z].z, u[z].w};
+        uint16_t b[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (col + j < a.cols) y[j] = b[j];
+        for (int j = 0; j < 4; ++j) {
+          float v = int8_scaled(gs[j], xs, s0[j]);
+          if (SILU)
+            v = int8_silu_mul(v, int8_scaled(us[j], xs, s1[j]));
+          else if (a.bias)
+            v = __fadd_rn(v, s1[j]);
+          b[j] = f32_to_bf16_bits(v);
+        }
+        uint16_t* y = a.y + (int64_t)i * a.cols + col;
+        if (a.cols % 4 == 0) {
+          if (col < a.cols)
+            *reinterpret_cast<uint2*>(y) = make_uint2(b[0] | ((uint32_t)b[1] << 16), b[2] | ((uint32_t)b[3] << 16));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (col + j < a.cols) y[j] = b[j];
+        }
       }
     }
   }
@@ -611,20 +633,66 @@ bool encode_rows(CUtensorMap* map, const void* p, int64_t rows, int64_t k, int b
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// About how long a launch takes, in ns, by what it was fitted to: n x k weights of 512^2 to 16384 x 4096 and 5120 x
+// 17408, 2 to 128 rows, codes given, in a graph.
+int64_t stream_ns(int64_t cols, int64_t k, bool silu) { return (silu ? 2 : 1) * cols * k / 6200; }  // of the weights
+
+struct PairPlan {
+  int tile_n;
+  int64_t ns;
+};
+
+// The columns of a tile: wide ones take fewer cycles a product, but may leave pairs of SMs idle in the last wave.
+// A chunk of K measures 400 cycles for up to 80 columns, and 300 + 1.25 a column from there (64 pairs of SMs at a time:
+// the traffic from L2, 12 TB/s, and 390 cycles of barriers a stage that even an empty one takes; 512 at 256 columns by
+// the MMAs alone).  512 rows, 5120 x 17408, tiles of 96, 128, 160, 192, 256: 63, 64, 42, 44, 48 us.
+PairPlan pair_plan(int64_t m, int64_t cols, int64_t k, bool silu) {
+  const int clusters = device_sms() / 2;
+  const int64_t kc = ceil_div(k, kChunkK), m_tiles = ceil_div(m, kPairRows);
+  int64_t least = INT64_MAX;
+  PairPlan best{};
+  for (int n = 256; n >= 64; n -= 32) {
+    const int64_t waves = ceil_div(m_tiles * ceil_div(cols, silu ? n / 2 : n), clusters);
+    const int64_t cycles = waves * kc * std::max(400, 300 + 5 * n / 4) + 4 * n;
+    if (cycles < least) least = cycles, best.tile_n = n;
+  }
+  const int64_t loop = least * 10 / 19, stream = stream_ns(cols, k, silu);
+  best.ns = 2800 + std::max(loop, stream) + std::min(loop, stream) / 2;
+  return best;
+}
+
+struct FewPlan {
+  int splits;
+  int64_t ns;
+};
+
+// Clusters of 1, 2, ... CTAs that are resident at a time, an SM each or two an SM (measured; a cluster stays
+// within a part of the GPU).  The most CTAs that start at once: with one more wave of clusters 5120 x 17408 takes
+// 24 us, cut into 8, and 18.0, cut into 6.  Short ranges of K do better with one CTA an SM, beside which the next
+// kernel's can start: 4096 x 4096 cut into 4 and 8 6.5 and 7.2 us, 4096 x 12288 13.7 and 12.0.
+FewPlan few_plan(int64_t m, int64_t cols, int64_t k, bool silu) {
+  constexpr int kOneAnSm[] = {148, 74, 45, 33, 26, 22, 15, 15}, kTwoAnSm[] = {296, 148, 90, 68, 54, 45, 36, 33};
+  const int64_t tiles = ceil_div(cols, silu ? 64 : 128), kc = ceil_div(k, kChunkK);
+  int one = 1, two = 1;
+  for (int c = 2; c <= kFewMaxSplits && c <= kc; ++c) {
+    if (tiles <= kOneAnSm[c - 1]) one = c;
+    if (tiles <= kTwoAnSm[c - 1]) two = c;
+  }
+  FewPlan p;
+  p.splits = ceil_div(kc, one) <= 12 ? one : two;
+  const int64_t rounds = ceil_div(tiles, kTwoAnSm[p.splits - 1]), loop = 250 * rounds * ceil_div(kc, p.splits);
+  p.ns = 3400 + 200 * p.splits + 40 * ceil_div(m, 16) * 16 + std::max(loop, stream_ns(cols, k, silu));
+  return p;
+}
+
 template <bool SILU>
 cudaError_t launch_pair(const Int8Product& p, cudaStream_t s) {
   const int64_t cols = SILU ? p.n / 2 : p.n;
   const int clusters = device_sms() / 2;
   PairArgs a{p.xs, p.ws, p.bias, p.y, p.m, cols, (int)ceil_div(p.k, kChunkK), 256, (int)ceil_div(p.m, kPairRows), 0, 0};
-  // The widest tile, or one of fewer columns that leaves fewer pairs of SMs idle.
-  int64_t best = INT64_MAX;
-  for (int n = 256; n >= 64; n -= 32) {
-    const int64_t waves = ceil_div(a.m_tiles * ceil_div(cols, SILU ? n / 2 : n), clusters);
-    const int64_t cost = waves * (a.kc * std::max(2 * n, 220 + n) + 1500);
-    if (cost < best) best = cost, a.tile_n = n;
-  }
+  a.tile_n = pair_plan(p.m, cols, p.k, SILU).tile_n;
   a.n_tiles = (int)ceil_div(cols, SILU ? a.tile_n / 2 : a.tile_n);
-  a.stages = std::min(kPairMaxStages, kPairRing / (kPairOperand + a.tile_n / 2 * kChunkK));
+  a.stages = std::min(kPairMaxStages, kPairRing / (kPairUnit * (kPairOperand + a.tile_n / 2 * kChunkK)));
   CUtensorMap xmap, wmap;
   if (!encode_rows(&xmap, p.x, p.m, p.k, 128) || !encode_rows(&wmap, p.w, p.n, p.k, a.tile_n / 2)) return cudaErrorInvalidValue;
   auto kern = int8_pair_kernel<SILU>;
@@ -641,17 +709,7 @@ cudaError_t launch_few(const Int8Product& p, cudaStream_t s) {
   const int64_t cols = SILU ? p.n / 2 : p.n, tiles = ceil_div(cols, SILU ? 64 : 128);
   FewArgs a{p.xs, p.ws, p.bias, p.y, cols, (int)p.m, (int)ceil_div(p.k, kChunkK), (int)ceil_div(p.m, 16) * 16, 0};
   a.stages = std::min(kFewMaxStages, kFewRing / (kFewWeights + a.n * kChunkK));
-  // Clusters of 1, 2, ... CTAs that are resident at a time, an SM each or two an SM (measured; a cluster stays
-  // within a part of the GPU).  The most CTAs that start at once: with one more wave of clusters 5120 x 17408 takes
-  // 24 us, cut into 8, and 18.0, cut into 6.  Short ranges of K do better with one CTA an SM, beside which the next
-  // kernel's can start: 4096 x 4096 cut into 4 and 8 6.5 and 7.2 us, 4096 x 12288 13.7 and 12.0.
-  constexpr int kOneAnSm[] = {148, 74, 45, 33, 26, 22, 15, 15}, kTwoAnSm[] = {296, 148, 90, 68, 54, 45, 36, 33};
-  int one = 1, two = 1;
-  for (int c = 2; c <= kFewMaxSplits && c <= a.kc; ++c) {
-    if (tiles <= kOneAnSm[c - 1]) one = c;
-    if (tiles <= kTwoAnSm[c - 1]) two = c;
-  }
-  const unsigned splits = (unsigned)(ceil_div(a.kc, one) <= 12 ? one : two);
+  const unsigned splits = (unsigned)few_plan(p.m, cols, p.k, SILU).splits;
   CUtensorMap xmap, wmap;
   if (!encode_rows(&xmap, p.x, p.m, p.k, a.n) || !encode_rows(&wmap, p.w, p.n, p.k, SILU ? 64 : 128)) return cudaErrorInvalidValue;
   auto kern = int8_few_kernel<SILU>;
@@ -660,13 +718,21 @@ cudaError_t launch_few(const Int8Product& p, cudaStream_t s) {
   return launch_pdl_clusters(kern, dim3((unsigned)(tiles * splits)), splits, dim3(kFewThreads), kFewSmem, s, xmap, wmap, a);
 }
 
-constexpr int64_t kFewRows = 128;
+constexpr int64_t kFewRows = 128;  // (the sums of 128 rows are two thirds of the ring)
+
+// Few rows of large weights are cut along K; small weights, whose tiles the pairs of SMs take in one wave, are not worth
+// a cluster's exchange of sums.  Cut and in pairs, in us: 512 x 512, 2 and 128 rows 3.7, 7.4 and 3.6, 3.9; 2048 x 2048, 2,
+// 16, 32, 128 rows 5.3, 6.3, 6.9, 9.8 and 7.2, 6.0, 6.0, 6.1; 4096 x 4096, 16, 64, 128 rows 7.5, 8.5, 11.9 and 13, 10.9,
+// 11.1; 5120 x 17408, 128 rows 26 and 34.
+bool use_few(int64_t m, int64_t cols, int64_t k, bool silu) {
+  return m <= kFewRows && few_plan(m, cols, k, silu).ns < pair_plan(m, cols, k, silu).ns;
+}
 
 }  // namespace
 
 cudaError_t launch_int8_product(const Int8Product& p, cudaStream_t s) {
   ProfScope prof(s, p.silu_mul ? "int8_gate_up" : "int8_product");
-  if (p.m <= kFewRows) return p.silu_mul ? launch_few<true>(p, s) : launch_few<false>(p, s);
+  if (use_few(p.m, p.silu_mul ? p.n / 2 : p.n, p.k, p.silu_mul)) return p.silu_mul ? launch_few<true>(p, s) : launch_few<false>(p, s);
   return p.silu_mul ? launch_pair<true>(p, s) : launch_pair<false>(p, s);
 }
 
