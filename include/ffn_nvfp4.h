@@ -443,11 +443,9 @@ ffn_status ffn_int8_quantize(const void* x_bf16, int64_t m, int64_t k, int64_t r
  * order, each rounded once to fp32.  m == 0 is a no-op.  Allocates nothing and
  * does not synchronise.  The workspace (ffn_int8_linear_workspace_size bytes;
  * not needed with x_scales) may be shared by calls on one stream, and its size
- * serves every smaller m.  Launched with programmatic stream serialisation: the
- * weights may be read while the kernel before in the stream is finishing, all
- * else after it has completed.  So a weight must not come from a kernel that
- * lets the next one start early (those of this library that write weights,
- * ffn_int8_quantize among them, do not).
+ * serves every smaller m.  Stream order is kept for every buffer, the weights
+ * among them: the launches use programmatic stream serialisation, but a call's
+ * first one reads and writes nothing before the work ahead of it has completed.
  * Errors: FFN_ERR_SHAPE unless k is a positive multiple of 32 and n > 0, or for
  * buffers of more than 2^40 elements; FFN_ERR_UNSUPPORTED for k > FFN_INT8_MAX_K. */
 ffn_status ffn_int8_linear_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
@@ -463,7 +461,7 @@ ffn_status ffn_int8_linear(const void* x, const float* x_scales, int64_t m, cons
  * Numerics: gate and up stay fp32 (their exact sums times the two scales);
  * h = silu(gate) * up is rounded to bf16 and quantised as ffn_int8_quantize
  * does; the down projection is ffn_int8_linear's.  Everything else (workspace,
- * launch order, m == 0, errors) as for ffn_int8_linear, with
+ * stream order, m == 0, errors) as for ffn_int8_linear, with
  * ffn_int8_workspace_size bytes, which are always needed. */
 ffn_status ffn_int8_workspace_size(int64_t m, int64_t hidden, int64_t inter, size_t* bytes);
 ffn_status ffn_int8_forward(const void* x, const float* x_scales, int64_t m, int64_t hidden, int64_t inter,

@@ -46,10 +46,11 @@ cudaError_t product(ffn::Int8Product p, uint8_t* codes, uint8_t* scales, cudaStr
   if (!p.xs) {
     int8_t* xq = reinterpret_cast<int8_t*>(codes);
     float* xs = reinterpret_cast<float*>(scales);
-    const cudaError_t e = ffn::launch_int8_quantize(p.x, p.m, p.k, p.k, xq, xs, true, s);
+    const cudaError_t e = ffn::launch_int8_quantize(p.x, p.m, p.k, p.k, xq, xs, s);
     if (e != cudaSuccess) return e;
     p.x = xq;
     p.xs = xs;
+    p.first = false;
   }
   return ffn::launch_int8_product(p, s);
 }
@@ -83,7 +84,7 @@ ffn_status ffn_int8_quantize(const void* x_bf16, int64_t m, int64_t k, int64_t r
   if (!aligned16(x_bf16) || row_stride % 8 || !aligned16(codes) || !aligned(scales, 4)) return FFN_ERR_ALIGNMENT;
   if (ffn_status st = ffn::moe_precheck()) return st;
   return ffn::moe_status(
-      ffn::launch_int8_quantize(x_bf16, m, k, row_stride, codes, scales, false, reinterpret_cast<cudaStream_t>(stream)));
+      ffn::launch_int8_quantize(x_bf16, m, k, row_stride, codes, scales, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 ffn_status ffn_int8_linear_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
@@ -107,7 +108,7 @@ ffn_status ffn_int8_linear(const void* x, const float* x_scales, int64_t m, cons
   if (ffn_status st = ffn::moe_precheck()) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const ffn::Int8Product p{x, x_scales, m, w, w_scales, static_cast<const uint16_t*>(bias), n, k, static_cast<uint16_t*>(y), false};
+  const ffn::Int8Product p{x, x_scales, m, w, w_scales, static_cast<const uint16_t*>(bias), n, k, static_cast<uint16_t*>(y), false, true};
   return ffn::moe_status(product(p, ws + c.xq, ws + c.xs, s));
 }
 
@@ -134,10 +135,10 @@ ffn_status ffn_int8_forward(const void* x, const float* x_scales, int64_t m, int
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint16_t* h = reinterpret_cast<uint16_t*>(ws + c.h);
-  cudaError_t e = product(ffn::Int8Product{x, x_scales, m, gate_up, gate_up_scales, nullptr, 2 * inter, hidden, h, true},
+  cudaError_t e = product(ffn::Int8Product{x, x_scales, m, gate_up, gate_up_scales, nullptr, 2 * inter, hidden, h, true, true},
                           ws + c.xq, ws + c.xs, s);
   if (e == cudaSuccess)
-    e = product(ffn::Int8Product{h, nullptr, m, down, down_scales, nullptr, hidden, inter, static_cast<uint16_t*>(out), false},
+    e = product(ffn::Int8Product{h, nullptr, m, down, down_scales, nullptr, hidden, inter, static_cast<uint16_t*>(out), false, false},
                 ws + c.hq, ws + c.hs, s);
   return ffn::moe_status(e);
 }

@@ -7,9 +7,8 @@
 namespace ffn {
 
 // codes and scales of bf16 rows of k columns (a multiple of 8), row i at i * stride.
-// chained: the next launch is a product of these rows.
 cudaError_t launch_int8_quantize(const void* x, int64_t m, int64_t k, int64_t stride, int8_t* codes, float* scales,
-                                 bool chained, cudaStream_t s);
+                                 cudaStream_t s);
 
 // One projection of int8 rows.  Plain: y bf16 [m, n].  With silu_mul the weight
 // holds n / 2 gate rows, then n / 2 up rows, and y is h bf16 [m, n / 2].
@@ -23,6 +22,10 @@ struct Int8Product {
   int64_t n, k;
   uint16_t* y;
   bool silu_mul;
+  // The first launch of a call: what is before it in the stream may be writing the
+  // weights.  A later one starts when an earlier one of the call has waited for all
+  // that, and reads weights ahead of its own wait.
+  bool first;
 };
 cudaError_t launch_int8_product(const Int8Product& p, cudaStream_t s);
 // The same for one row, bf16 as well, whose quantisation is part of it.

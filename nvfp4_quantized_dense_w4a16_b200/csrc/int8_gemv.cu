@@ -4,7 +4,7 @@
 // what happens before and after it.  So one launch does it all: a thread holds the
 // codes of its places in K for every weight row that its CTA takes, which it makes
 // itself from a bf16 row (whose largest magnitude is a maximum over the CTA), and the
-// first weights are under way before the kernel ahead in the stream has completed.
+// first weights are under way before it waits for the kernel ahead that makes the row.
 // Four products an instruction; a warp's sum is one reduction of integers.
 // In a graph, from a bf16 row (from codes): 4096 x 4096 6.6 us (5.7), 24576 x 4096 19.6
 // (18.1, 5.6 TB/s), 4096 x 12288 12.4 (10.0); quantisation and the product on the tensor
@@ -37,6 +37,7 @@ struct GemvArgs {
   int64_t k, cols;   // cols of y; with silu_mul the weight has 2 * cols rows
   int per_cta;       // columns of y of a CTA
   int lanes;         // threads along K: a power of two from 32 on
+  bool first;        // (Int8Product::first)
 };
 
 __device__ __forceinline__ int4 load_weights(const int8_t* p) {
@@ -78,6 +79,7 @@ __global__ void __launch_bounds__(kThreads, 2) int8_gemv_kernel(const GemvArgs a
     }
   };
   const int blocks = (rows + kBlockRows - 1) / kBlockRows;
+  if (a.first) griddep_wait();
   fetch(g, min(rows, kBlockRows));
   griddep_wait();
   griddep_launch_dependents();
@@ -165,7 +167,7 @@ bool int8_gemv_serves(int64_t m, int64_t k) { return m == 1 && k <= kMaxVecs * k
 
 cudaError_t launch_int8_gemv(const Int8Product& p, cudaStream_t s) {
   const int64_t cols = p.silu_mul ? p.n / 2 : p.n;
-  GemvArgs a{p.x, p.xs, p.w, p.ws, p.bias, p.y, p.k, cols, 0, 0};
+  GemvArgs a{p.x, p.xs, p.w, p.ws, p.bias, p.y, p.k, cols, 0, 0, p.first};
   // Threads along K and vectors a thread: the fewest idle places, then the most threads.
   const int vecs = (int)(p.k / kVecBytes);
   int v = 0, least = INT32_MAX;

@@ -14,16 +14,13 @@ using namespace sm100;
 // A row stays in registers between its largest magnitude and its codes: a group of
 // `threads` threads (a warp or more of a CTA's 256, or the CTA) holds N vectors of 8
 // values each; longer rows are read twice.  Bound by memory traffic, 3 bytes a value,
-// for many rows; by its latency for few.  CHAINED: the next kernel is a product of
-// this call, which waits before it reads the rows, and may start.  A quantisation by
-// itself may be that of a weight, which a product reads without waiting: it lets
-// nothing start before its end.
-template <int N, bool CHAINED>
+// for many rows; by its latency for few.
+template <int N>
 __global__ void __launch_bounds__(512)
     int8_quantize_kernel(const uint16_t* __restrict__ x, int64_t m, int64_t k, int64_t stride, int threads,
                          int8_t* __restrict__ codes, float* __restrict__ scales) {
   griddep_wait();
-  if (CHAINED) griddep_launch_dependents();
+  griddep_launch_dependents();
   __shared__ uint32_t part[16];
   const int groups = blockDim.x / threads, g = threadIdx.x / threads, mine = threadIdx.x - g * threads;
   const int warps = threads / 32, first = g * warps;
@@ -60,17 +57,16 @@ __global__ void __launch_bounds__(512)
 
 template <int N>
 cudaError_t launch_one(const void* x, int64_t m, int64_t k, int64_t stride, int threads, int8_t* codes, float* scales,
-                       bool chained, cudaStream_t s) {
+                       cudaStream_t s) {
   const int block = threads > 256 ? threads : 256 / threads * threads, groups = block / threads;
-  auto kern = chained ? int8_quantize_kernel<N, true> : int8_quantize_kernel<N, false>;
-  return launch_pdl(kern, dim3((unsigned)((m + groups - 1) / groups)), dim3(block), 0, s, static_cast<const uint16_t*>(x), m, k,
+  return launch_pdl(int8_quantize_kernel<N>, dim3((unsigned)((m + groups - 1) / groups)), dim3(block), 0, s, static_cast<const uint16_t*>(x), m, k,
                     stride, threads, codes, scales);
 }
 
 }  // namespace
 
 cudaError_t launch_int8_quantize(const void* x, int64_t m, int64_t k, int64_t stride, int8_t* codes, float* scales,
-                                 bool chained, cudaStream_t s) {
+                                 cudaStream_t s) {
   ProfScope prof(s, "int8_quantize");
   // Few rows: two vectors a thread; many: four, so that a row's cost is shared by as many values.
   const int64_t vecs = k / 8;
@@ -78,8 +74,8 @@ cudaError_t launch_int8_quantize(const void* x, int64_t m, int64_t k, int64_t st
   const int per = few ? 2 : 4;
   const int64_t want = (vecs + 32 * per - 1) / (32 * per) * 32;
   const int threads = (int)(want < 512 ? want : 512);
-  if (few && vecs <= 2 * 512) return launch_one<2>(x, m, k, stride, threads, codes, scales, chained, s);
-  return launch_one<4>(x, m, k, stride, threads, codes, scales, chained, s);
+  if (few && vecs <= 2 * 512) return launch_one<2>(x, m, k, stride, threads, codes, scales, s);
+  return launch_one<4>(x, m, k, stride, threads, codes, scales, s);
 }
 
 }  // namespace ffn

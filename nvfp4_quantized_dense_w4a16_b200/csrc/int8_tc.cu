@@ -14,8 +14,8 @@
 // tile into ranges, and each CTA adds a share of the others' sums, read from their
 // shared memory.  Sums are whole numbers: the cut does not change a bit.
 //
-// Weights are loaded before the kernel ahead in the stream has completed, rows
-// after it.  Every wait is bounded; on expiry a device error bit is raised, the
+// Weights are loaded before the kernel ahead that makes the rows has completed (but
+// for the first launch of a call), rows after it.  Every wait is bounded; on expiry a device error bit is raised, the
 // CTAs free their tensor memory and exit.
 #include <cudaTypedefs.h>
 
@@ -128,6 +128,7 @@ struct PairArgs {
   int tile_n;       // weight rows of a tile: a multiple of 32 up to 256
   int m_tiles, n_tiles;
   int stages;       // of the ring
+  bool first;       // (Int8Product::first)
 };
 
 constexpr int kPairRows = 256;
@@ -239,6 +240,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
         x.next(a, step, total, half, rank);
       };
       int ahead = 0, u = 0;
+      if (a.first) griddep_wait();
       for (; ahead < stages && w.t < total; ++ahead) load_weights();
       griddep_wait();
       griddep_launch_dependents();
@@ -255,7 +257,9 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 1) {
     // --------------------------------------------- MMAs, CTA 0's for both
+    // (all roles wait for the kernel ahead: the limits of their waits begin after it)
     const uint32_t idesc = idesc_s8_s32(kPairRows, a.tile_n);
+    griddep_wait();
     int s = 0, i = 0;
     uint32_t parity = 0;
     bool ok = true;
@@ -412,6 +416,7 @@ struct FewArgs {
   int m, kc;
   int n;       // the MMA's N: rows of x, a multiple of 16
   int stages;  // of the ring
+  bool first;  // (Int8Product::first)
 };
 
 constexpr int kFewThreads = 192;  // a producer, an issuer, four warps for the sums
@@ -478,6 +483,7 @@ __global__ void __launch_bounds__(kFewThreads)
       };
       auto load_rows = [&](int s, int k) { tma_load_2d(ring + s * stage_bytes + kFewWeights, &xmap, k, 0, &full[s]); };
       const int ahead = min(units, a.stages);
+      if (a.first) griddep_wait();
       for (int u = 0; u < ahead; ++u) load_weights(u, (c0 + u) * kChunkK);
       griddep_wait();
       griddep_launch_dependents();
@@ -494,6 +500,7 @@ __global__ void __launch_bounds__(kFewThreads)
     }
   } else if (warp == 1) {
     const uint32_t idesc = idesc_s8_s32(128, a.n);
+    griddep_wait();
     int s = 0;
     uint32_t parity = 0;
     for (int u = 0; u < units; ++u) {
@@ -689,7 +696,7 @@ template <bool SILU>
 cudaError_t launch_pair(const Int8Product& p, cudaStream_t s) {
   const int64_t cols = SILU ? p.n / 2 : p.n;
   const int clusters = device_sms() / 2;
-  PairArgs a{p.xs, p.ws, p.bias, p.y, p.m, cols, (int)ceil_div(p.k, kChunkK), 256, (int)ceil_div(p.m, kPairRows), 0, 0};
+  PairArgs a{p.xs, p.ws, p.bias, p.y, p.m, cols, (int)ceil_div(p.k, kChunkK), 256, (int)ceil_div(p.m, kPairRows), 0, 0, p.first};
   a.tile_n = pair_plan(p.m, cols, p.k, SILU).tile_n;
   a.n_tiles = (int)ceil_div(cols, SILU ? a.tile_n / 2 : a.tile_n);
   a.stages = std::min(kPairMaxStages, kPairRing / (kPairUnit * (kPairOperand + a.tile_n / 2 * kChunkK)));
@@ -707,7 +714,7 @@ cudaError_t launch_pair(const Int8Product& p, cudaStream_t s) {
 template <bool SILU>
 cudaError_t launch_few(const Int8Product& p, cudaStream_t s) {
   const int64_t cols = SILU ? p.n / 2 : p.n, tiles = ceil_div(cols, SILU ? 64 : 128);
-  FewArgs a{p.xs, p.ws, p.bias, p.y, cols, (int)p.m, (int)ceil_div(p.k, kChunkK), (int)ceil_div(p.m, 16) * 16, 0};
+  FewArgs a{p.xs, p.ws, p.bias, p.y, cols, (int)p.m, (int)ceil_div(p.k, kChunkK), (int)ceil_div(p.m, 16) * 16, 0, p.first};
   a.stages = std::min(kFewMaxStages, kFewRing / (kFewWeights + a.n * kChunkK));
   const unsigned splits = (unsigned)few_plan(p.m, cols, p.k, SILU).splits;
   CUtensorMap xmap, wmap;
