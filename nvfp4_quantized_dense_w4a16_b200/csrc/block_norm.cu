@@ -16,6 +16,8 @@
 // 88 instructions a value); rows prefetched into a ring 93 and 139; 32 values a thread
 // and packed fp32 arithmetic 59 and 79; groups of one CTA that share the columns'
 // coefficients 47 and 77; the hardware's exponential and quotient in tanh 69.
+#include <algorithm>
+
 #include "ffn_nvfp4.h"
 #include "int8.cuh"
 #include "int8.h"
@@ -373,7 +375,7 @@ __device__ __forceinline__ void output_row(Row<WARP>& row, const BlockArgs& a, i
 }
 
 // R: the residual is bf16; WARP: a warp for each row, else the CTA; V: values of an
-// access (8, or 1 where a tensor's rows are not whole 16 bytes); N: accesses a thread.
+// access; N: accesses a thread.
 template <bool R, bool WARP, int V, int N, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const BlockArgs a) {
   __shared__ __align__(16) uint32_t parts[64];
@@ -812,6 +814,123 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
   }
 }
 
+// ----------------------------------------- rows that are not whole 16 bytes
+
+__device__ __forceinline__ float load_one(const void* p, bool bf16, int64_t at) {
+  return bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
+}
+
+// A CTA a row, values one by one; the row is in shared memory, where a thread only touches its own.
+// Loops of few instructions: with a row unrolled in registers (8 values a thread, each with its types
+// and gates) the code was long and 203 rows of 1037, layer norm, took 5.9 to 9.6 us; so they take 4.8.
+template <bool R, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) block_norm_any_kernel(const BlockArgs a) {
+  extern __shared__ float v[];
+  __shared__ __align__(16) uint32_t parts[64];
+  Row<false> row{parts};
+  constexpr int kAtOnce = 4;  // values of a thread under way
+  const int mine = threadIdx.x, threads = blockDim.x, h = a.hidden;
+  for (int i = mine; i < 64; i += threads) parts[i] = 0;
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  const float share = 1.0f / (float)h;
+  auto factors = [&](const NormArgs& n) {
+    float mean = 0.0f, eps = n.eps, squares;
+    for (bool again = false;; again = true) {
+      float s = 0.0f;
+      if (n.layer) {
+        for (int i = mine; i < h; i += threads) s += v[i];
+        mean = row.sum(s) * share;
+        s = 0.0f;
+      }
+      for (int i = mine; i < h; i += threads) {
+        const float d = v[i] - mean;
+        s = fmaf(d, d, s);
+      }
+      squares = row.sum(s);
+      if (again || squares < __uint_as_float(0x7f800000u)) break;
+      eps = 0.0f;  // (nothing beside the squares of such a row)
+      for (int i = mine; i < h; i += threads) v[i] *= 2.6469780e-23f;  // 2^-75
+    }
+    const float factor = rsqrtf(fmaf(squares, share, eps));
+    return NormFactors{factor, -mean * factor};
+  };
+  for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x) {
+    const uint16_t* y = a.y + r * a.y_stride;
+    for (int i0 = mine; i0 < h; i0 += kAtOnce * threads) {
+      float t[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int i = i0 + j * threads;
+        if (i < h) t[j] = a.y ? bf16_bits_to_float(y[i]) : load_one(a.residual, R, r * a.residual_stride + i);
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (i0 + j * threads < h) v[i0 + j * threads] = t[j];
+    }
+    if (a.y) {
+      NormFactors f{1.0f, 0.0f};
+      if (a.post.on) f = factors(a.post);
+      for (int i0 = mine; i0 < h; i0 += kAtOnce * threads) {
+        float x[kAtOnce], g[kAtOnce], w[kAtOnce], b[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int i = i0 + j * threads;
+          g[j] = w[j] = 1.0f, b[j] = 0.0f;
+          if (i >= h) continue;
+          x[j] = load_one(a.residual, R, r * a.residual_stride + i);
+          if (a.gate) g[j] = load_one(a.gate, a.gate_bf16, r * a.gate_row_stride + (a.gate_cols ? i : 0));
+          if (a.post.weight) w[j] = a.post.offset + load_one(a.post.weight, a.post.bf16, i);
+          if (a.post.bias) b[j] = load_one(a.post.bias, a.post.bf16, i);
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int i = i0 + j * threads;
+          if (i >= h) break;
+          const float z = fmaf(fmaf(v[i], f.factor, f.shift), w[j], b[j]);
+          float s = fmaf(a.residual_scale, x[j], a.branch_scale * (gate_value(g[j], a.gate ? a.gate_activation : 0) * z));
+          if (R) s = bf16_round(s);
+          v[i] = s;
+          if (!a.residual_out) continue;
+          if (R)
+            static_cast<uint16_t*>(a.residual_out)[r * a.residual_out_stride + i] = f32_to_bf16_bits(s);
+          else
+            static_cast<float*>(a.residual_out)[r * a.residual_out_stride + i] = s;
+        }
+      }
+    }
+    if (!a.pre.on) continue;
+    const NormFactors f = factors(a.pre);
+    uint32_t top = 0;
+    for (int i0 = mine; i0 < h; i0 += kAtOnce * threads) {
+      float w[kAtOnce], b[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int i = i0 + j * threads;
+        w[j] = 1.0f, b[j] = 0.0f;
+        if (i < h && a.pre.weight) w[j] = a.pre.offset + load_one(a.pre.weight, a.pre.bf16, i);
+        if (i < h && a.pre.bias) b[j] = load_one(a.pre.bias, a.pre.bf16, i);
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int i = i0 + j * threads;
+        if (i >= h) break;
+        const uint16_t x = f32_to_bf16_bits(fmaf(fmaf(v[i], f.factor, f.shift), w[j], b[j]));
+        if (a.out_scales)
+          top = max(top, x & 0x7fffu), v[i] = bf16_bits_to_float(x);
+        else
+          static_cast<uint16_t*>(a.out)[r * a.out_stride + i] = x;
+      }
+    }
+    if (!a.out_scales) continue;
+    // The codes are those of the row as it would be stored in bf16.
+    const Int8Row q(row.max(top));
+    for (int i = mine; i < h; i += threads) static_cast<int8_t*>(a.out)[r * a.out_stride + i] = (int8_t)q.code(v[i]);
+    if (mine == 0) a.out_scales[r] = q.scale;
+  }
+}
+
 template <bool R, bool WARP, int V, int N, int THREADS>
 cudaError_t launch_one(const BlockArgs& a, int threads, cudaStream_t s) {
   const int64_t per_cta = WARP ? threads / 32 : 1;
@@ -847,9 +966,18 @@ template <bool R>
 cudaError_t launch_rows(const BlockArgs& a, bool vec, cudaStream_t s) {
   const int h = a.hidden;
   if (!vec) {
-    if (h <= 256) return launch_one<R, true, 1, 8, 256>(a, 256, s);
-    if (h <= 4096) return launch_one<R, false, 1, 8, 512>(a, round_up_32((h + 7) / 8), s);
-    return launch_one<R, false, 1, 32, 1024>(a, round_up_32((h + 31) / 32), s);
+    // 4 values a thread while all rows are under way at once; then 8, and registers for 3 CTAs of 512 threads on an SM
+    // (2074 rows of 2797, layer norms before and after, 107 and 61 us; 476 rows of 497 7.0 and 11.4).
+    const int four = std::min(1024, round_up_32((h + 3) / 4));
+    const bool few = a.m <= (int64_t)device_sms() * (1024 / four) || h > 8192;
+    auto kern = few ? block_norm_any_kernel<R, 1024, 1> : block_norm_any_kernel<R, 512, 3>;
+    const int threads = few ? four : std::min(512, round_up_32((h + 7) / 8)), bytes = 4 * h;
+    // set on every launch: the attribute belongs to the current device's context
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t most = 8 * (int64_t)device_sms();  // (the longest rows' CTAs wait for room)
+    ProfScope prof(s, "block_norm");
+    return launch_pdl(kern, dim3((unsigned)(a.m < most ? a.m : most)), dim3(threads), bytes, s, a);
   }
   // The streaming kernel, from where its start (one CTA an SM, the columns' coefficients) is made up for: bf16
   // residual, both norms, streaming and by rows, in us: 600 rows of 384, 1024, 2048, 4096 4.6, 5.3, 5.6, 6.5 and 3.6,

@@ -12,7 +12,8 @@
 // rows and the 64 up rows of the same columns), x is its N.  Bound by the stream
 // of the weights, which all SMs have to share: a cluster of CTAs cuts the K of a
 // tile into ranges, and each CTA adds a share of the others' sums, read from their
-// shared memory.  Sums are whole numbers: the cut does not change a bit.
+// shared memory.  Sums are whole numbers: the cut does not change a bit.  More than
+// 128 rows go in blocks, each with the weights to itself.
 //
 // Weights are loaded before the kernel ahead that makes the rows has completed (but
 // for the first launch of a call), rows after it.  Every wait is bounded; on expiry a device error bit is raised, the
@@ -362,21 +363,21 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
                 make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
         }
         __syncwarp();
-        // four lanes store 64 bytes of a row
-        const int64_t col = col0 + 16 * p + 8 * (lane & 3);
+        const int64_t col = col0 + 16 * p;
+        if (wide) {  // four lanes store 64 bytes of a row
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const int r = 8 * z + (lane >> 2);
-          if (row0 + r >= a.m || 8 * (lane & 3) >= width || col >= a.cols) continue;
-          const uint4 v = *reinterpret_cast<const uint4*>(out + r * 64 + 16 * ((lane & 3) ^ ((r >> 1) & 3)));
-          uint16_t* y = a.y + (row0 + r) * a.cols + col;
-          if (wide) {
-            *reinterpret_cast<uint4*>(y) = v;
-          } else {
-            const uint32_t e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (col + j < a.cols) y[j] = (uint16_t)(e[j >> 1] >> (16 * (j & 1)));
+          for (int z = 0; z < 4; ++z) {
+            const int r = 8 * z + (lane >> 2), c = 8 * (lane & 3);
+            if (row0 + r < a.m && c < width && col + c < a.cols)
+              *reinterpret_cast<uint4*>(a.y + (row0 + r) * a.cols + col + c) =
+                  *reinterpret_cast<const uint4*>(out + r * 64 + 16 * ((lane & 3) ^ ((r >> 1) & 3)));
+          }
+        } else {  // rows at any two bytes: a warp stores one at a time (6241 x 13289 from K = 128:
+          // 157 us, 13296 columns 83; two bytes a lane in 16-byte runs took 391)
+          const int rows = (int)min((int64_t)32, a.m - row0);
+          for (int r = 0; r < rows; ++r) {
+            const uint16_t v = *reinterpret_cast<const uint16_t*>(out + r * 64 + 16 * ((lane >> 3) ^ ((r >> 1) & 3)) + 2 * (lane & 7));
+            if (lane < width && col + lane < a.cols) a.y[(row0 + r) * a.cols + col + lane] = v;
           }
         }
         __syncwarp();
@@ -413,8 +414,9 @@ struct FewArgs {
   const uint16_t* bias;
   uint16_t* y;
   int64_t cols;
-  int m, kc;
-  int n;       // the MMA's N: rows of x, a multiple of 16
+  int64_t m;
+  int kc;
+  int n;       // the MMA's N: rows of x of a CTA, a multiple of 16
   int stages;  // of the ring
   bool first;  // (Int8Product::first)
 };
@@ -444,6 +446,7 @@ __global__ void __launch_bounds__(kFewThreads)
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(splits));
   const int rank = (int)cluster_rank();
   const int64_t tile = blockIdx.x / splits;
+  const int row0 = (int)blockIdx.y * a.n, rows = (int)min((int64_t)a.n, a.m - row0);
   const int c0 = (int)((int64_t)a.kc * rank / splits), c1 = (int)((int64_t)a.kc * (rank + 1) / splits), units = c1 - c0;
   const int stage_bytes = kFewWeights + a.n * kChunkK;
   const uint32_t columns = a.n <= 32 ? 32 : a.n <= 64 ? 64 : 128;  // of tensor memory
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(kFewThreads)
           tma_load_2d(at, &wmap, k, (int)(tile * 128), &full[s]);
         }
       };
-      auto load_rows = [&](int s, int k) { tma_load_2d(ring + s * stage_bytes + kFewWeights, &xmap, k, 0, &full[s]); };
+      auto load_rows = [&](int s, int k) { tma_load_2d(ring + s * stage_bytes + kFewWeights, &xmap, k, row0, &full[s]); };
       const int ahead = min(units, a.stages);
       if (a.first) griddep_wait();
       for (int u = 0; u < ahead; ++u) load_weights(u, (c0 + u) * kChunkK);
@@ -558,7 +561,7 @@ __global__ void __launch_bounds__(kFewThreads)
     const int wq = warp - 2, mine = 4 * (SILU ? lane & 15 : lane);
     const int first = (rank * 4 + wq) * kPer + (SILU ? lane >> 4 : 0), step = (int)splits * 4 * kPer;
     ok = __all_sync(0xffffffffu, bad == 0);
-    for (int i0 = first; ok && i0 < a.m; i0 += kAtOnce * step) {
+    for (int i0 = first; ok && i0 < rows; i0 += kAtOnce * step) {
       int4 g[kAtOnce], u[kAtOnce];
 #pragma unroll
       for (int z = 0; z < kAtOnce; ++z) g[z] = u[z] = make_int4(0, 0, 0, 0);
@@ -580,8 +583,8 @@ __global__ void __launch_bounds__(kFewThreads)
 #pragma unroll
       for (int z = 0; z < kAtOnce; ++z) {
         const int i = i0 + z * step;
-        if (i >= a.m) break;
-        const float xs = a.xs[i];
+        if (i >= rows) break;
+        const float xs = a.xs[row0 + i];
         const int gs[4] = {g[z].x, g[z].y, g[z].z, g[z].w}, us[4] = {u[z].x, u[z].y, u[z].z, u[z].w};
         uint16_t b[4];
 #pragma unroll
@@ -593,7 +596,7 @@ __global__ void __launch_bounds__(kFewThreads)
             v = __fadd_rn(v, s1[j]);
           b[j] = f32_to_bf16_bits(v);
         }
-        uint16_t* y = a.y + (int64_t)i * a.cols + col;
+        uint16_t* y = a.y + (int64_t)(row0 + i) * a.cols + col;
         if (a.cols % 4 == 0) {
           if (col < a.cols)
             *reinterpret_cast<uint2*>(y) = make_uint2(b[0] | ((uint32_t)b[1] << 16), b[2] | ((uint32_t)b[3] << 16));
@@ -670,8 +673,11 @@ PairPlan pair_plan(int64_t m, int64_t cols, int64_t k, bool silu) {
 
 struct FewPlan {
   int splits;
+  int blocks, n;  // of rows, n each
   int64_t ns;
 };
+
+constexpr int64_t kFewBlock = 128;  // rows of a CTA, at most: their sums are two thirds of the ring
 
 // Clusters of 1, 2, ... CTAs that are resident at a time, an SM each or two an SM (measured; a cluster stays
 // within a part of the GPU).  The most CTAs that start at once: with one more wave of clusters 5120 x 17408 takes
@@ -679,16 +685,18 @@ struct FewPlan {
 // kernel's can start: 4096 x 4096 cut into 4 and 8 6.5 and 7.2 us, 4096 x 12288 13.7 and 12.0.
 FewPlan few_plan(int64_t m, int64_t cols, int64_t k, bool silu) {
   constexpr int kOneAnSm[] = {148, 74, 45, 33, 26, 22, 15, 15}, kTwoAnSm[] = {296, 148, 90, 68, 54, 45, 36, 33};
-  const int64_t tiles = ceil_div(cols, silu ? 64 : 128), kc = ceil_div(k, kChunkK);
+  FewPlan p;
+  p.blocks = (int)ceil_div(m, kFewBlock);
+  p.n = (int)ceil_div(ceil_div(m, p.blocks), 16) * 16;
+  const int64_t tiles = p.blocks * ceil_div(cols, silu ? 64 : 128), kc = ceil_div(k, kChunkK);
   int one = 1, two = 1;
   for (int c = 2; c <= kFewMaxSplits && c <= kc; ++c) {
     if (tiles <= kOneAnSm[c - 1]) one = c;
     if (tiles <= kTwoAnSm[c - 1]) two = c;
   }
-  FewPlan p;
   p.splits = ceil_div(kc, one) <= 12 ? one : two;
-  const int64_t rounds = ceil_div(tiles, kTwoAnSm[p.splits - 1]), loop = 250 * rounds * ceil_div(kc, p.splits);
-  p.ns = 3400 + 200 * p.splits + 40 * ceil_div(m, 16) * 16 + std::max(loop, stream_ns(cols, k, silu));
+  const int64_t rounds = ceil_div(tiles, kTwoAnSm[p.splits - 1]), loop = (250 + 13 * p.n / 10) * rounds * ceil_div(kc, p.splits);
+  p.ns = 3400 + 200 * p.splits + 40 * p.n + std::max(loop, stream_ns(cols, k, silu));
   return p;
 }
 
@@ -714,23 +722,25 @@ cudaError_t launch_pair(const Int8Product& p, cudaStream_t s) {
 template <bool SILU>
 cudaError_t launch_few(const Int8Product& p, cudaStream_t s) {
   const int64_t cols = SILU ? p.n / 2 : p.n, tiles = ceil_div(cols, SILU ? 64 : 128);
-  FewArgs a{p.xs, p.ws, p.bias, p.y, cols, (int)p.m, (int)ceil_div(p.k, kChunkK), (int)ceil_div(p.m, 16) * 16, 0, p.first};
+  const FewPlan plan = few_plan(p.m, cols, p.k, SILU);
+  FewArgs a{p.xs, p.ws, p.bias, p.y, cols, p.m, (int)ceil_div(p.k, kChunkK), plan.n, 0, p.first};
   a.stages = std::min(kFewMaxStages, kFewRing / (kFewWeights + a.n * kChunkK));
-  const unsigned splits = (unsigned)few_plan(p.m, cols, p.k, SILU).splits;
+  const unsigned splits = (unsigned)plan.splits;
   CUtensorMap xmap, wmap;
   if (!encode_rows(&xmap, p.x, p.m, p.k, a.n) || !encode_rows(&wmap, p.w, p.n, p.k, SILU ? 64 : 128)) return cudaErrorInvalidValue;
   auto kern = int8_few_kernel<SILU>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl_clusters(kern, dim3((unsigned)(tiles * splits)), splits, dim3(kFewThreads), kFewSmem, s, xmap, wmap, a);
+  return launch_pdl_clusters(kern, dim3((unsigned)(tiles * splits), (unsigned)plan.blocks), splits, dim3(kFewThreads), kFewSmem, s, xmap, wmap, a);
 }
 
-constexpr int64_t kFewRows = 128;  // (the sums of 128 rows are two thirds of the ring)
+constexpr int64_t kFewRows = 512;
 
 // Few rows of large weights are cut along K; small weights, whose tiles the pairs of SMs take in one wave, are not worth
 // a cluster's exchange of sums.  Cut and in pairs, in us: 512 x 512, 2 and 128 rows 3.7, 7.4 and 3.6, 3.9; 2048 x 2048, 2,
 // 16, 32, 128 rows 5.3, 6.3, 6.9, 9.8 and 7.2, 6.0, 6.0, 6.1; 4096 x 4096, 16, 64, 128 rows 7.5, 8.5, 11.9 and 13, 10.9,
-// 11.1; 5120 x 17408, 128 rows 26 and 34.
+// 11.1; 5120 x 17408, 128 rows 26 and 34.  In blocks of rows: 225 rows of 576 x 12256 12.2 and 23.8, of 4096 x 4096 13.8
+// and 11.4; 512 of 1024 x 8192 14.5 and 17.4, of 5120 x 17408 63 and 43.
 bool use_few(int64_t m, int64_t cols, int64_t k, bool silu) {
   return m <= kFewRows && few_plan(m, cols, k, silu).ns < pair_plan(m, cols, k, silu).ns;
 }

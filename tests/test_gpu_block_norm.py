@@ -86,8 +86,8 @@ def check(native, m, hidden, residual=torch.bfloat16, weight=torch.bfloat16, kin
     return got
 
 
-HIDDEN = [1, 2, 7, 8, 31, 32, 33, 64, 100, 248, 256, 257, 264, 384, 512, 520, 1000, 1024, 1032, 1037, 2048, 4096, 4097, 5120, 8192, 8200, 9001,
-          16384, 16392, 20000, 32768, 32767]
+HIDDEN = [1, 2, 7, 8, 31, 32, 33, 64, 100, 248, 250, 256, 257, 258, 264, 384, 512, 520, 1000, 1024, 1032, 1037, 2046, 2047, 2048, 2049, 2050, 4094, 4096, 4097, 4098, 5120, 8191, 8192, 8194, 8200, 9001, 9002,
+          16384, 16392, 20000, 32766, 32768, 32767]
 
 
 @pytest.mark.parametrize("hidden", HIDDEN)
@@ -187,6 +187,24 @@ def test_quantised_is_the_quantisation_of_the_plain_output(native, hidden, branc
     res4, x = native.ffn_block_norm(odd[:, 1:], pre=pre, **kw)
     rc, rs = native.ffn_int8_quantize(x)
     assert same_bits(res3, res4) and torch.equal(c, rc) and torch.equal(s, rs)
+
+
+@pytest.mark.parametrize("hidden", [64, 1056])
+def test_quantised_rows_that_are_not_whole_16_bytes(native, hidden):
+    """Tensors at every alignment of an element: accesses of 8, of 2 and of 1 give the same bits."""
+    m = 7
+    y, r = rows(m, hidden, 20).cuda(), rows(m, hidden, 21).float().cuda()
+    pre, post = make_norm(native, hidden, seed=1)[0], make_norm(native, hidden, seed=2)[0]
+    ref = native.ffn_block_norm(r, y=y, post=post, pre=pre, quantize=True)
+    for off in (1, 2, 3, 4, 6, 8):
+        wy, wr = torch.empty((m, hidden + 10), dtype=torch.bfloat16, device="cuda"), torch.empty((m, hidden + 10), device="cuda")
+        wy[:, off:off + hidden], wr[:, off:off + hidden] = y, r
+        res, c, s = native.ffn_block_norm(wr[:, off:off + hidden], y=wy[:, off:off + hidden], post=post, pre=pre, quantize=True)
+        err = (res - ref[0]).abs()
+        assert torch.all(err <= 2.0 ** -20 * ref[0].abs() + 2.0 ** -20)  # sums in another order
+        x = native.ffn_block_norm(wr[:, off:off + hidden], y=wy[:, off:off + hidden], post=post, pre=pre)[1]
+        rc, rs = native.ffn_int8_quantize(x)
+        assert torch.equal(c, rc) and torch.equal(s, rs)
 
 
 @pytest.mark.parametrize("hidden", [64, 77, 1056, 1055])

@@ -129,7 +129,8 @@ def test_linear_matches_bit_for_bit(native, m, n, k, with_bias):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 40, 131040), (3, 24, 131040), (20, 40, 131040), (150, 24, 65536), (300, 136, 131040), (2, 30000, 64),
-                                   (40, 20001, 64), (5000, 8, 64), (3000, 33, 96), (7, 8, 17408)])
+                                   (40, 20001, 64), (5000, 8, 64), (3000, 33, 96), (7, 8, 17408), (200, 40, 17408), (385, 72, 8192), (512, 130, 12288),
+                                   (260, 129, 20000 // 32 * 32), (130, 9, 40000), (1, 3, 32768), (1, 5, 32800), (1, 7000, 8224), (1, 20001, 96)])
 def test_linear_long_axes(native, m, n, k):
     check_linear(native, m, n, k, full=True, seed=m)
 
@@ -306,6 +307,30 @@ def test_on_another_stream(native, m):
         y2 = native.ffn_int8_linear(c, weights[0], weights[1], x_scales=s)
     torch.cuda.current_stream().wait_stream(side)
     assert same_bits(out, ref) and same_bits(y, ref_lin) and same_bits(y2, ref_lin)
+
+
+@pytest.mark.parametrize("m", [1, 2, 30, 300])
+def test_weights_written_right_before_the_call(native, m):
+    """A weight that the work ahead in the stream still writes, a kernel of another library or the quantisation here."""
+    n, k = 6000, 2048
+    x, full, ws = rows(m, k, 75).cuda(), [codes(n, k, 76 + i).cuda() for i in range(2)], scales(n, k, 78).cuda()
+    xq, xs = native.ffn_int8_quantize(x)
+    refs = [native.ffn_int8_linear(x, w, ws) for w in full]
+    big = [rows(n, k, 79 + i).cuda() for i in range(2)]
+    quantised = [native.ffn_int8_quantize(b) for b in big]
+    refs_q = [native.ffn_int8_linear(x, *q) for q in quantised]
+    torch.cuda.synchronize()
+    w, c, s = torch.empty_like(full[0]), torch.empty_like(full[0]), torch.empty_like(ws)
+    for i in (0, 1, 0, 1):
+        w.copy_(full[i])
+        y = native.ffn_int8_linear(x, w, ws)
+        w.copy_(full[1 - i])
+        y2 = native.ffn_int8_linear(xq, w, ws, x_scales=xs)
+        native.ffn_int8_quantize(big[i], codes=c, scales=s)
+        y3 = native.ffn_int8_linear(xq, c, s, x_scales=xs)
+        native.ffn_int8_quantize(big[1 - i], codes=c, scales=s)
+        y4 = native.ffn_int8_linear(x, c, s)
+        assert same_bits(y, refs[i]) and same_bits(y2, refs[1 - i]) and same_bits(y3, refs_q[i]) and same_bits(y4, refs_q[1 - i])
 
 
 @pytest.mark.parametrize("m", [1, 20, 140, 300])
