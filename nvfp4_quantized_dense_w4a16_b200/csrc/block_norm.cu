@@ -92,31 +92,29 @@ __device__ __forceinline__ void load_any(const void* p, bool bf16, int64_t at, f
 
 // The same in two steps, so that a load can stand far before its use: the words as
 // they are, and their values.  WIDE: they may be fp32, else they are bf16.
-template <int V, bool WIDE>
+template <bool WIDE>
 struct Raw {
-  static constexpr int kWords = V == 1 ? 1 : WIDE ? V : V / 2;
-  uint32_t w[kWords];
+  uint32_t w[WIDE ? 8 : 4];
   __device__ __forceinline__ void load(const void* p, bool bf16, int64_t at) {
-    if (V == 1) {
-      w[0] = !WIDE || bf16 ? static_cast<const uint16_t*>(p)[at] : static_cast<const uint32_t*>(p)[at];
-    } else if (!WIDE || bf16) {
+    if (!WIDE || bf16) {
       const uint4 t = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-      w[0] = t.x, w[1 % kWords] = t.y, w[2 % kWords] = t.z, w[3 % kWords] = t.w;
+      w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
     } else {
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const uint4 t = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at)[i];
-        w[(4 * i) % kWords] = t.x, w[(4 * i + 1) % kWords] = t.y, w[(4 * i + 2) % kWords] = t.z, w[(4 * i + 3) % kWords] = t.w;
+        w[(4 * i) % (WIDE ? 8 : 4)] = t.x, w[(4 * i + 1) % (WIDE ? 8 : 4)] = t.y;
+        w[(4 * i + 2) % (WIDE ? 8 : 4)] = t.z, w[(4 * i + 3) % (WIDE ? 8 : 4)] = t.w;
       }
     }
   }
-  __device__ __forceinline__ void get(bool bf16, float (&o)[V]) const {
+  __device__ __forceinline__ void get(bool bf16, float (&o)[8]) const {
     if (WIDE && !bf16) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = __uint_as_float(w[i % kWords]);
+      for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(w[i % (WIDE ? 8 : 4)]);
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = __uint_as_float(V == 1 || i % 2 == 0 ? w[i / 2] << 16 : w[i / 2] & 0xffff0000u);
+      for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(i % 2 == 0 ? w[i / 2] << 16 : w[i / 2] & 0xffff0000u);
     }
   }
 };
@@ -125,13 +123,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
 }
 
-template <int V>
-__device__ __forceinline__ void store_bf16(uint16_t* p, const float (&v)[V]) {
-  if (V == 8)
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1 % V]), pack_bf16(v[2 % V], v[3 % V]),
-                                              pack_bf16(v[4 % V], v[5 % V]), pack_bf16(v[6 % V], v[7 % V]));
-  else
-    *p = f32_to_bf16_bits(v[0]);
+__device__ __forceinline__ void store_bf16(uint16_t* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
 __device__ __forceinline__ float from_bits(uint32_t w, float) { return __uint_as_float(w); }
@@ -170,14 +163,14 @@ struct Row {
   }
 };
 
-// A norm of a row's N sets of V values, set i of this thread at column at(i), is
+// A norm of a row's N sets of 8 values, set i of this thread at column at(i), is
 // v * factor + shift before its weight and bias.
 struct NormFactors {
   float factor, shift;
 };
 
-template <bool WARP, int V, int N, typename At>
-__device__ __forceinline__ float row_squares(Row<WARP>& row, bool layer, int hidden, const float (&v)[N][V], At at, float* mean) {
+template <bool WARP, int N, typename At>
+__device__ __forceinline__ float row_squares(Row<WARP>& row, bool layer, int hidden, const float (&v)[N][8], At at, float* mean) {
   *mean = 0.0f;
   float s = 0.0f;
   if (layer) {
@@ -185,14 +178,14 @@ __device__ __forceinline__ float row_squares(Row<WARP>& row, bool layer, int hid
     for (int i = 0; i < N; ++i)
       if (at(i) < hidden)
 #pragma unroll
-        for (int j = 0; j < V; ++j) s += v[i][j];
+        for (int j = 0; j < 8; ++j) s += v[i][j];
     *mean = row.sum(s) * (1.0f / (float)hidden);
     s = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (at(i) < hidden)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
+        for (int j = 0; j < 8; ++j) {
           const float d = v[i][j] - *mean;
           s = fmaf(d, d, s);
         }
@@ -201,34 +194,34 @@ __device__ __forceinline__ float row_squares(Row<WARP>& row, bool layer, int hid
     for (int i = 0; i < N; ++i)
       if (at(i) < hidden)
 #pragma unroll
-        for (int j = 0; j < V; ++j) s = fmaf(v[i][j], v[i][j], s);
+        for (int j = 0; j < 8; ++j) s = fmaf(v[i][j], v[i][j], s);
   }
   return row.sum(s);
 }
 
 // The squares of values beyond 2^64 would pass fp32's range: such a row is scaled
 // by 2^-75 and summed once more.
-template <bool WARP, int V, int N, typename At>
-__device__ __forceinline__ NormFactors norm_factors(Row<WARP>& row, const NormArgs& a, int hidden, float (&v)[N][V], At at) {
+template <bool WARP, int N, typename At>
+__device__ __forceinline__ NormFactors norm_factors(Row<WARP>& row, const NormArgs& a, int hidden, float (&v)[N][8], At at) {
   const float share = 1.0f / (float)hidden;
   float mean, eps = a.eps;
-  float squares = row_squares<WARP, V, N>(row, a.layer, hidden, v, at, &mean);
+  float squares = row_squares<WARP, N>(row, a.layer, hidden, v, at, &mean);
   if (!(squares < __uint_as_float(0x7f800000u))) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[i][j] *= 2.6469780e-23f;  // 2^-75
+      for (int j = 0; j < 8; ++j) v[i][j] *= 2.6469780e-23f;  // 2^-75
     eps = 0.0f;  // (nothing beside the squares)
-    squares = row_squares<WARP, V, N>(row, a.layer, hidden, v, at, &mean);
+    squares = row_squares<WARP, N>(row, a.layer, hidden, v, at, &mean);
   }
   const float factor = rsqrtf(fmaf(squares, share, eps));
   return NormFactors{factor, -mean * factor};
 }
 
 // A norm's weights (and biases) at this thread's columns, loaded before the sums that they follow.
-template <int V, int N, bool WIDE>
+template <int N>
 struct Weights {
-  Raw<V, WIDE> weight[N], bias[N];
+  Raw<true> weight[N], bias[N];
   template <typename At>
   __device__ __forceinline__ void load(const NormArgs& a, int hidden, At at) {
 #pragma unroll
@@ -238,19 +231,19 @@ struct Weights {
         if (a.bias) bias[i].load(a.bias, a.bf16, at(i));
       }
   }
-  __device__ __forceinline__ void apply(const NormArgs& a, const NormFactors& f, int i, float (&v)[V]) const {
-    float t[V];
+  __device__ __forceinline__ void apply(const NormArgs& a, const NormFactors& f, int i, float (&v)[8]) const {
+    float t[8];
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = fmaf(v[j], f.factor, f.shift);
+    for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j], f.factor, f.shift);
     if (a.weight) {
       weight[i].get(a.bf16, t);
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] *= a.offset + t[j];
+      for (int j = 0; j < 8; ++j) v[j] *= a.offset + t[j];
     }
     if (a.bias) {
       bias[i].get(a.bf16, t);
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] += t[j];
+      for (int j = 0; j < 8; ++j) v[j] += t[j];
     }
   }
 };
@@ -277,9 +270,9 @@ __device__ __forceinline__ float gate_value(float g, int activation) {
 }
 
 // The new residual of row r from v, the values of y, stored and left in v: each N sets of
-// V values at columns at(i), the residual's and (with gate_cols) the gates' by load_res and load_gate.
-template <bool R, bool WARP, int V, int N, bool WIDE, typename LoadRes, typename LoadGate, typename At>
-__device__ __forceinline__ void residual_row(Row<WARP>& row, const BlockArgs& a, int64_t r, float (&v)[N][V], LoadRes load_res,
+// 8 values at columns at(i), the residual's and (with gate_cols) the gates' by load_res and load_gate.
+template <bool R, bool WARP, int N, typename LoadRes, typename LoadGate, typename At>
+__device__ __forceinline__ void residual_row(Row<WARP>& row, const BlockArgs& a, int64_t r, float (&v)[N][8], LoadRes load_res,
                                              LoadGate load_gate, At at) {
   if (!a.y) {
 #pragma unroll
@@ -288,10 +281,10 @@ __device__ __forceinline__ void residual_row(Row<WARP>& row, const BlockArgs& a,
     return;
   }
   NormFactors f = {};
-  Weights<V, N, WIDE> w;
+  Weights<N> w;
   if (a.post.on) {
     w.load(a.post, a.hidden, at);
-    f = norm_factors<WARP, V, N>(row, a.post, a.hidden, v, at);
+    f = norm_factors<WARP, N>(row, a.post, a.hidden, v, at);
   }
   float scale = a.branch_scale;
   if (a.gate && !a.gate_cols) {
@@ -302,54 +295,49 @@ __device__ __forceinline__ void residual_row(Row<WARP>& row, const BlockArgs& a,
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (at(i) < a.hidden) {
-      float t[V];
+      float t[8];
       if (a.post.on) w.apply(a.post, f, i, v[i]);
       if (a.gate && a.gate_cols) {
         load_gate(i, t);
         if (a.gate_activation != FFN_GATE_NONE)
 #pragma unroll
-          for (int j = 0; j < V; ++j) t[j] = gate_value(t[j], a.gate_activation);
+          for (int j = 0; j < 8; ++j) t[j] = gate_value(t[j], a.gate_activation);
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[i][j] *= t[j];
+        for (int j = 0; j < 8; ++j) v[i][j] *= t[j];
       }
       load_res(i, t);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
+      for (int j = 0; j < 8; ++j) {
         const float x = fmaf(a.residual_scale, t[j], scale * v[i][j]);
         v[i][j] = R ? bf16_round(x) : x;
       }
       if (a.residual_out) {
         if (R) {
-          store_bf16<V>(static_cast<uint16_t*>(a.residual_out) + r * a.residual_out_stride + at(i), v[i]);
+          store_bf16(static_cast<uint16_t*>(a.residual_out) + r * a.residual_out_stride + at(i), v[i]);
         } else {
           float* o = static_cast<float*>(a.residual_out) + r * a.residual_out_stride + at(i);
-          if (V == 8) {
 #pragma unroll
-            for (int q = 0; q < V / 4; ++q)
-              reinterpret_cast<float4*>(o)[q] =
-                  make_float4(v[i][(4 * q) % V], v[i][(4 * q + 1) % V], v[i][(4 * q + 2) % V], v[i][(4 * q + 3) % V]);
-          } else {
-            *o = v[i][0];
-          }
+          for (int q = 0; q < 2; ++q)
+            reinterpret_cast<float4*>(o)[q] = make_float4(v[i][4 * q], v[i][4 * q + 1], v[i][4 * q + 2], v[i][4 * q + 3]);
         }
       }
     }
 }
 
 // The norm of the new residual, and its stores.
-template <bool WARP, int V, int N, bool WIDE, typename At>
-__device__ __forceinline__ void output_row(Row<WARP>& row, const BlockArgs& a, int64_t r, int mine, float (&res)[N][V], At at) {
+template <bool WARP, int N, typename At>
+__device__ __forceinline__ void output_row(Row<WARP>& row, const BlockArgs& a, int64_t r, int mine, float (&res)[N][8], At at) {
   if (!a.pre.on) return;
-  Weights<V, N, WIDE> w;
+  Weights<N> w;
   w.load(a.pre, a.hidden, at);
-  const NormFactors f = norm_factors<WARP, V, N>(row, a.pre, a.hidden, res, at);
+  const NormFactors f = norm_factors<WARP, N>(row, a.pre, a.hidden, res, at);
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (at(i) < a.hidden) w.apply(a.pre, f, i, res[i]);
   if (!a.out_scales) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (at(i) < a.hidden) store_bf16<V>(static_cast<uint16_t*>(a.out) + r * a.out_stride + at(i), res[i]);
+      if (at(i) < a.hidden) store_bf16(static_cast<uint16_t*>(a.out) + r * a.out_stride + at(i), res[i]);
     return;
   }
   // The codes are those of the row as it would be stored in bf16.
@@ -358,31 +346,28 @@ __device__ __forceinline__ void output_row(Row<WARP>& row, const BlockArgs& a, i
   for (int i = 0; i < N; ++i)
     if (at(i) < a.hidden)
 #pragma unroll
-      for (int j = 0; j < V; ++j) top = max(top, (uint32_t)(f32_to_bf16_bits(res[i][j]) & 0x7fffu));
+      for (int j = 0; j < 8; ++j) top = max(top, (uint32_t)(f32_to_bf16_bits(res[i][j]) & 0x7fffu));
   const Int8Row q(row.max(top));
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (at(i) < a.hidden) {
       int8_t* o = static_cast<int8_t*>(a.out) + r * a.out_stride + at(i);
-      if (V == 8)
-        *reinterpret_cast<uint2*>(o) =
-            int8_encode8(q, make_uint4(pack_bf16(res[i][0], res[i][1 % V]), pack_bf16(res[i][2 % V], res[i][3 % V]),
-                                       pack_bf16(res[i][4 % V], res[i][5 % V]), pack_bf16(res[i][6 % V], res[i][7 % V])));
-      else
-        *o = (int8_t)q.code(bf16_round(res[i][0]));
+      *reinterpret_cast<uint2*>(o) =
+          int8_encode8(q, make_uint4(pack_bf16(res[i][0], res[i][1]), pack_bf16(res[i][2], res[i][3]),
+                                     pack_bf16(res[i][4], res[i][5]), pack_bf16(res[i][6], res[i][7])));
     }
   if (mine == 0) a.out_scales[r] = q.scale;
 }
 
-// R: the residual is bf16; WARP: a warp for each row, else the CTA; V: values of an
-// access; N: accesses a thread.
-template <bool R, bool WARP, int V, int N, int THREADS>
+// R: the residual is bf16; WARP: a warp for each row, else the CTA; N: accesses of
+// 8 values a thread.
+template <bool R, bool WARP, int N, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const BlockArgs a) {
   __shared__ __align__(16) uint32_t parts[64];
   Row<WARP> row{parts};
   const int threads = WARP ? 32 : blockDim.x, mine = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int per_cta = WARP ? blockDim.x >> 5 : 1;
-  auto at = [&](int i) { return V * (mine + i * threads); };
+  auto at = [&](int i) { return 8 * (mine + i * threads); };
   if (!WARP) {
     if (threadIdx.x < 64) parts[threadIdx.x] = 0;
     if (blockDim.x < 64 && threadIdx.x < 32) parts[threadIdx.x + 32] = 0;
@@ -393,19 +378,19 @@ __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const BlockArgs 
   for (int64_t r = blockIdx.x * (int64_t)per_cta + (WARP ? threadIdx.x >> 5 : 0); r < a.m;
        r += (int64_t)gridDim.x * per_cta) {
     // all loads first: a row's latency counts here
-    float v[N][V];
-    Raw<V, !R> res[N];
-    Raw<V, true> g[N];
+    float v[N][8];
+    Raw<!R> res[N];
+    Raw<true> g[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (at(i) < a.hidden) {
-        if (a.y) load_bf16<V>(a.y + r * a.y_stride + at(i), v[i]);
+        if (a.y) load_bf16<8>(a.y + r * a.y_stride + at(i), v[i]);
         res[i].load(a.residual, R, r * a.residual_stride + at(i));
         if (a.gate && a.gate_cols) g[i].load(a.gate, a.gate_bf16, r * a.gate_row_stride + at(i));
       }
-    residual_row<R, WARP, V, N, true>(
-        row, a, r, v, [&](int i, float(&t)[V]) { res[i].get(R, t); }, [&](int i, float(&t)[V]) { g[i].get(a.gate_bf16, t); }, at);
-    output_row<WARP, V, N, true>(row, a, r, mine, v, at);
+    residual_row<R, WARP, N>(
+        row, a, r, v, [&](int i, float(&t)[8]) { res[i].get(R, t); }, [&](int i, float(&t)[8]) { g[i].get(a.gate_bf16, t); }, at);
+    output_row<WARP, N>(row, a, r, mine, v, at);
   }
 }
 
@@ -931,12 +916,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) block_norm_any_kernel(const Blo
   }
 }
 
-template <bool R, bool WARP, int V, int N, int THREADS>
+template <bool R, bool WARP, int N, int THREADS>
 cudaError_t launch_one(const BlockArgs& a, int threads, cudaStream_t s) {
   const int64_t per_cta = WARP ? threads / 32 : 1;
   const int64_t ctas = (a.m + per_cta - 1) / per_cta, most = (int64_t)device_sms() * (2048 / threads);
   ProfScope prof(s, "block_norm");
-  return launch_pdl(block_norm_kernel<R, WARP, V, N, THREADS>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(threads),
+  return launch_pdl(block_norm_kernel<R, WARP, N, THREADS>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(threads),
                     0, s, a);
 }
 
@@ -995,12 +980,12 @@ cudaError_t launch_rows(const BlockArgs& a, bool vec, cudaStream_t s) {
       return launch_pdl(kern, dim3(device_sms()), dim3(p.threads * p.groups), bytes, s, a, p);
     }
   }
-  if (h <= 256) return launch_one<R, true, 8, 1, 256>(a, 256, s);
-  if (h <= 512) return launch_one<R, true, 8, 2, 256>(a, 256, s);
-  if (h <= 1024) return launch_one<R, true, 8, 4, 256>(a, 256, s);
-  if (h <= 8192) return launch_one<R, false, 8, 2, 512>(a, round_up_32((h + 15) / 16), s);
-  if (h <= 16384) return launch_one<R, false, 8, 4, 512>(a, round_up_32((h + 31) / 32), s);
-  return launch_one<R, false, 8, 4, 1024>(a, round_up_32((h + 31) / 32), s);
+  if (h <= 256) return launch_one<R, true, 1, 256>(a, 256, s);
+  if (h <= 512) return launch_one<R, true, 2, 256>(a, 256, s);
+  if (h <= 1024) return launch_one<R, true, 4, 256>(a, 256, s);
+  if (h <= 8192) return launch_one<R, false, 2, 512>(a, round_up_32((h + 15) / 16), s);
+  if (h <= 16384) return launch_one<R, false, 4, 512>(a, round_up_32((h + 31) / 32), s);
+  return launch_one<R, false, 4, 1024>(a, round_up_32((h + 31) / 32), s);
 }
 
 bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1u)) == 0; }
