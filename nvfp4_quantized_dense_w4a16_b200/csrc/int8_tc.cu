@@ -321,6 +321,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
           sc[256 + j] = in && a.bias ? bf16_bits_to_float(a.bias[col0 + j]) : 0.0f;
         }
       }
+      __syncwarp();  // (the barriers want whole warps)
       named_bar_sync(1 + g, 128);
       bool ok = mbar_wait(&accfull[buf], (i >> 1) & 1, abort_flag, err, 8);
       ok = __all_sync(0xffffffffu, ok);
@@ -608,6 +609,7 @@ __global__ void __launch_bounds__(kFewThreads)
       }
     }
   }
+  __syncwarp();    // (half warps leave the loop above on their own; the barrier wants whole warps)
   cluster_sync();  // no CTA leaves while another reads its sums
   if (warp == 1) {
     tc_fence_after();
