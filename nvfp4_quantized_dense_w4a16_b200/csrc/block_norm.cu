@@ -490,12 +490,16 @@ struct Group {
   uint32_t* parts;  // two sets of 16 words, zeros behind the last warp's
   int id, threads, warp;
   int turn = 0;
+  __device__ __forceinline__ void sync() {
+    __syncwarp();  // (the barrier wants whole warps)
+    named_bar_sync(id, threads);
+  }
   __device__ __forceinline__ float sum(float v) {
     v = warp_sum(v);
     uint32_t* p = parts + 16 * turn;
     turn ^= 1;
     if ((threadIdx.x & 31) == 0) p[warp] = __float_as_uint(v);
-    named_bar_sync(id, threads);
+    sync();
     float s[4] = {};
 #pragma unroll
     for (int w = 0; w < 4; ++w)
@@ -510,13 +514,14 @@ struct Group {
     uint32_t* p = parts + 16 * turn;
     turn ^= 1;
     if ((threadIdx.x & 31) == 0) p[warp] = v;
-    named_bar_sync(id, threads);
+    sync();
     v = 0;
     for (int w = 0; w < threads / 32; ++w) v = ::max(v, p[w]);
     return v;
   }
   __device__ __forceinline__ bool all(bool ok) {
     uint32_t r;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
@@ -687,7 +692,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
       load_any<1>(a.gate, a.gate_bf16, r * a.gate_row_stride, t);
       g1 = gate_value(t[0], a.gate_activation);
     }
-    bool ok = mbar_wait(&bar[s], parity, abort_flag, &g_norm_device_error, 1);
+    // The group agrees that the row's copy has landed before it uses any of it: a row that is given up is not stored.
+    if (!row.all(mbar_wait(&bar[s], parity, abort_flag, &g_norm_device_error, 1))) {
+      if (mine == 0)  // (the copies in flight land before the CTA leaves)
+        for (int64_t q = r; q < a.m && q < r + p.slots * step; q += step) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait(&bar[s], parity) && clock64() - t0 < kWaitLimitCycles) {
+          }
+          if (++s == p.slots) s = 0, parity ^= 1;
+        }
+      return;
+    }
     const uint8_t* from = ring + s * p.slot_bytes;
     float2 v[N][U / 2];
 #pragma unroll
@@ -742,18 +757,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
         }
       }
     }
-    ok = row.all(ok);  // and all have read the slot
+    row.sync();  // all have read the slot
     const int64_t next = r + p.slots * step;
-    if (!ok) {  // (the copies in flight land before the CTA leaves)
-      if (mine == 0)
-        for (int64_t q = r; q < a.m && q < next; q += step) {
-          const long long t0 = clock64();
-          while (!mbar_try_wait(&bar[s], parity) && clock64() - t0 < kWaitLimitCycles) {
-          }
-          if (++s == p.slots) s = 0, parity ^= 1;
-        }
-      return;
-    }
     if (mine == 0 && next < a.m) copy(next, s);
     if (++s == p.slots) s = 0, parity ^= 1;
     if (!a.pre.on) continue;
