@@ -715,40 +715,62 @@ GATE_ACTIVATIONS = {"none": 0, "sigmoid": 1, "tanh": 2}
 
 class Norm:
     """norm(v) = v / sqrt(mean(v^2) + eps) * (offset + weight) + bias; kind "layer": of v - mean(v).  weight and bias:
-    float32 or bfloat16 [hidden] of one type, or None.  Holds the tensors; their values are read by each call."""
+    float32 or bfloat16 [hidden] of one type, or None.  Holds the tensors; each call reads them where they are then, in
+    another storage and of another type as well (after `weight.data = other`, a module's `to`), and takes the attributes
+    weight, bias, kind, eps and offset as they were last set."""
 
     def __init__(self, weight=None, bias=None, kind="rms", eps: float = 1e-6, offset: float = 0.0):
+        self.__dict__.update(weight=weight, bias=bias, kind=kind, eps=eps, offset=offset)
+        self._bind(self.__dict__)
+
+    def __setattr__(self, name, value):
+        if name not in ("weight", "bias", "kind", "eps", "offset"):
+            raise AttributeError(f"{name} of a Norm cannot be set")
+        self._bind({**self.__dict__, name: value})  # (refuses what does not fit the others)
+        self.__dict__[name] = value
+
+    def _bind(self, given):
+        weight, bias, kind = given["weight"], given["bias"], given["kind"]
         if kind not in NORM_KINDS:
             raise ValueError(f"kind must be one of {', '.join(map(repr, NORM_KINDS))}, got {kind!r}")
-        given = [t for t in (weight, bias) if t is not None]
+        tensors = [t for t in (weight, bias) if t is not None]
         for name, t in (("weight", weight), ("bias", bias)):
             if t is not None:
                 _need(t, name, t.dtype if isinstance(t, torch.Tensor) and t.dtype in _VALUE_TYPES else torch.bfloat16)
-                if t.dim() != 1 or t.shape != given[0].shape or t.dtype != given[0].dtype or t.device != given[0].device:
+                if t.dim() != 1 or t.shape != tensors[0].shape or t.dtype != tensors[0].dtype or t.device != tensors[0].device:
                     raise ValueError("weight and bias must be vectors of one length, type and device")
-        self.weight, self.bias, self.kind, self.eps, self.offset = weight, bias, kind, eps, offset
-        self.hidden = given[0].numel() if given else None
-        self.device_index = given[0].get_device() if given else None
-        self._struct = _NormStruct(NORM_KINDS[kind], _VALUE_TYPES[given[0].dtype] if given else 0,
-                                   None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
-                                   eps, offset)
-        self._address = ctypes.addressof(self._struct)
+                if t.numel() and not t.data_ptr():
+                    raise ValueError(f"{name} has no storage")
+        addresses = [None if t is None else t.data_ptr() for t in (weight, bias)]
+        struct = _NormStruct(NORM_KINDS[kind], _VALUE_TYPES[tensors[0].dtype] if tensors else 0, *addresses, given["eps"], given["offset"])
+        hidden = tensors[0].numel() if tensors else None
+        device = tensors[0].get_device() if tensors else None
+        # Another storage, type or device of a tensor shows in its address, as the one bound here is kept until then.
+        bound = (ctypes.addressof(struct), hidden, device, weight, bias, *addresses, struct, [t.detach() for t in tensors])
+        self.__dict__.update(_bound=bound, hidden=hidden, device_index=device)
+        return bound
 
 
 # struct ffn_block_norm_args
 _BLOCK_NORM = struct.Struct("@PqPPiiqqPiqPqffPPqP")
 
 
-def _norm_address(norm, name, hidden, dev):
+def _norm_now(norm, name, hidden, dev):
+    """The address of the struct of a norm's tensors as they are now, and what keeps it until the call returns."""
     if norm is None:
-        return 0
-    if not isinstance(norm, Norm):
+        return (0,)
+    if type(norm) is not Norm and not isinstance(norm, Norm):
         raise TypeError(f"{name} must be a Norm")
-    if norm.hidden is not None and (norm.hidden != hidden or norm.device_index != dev):
-        if norm.hidden != hidden:
-            raise ValueError(f"{name} has {norm.hidden} weights, the rows {hidden} values")
-        raise ValueError(f"{name} is on cuda:{norm.device_index}, the current device is cuda:{dev}")
-    return norm._address
+    bound = norm._bound
+    _, length, device, weight, bias, weight_at, bias_at, _, _ = bound
+    if weight is not None and weight.data_ptr() != weight_at or bias is not None and bias.data_ptr() != bias_at:
+        bound = norm._bind(norm.__dict__)
+        length, device = bound[1:3]
+    if length is not None and (length != hidden or device != dev):
+        if length != hidden:
+            raise ValueError(f"{name} has {length} weights, the rows {hidden} values")
+        raise ValueError(f"{name} is on cuda:{device}, the current device is cuda:{dev}")
+    return bound
 
 
 def _rows_of(t, name, dtypes, shape, dev) -> int:
@@ -829,11 +851,12 @@ def ffn_block_norm(residual: torch.Tensor, y=None, post: Norm | None = None, gat
                 _demand(out_scales, "out_scales", torch.float32, (m,), dev)
         elif out_scales is not None:
             raise ValueError("out_scales needs quantize")
+    post_now, pre_now = _norm_now(post, "post", hidden, dev), _norm_now(pre, "pre", hidden, dev)
     args = _BLOCK_NORM.pack(
-        0 if y is None else y.data_ptr(), y_ld, _norm_address(post, "post", hidden, dev), 0 if gate is None else gate.data_ptr(),
+        0 if y is None else y.data_ptr(), y_ld, post_now[0], 0 if gate is None else gate.data_ptr(),
         0 if gate is None else _VALUE_TYPES[gate.dtype], GATE_ACTIVATIONS[gate_activation], gate_row, gate_col,
         residual.data_ptr(), _VALUE_TYPES[dtype], r_ld, 0 if residual_out is None else residual_out.data_ptr(), ro_ld,
-        residual_scale, branch_scale, _norm_address(pre, "pre", hidden, dev), 0 if out is None else out.data_ptr(), out_ld,
+        residual_scale, branch_scale, pre_now[0], 0 if out is None else out.data_ptr(), out_ld,
         0 if out_scales is None else out_scales.data_ptr())
     st = lib.ffn_block_norm(args, m, hidden, _stream_of(stream, dev))
     if st:
