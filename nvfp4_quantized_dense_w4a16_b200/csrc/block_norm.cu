@@ -169,6 +169,20 @@ struct NormFactors {
   float factor, shift;
 };
 
+// Squares of values beyond 2^64 pass fp32's range: such a row is scaled by 2^-75 and summed once more (eps by its
+// square, of which nothing is left but that a row without variance does not divide by zero).
+struct Resum {
+  float eps, by = 1.0f;
+  bool scaled = false;
+  __device__ __forceinline__ bool wanted(float squares) {
+    if (squares < __uint_as_float(0x7f800000u) || scaled) return false;
+    scaled = true;
+    by = 2.6469780e-23f;                        // 2^-75
+    eps = fmaxf(eps * by * by, 1.1754944e-38f);  // 2^-126
+    return true;
+  }
+};
+
 template <bool WARP, int N, typename At>
 __device__ __forceinline__ float row_squares(Row<WARP>& row, bool layer, int hidden, const float (&v)[N][8], At at, float* mean) {
   *mean = 0.0f;
@@ -199,22 +213,17 @@ __device__ __forceinline__ float row_squares(Row<WARP>& row, bool layer, int hid
   return row.sum(s);
 }
 
-// The squares of values beyond 2^64 would pass fp32's range: such a row is scaled
-// by 2^-75 and summed once more.
 template <bool WARP, int N, typename At>
 __device__ __forceinline__ NormFactors norm_factors(Row<WARP>& row, const NormArgs& a, int hidden, float (&v)[N][8], At at) {
   const float share = 1.0f / (float)hidden;
-  float mean, eps = a.eps;
-  float squares = row_squares<WARP, N>(row, a.layer, hidden, v, at, &mean);
-  if (!(squares < __uint_as_float(0x7f800000u))) {
+  float mean, squares;
+  Resum re{a.eps};
+  while (re.wanted(squares = row_squares<WARP, N>(row, a.layer, hidden, v, at, &mean)))
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= 2.6469780e-23f;  // 2^-75
-    eps = 0.0f;  // (nothing beside the squares)
-    squares = row_squares<WARP, N>(row, a.layer, hidden, v, at, &mean);
-  }
-  const float factor = rsqrtf(fmaf(squares, share, eps));
+      for (int j = 0; j < 8; ++j) v[i][j] *= re.by;
+  const float factor = rsqrtf(fmaf(squares, share, re.eps));
   return NormFactors{factor, -mean * factor};
 }
 
@@ -535,8 +544,8 @@ struct Group {
 template <int U, int N>
 __device__ __forceinline__ NormFactors norm_factors2(Group& row, const NormArgs& a, float share, float2 (&v)[N][U / 2],
                                                      const bool (&in)[N]) {
-  float mean = 0.0f, eps = a.eps, squares;
-  for (bool again = false;; again = true) {
+  float mean = 0.0f, squares;
+  for (Resum re{a.eps};;) {
     float2 s[2] = {both(0.0f), both(0.0f)};
     if (a.layer) {
 #pragma unroll
@@ -562,15 +571,16 @@ __device__ __forceinline__ NormFactors norm_factors2(Group& row, const NormArgs&
     }
     s[0] = add2(s[0], s[1]);
     squares = row.sum(s[0].x + s[0].y);
-    if (again || squares < __uint_as_float(0x7f800000u)) break;
-    eps = 0.0f;  // (nothing beside the squares of such a row)
+    if (!re.wanted(squares)) {
+      const float factor = rsqrtf(fmaf(squares, share, re.eps));
+      return NormFactors{factor, -mean * factor};
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i)
+      if (in[i])
 #pragma unroll
-      for (int j = 0; j < U / 2; ++j) v[i][j] = mul2(v[i][j], both(2.6469780e-23f));  // 2^-75
+        for (int j = 0; j < U / 2; ++j) v[i][j] = mul2(v[i][j], both(re.by));
   }
-  const float factor = rsqrtf(fmaf(squares, share, eps));
-  return NormFactors{factor, -mean * factor};
 }
 
 // Coefficients of the columns in shared memory, fp32: 16 bytes at a time, those of a set of 8 in two planes.
@@ -826,8 +836,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) block_norm_any_kernel(const Blo
   griddep_launch_dependents();
   const float share = 1.0f / (float)h;
   auto factors = [&](const NormArgs& n) {
-    float mean = 0.0f, eps = n.eps, squares;
-    for (bool again = false;; again = true) {
+    float mean = 0.0f, squares;
+    for (Resum re{n.eps};;) {
       float s = 0.0f;
       if (n.layer) {
         for (int i = mine; i < h; i += threads) s += v[i];
@@ -839,12 +849,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) block_norm_any_kernel(const Blo
         s = fmaf(d, d, s);
       }
       squares = row.sum(s);
-      if (again || squares < __uint_as_float(0x7f800000u)) break;
-      eps = 0.0f;  // (nothing beside the squares of such a row)
-      for (int i = mine; i < h; i += threads) v[i] *= 2.6469780e-23f;  // 2^-75
+      if (!re.wanted(squares)) {
+        const float factor = rsqrtf(fmaf(squares, share, re.eps));
+        return NormFactors{factor, -mean * factor};
+      }
+      for (int i = mine; i < h; i += threads) v[i] *= re.by;
     }
-    const float factor = rsqrtf(fmaf(squares, share, eps));
-    return NormFactors{factor, -mean * factor};
   };
   for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x) {
     const uint16_t* y = a.y + r * a.y_stride;

@@ -30,3 +30,23 @@ def test_a_norm_follows_its_weights(native, m, hidden):
     other.data = rows(1, hidden, 4)[0]
     with pytest.raises(ValueError, match="CUDA tensor"):
         call(n)
+
+
+#: Rows of every kernel: a warp's, a CTA's, one by one, few and many, and the streaming kernel's.
+PLACES = [(3, 96), (4, 1024), (5, 2048), (4, 20000), (5, 99), (3, 9001), (1500, 1037), (2100, 384), (700, 2048), (450, 5120)]
+
+
+@pytest.mark.parametrize("m,hidden", [(3, 256), (4, 1024), (5, 2048), (3, 16384), (700, 2048), (450, 4096)])
+def test_a_row_of_one_huge_power_of_two(native, m, hidden):
+    """Its sum passes fp32's range, its scaled sums are exact: a layer norm without variance is its bias."""
+    n, p = make_norm(native, hidden, "layer", torch.float32, seed=3)
+    r = rows(m, hidden, 4).float()
+    good = native.ffn_block_norm(r.cuda(), pre=n)[1]
+    r[1] = 2.0 ** 120
+    x = native.ffn_block_norm(r.cuda(), pre=n)[1]
+    assert same_bits(x[1].cpu(), torch.from_numpy(p["bias"]).to(torch.bfloat16))
+    assert same_bits(x[2:], good[2:]) and same_bits(x[0], good[0])
+    odd = torch.empty((m, hidden + 1))  # (rows that are not whole 16 bytes)
+    odd[:, 1:] = r
+    x = native.ffn_block_norm(odd.cuda()[:, 1:], pre=n)[1]
+    assert same_bits(x[1].cpu(), torch.from_numpy(p["bias"]).to(torch.bfloat16)) and torch.all(torch.isfinite(x))
