@@ -137,8 +137,15 @@ __device__ __forceinline__ uint32_t to_bits(uint32_t v) { return v; }
 // barrier is enough.  Words behind the last warp's are zeros.
 template <bool WARP>
 struct Row {
-  uint32_t* parts;
+  uint32_t* parts;  // (one word more, of the row's first value)
   int turn = 0;
+  // The first thread's v.
+  __device__ __forceinline__ float first(float v) {
+    if (WARP) return __shfl_sync(0xffffffffu, v, 0);
+    if (threadIdx.x == 0) parts[64] = __float_as_uint(v);
+    __syncthreads();
+    return __uint_as_float(parts[64]);
+  }
   template <typename T, typename F>
   __device__ __forceinline__ T over(T v, F f) {
 #pragma unroll
@@ -168,6 +175,12 @@ struct Row {
 struct NormFactors {
   float factor, shift;
 };
+
+// A layer norm is taken of (v - c) / 2, c the row's first value.  Of values that hardly differ, a mean of v would be off
+// by more than they differ (and of equal ones the norm would be that of the mean's rounding), or there is no number
+// near enough; their v - c is exact, and other rows' off by 2^-24 of a difference that is in the row.  Halves, as v - c
+// may pass fp32's range.
+__device__ __forceinline__ float layer_eps(float eps) { return fmaxf(0.25f * eps, 1.4012985e-45f); }
 
 // Squares of values beyond 2^64 pass fp32's range: such a row is scaled by 2^-75 and summed once more (eps by its
 // square, of which nothing is left but that a row without variance does not divide by zero).
@@ -213,12 +226,19 @@ __device__ __forceinline__ float row_squares(Row<WARP>& row, bool layer, int hid
   return row.sum(s);
 }
 
-template <bool WARP, int N, typename At>
+template <bool LAYER, bool WARP, int N, typename At>
 __device__ __forceinline__ NormFactors norm_factors(Row<WARP>& row, const NormArgs& a, int hidden, float (&v)[N][8], At at) {
   const float share = 1.0f / (float)hidden;
   float mean, squares;
-  Resum re{a.eps};
-  while (re.wanted(squares = row_squares<WARP, N>(row, a.layer, hidden, v, at, &mean)))
+  if (LAYER && a.layer) {
+    const float c = -0.5f * row.first(v[0][0]);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = fmaf(0.5f, v[i][j], c);
+  }
+  Resum re{a.layer ? layer_eps(a.eps) : a.eps};
+  while (re.wanted(squares = row_squares<WARP, N>(row, LAYER && a.layer, hidden, v, at, &mean)))
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -280,7 +300,7 @@ __device__ __forceinline__ float gate_value(float g, int activation) {
 
 // The new residual of row r from v, the values of y, stored and left in v: each N sets of
 // 8 values at columns at(i), the residual's and (with gate_cols) the gates' by load_res and load_gate.
-template <bool R, bool WARP, int N, typename LoadRes, typename LoadGate, typename At>
+template <bool R, bool LAYER, bool WARP, int N, typename LoadRes, typename LoadGate, typename At>
 __device__ __forceinline__ void residual_row(Row<WARP>& row, const BlockArgs& a, int64_t r, float (&v)[N][8], LoadRes load_res,
                                              LoadGate load_gate, At at) {
   if (!a.y) {
@@ -293,7 +313,7 @@ __device__ __forceinline__ void residual_row(Row<WARP>& row, const BlockArgs& a,
   Weights<N> w;
   if (a.post.on) {
     w.load(a.post, a.hidden, at);
-    f = norm_factors<WARP, N>(row, a.post, a.hidden, v, at);
+    f = norm_factors<LAYER, WARP, N>(row, a.post, a.hidden, v, at);
   }
   float scale = a.branch_scale;
   if (a.gate && !a.gate_cols) {
@@ -334,12 +354,12 @@ __device__ __forceinline__ void residual_row(Row<WARP>& row, const BlockArgs& a,
 }
 
 // The norm of the new residual, and its stores.
-template <bool WARP, int N, typename At>
+template <bool LAYER, bool WARP, int N, typename At>
 __device__ __forceinline__ void output_row(Row<WARP>& row, const BlockArgs& a, int64_t r, int mine, float (&res)[N][8], At at) {
   if (!a.pre.on) return;
   Weights<N> w;
   w.load(a.pre, a.hidden, at);
-  const NormFactors f = norm_factors<WARP, N>(row, a.pre, a.hidden, res, at);
+  const NormFactors f = norm_factors<LAYER, WARP, N>(row, a.pre, a.hidden, res, at);
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (at(i) < a.hidden) w.apply(a.pre, f, i, res[i]);
@@ -368,11 +388,11 @@ __device__ __forceinline__ void output_row(Row<WARP>& row, const BlockArgs& a, i
   if (mine == 0) a.out_scales[r] = q.scale;
 }
 
-// R: the residual is bf16; WARP: a warp for each row, else the CTA; N: accesses of
-// 8 values a thread.
-template <bool R, bool WARP, int N, int THREADS>
+// R: the residual is bf16; LAYER: a norm may be a layer norm; WARP: a warp for each
+// row, else the CTA; N: accesses of 8 values a thread.
+template <bool R, bool LAYER, bool WARP, int N, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const BlockArgs a) {
-  __shared__ __align__(16) uint32_t parts[64];
+  __shared__ __align__(16) uint32_t parts[65];
   Row<WARP> row{parts};
   const int threads = WARP ? 32 : blockDim.x, mine = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int per_cta = WARP ? blockDim.x >> 5 : 1;
@@ -397,9 +417,9 @@ __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const BlockArgs 
         res[i].load(a.residual, R, r * a.residual_stride + at(i));
         if (a.gate && a.gate_cols) g[i].load(a.gate, a.gate_bf16, r * a.gate_row_stride + at(i));
       }
-    residual_row<R, WARP, N>(
+    residual_row<R, LAYER, WARP, N>(
         row, a, r, v, [&](int i, float(&t)[8]) { res[i].get(R, t); }, [&](int i, float(&t)[8]) { g[i].get(a.gate_bf16, t); }, at);
-    output_row<WARP, N>(row, a, r, mine, v, at);
+    output_row<LAYER, WARP, N>(row, a, r, mine, v, at);
   }
 }
 
@@ -540,14 +560,21 @@ struct Group {
   }
 };
 
-// The factors of a norm for N sets of U values; columns behind the row are zeros.
-template <int U, int N>
+// The factors of a norm for N sets of U values, the row's first value c; columns behind the row are zeros.
+template <bool LAYER, int U, int N>
 __device__ __forceinline__ NormFactors norm_factors2(Group& row, const NormArgs& a, float share, float2 (&v)[N][U / 2],
-                                                     const bool (&in)[N]) {
+                                                     const bool (&in)[N], float c) {
   float mean = 0.0f, squares;
-  for (Resum re{a.eps};;) {
+  if (LAYER && a.layer) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (in[i])
+#pragma unroll
+        for (int j = 0; j < U / 2; ++j) v[i][j] = fma2(both(0.5f), v[i][j], both(-0.5f * c));
+  }
+  for (Resum re{a.layer ? layer_eps(a.eps) : a.eps};;) {
     float2 s[2] = {both(0.0f), both(0.0f)};
-    if (a.layer) {
+    if (LAYER && a.layer) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -601,7 +628,7 @@ __device__ __forceinline__ void store_plane(float4* c, int vecs, int vec, const 
 struct StreamPlan {
   int threads, groups, slots;  // threads of a group; groups of a CTA, one CTA an SM; slots of a group
   int slot_bytes;
-  bool shift;                  // the norms may have a mean or a bias
+  bool shift;                  // a norm has a mean or a bias (SHIFT of the kernel)
 };
 
 constexpr int kStreamValues = 32;    // of a thread
@@ -613,13 +640,16 @@ constexpr int kStreamThreads = 768;  // of a CTA, at most
 // rows is made once, in shared memory: the norms' weights, with a gate of the channels
 // and the branch's scale in the first.  A thread has N sets of U values, 32 in all: what a row
 // costs apart from its values (two sums over the group) is shared by as many.  U: 8, or 4
-// where the residual is fp32, so that neighbouring lanes access neighbouring 16 bytes.
-template <bool R>
+// where the residual is fp32, so that neighbouring lanes access neighbouring 16 bytes.  SHIFT: a norm has a mean or a
+// bias; what others do not need would cost them registers (4096 x 5120, bf16, gates by row: 39.6 us with six values
+// spilled, 35.7 without).
+template <bool R, bool SHIFT>
 __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(const BlockArgs a, const StreamPlan p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) uint32_t parts[15][32];
   __shared__ uint64_t full[32];
   __shared__ int abort_word;
+  __shared__ float first_value[15];  // of each group's new residual
   volatile int* abort_flag = &abort_word;
   const int g = threadIdx.x / p.threads, mine = threadIdx.x - g * p.threads;
   Group row{parts[g], 1 + g, p.threads, mine >> 5};
@@ -633,7 +663,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
   float4* w2 = w1 + a.hidden / 4;
   float4* b1 = w2 + a.hidden / 4;  // (with shift)
   float4* b2 = b1 + a.hidden / 4;
-  uint8_t* ring = reinterpret_cast<uint8_t*>(p.shift ? b2 + a.hidden / 4 : b1) + g * p.slots * p.slot_bytes;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(SHIFT ? b2 + a.hidden / 4 : b1) + g * p.slots * p.slot_bytes;
   uint64_t* bar = full + g * p.slots;
   // A slot: y, the residual, the gates if each row has its own.
   const bool own_gates = a.gate && a.gate_cols && a.gate_row_stride != 0, channel_gates = a.gate && a.gate_cols && !own_gates;
@@ -655,11 +685,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
       bulk_load(to + y_bytes + r_bytes, static_cast<const uint8_t*>(a.gate) + r * a.gate_row_stride * (a.gate_bf16 ? 2 : 4),
                 g_bytes, &bar[s]);
   };
-  const int64_t first = blockIdx.x + (int64_t)g * gridDim.x, step = (int64_t)gridDim.x * p.groups;
+  // (rows in 32 bits: of 80 registers none is left, and what is spilled comes back from L2)
+  const int m = (int)a.m, first = blockIdx.x + g * gridDim.x, step = gridDim.x * p.groups;
   griddep_wait();
   griddep_launch_dependents();
   if (mine == 0)
-    for (int s = 0; s < p.slots && first + s * step < a.m; ++s) copy(first + s * step, s);
+    for (int s = 0; s < p.slots && first + s * step < m; ++s) copy(first + s * step, s);
   for (int i = threadIdx.x; i < vecs; i += blockDim.x) {
     float2 w[U / 2], t[U / 2];
     for (int j = 0; j < U / 2; ++j) w[j] = both(a.branch_scale);
@@ -669,7 +700,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
       for (int j = 0; j < U / 2; ++j)
         w[j] = mul2(w[j], t[j]);
     }
-    if (p.shift) {
+    if (SHIFT) {
       for (int j = 0; j < U / 2; ++j) t[j] = both(0.0f);
       if (a.post.bias) load_u<U>(a.post.bias, a.post.bf16, U * i, t);
       for (int j = 0; j < U / 2; ++j) t[j] = mul2(t[j], w[j]);
@@ -681,7 +712,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
     }
     store_plane<U>(w1, vecs, i, w);
     for (int j = 0; j < U / 2; ++j) w[j] = both(1.0f), t[j] = both(0.0f);
-    if (p.shift) {
+    if (SHIFT) {
       if (a.pre.bias) load_u<U>(a.pre.bias, a.pre.bf16, U * i, t);
       store_plane<U>(b2, vecs, i, t);
     }
@@ -695,17 +726,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
   const float share = 1.0f / (float)a.hidden;
   int s = 0;
   uint32_t parity = 0;
-  for (int64_t r = first; r < a.m; r += step) {
+  for (int r = first; r < m; r += step) {
     float g1 = 1.0f;  // the row's gate
     if (a.gate && !a.gate_cols) {
       float t[1];
-      load_any<1>(a.gate, a.gate_bf16, r * a.gate_row_stride, t);
+      load_any<1>(a.gate, a.gate_bf16, (int64_t)r * a.gate_row_stride, t);
       g1 = gate_value(t[0], a.gate_activation);
     }
     // The group agrees that the row's copy has landed before it uses any of it: a row that is given up is not stored.
     if (!row.all(mbar_wait(&bar[s], parity, abort_flag, &g_norm_device_error, 1))) {
       if (mine == 0)  // (the copies in flight land before the CTA leaves)
-        for (int64_t q = r; q < a.m && q < r + p.slots * step; q += step) {
+        for (int q = r; q < m && q < r + p.slots * step; q += step) {
           const long long t0 = clock64();
           while (!mbar_try_wait(&bar[s], parity) && clock64() - t0 < kWaitLimitCycles) {
           }
@@ -723,13 +754,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
     }
     if (a.y) {
       NormFactors f{1.0f, 0.0f};
-      if (a.post.on) f = norm_factors2<U, N>(row, a.post, share, v, in);
+      if (a.post.on) f = norm_factors2<SHIFT, U, N>(row, a.post, share, v, in, bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(from)));
       f.factor *= g1, f.shift *= g1;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         if (!in[i]) continue;
         float2 t[U / 2];
-        if (p.shift) {
+        if (SHIFT) {
 #pragma unroll
           for (int j = 0; j < U / 2; ++j) v[i][j] = fma2(v[i][j], both(f.factor), both(f.shift));
         } else {
@@ -739,7 +770,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
         load_plane<U>(w1, vecs, vec(i), t);
 #pragma unroll
         for (int j = 0; j < U / 2; ++j) v[i][j] = mul2(v[i][j], t[j]);
-        if (p.shift) {
+        if (SHIFT) {
           load_plane<U>(b1, vecs, vec(i), t);
 #pragma unroll
           for (int j = 0; j < U / 2; ++j) v[i][j] = fma2(both(g1), t[j], v[i][j]);
@@ -758,28 +789,29 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
 #pragma unroll
           for (int j = 0; j < U / 2; ++j) q[j] = pack2(v[i][j]), v[i][j] = unpack2(q[j]);
           if (a.residual_out)
-            store_words<U>(static_cast<uint16_t*>(a.residual_out) + r * a.residual_out_stride + U * vec(i), q);
+            store_words<U>(static_cast<uint16_t*>(a.residual_out) + (int64_t)r * a.residual_out_stride + U * vec(i), q);
         } else if (a.residual_out) {
-          float* o = static_cast<float*>(a.residual_out) + r * a.residual_out_stride + U * vec(i);
+          float* o = static_cast<float*>(a.residual_out) + (int64_t)r * a.residual_out_stride + U * vec(i);
 #pragma unroll
           for (int j = 0; j < U / 4; ++j)
             reinterpret_cast<float4*>(o)[j] = make_float4(v[i][2 * j].x, v[i][2 * j].y, v[i][2 * j + 1].x, v[i][2 * j + 1].y);
         }
       }
     }
+    if (SHIFT && mine == 0) first_value[g] = v[0][0].x;
     row.sync();  // all have read the slot
-    const int64_t next = r + p.slots * step;
-    if (mine == 0 && next < a.m) copy(next, s);
+    const int next = r + p.slots * step;
+    if (mine == 0 && next < m) copy(next, s);
     if (++s == p.slots) s = 0, parity ^= 1;
     if (!a.pre.on) continue;
-    const NormFactors f = norm_factors2<U, N>(row, a.pre, share, v, in);
+    const NormFactors f = norm_factors2<SHIFT, U, N>(row, a.pre, share, v, in, first_value[g]);
     uint32_t q[N][U / 2];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (!in[i]) continue;
       float2 t[U / 2];
       load_plane<U>(w2, vecs, vec(i), t);
-      if (p.shift) {
+      if (SHIFT) {
         float2 u[U / 2];
         load_plane<U>(b2, vecs, vec(i), u);
 #pragma unroll
@@ -790,7 +822,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
       }
 #pragma unroll
       for (int j = 0; j < U / 2; ++j) q[i][j] = pack2(v[i][j]);
-      if (!a.out_scales) store_words<U>(static_cast<uint16_t*>(a.out) + r * a.out_stride + U * vec(i), q[i]);
+      if (!a.out_scales) store_words<U>(static_cast<uint16_t*>(a.out) + (int64_t)r * a.out_stride + U * vec(i), q[i]);
     }
     if (!a.out_scales) continue;
     uint32_t top = 0;
@@ -803,7 +835,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (in[i]) {
-        int8_t* o = static_cast<int8_t*>(a.out) + r * a.out_stride + U * vec(i);
+        int8_t* o = static_cast<int8_t*>(a.out) + (int64_t)r * a.out_stride + U * vec(i);
         const uint2 c = int8_encode8(codes, make_uint4(q[i][0], q[i][1], U == 8 ? q[i][2 % (U / 2)] : 0u, U == 8 ? q[i][3 % (U / 2)] : 0u));
         if (U == 8)
           *reinterpret_cast<uint2*>(o) = c;
@@ -826,7 +858,7 @@ __device__ __forceinline__ float load_one(const void* p, bool bf16, int64_t at) 
 template <bool R, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) block_norm_any_kernel(const BlockArgs a) {
   extern __shared__ float v[];
-  __shared__ __align__(16) uint32_t parts[64];
+  __shared__ __align__(16) uint32_t parts[65];
   Row<false> row{parts};
   constexpr int kAtOnce = 4;  // values of a thread under way
   const int mine = threadIdx.x, threads = blockDim.x, h = a.hidden;
@@ -835,25 +867,32 @@ __global__ void __launch_bounds__(THREADS, CTAS) block_norm_any_kernel(const Blo
   griddep_wait();
   griddep_launch_dependents();
   const float share = 1.0f / (float)h;
+  // A norm of the row, (v - c) * factor + shift before its weight and bias.  v stays as it is, so that differences beyond
+  // fp32's range are found by their sums, and the row is scaled.
+  struct Normed {
+    float c, factor, shift;
+    __device__ __forceinline__ float operator()(float v) const { return fmaf(v - c, factor, shift); }
+  };
   auto factors = [&](const NormArgs& n) {
-    float mean = 0.0f, squares;
+    float c = n.layer ? row.first(v[0]) : 0.0f;
     for (Resum re{n.eps};;) {
-      float s = 0.0f;
+      float mean = 0.0f, s = 0.0f;
       if (n.layer) {
-        for (int i = mine; i < h; i += threads) s += v[i];
+        for (int i = mine; i < h; i += threads) s += v[i] - c;
         mean = row.sum(s) * share;
         s = 0.0f;
       }
       for (int i = mine; i < h; i += threads) {
-        const float d = v[i] - mean;
+        const float d = (v[i] - c) - mean;
         s = fmaf(d, d, s);
       }
-      squares = row.sum(s);
+      const float squares = row.sum(s);
       if (!re.wanted(squares)) {
         const float factor = rsqrtf(fmaf(squares, share, re.eps));
-        return NormFactors{factor, -mean * factor};
+        return Normed{c, factor, -mean * factor};
       }
       for (int i = mine; i < h; i += threads) v[i] *= re.by;
+      c *= re.by;
     }
   };
   for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x) {
@@ -870,7 +909,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) block_norm_any_kernel(const Blo
         if (i0 + j * threads < h) v[i0 + j * threads] = t[j];
     }
     if (a.y) {
-      NormFactors f{1.0f, 0.0f};
+      Normed f{0.0f, 1.0f, 0.0f};
       if (a.post.on) f = factors(a.post);
       for (int i0 = mine; i0 < h; i0 += kAtOnce * threads) {
         float x[kAtOnce], g[kAtOnce], w[kAtOnce], b[kAtOnce];
@@ -888,7 +927,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) block_norm_any_kernel(const Blo
         for (int j = 0; j < kAtOnce; ++j) {
           const int i = i0 + j * threads;
           if (i >= h) break;
-          const float z = fmaf(fmaf(v[i], f.factor, f.shift), w[j], b[j]);
+          const float z = fmaf(f(v[i]), w[j], b[j]);
           float s = fmaf(a.residual_scale, x[j], a.branch_scale * (gate_value(g[j], a.gate ? a.gate_activation : 0) * z));
           if (R) s = bf16_round(s);
           v[i] = s;
@@ -901,7 +940,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) block_norm_any_kernel(const Blo
       }
     }
     if (!a.pre.on) continue;
-    const NormFactors f = factors(a.pre);
+    const Normed f = factors(a.pre);
     uint32_t top = 0;
     for (int i0 = mine; i0 < h; i0 += kAtOnce * threads) {
       float w[kAtOnce], b[kAtOnce];
@@ -916,7 +955,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) block_norm_any_kernel(const Blo
       for (int j = 0; j < kAtOnce; ++j) {
         const int i = i0 + j * threads;
         if (i >= h) break;
-        const uint16_t x = f32_to_bf16_bits(fmaf(fmaf(v[i], f.factor, f.shift), w[j], b[j]));
+        const uint16_t x = f32_to_bf16_bits(fmaf(f(v[i]), w[j], b[j]));
         if (a.out_scales)
           top = max(top, x & 0x7fffu), v[i] = bf16_bits_to_float(x);
         else
@@ -936,7 +975,8 @@ cudaError_t launch_one(const BlockArgs& a, int threads, cudaStream_t s) {
   const int64_t per_cta = WARP ? threads / 32 : 1;
   const int64_t ctas = (a.m + per_cta - 1) / per_cta, most = (int64_t)device_sms() * (2048 / threads);
   ProfScope prof(s, "block_norm");
-  return launch_pdl(block_norm_kernel<R, WARP, N, THREADS>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(threads),
+  auto kern = a.post.layer || a.pre.layer ? block_norm_kernel<R, true, WARP, N, THREADS> : block_norm_kernel<R, false, WARP, N, THREADS>;
+  return launch_pdl(kern, dim3((unsigned)(ctas < most ? ctas : most)), dim3(threads),
                     0, s, a);
 }
 
@@ -983,10 +1023,10 @@ cudaError_t launch_rows(const BlockArgs& a, bool vec, cudaStream_t s) {
   // residual, both norms, streaming and by rows, in us: 600 rows of 384, 1024, 2048, 4096 4.6, 5.3, 5.6, 6.5 and 3.6,
   // 5.9, 6.9, 10.5; 2400 rows of 384, 768, 1536, 4096 6.9, 7.7, 10.0, 19.8 and 8.3, 12.0, 14.7, 37.6; of 256 (a warp a
   // row, 8 values a lane) 6.3 and 4.3, 32000 rows 33 and 28.
-  if (h > 256 && a.m >= 2 * device_sms() && a.m * h >= 800000) {
+  if (h > 256 && a.m >= 2 * device_sms() && a.m * h >= 800000 && a.m <= INT32_MAX / 2) {
     const StreamPlan p = plan_stream(a, R);
     if (p.groups > 0) {
-      auto kern = block_norm_stream_kernel<R>;
+      auto kern = p.shift ? block_norm_stream_kernel<R, true> : block_norm_stream_kernel<R, false>;
       const int bytes = stream_coefs(a, p.shift) + p.groups * p.slots * p.slot_bytes;
       // set on every launch: the attribute belongs to the current device's context
       cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);

@@ -50,3 +50,53 @@ def test_a_row_of_one_huge_power_of_two(native, m, hidden):
     odd[:, 1:] = r
     x = native.ffn_block_norm(odd.cuda()[:, 1:], pre=n)[1]
     assert same_bits(x[1].cpu(), torch.from_numpy(p["bias"]).to(torch.bfloat16)) and torch.all(torch.isfinite(x))
+
+
+#: Rows of every kernel: a warp's, a CTA's, one by one (few, many, long), and the streaming kernel's.
+PLACES = [(3, 96), (4, 1000), (5, 2048), (4, 20000), (5, 99), (3, 9001), (1500, 1037), (2100, 384), (700, 2000), (450, 5120)]
+
+
+def near_constant_error(v, p):
+    """norm_error, of a row that has given up its mean.
+
+    What is left of the mean then is at most 128 of the root of the variance and eps (else it is given up once more), so
+    its error of 72 half steps is taken of 128 + 1 of them in the place of the mean magnitude.  The subtraction is off by
+    half a step of each difference, which is one of norm_error's 48.  Where the mean is not given up it is below 128 too."""
+    v = np.asarray(v, dtype=np.float64)
+    t = np.abs(I.norm(v, **dict(p, weight=None, bias=None)))
+    err = (49 * t + 72 * 129 * (1 + 2 * t)) * (1.0 if p["weight"] is None else np.abs(p["offset"] + p["weight"]))
+    return HALF * (err + (0 if p["bias"] is None else 2 * np.abs(p["bias"])))
+
+
+def check_near_constant(native, r, hidden):
+    """fp32 rows as the residual, and, where they are bf16 numbers, as y."""
+    n, p = make_norm(native, hidden, "layer", torch.float32, seed=3)
+    ref, err = I.norm(r.double().numpy(), **p), near_constant_error(r.double().numpy(), p)
+    x = bf16_to_f64(native.ffn_block_norm(r.cuda(), pre=n)[1])
+    assert np.all(np.abs(x - ref) <= err + 2.0 ** -8 * (np.abs(ref) + err)), np.nanmax(np.abs(x - ref))
+    if torch.equal(r, r.to(torch.bfloat16).float()):
+        z = native.ffn_block_norm(torch.zeros_like(r).cuda(), y=r.to(torch.bfloat16).cuda(), post=n)[0].double().cpu().numpy()
+        assert np.all(np.abs(z - ref) <= err + HALF * (4 * np.abs(ref) + err)), np.nanmax(np.abs(z - ref))
+
+
+@pytest.mark.parametrize("m,hidden", PLACES)
+def test_layer_norms_of_rows_of_one_value(native, m, hidden):
+    """Their bias: the rounding of a mean is not normalised in the place of values."""
+    r = rows(m, hidden, 4).to(torch.bfloat16).float()
+    for value in (1000.0, -1.1e6, 2.2e10, 1.3e30, -3.3895314e38, 3e-5):
+        r[1] = value
+        check_near_constant(native, r.to(torch.bfloat16).float(), hidden)
+    r[1] = 1234.567  # (not a bf16 number)
+    check_near_constant(native, r, hidden)
+
+
+@pytest.mark.parametrize("m,hidden", PLACES)
+def test_layer_norms_of_values_that_hardly_differ(native, m, hidden):
+    """A mean of up to 2^23 times what they differ by, neighbouring numbers at the end."""
+    g = torch.Generator().manual_seed(hidden)
+    r = rows(m, hidden, 4).float()
+    for i, ratio in enumerate((100.0, 130.0, 2e3, 1e5, 3e6)):
+        r[1:3] = (ratio * torch.randn((2, 1), generator=g, dtype=torch.float64) + torch.randn((2, hidden), generator=g, dtype=torch.float64)).float()
+        check_near_constant(native, r, hidden)
+    r[1] = torch.where(torch.rand(hidden, generator=g) < 0.5, 1e6, np.float32(np.nextafter(np.float32(1e6), np.float32(2e6))).item())
+    check_near_constant(native, r, hidden)
