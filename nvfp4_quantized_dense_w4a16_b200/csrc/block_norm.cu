@@ -984,6 +984,13 @@ int round_up_32(int v) { return (v + 31) / 32 * 32; }
 
 constexpr int kStreamBytes = 224 * 1024;  // of shared memory
 
+// Set on every launch, as the attribute belongs to the current device's context, and to the most that any launch of the
+// kernel takes: with its own size a call would refuse that of another thread, between the two steps of its launch.
+template <typename Kernel>
+cudaError_t allow_shared(Kernel kern, int bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 int stream_coefs(const BlockArgs& a, bool shift) { return (shift ? 4 : 2) * 4 * a.hidden; }
 
 // As many groups as fit (15 named barriers, 1024 threads), and a second slot for each where there is room;
@@ -1012,9 +1019,10 @@ cudaError_t launch_rows(const BlockArgs& a, bool vec, cudaStream_t s) {
     const bool few = a.m <= (int64_t)device_sms() * (1024 / four) || h > 8192;
     auto kern = few ? block_norm_any_kernel<R, 1024, 1> : block_norm_any_kernel<R, 512, 3>;
     const int threads = few ? four : std::min(512, round_up_32((h + 7) / 8)), bytes = 4 * h;
-    // set on every launch: the attribute belongs to the current device's context
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
+    if (few) {
+      const cudaError_t e = allow_shared(kern, 4 * FFN_NORM_MAX_HIDDEN);
+      if (e != cudaSuccess) return e;
+    }
     const int64_t most = 8 * (int64_t)device_sms();  // (the longest rows' CTAs wait for room)
     ProfScope prof(s, "block_norm");
     return launch_pdl(kern, dim3((unsigned)(a.m < most ? a.m : most)), dim3(threads), bytes, s, a);
@@ -1028,8 +1036,7 @@ cudaError_t launch_rows(const BlockArgs& a, bool vec, cudaStream_t s) {
     if (p.groups > 0) {
       auto kern = p.shift ? block_norm_stream_kernel<R, true> : block_norm_stream_kernel<R, false>;
       const int bytes = stream_coefs(a, p.shift) + p.groups * p.slots * p.slot_bytes;
-      // set on every launch: the attribute belongs to the current device's context
-      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      const cudaError_t e = allow_shared(kern, kStreamBytes);
       if (e != cudaSuccess) return e;
       ProfScope prof(s, "block_norm");
       return launch_pdl(kern, dim3(device_sms()), dim3(p.threads * p.groups), bytes, s, a, p);

@@ -100,3 +100,46 @@ def test_layer_norms_of_values_that_hardly_differ(native, m, hidden):
         check_near_constant(native, r, hidden)
     r[1] = torch.where(torch.rand(hidden, generator=g) < 0.5, 1e6, np.float32(np.nextafter(np.float32(1e6), np.float32(2e6))).item())
     check_near_constant(native, r, hidden)
+
+
+@pytest.mark.parametrize("shapes", [[(500, 2048), (400, 8192)], [(5, 99), (5, 30001)]])
+def test_calls_from_several_threads(native, shapes):
+    """Rows of different widths through the same kernel at once, each thread on its own stream: each has its shared
+    memory whatever the others ask for.  (Two seconds; the C entry itself, so that the calls meet.)"""
+    import ctypes
+    import threading
+    import time
+    from test_int8_abi import BlockArgs
+    calls = []
+    for m, hidden in 2 * shapes:
+        r, y = rows(m, hidden, 1).cuda(), rows(m, hidden, 2).cuda()
+        n = make_norm(native, hidden, seed=1)[0]
+        out, res = torch.empty_like(r), torch.empty_like(r)
+        norm = native._norm_now(n, "pre", hidden, 0)[0] if hasattr(native, "_norm_now") else n._address
+        a = BlockArgs(y=y.data_ptr(), y_stride=hidden, post=norm, residual=r.data_ptr(), residual_type=1, residual_stride=hidden,
+                      residual_out=res.data_ptr(), residual_out_stride=hidden, residual_scale=1.0, branch_scale=1.0, pre=norm,
+                      out=out.data_ptr(), out_stride=hidden)
+        calls.append((m, hidden, a, (r, y, n, out, res), torch.cuda.Stream(), native.ffn_block_norm(r, y=y, post=n, pre=n)))
+    torch.cuda.synchronize()
+    until, bad = time.monotonic() + 2, []
+
+    def work(m, hidden, a, keep, stream, first):
+        torch.cuda.set_device(0)
+        call, at, raw, n = native.lib.ffn_block_norm, ctypes.byref(a), stream.cuda_stream, 0
+        while time.monotonic() < until and not bad:
+            for _ in range(200):
+                status = call(at, m, hidden, raw)
+                if status:
+                    bad.append((m, hidden, n, status))
+                    break
+            n += 200
+            stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=c) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+    for _, _, _, (_, _, _, out, res), _, first in calls:
+        assert same_bits(out, first[1]) and same_bits(res, first[0])
