@@ -53,6 +53,8 @@ struct BlockArgs {
   NormArgs post, pre;
 };
 
+__device__ __host__ __forceinline__ bool finite(float v) { return v - v == 0.0f; }
+
 // V consecutive values of a tensor as fp32.
 template <int V>
 __device__ __forceinline__ void load_bf16(const uint16_t* p, float (&o)[V]) {
@@ -315,17 +317,19 @@ __device__ __forceinline__ void residual_row(Row<WARP>& row, const BlockArgs& a,
     w.load(a.post, a.hidden, at);
     f = norm_factors<LAYER, WARP, N>(row, a.post, a.hidden, v, at);
   }
-  float scale = a.branch_scale;
+  float g1 = 1.0f;  // the row's gate
   if (a.gate && !a.gate_cols) {
     float t[1];
     load_any<1>(a.gate, a.gate_bf16, r * a.gate_row_stride, t);
-    scale *= gate_value(t[0], a.gate_activation);
+    g1 = gate_value(t[0], a.gate_activation);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (at(i) < a.hidden) {
       float t[8];
       if (a.post.on) w.apply(a.post, f, i, v[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= a.branch_scale;
       if (a.gate && a.gate_cols) {
         load_gate(i, t);
         if (a.gate_activation != FFN_GATE_NONE)
@@ -333,11 +337,14 @@ __device__ __forceinline__ void residual_row(Row<WARP>& row, const BlockArgs& a,
           for (int j = 0; j < 8; ++j) t[j] = gate_value(t[j], a.gate_activation);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] *= t[j];
+      } else if (a.gate) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= g1;
       }
       load_res(i, t);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float x = fmaf(a.residual_scale, t[j], scale * v[i][j]);
+        const float x = fmaf(a.residual_scale, t[j], v[i][j]);
         v[i][j] = R ? bf16_round(x) : x;
       }
       if (a.residual_out) {
@@ -421,6 +428,135 @@ __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const BlockArgs 
         row, a, r, v, [&](int i, float(&t)[8]) { res[i].get(R, t); }, [&](int i, float(&t)[8]) { g[i].get(a.gate_bf16, t); }, at);
     output_row<LAYER, WARP, N>(row, a, r, mine, v, at);
   }
+}
+
+// ----------------------------------------- rows that are not whole 16 bytes
+
+__device__ __forceinline__ float load_one(const void* p, bool bf16, int64_t at) {
+  return bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
+}
+
+// A CTA a row, values one by one; the row is in shared memory, where a thread only touches its own.
+// Loops of few instructions: with a row unrolled in registers (8 values a thread, each with its types
+// and gates) the code was long and 203 rows of 1037, layer norm, took 5.9 to 9.6 us; so they take 4.8.
+template <bool R>
+__device__ __forceinline__ void any_rows(const BlockArgs& a, float* v, uint32_t* parts) {
+  Row<false> row{parts};
+  constexpr int kAtOnce = 4;  // values of a thread under way
+  const int mine = threadIdx.x, threads = blockDim.x, h = a.hidden;
+  const float share = 1.0f / (float)h;
+  // A norm of the row, (v - c) * factor + shift before its weight and bias.  v stays as it is, so that differences beyond
+  // fp32's range are found by their sums, and the row is scaled.
+  struct Normed {
+    float c, factor, shift;
+    __device__ __forceinline__ float operator()(float v) const { return fmaf(v - c, factor, shift); }
+  };
+  auto factors = [&](const NormArgs& n) {
+    float c = n.layer ? row.first(v[0]) : 0.0f;
+    for (Resum re{n.eps};;) {
+      float mean = 0.0f, s = 0.0f;
+      if (n.layer) {
+        for (int i = mine; i < h; i += threads) s += v[i] - c;
+        mean = row.sum(s) * share;
+        s = 0.0f;
+      }
+      for (int i = mine; i < h; i += threads) {
+        const float d = (v[i] - c) - mean;
+        s = fmaf(d, d, s);
+      }
+      const float squares = row.sum(s);
+      if (!re.wanted(squares)) {
+        const float factor = rsqrtf(fmaf(squares, share, re.eps));
+        return Normed{c, factor, -mean * factor};
+      }
+      for (int i = mine; i < h; i += threads) v[i] *= re.by;
+      c *= re.by;
+    }
+  };
+  for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x) {
+    const uint16_t* y = a.y + r * a.y_stride;
+    for (int i0 = mine; i0 < h; i0 += kAtOnce * threads) {
+      float t[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int i = i0 + j * threads;
+        if (i < h) t[j] = a.y ? bf16_bits_to_float(y[i]) : load_one(a.residual, R, r * a.residual_stride + i);
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (i0 + j * threads < h) v[i0 + j * threads] = t[j];
+    }
+    if (a.y) {
+      Normed f{0.0f, 1.0f, 0.0f};
+      if (a.post.on) f = factors(a.post);
+      for (int i0 = mine; i0 < h; i0 += kAtOnce * threads) {
+        float x[kAtOnce], g[kAtOnce], w[kAtOnce], b[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int i = i0 + j * threads;
+          g[j] = w[j] = 1.0f, b[j] = 0.0f;
+          if (i >= h) continue;
+          x[j] = load_one(a.residual, R, r * a.residual_stride + i);
+          if (a.gate) g[j] = load_one(a.gate, a.gate_bf16, r * a.gate_row_stride + (a.gate_cols ? i : 0));
+          if (a.post.weight) w[j] = a.post.offset + load_one(a.post.weight, a.post.bf16, i);
+          if (a.post.bias) b[j] = load_one(a.post.bias, a.post.bf16, i);
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int i = i0 + j * threads;
+          if (i >= h) break;
+          const float z = fmaf(f(v[i]), w[j], b[j]);
+          float s = fmaf(a.residual_scale, x[j], a.branch_scale * z * gate_value(g[j], a.gate ? a.gate_activation : 0));
+          if (R) s = bf16_round(s);
+          v[i] = s;
+          if (!a.residual_out) continue;
+          if (R)
+            static_cast<uint16_t*>(a.residual_out)[r * a.residual_out_stride + i] = f32_to_bf16_bits(s);
+          else
+            static_cast<float*>(a.residual_out)[r * a.residual_out_stride + i] = s;
+        }
+      }
+    }
+    if (!a.pre.on) continue;
+    const Normed f = factors(a.pre);
+    uint32_t top = 0;
+    for (int i0 = mine; i0 < h; i0 += kAtOnce * threads) {
+      float w[kAtOnce], b[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int i = i0 + j * threads;
+        w[j] = 1.0f, b[j] = 0.0f;
+        if (i < h && a.pre.weight) w[j] = a.pre.offset + load_one(a.pre.weight, a.pre.bf16, i);
+        if (i < h && a.pre.bias) b[j] = load_one(a.pre.bias, a.pre.bf16, i);
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int i = i0 + j * threads;
+        if (i >= h) break;
+        const uint16_t x = f32_to_bf16_bits(fmaf(f(v[i]), w[j], b[j]));
+        if (a.out_scales)
+          top = max(top, x & 0x7fffu), v[i] = bf16_bits_to_float(x);
+        else
+          static_cast<uint16_t*>(a.out)[r * a.out_stride + i] = x;
+      }
+    }
+    if (!a.out_scales) continue;
+    // The codes are those of the row as it would be stored in bf16.
+    const Int8Row q(row.max(top));
+    for (int i = mine; i < h; i += threads) static_cast<int8_t*>(a.out)[r * a.out_stride + i] = (int8_t)q.code(v[i]);
+    if (mine == 0) a.out_scales[r] = q.scale;
+  }
+}
+
+template <bool R, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) block_norm_any_kernel(const BlockArgs a) {
+  extern __shared__ float v[];
+  __shared__ __align__(16) uint32_t parts[65];
+  for (int i = threadIdx.x; i < 64; i += blockDim.x) parts[i] = 0;
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  any_rows<R>(a, v, parts);
 }
 
 // ------------------------------------------------- many rows of whole 16 bytes
@@ -514,19 +650,22 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
+// Sums and maxima of a group's row stand in sets of words of their own, in the order in which a row meets them: a set is
+// written again a row later only, behind other barriers.
+constexpr int kMeanSet = 0, kSquaresSet = 1, kMaxSet = 4, kSets = 5;  // (of the post norm; of the pre norm 2 more)
+constexpr int kSetWords = 72;  // 24 warps, each group's from a multiple of 4 on
+
 // The threads of a CTA that hold a row: some of its warps, with a named barrier.
 struct Group {
-  uint32_t* parts;  // two sets of 16 words, zeros behind the last warp's
+  uint32_t* parts;  // the group's words of the first set, zeros behind the last warp's
   int id, threads, warp;
-  int turn = 0;
   __device__ __forceinline__ void sync() {
     __syncwarp();  // (the barrier wants whole warps)
     named_bar_sync(id, threads);
   }
-  __device__ __forceinline__ float sum(float v) {
+  __device__ __forceinline__ float sum(float v, int set) {
     v = warp_sum(v);
-    uint32_t* p = parts + 16 * turn;
-    turn ^= 1;
+    uint32_t* p = parts + kSetWords * set;
     if ((threadIdx.x & 31) == 0) p[warp] = __float_as_uint(v);
     sync();
     float s[4] = {};
@@ -540,8 +679,7 @@ struct Group {
   }
   __device__ __forceinline__ uint32_t max(uint32_t v) {
     v = __reduce_max_sync(0xffffffffu, v);
-    uint32_t* p = parts + 16 * turn;
-    turn ^= 1;
+    uint32_t* p = parts + kSetWords * kMaxSet;
     if ((threadIdx.x & 31) == 0) p[warp] = v;
     sync();
     v = 0;
@@ -561,7 +699,7 @@ struct Group {
 };
 
 // The factors of a norm for N sets of U values, the row's first value c; columns behind the row are zeros.
-template <bool LAYER, int U, int N>
+template <bool LAYER, int WHICH, int U, int N>
 __device__ __forceinline__ NormFactors norm_factors2(Group& row, const NormArgs& a, float share, float2 (&v)[N][U / 2],
                                                      const bool (&in)[N], float c) {
   float mean = 0.0f, squares;
@@ -580,7 +718,7 @@ __device__ __forceinline__ NormFactors norm_factors2(Group& row, const NormArgs&
 #pragma unroll
         for (int j = 0; j < U / 2; ++j) s[j & 1] = add2(s[j & 1], v[i][j]);
       s[0] = add2(s[0], s[1]);
-      mean = row.sum(s[0].x + s[0].y) * share;
+      mean = row.sum(s[0].x + s[0].y, kMeanSet + 2 * WHICH) * share;
       s[0] = s[1] = both(0.0f);
 #pragma unroll
       for (int i = 0; i < N; ++i)
@@ -597,7 +735,7 @@ __device__ __forceinline__ NormFactors norm_factors2(Group& row, const NormArgs&
         for (int j = 0; j < U / 2; ++j) s[j & 1] = fma2(v[i][j], v[i][j], s[j & 1]);
     }
     s[0] = add2(s[0], s[1]);
-    squares = row.sum(s[0].x + s[0].y);
+    squares = row.sum(s[0].x + s[0].y, kSquaresSet + 2 * WHICH);
     if (!re.wanted(squares)) {
       const float factor = rsqrtf(fmaf(squares, share, re.eps));
       return NormFactors{factor, -mean * factor};
@@ -607,6 +745,7 @@ __device__ __forceinline__ NormFactors norm_factors2(Group& row, const NormArgs&
       if (in[i])
 #pragma unroll
         for (int j = 0; j < U / 2; ++j) v[i][j] = mul2(v[i][j], both(re.by));
+    row.sync();  // (the sets once more)
   }
 }
 
@@ -628,11 +767,18 @@ __device__ __forceinline__ void store_plane(float4* c, int vecs, int vec, const 
 struct StreamPlan {
   int threads, groups, slots;  // threads of a group; groups of a CTA, one CTA an SM; slots of a group
   int slot_bytes;
+  float share;                 // 1 / hidden
   bool shift;                  // a norm has a mean or a bias (SHIFT of the kernel)
 };
 
 constexpr int kStreamValues = 32;    // of a thread
 constexpr int kStreamThreads = 768;  // of a CTA, at most
+
+// any_rows in a kernel whose registers it should not take.
+template <bool R>
+__device__ __noinline__ void rows_apart(const BlockArgs& a, float* v, uint32_t* parts) {
+  any_rows<R>(a, v, parts);
+}
 
 // One persistent CTA an SM, groups of whose warps work on a row each: as many rows
 // are under way as their inputs find room for in shared memory (bulk copies, the next
@@ -644,15 +790,15 @@ constexpr int kStreamThreads = 768;  // of a CTA, at most
 // bias; what others do not need would cost them registers (4096 x 5120, bf16, gates by row: 39.6 us with six values
 // spilled, 35.7 without).
 template <bool R, bool SHIFT>
-__global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(const BlockArgs a, const StreamPlan p) {
+__global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(const __grid_constant__ BlockArgs a, const __grid_constant__ StreamPlan p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) uint32_t parts[15][32];
+  __shared__ __align__(16) uint32_t parts[kSets * kSetWords];
   __shared__ uint64_t full[32];
   __shared__ int abort_word;
   __shared__ float first_value[15];  // of each group's new residual
   volatile int* abort_flag = &abort_word;
   const int g = threadIdx.x / p.threads, mine = threadIdx.x - g * p.threads;
-  Group row{parts[g], 1 + g, p.threads, mine >> 5};
+  Group row{parts + (p.threads / 32 + 3) / 4 * 4 * g, 1 + g, p.threads, mine >> 5};
   constexpr int U = R ? 8 : 4, N = kStreamValues / U;
   const int vecs = a.hidden / U;
   auto vec = [&](int i) { return mine + i * p.threads; };
@@ -669,7 +815,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
   const bool own_gates = a.gate && a.gate_cols && a.gate_row_stride != 0, channel_gates = a.gate && a.gate_cols && !own_gates;
   const int y_bytes = a.y ? 2 * a.hidden : 0, r_bytes = (R ? 2 : 4) * a.hidden;
   const int g_bytes = own_gates ? (a.gate_bf16 ? 2 : 4) * a.hidden : 0;
-  for (int i = threadIdx.x; i < 15 * 32; i += blockDim.x) (&parts[0][0])[i] = 0;
+  for (int i = threadIdx.x; i < kSets * kSetWords; i += blockDim.x) parts[i] = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.groups * p.slots; ++s) mbar_init(&full[s], 1);
     abort_word = 0;
@@ -691,6 +837,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
   griddep_launch_dependents();
   if (mine == 0)
     for (int s = 0; s < p.slots && first + s * step < m; ++s) copy(first + s * step, s);
+  bool ok = true;  // the first coefficients are finite
   for (int i = threadIdx.x; i < vecs; i += blockDim.x) {
     float2 w[U / 2], t[U / 2];
     for (int j = 0; j < U / 2; ++j) w[j] = both(a.branch_scale);
@@ -703,13 +850,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
     if (SHIFT) {
       for (int j = 0; j < U / 2; ++j) t[j] = both(0.0f);
       if (a.post.bias) load_u<U>(a.post.bias, a.post.bf16, U * i, t);
-      for (int j = 0; j < U / 2; ++j) t[j] = mul2(t[j], w[j]);
+      for (int j = 0; j < U / 2; ++j) t[j] = mul2(t[j], w[j]), ok = ok && finite(t[j].x) && finite(t[j].y);
       store_plane<U>(b1, vecs, i, t);
     }
     if (a.post.weight) {
       load_u<U>(a.post.weight, a.post.bf16, U * i, t);
       for (int j = 0; j < U / 2; ++j) w[j] = mul2(add2(t[j], both(a.post.offset)), w[j]);
     }
+    for (int j = 0; j < U / 2; ++j) ok = ok && finite(w[j].x) && finite(w[j].y);
     store_plane<U>(w1, vecs, i, w);
     for (int j = 0; j < U / 2; ++j) w[j] = both(1.0f), t[j] = both(0.0f);
     if (SHIFT) {
@@ -722,8 +870,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
     }
     store_plane<U>(w2, vecs, i, w);
   }
-  __syncthreads();
-  const float share = 1.0f / (float)a.hidden;
+  if (!__syncthreads_and(ok) && channel_gates) {
+    // A gate of channels is part of coefficients that are not finite (an infinity, of which 0 * inf would come where a
+    // value is 0): these rows are computed in the order of their definition, once the copies have landed.
+    if (mine == 0)
+      for (int s = 0; s < p.slots && first + s * step < m; ++s)
+        mbar_wait(&bar[s], 0, abort_flag, &g_norm_device_error, 1);
+    if (__syncthreads_and(*abort_flag == 0)) rows_apart<R>(a, reinterpret_cast<float*>(smem), parts);
+    return;
+  }
+  const float share = p.share;
   int s = 0;
   uint32_t parity = 0;
   for (int r = first; r < m; r += step) {
@@ -754,8 +910,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
     }
     if (a.y) {
       NormFactors f{1.0f, 0.0f};
-      if (a.post.on) f = norm_factors2<SHIFT, U, N>(row, a.post, share, v, in, bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(from)));
-      f.factor *= g1, f.shift *= g1;
+      if (a.post.on) f = norm_factors2<SHIFT, 0, U, N>(row, a.post, share, v, in, bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(from)));
+      if (!SHIFT) {  // (a row's gate, then, is part of its factor, or takes its place where that would be beyond fp32)
+        if (finite(g1) && !finite(f.factor * g1)) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < U / 2; ++j) v[i][j] = mul2(v[i][j], both(f.factor));
+          f.factor = 1.0f;
+        }
+        f.factor *= g1;
+      }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         if (!in[i]) continue;
@@ -773,7 +938,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
         if (SHIFT) {
           load_plane<U>(b1, vecs, vec(i), t);
 #pragma unroll
-          for (int j = 0; j < U / 2; ++j) v[i][j] = fma2(both(g1), t[j], v[i][j]);
+          for (int j = 0; j < U / 2; ++j) v[i][j] = add2(v[i][j], t[j]);
+        }
+        if (SHIFT && a.gate && !a.gate_cols) {
+#pragma unroll
+          for (int j = 0; j < U / 2; ++j) v[i][j] = mul2(v[i][j], both(g1));
         }
         if (own_gates) {
           load_u<U>(from + y_bytes + r_bytes, a.gate_bf16, U * vec(i), t);
@@ -804,7 +973,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
     if (mine == 0 && next < m) copy(next, s);
     if (++s == p.slots) s = 0, parity ^= 1;
     if (!a.pre.on) continue;
-    const NormFactors f = norm_factors2<SHIFT, U, N>(row, a.pre, share, v, in, first_value[g]);
+    const NormFactors f = norm_factors2<SHIFT, 1, U, N>(row, a.pre, share, v, in, first_value[g]);
     uint32_t q[N][U / 2];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -846,130 +1015,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
   }
 }
 
-// ----------------------------------------- rows that are not whole 16 bytes
-
-__device__ __forceinline__ float load_one(const void* p, bool bf16, int64_t at) {
-  return bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
-}
-
-// A CTA a row, values one by one; the row is in shared memory, where a thread only touches its own.
-// Loops of few instructions: with a row unrolled in registers (8 values a thread, each with its types
-// and gates) the code was long and 203 rows of 1037, layer norm, took 5.9 to 9.6 us; so they take 4.8.
-template <bool R, int THREADS, int CTAS>
-__global__ void __launch_bounds__(THREADS, CTAS) block_norm_any_kernel(const BlockArgs a) {
-  extern __shared__ float v[];
-  __shared__ __align__(16) uint32_t parts[65];
-  Row<false> row{parts};
-  constexpr int kAtOnce = 4;  // values of a thread under way
-  const int mine = threadIdx.x, threads = blockDim.x, h = a.hidden;
-  for (int i = mine; i < 64; i += threads) parts[i] = 0;
-  __syncthreads();
-  griddep_wait();
-  griddep_launch_dependents();
-  const float share = 1.0f / (float)h;
-  // A norm of the row, (v - c) * factor + shift before its weight and bias.  v stays as it is, so that differences beyond
-  // fp32's range are found by their sums, and the row is scaled.
-  struct Normed {
-    float c, factor, shift;
-    __device__ __forceinline__ float operator()(float v) const { return fmaf(v - c, factor, shift); }
-  };
-  auto factors = [&](const NormArgs& n) {
-    float c = n.layer ? row.first(v[0]) : 0.0f;
-    for (Resum re{n.eps};;) {
-      float mean = 0.0f, s = 0.0f;
-      if (n.layer) {
-        for (int i = mine; i < h; i += threads) s += v[i] - c;
-        mean = row.sum(s) * share;
-        s = 0.0f;
-      }
-      for (int i = mine; i < h; i += threads) {
-        const float d = (v[i] - c) - mean;
-        s = fmaf(d, d, s);
-      }
-      const float squares = row.sum(s);
-      if (!re.wanted(squares)) {
-        const float factor = rsqrtf(fmaf(squares, share, re.eps));
-        return Normed{c, factor, -mean * factor};
-      }
-      for (int i = mine; i < h; i += threads) v[i] *= re.by;
-      c *= re.by;
-    }
-  };
-  for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x) {
-    const uint16_t* y = a.y + r * a.y_stride;
-    for (int i0 = mine; i0 < h; i0 += kAtOnce * threads) {
-      float t[kAtOnce];
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const int i = i0 + j * threads;
-        if (i < h) t[j] = a.y ? bf16_bits_to_float(y[i]) : load_one(a.residual, R, r * a.residual_stride + i);
-      }
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j)
-        if (i0 + j * threads < h) v[i0 + j * threads] = t[j];
-    }
-    if (a.y) {
-      Normed f{0.0f, 1.0f, 0.0f};
-      if (a.post.on) f = factors(a.post);
-      for (int i0 = mine; i0 < h; i0 += kAtOnce * threads) {
-        float x[kAtOnce], g[kAtOnce], w[kAtOnce], b[kAtOnce];
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          const int i = i0 + j * threads;
-          g[j] = w[j] = 1.0f, b[j] = 0.0f;
-          if (i >= h) continue;
-          x[j] = load_one(a.residual, R, r * a.residual_stride + i);
-          if (a.gate) g[j] = load_one(a.gate, a.gate_bf16, r * a.gate_row_stride + (a.gate_cols ? i : 0));
-          if (a.post.weight) w[j] = a.post.offset + load_one(a.post.weight, a.post.bf16, i);
-          if (a.post.bias) b[j] = load_one(a.post.bias, a.post.bf16, i);
-        }
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          const int i = i0 + j * threads;
-          if (i >= h) break;
-          const float z = fmaf(f(v[i]), w[j], b[j]);
-          float s = fmaf(a.residual_scale, x[j], a.branch_scale * (gate_value(g[j], a.gate ? a.gate_activation : 0) * z));
-          if (R) s = bf16_round(s);
-          v[i] = s;
-          if (!a.residual_out) continue;
-          if (R)
-            static_cast<uint16_t*>(a.residual_out)[r * a.residual_out_stride + i] = f32_to_bf16_bits(s);
-          else
-            static_cast<float*>(a.residual_out)[r * a.residual_out_stride + i] = s;
-        }
-      }
-    }
-    if (!a.pre.on) continue;
-    const Normed f = factors(a.pre);
-    uint32_t top = 0;
-    for (int i0 = mine; i0 < h; i0 += kAtOnce * threads) {
-      float w[kAtOnce], b[kAtOnce];
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const int i = i0 + j * threads;
-        w[j] = 1.0f, b[j] = 0.0f;
-        if (i < h && a.pre.weight) w[j] = a.pre.offset + load_one(a.pre.weight, a.pre.bf16, i);
-        if (i < h && a.pre.bias) b[j] = load_one(a.pre.bias, a.pre.bf16, i);
-      }
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const int i = i0 + j * threads;
-        if (i >= h) break;
-        const uint16_t x = f32_to_bf16_bits(fmaf(f(v[i]), w[j], b[j]));
-        if (a.out_scales)
-          top = max(top, x & 0x7fffu), v[i] = bf16_bits_to_float(x);
-        else
-          static_cast<uint16_t*>(a.out)[r * a.out_stride + i] = x;
-      }
-    }
-    if (!a.out_scales) continue;
-    // The codes are those of the row as it would be stored in bf16.
-    const Int8Row q(row.max(top));
-    for (int i = mine; i < h; i += threads) static_cast<int8_t*>(a.out)[r * a.out_stride + i] = (int8_t)q.code(v[i]);
-    if (mine == 0) a.out_scales[r] = q.scale;
-  }
-}
-
 template <bool R, bool WARP, int N, int THREADS>
 cudaError_t launch_one(const BlockArgs& a, int threads, cudaStream_t s) {
   const int64_t per_cta = WARP ? threads / 32 : 1;
@@ -999,6 +1044,7 @@ StreamPlan plan_stream(const BlockArgs& a, bool bf16) {
   StreamPlan p = {};
   const int own_gate = a.gate && a.gate_cols && a.gate_row_stride != 0 ? (a.gate_bf16 ? 2 : 4) : 0;
   p.shift = a.post.layer || a.post.bias || a.pre.layer || a.pre.bias;
+  p.share = 1.0f / (float)a.hidden;
   p.threads = round_up_32((a.hidden + kStreamValues - 1) / kStreamValues);
   p.slot_bytes = a.hidden * ((a.y ? 2 : 0) + (bf16 ? 2 : 4) + own_gate);
   const int slots = (kStreamBytes - stream_coefs(a, p.shift)) / p.slot_bytes, most = kStreamThreads / p.threads < 15 ? kStreamThreads / p.threads : 15;
@@ -1053,8 +1099,6 @@ cudaError_t launch_rows(const BlockArgs& a, bool vec, cudaStream_t s) {
 bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1u)) == 0; }
 bool valid_type(int t) { return t == FFN_VALUE_F32 || t == FFN_VALUE_BF16; }
 unsigned size_of(int type) { return type == FFN_VALUE_BF16 ? 2 : 4; }
-bool finite(float v) { return v - v == 0.0f; }
-
 ffn_status check_norm(const ffn_norm* n) {
   if (!n) return FFN_OK;
   if ((n->kind != FFN_NORM_RMS && n->kind != FFN_NORM_LAYER) || !valid_type(n->type) || !finite(n->eps) || !(n->eps > 0.0f) ||

@@ -143,3 +143,50 @@ def test_calls_from_several_threads(native, shapes):
     assert not bad, bad
     for _, _, _, (_, _, _, out, res), _, first in calls:
         assert same_bits(out, first[1]) and same_bits(res, first[0])
+
+
+def same_kind(got, ref, scale):
+    """Infinities with their signs and NaN in the same places; elsewhere within 2^-6 of the largest factor there."""
+    got = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(ref)) and np.array_equal(np.isposinf(got), np.isposinf(ref)) \
+        and np.array_equal(np.isneginf(got), np.isneginf(ref))
+    ok = np.isfinite(ref)
+    assert np.all(np.abs(got[ok] - ref[ok]) <= 2.0 ** -6 * (np.abs(ref[ok]) + scale))
+
+
+@pytest.mark.parametrize("m,hidden", PLACES)
+@pytest.mark.parametrize("post", ["rms", "layer", None])
+@pytest.mark.parametrize("gate", ["row", "channel", "full"])
+def test_infinite_gates(native, m, hidden, post, gate):
+    """Gates, or products with them, that are not finite, whichever kernel takes the rows: an infinity of z's sign, NaN where z is 0."""
+    inf, nan = float("inf"), float("nan")
+    shape = {"row": (m, 1), "channel": (1, hidden), "full": (m, hidden)}[gate]
+    g = torch.randn(shape, generator=torch.Generator().manual_seed(1))
+    g.view(-1)[:3] = torch.tensor([inf, -inf, nan if gate != "channel" else 3e38])
+    y, r = rows(m, hidden, 2), rows(m, hidden, 3).float()
+    y[:, 1::7] = 0.0
+    n, p = (None, None) if post is None else make_norm(native, hidden, post, torch.float32, seed=4)
+    pre = make_norm(native, hidden, "layer", torch.float32, seed=5)[0]
+    res, x = native.ffn_block_norm(r.cuda(), y=y.cuda(), post=n, gate=g.cuda(), pre=pre, branch_scale=0.5)
+    with np.errstate(invalid="ignore", over="ignore"):
+        z = y.double().numpy() if n is None else I.norm(y.double().numpy(), **p)
+        ref = (r.double().numpy() + 0.5 * g.double().numpy() * z).astype(np.float32).astype(np.float64)  # (the residual's type)
+    same_kind(res, ref, 8.0)
+    bad = ~np.isfinite(ref).all(1)
+    assert np.array_equal(np.isnan(x.float().cpu().numpy()).any(1), bad)
+
+
+@pytest.mark.parametrize("m,hidden", PLACES)
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("gate", ["row", "channel", "full"])
+def test_large_gates_of_small_values(native, m, hidden, kind, gate):
+    """A gate times a norm's factor, 1000 for values far below the root of eps, may pass fp32's range where the product
+    with the value does not."""
+    shape = {"row": (m, 1), "channel": (1, hidden), "full": (m, hidden)}[gate]
+    g = 1e36 * (1 + torch.rand(shape, generator=torch.Generator().manual_seed(1)))
+    y, r = (1e-8 * rows(m, hidden, 2).float()).to(torch.bfloat16), 1e30 * rows(m, hidden, 3).float()
+    n, p = make_norm(native, hidden, kind, torch.float32, bias=False, seed=4)
+    res = native.ffn_block_norm(r.cuda(), y=y.cuda(), post=n, gate=g.cuda(), branch_scale=0.5)[0]
+    ref = r.double().numpy() + 0.5 * g.double().numpy() * I.norm(y.double().numpy(), **p)
+    assert np.all(np.isfinite(ref.astype(np.float32)))
+    same_kind(res, ref, 1e27)
