@@ -24,7 +24,7 @@ def body(text, start):
 
 def test_the_streaming_norm_stores_nothing_of_a_copy_that_has_not_landed():
     """The group's vote on the wait stands before the first use of the row, with a way out, in the loop over the rows."""
-    loop = body(code("block_norm.cu"), "block_norm_stream_kernel(const BlockArgs a")
+    loop = body(code("block_norm.cu"), "block_norm_stream_kernel(const")
     loop = loop[loop.index("r += step) {"):]
     wait, use, store = loop.index("mbar_wait("), loop.index("from = ring"), loop.index("residual_out)")
     vote = loop.index("row.all(")
