@@ -529,8 +529,10 @@ typedef struct ffn_block_norm_args {
 /* One launch; m == 0 is a no-op; allocates nothing and does not synchronise.
  * Outputs may not overlap inputs but as said above.  Any hidden from 1 on, at
  * any stride >= hidden; tensors are aligned to their elements (rows of whole 16
- * bytes take a faster path).  A row with a NaN, or an infinity in what a norm
- * reads, has NaN for x' (codes 0, scale NaN).  Errors: FFN_ERR_INVALID_ARG for
+ * bytes take a faster path).  A row with a NaN in what a norm reads is NaN behind
+ * it; with an infinity it is NaN behind a layer norm, and behind an RMS norm NaN at
+ * the infinity and 0 * (offset + weight) + bias elsewhere, as the formula has it.  A
+ * quantised x' with a NaN has codes 0 and the scale NaN.  Errors: FFN_ERR_INVALID_ARG for
  * a missing tensor, an unknown enum value, a stride below hidden, scales that
  * are not finite or an eps that is not finite and positive;
  * FFN_ERR_UNSUPPORTED for hidden > FFN_NORM_MAX_HIDDEN; FFN_ERR_SHAPE for m rows

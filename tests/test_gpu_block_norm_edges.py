@@ -190,3 +190,24 @@ def test_large_gates_of_small_values(native, m, hidden, kind, gate):
     ref = r.double().numpy() + 0.5 * g.double().numpy() * I.norm(y.double().numpy(), **p)
     assert np.all(np.isfinite(ref.astype(np.float32)))
     same_kind(res, ref, 1e27)
+
+
+@pytest.mark.parametrize("m,hidden", PLACES)
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_infinities_in_what_a_norm_reads(native, m, hidden, kind):
+    """The formula's course in every kernel: NaN rows, or zeros (and the bias) around the NaN of an infinity."""
+    n, p = make_norm(native, hidden, kind, torch.float32, seed=3)
+    r = rows(m, hidden, 4).float()
+    r[0, 0], r[1, hidden // 2], r[2, hidden - 1] = float("inf"), -float("inf"), float("nan")
+    with np.errstate(invalid="ignore"):
+        ref = I.norm(r.double().numpy(), **p)
+    assert np.isnan(ref[2]).all() and np.isnan(ref[:2]).sum() == (2 if kind == "rms" else 2 * hidden)
+    x = native.ffn_block_norm(r.cuda(), pre=n)[1]
+    same_kind(x, ref, 2.0 ** -3)
+    if hidden % 32 == 0:
+        c, s = native.ffn_block_norm(r.cuda(), pre=n, quantize=True)[1:]
+        assert torch.isnan(s).nonzero().flatten().tolist() == [0, 1, 2] and torch.all(c[:3] == 0)
+    y = r.to(torch.bfloat16)
+    z = native.ffn_block_norm(torch.zeros_like(r).cuda(), y=y.cuda(), post=n)[0]
+    with np.errstate(invalid="ignore"):
+        same_kind(z, I.norm(y.double().numpy(), **p), 2.0 ** -3)
