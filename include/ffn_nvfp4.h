@@ -469,6 +469,29 @@ ffn_status ffn_int8_forward(const void* x, const float* x_scales, int64_t m, int
                             const float* down_scales, void* out, void* workspace, size_t workspace_bytes,
                             void* stream);
 
+/* The kernel that a product of these layers takes, without launching anything and
+ * callable without a GPU, as ffn_nvfp4_projection_plan (whose roles it has:
+ * FFN_ROLE_LINEAR for ffn_int8_linear; FFN_ROLE_GATE_UP with n = 2 * inter and
+ * k = hidden, and FFN_ROLE_DOWN, for ffn_int8_forward).  The choice is by
+ * estimated times, so sizes that are near to one another may take different
+ * kernels; the results do not differ.  Errors as for ffn_int8_linear. */
+typedef enum ffn_int8_kernel {
+  FFN_INT8_NONE = 0,     /* m == 0: nothing is launched                        */
+  FFN_INT8_ROW = 1,      /* one row, on the CUDA cores                         */
+  FFN_INT8_CLUSTERS = 2, /* weight rows by tiles of 128, clusters cut K        */
+  FFN_INT8_PAIRS = 3     /* pairs of CTAs, tiles of 256 rows of x              */
+} ffn_int8_kernel;
+typedef struct ffn_int8_plan {
+  int kernel;       /* ffn_int8_kernel                                         */
+  int tile_rows;    /* rows of x of a tile                                     */
+  int tile_columns; /* weight rows of a tile (FFN_INT8_ROW: of a CTA)          */
+  int k_splits;     /* ranges of K                                             */
+  int grid;         /* CTAs                                                    */
+  int turns;        /* tiles (FFN_INT8_ROW: blocks of 128 weight rows) that a
+                       CTA or a pair takes one after another, at most          */
+} ffn_int8_plan;
+ffn_status ffn_int8_projection_plan(int64_t m, int64_t n, int64_t k, int role, ffn_int8_plan* out);
+
 /* ---------------------------------------------------------------------------
  * What stands between two layers: the norm after a layer, its gate, the
  * residual, and the norm before the next layer, in one pass over the rows.

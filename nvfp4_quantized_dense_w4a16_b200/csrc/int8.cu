@@ -112,6 +112,16 @@ ffn_status ffn_int8_linear(const void* x, const float* x_scales, int64_t m, cons
   return ffn::moe_status(product(p, ws + c.xq, ws + c.xs, s));
 }
 
+ffn_status ffn_int8_projection_plan(int64_t m, int64_t n, int64_t k, int role, ffn_int8_plan* out) {
+  if (!out || role < FFN_ROLE_LINEAR || role > FFN_ROLE_DOWN) return FFN_ERR_INVALID_ARG;
+  if (ffn_status st = check_linear(m, n, k)) return st;
+  const bool gate_up = role == FFN_ROLE_GATE_UP;
+  if (gate_up && n % 2) return FFN_ERR_SHAPE;
+  *out = ffn_int8_plan{};
+  if (m > 0) *out = ffn::int8_gemv_serves(m, k) ? ffn::int8_gemv_plan(n, k, gate_up) : ffn::int8_product_plan(m, n, k, gate_up);
+  return FFN_OK;
+}
+
 ffn_status ffn_int8_workspace_size(int64_t m, int64_t hidden, int64_t inter, size_t* bytes) {
   if (!bytes) return FFN_ERR_INVALID_ARG;
   if (ffn_status st = check_layer(m, hidden, inter)) return st;

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "ffn_nvfp4.h"
+
 namespace ffn {
 
 // codes and scales of bf16 rows of k columns (a multiple of 8), row i at i * stride.
@@ -28,6 +30,9 @@ struct Int8Product {
   bool first;
 };
 cudaError_t launch_int8_product(const Int8Product& p, cudaStream_t s);
+// What these two choose for a product of n weight rows (gate and up rows, with silu_mul).
+ffn_int8_plan int8_product_plan(int64_t m, int64_t n, int64_t k, bool silu_mul);
+ffn_int8_plan int8_gemv_plan(int64_t n, int64_t k, bool silu_mul);
 // The same for one row, bf16 as well, whose quantisation is part of it.
 bool int8_gemv_serves(int64_t m, int64_t k);
 cudaError_t launch_int8_gemv(const Int8Product& p, cudaStream_t s);

@@ -161,32 +161,46 @@ cudaError_t launch_one(const GemvArgs& a, bool silu, int grid, cudaStream_t s) {
 
 constexpr int kMaxVecs = 4;  // of a thread: they stay in registers
 
+struct GemvShape {
+  int lanes = 0, vecs = 0, per_cta, grid;  // (GemvArgs); vectors a thread
+};
+GemvShape gemv_shape(int64_t cols, int64_t k, bool silu_mul) {
+  GemvShape g;
+  // Threads along K and vectors a thread: the fewest idle places, then the most threads.
+  const int vecs = (int)(k / kVecBytes);
+  int least = INT32_MAX;
+  for (int lanes = kThreads; lanes >= 32; lanes /= 2) {
+    const int need = (vecs + lanes - 1) / lanes;
+    if (need <= kMaxVecs && lanes * need < least) least = lanes * need, g.lanes = lanes, g.vecs = need;
+  }
+  // Two CTAs an SM share the columns evenly; each group of threads has a weight row at least.
+  const int64_t ctas = 2 * (int64_t)device_sms(), groups = kThreads / g.lanes;
+  g.per_cta = (int)std::max((cols + ctas - 1) / ctas, silu_mul ? (groups + 1) / 2 : groups);
+  g.grid = (int)((cols + g.per_cta - 1) / g.per_cta);
+  return g;
+}
+
 }  // namespace
 
 bool int8_gemv_serves(int64_t m, int64_t k) { return m == 1 && k <= kMaxVecs * kThreads * kVecBytes; }
 
 cudaError_t launch_int8_gemv(const Int8Product& p, cudaStream_t s) {
   const int64_t cols = p.silu_mul ? p.n / 2 : p.n;
-  GemvArgs a{p.x, p.xs, p.w, p.ws, p.bias, p.y, p.k, cols, 0, 0, p.first};
-  // Threads along K and vectors a thread: the fewest idle places, then the most threads.
-  const int vecs = (int)(p.k / kVecBytes);
-  int v = 0, least = INT32_MAX;
-  for (int lanes = kThreads; lanes >= 32; lanes /= 2) {
-    const int need = (vecs + lanes - 1) / lanes;
-    if (need <= kMaxVecs && lanes * need < least) least = lanes * need, a.lanes = lanes, v = need;
-  }
-  // Two CTAs an SM share the columns evenly; each group of threads has a weight row at least.
-  const int64_t ctas = 2 * (int64_t)device_sms(), groups = kThreads / a.lanes;
-  const int64_t per = std::max((cols + ctas - 1) / ctas, p.silu_mul ? (groups + 1) / 2 : groups);
-  a.per_cta = (int)per;
-  const int grid = (int)((cols + per - 1) / per);
+  const GemvShape g = gemv_shape(cols, p.k, p.silu_mul);
+  const GemvArgs a{p.x, p.xs, p.w, p.ws, p.bias, p.y, p.k, cols, g.per_cta, g.lanes, p.first};
   ProfScope prof(s, p.silu_mul ? "int8_gate_up" : "int8_product");
-  switch (v) {
-    case 1: return launch_one<1>(a, p.silu_mul, grid, s);
-    case 2: return launch_one<2>(a, p.silu_mul, grid, s);
-    case 3: return launch_one<3>(a, p.silu_mul, grid, s);
-    default: return launch_one<kMaxVecs>(a, p.silu_mul, grid, s);
+  switch (g.vecs) {
+    case 1: return launch_one<1>(a, p.silu_mul, g.grid, s);
+    case 2: return launch_one<2>(a, p.silu_mul, g.grid, s);
+    case 3: return launch_one<3>(a, p.silu_mul, g.grid, s);
+    default: return launch_one<kMaxVecs>(a, p.silu_mul, g.grid, s);
   }
+}
+
+ffn_int8_plan int8_gemv_plan(int64_t n, int64_t k, bool silu_mul) {
+  const GemvShape g = gemv_shape(silu_mul ? n / 2 : n, k, silu_mul);
+  const int rows = silu_mul ? 2 * g.per_cta : g.per_cta;
+  return ffn_int8_plan{FFN_INT8_ROW, 1, rows, 1, g.grid, (rows + kBlockRows - 1) / kBlockRows};
 }
 
 }  // namespace ffn

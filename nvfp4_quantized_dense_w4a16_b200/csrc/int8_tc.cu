@@ -749,6 +749,18 @@ bool use_few(int64_t m, int64_t cols, int64_t k, bool silu) {
 
 }  // namespace
 
+ffn_int8_plan int8_product_plan(int64_t m, int64_t n, int64_t k, bool silu_mul) {
+  const int64_t cols = silu_mul ? n / 2 : n;
+  if (use_few(m, cols, k, silu_mul)) {
+    const FewPlan f = few_plan(m, cols, k, silu_mul);
+    const int64_t tiles = ceil_div(cols, silu_mul ? 64 : 128);
+    return ffn_int8_plan{FFN_INT8_CLUSTERS, f.n, 128, f.splits, (int)(tiles * f.splits * f.blocks), 1};
+  }
+  const int tile_n = pair_plan(m, cols, k, silu_mul).tile_n;
+  const int64_t tiles = ceil_div(m, kPairRows) * ceil_div(cols, silu_mul ? tile_n / 2 : tile_n), pairs = std::min<int64_t>(tiles, device_sms() / 2);
+  return ffn_int8_plan{FFN_INT8_PAIRS, kPairRows, tile_n, 1, (int)(2 * pairs), (int)ceil_div(tiles, pairs)};
+}
+
 cudaError_t launch_int8_product(const Int8Product& p, cudaStream_t s) {
   ProfScope prof(s, p.silu_mul ? "int8_gate_up" : "int8_product");
   if (use_few(p.m, p.silu_mul ? p.n / 2 : p.n, p.k, p.silu_mul)) return p.silu_mul ? launch_few<true>(p, s) : launch_few<false>(p, s);

@@ -45,6 +45,14 @@ KERNEL_FAMILIES = {0: "none", 1: "tc_w4a16", 2: "tc_w4a4", 3: "gemv_w4a16", 4: "
 ROLES = {"linear": 0, "gate_up": 1, "down": 2}
 
 
+class Int8Plan(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int), ("tile_rows", ctypes.c_int), ("tile_columns", ctypes.c_int), ("k_splits", ctypes.c_int),
+                ("grid", ctypes.c_int), ("turns", ctypes.c_int)]
+
+
+INT8_KERNELS = {0: "none", 1: "row", 2: "clusters", 3: "pairs"}
+
+
 class MoeRouter(ctypes.Structure):
     _fields_ = [("scoring", ctypes.c_int), ("top_k", ctypes.c_int), ("groups", ctypes.c_int),
                 ("top_groups", ctypes.c_int), ("group_score", ctypes.c_int), ("renormalize", ctypes.c_int),
@@ -103,6 +111,7 @@ def _load() -> ctypes.CDLL:
         "ffn_int8_quantize": (ctypes.c_int, [vp, i64, i64, i64, vp, vp, vp]),
         "ffn_int8_linear_workspace_size": (ctypes.c_int, [i64, i64, i64, P(sz)]),
         "ffn_int8_linear": (ctypes.c_int, [vp, vp, i64, vp, vp, vp, i64, i64, vp, vp, sz, vp]),
+        "ffn_int8_projection_plan": (ctypes.c_int, [i64, i64, i64, ctypes.c_int, P(Int8Plan)]),
         "ffn_int8_workspace_size": (ctypes.c_int, [i64, i64, i64, P(sz)]),
         "ffn_int8_forward": (ctypes.c_int, [vp, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp]),
         "ffn_block_norm": (ctypes.c_int, [vp, i64, i64, vp]),
@@ -594,6 +603,15 @@ def ffn_int8_workspace_size(m: int, hidden: int, inter: int) -> int:
     out = ctypes.c_size_t()
     _check("ffn_int8_workspace_size", lib.ffn_int8_workspace_size(m, hidden, inter, ctypes.byref(out)))
     return out.value
+
+
+def ffn_int8_projection_plan(m: int, n: int, k: int, role: str = "linear") -> dict:
+    """The kernel that a product of m rows takes (nothing launched); role: 'linear', or the layer's 'gate_up'
+    (n = 2 * inter, k = hidden) or 'down'."""
+    p = Int8Plan()
+    _check("ffn_int8_projection_plan", lib.ffn_int8_projection_plan(m, n, k, ROLES[role], ctypes.byref(p)))
+    return {"kernel": INT8_KERNELS.get(p.kernel, str(p.kernel)), "tile_rows": p.tile_rows, "tile_columns": p.tile_columns,
+            "k_splits": p.k_splits, "grid": p.grid, "turns": p.turns}
 
 
 _Tensor = torch.Tensor
