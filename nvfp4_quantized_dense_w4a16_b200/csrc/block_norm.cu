@@ -1073,11 +1073,14 @@ cudaError_t launch_rows(const BlockArgs& a, bool vec, cudaStream_t s) {
     ProfScope prof(s, "block_norm");
     return launch_pdl(kern, dim3((unsigned)(a.m < most ? a.m : most)), dim3(threads), bytes, s, a);
   }
-  // The streaming kernel, from where its start (one CTA an SM, the columns' coefficients) is made up for: bf16
-  // residual, both norms, streaming and by rows, in us: 600 rows of 384, 1024, 2048, 4096 4.6, 5.3, 5.6, 6.5 and 3.6,
-  // 5.9, 6.9, 10.5; 2400 rows of 384, 768, 1536, 4096 6.9, 7.7, 10.0, 19.8 and 8.3, 12.0, 14.7, 37.6; of 256 (a warp a
-  // row, 8 values a lane) 6.3 and 4.3, 32000 rows 33 and 28.
-  if (h > 256 && a.m >= 2 * device_sms() && a.m * h >= 800000 && a.m <= INT32_MAX / 2) {
+  // The streaming kernel, for more rows than the kernels by rows have under way at once (8 warps or 512 threads an SM):
+  // their second wave costs as much as the first, the streaming kernel's start (the columns' coefficients) less.  Both
+  // norms, by rows and streaming, in us, bf16 residual: 450 and 600 rows of 2048 4.8, 7.1 and 5.2, 5.4; 150, 200 and
+  // 300 of 4096, 5120 and 4096 4.8, 8.2, 7.5 and 5.2, 5.4, 5.4; 140 and 149 of 8192 5.4, 8.8 and 5.9, 6.2; 1184 of 512 4.1 and
+  // 4.8, 1190 of 384 6.2 and 4.7; 2400 of 4096 20.2 and 12.7.  Rows of four accesses a lane are slow by a warp each: 640 of
+  // 1024 6.4 and 5.3 (fp32 6.6 and 6.5).  Of 256 (an access a lane) 600 rows take 3.2 and 4.4, 9600 10.2 and 11.9.
+  const int64_t at_once = (int64_t)device_sms() * (h <= 1024 ? 8 : std::max(1, 512 / round_up_32((h + 15) / 16)));
+  if (h > 256 && (a.m > at_once || (h > 512 && h <= 1024 && a.m * h >= 600000)) && a.m <= INT32_MAX / 2) {
     const StreamPlan p = plan_stream(a, R);
     if (p.groups > 0) {
       auto kern = p.shift ? block_norm_stream_kernel<R, true> : block_norm_stream_kernel<R, false>;

@@ -102,7 +102,7 @@ def test_layer_norms_of_values_that_hardly_differ(native, m, hidden):
     check_near_constant(native, r, hidden)
 
 
-@pytest.mark.parametrize("shapes", [[(500, 2048), (400, 8192)], [(5, 99), (5, 30001)]])
+@pytest.mark.parametrize("shapes", [[(600, 2048), (400, 8192)], [(5, 99), (5, 30001)]])
 def test_calls_from_several_threads(native, shapes):
     """Rows of different widths through the same kernel at once, each thread on its own stream: each has its shared
     memory whatever the others ask for.  (Two seconds; the C entry itself, so that the calls meet.)"""
