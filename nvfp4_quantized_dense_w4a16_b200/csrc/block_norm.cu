@@ -55,41 +55,19 @@ struct BlockArgs {
 
 __device__ __host__ __forceinline__ bool finite(float v) { return v - v == 0.0f; }
 
-// V consecutive values of a tensor as fp32.
-template <int V>
-__device__ __forceinline__ void load_bf16(const uint16_t* p, float (&o)[V]) {
-  if (V == 8) {
-    const uint4 t = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      o[2 * i] = __uint_as_float(w[i] << 16);
-      o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-    o[0] = bf16_bits_to_float(*p);
-  }
+__device__ __forceinline__ float load_one(const void* p, bool bf16, int64_t at) {
+  return bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
 }
 
-template <int V>
-__device__ __forceinline__ void load_f32(const float* p, float (&o)[V]) {
-  if (V == 8) {
+// 8 consecutive values as fp32.
+__device__ __forceinline__ void load_bf16(const uint16_t* p, float (&o)[8]) {
+  const uint4 t = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      const float4 t = reinterpret_cast<const float4*>(p)[i];
-      o[4 * i] = t.x, o[4 * i + 1] = t.y, o[4 * i + 2] = t.z, o[4 * i + 3] = t.w;
-    }
-  } else {
-    o[0] = *p;
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = __uint_as_float(w[i] << 16);
+    o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
-}
-
-template <int V>
-__device__ __forceinline__ void load_any(const void* p, bool bf16, int64_t at, float (&o)[V]) {
-  if (bf16)
-    load_bf16<V>(static_cast<const uint16_t*>(p) + at, o);
-  else
-    load_f32<V>(static_cast<const float*>(p) + at, o);
 }
 
 // The same in two steps, so that a load can stand far before its use: the words as
@@ -319,9 +297,7 @@ __device__ __forceinline__ void residual_row(Row<WARP>& row, const BlockArgs& a,
   }
   float g1 = 1.0f;  // the row's gate
   if (a.gate && !a.gate_cols) {
-    float t[1];
-    load_any<1>(a.gate, a.gate_bf16, r * a.gate_row_stride, t);
-    g1 = gate_value(t[0], a.gate_activation);
+    g1 = gate_value(load_one(a.gate, a.gate_bf16, r * a.gate_row_stride), a.gate_activation);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i)
@@ -420,7 +396,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const BlockArgs 
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (at(i) < a.hidden) {
-        if (a.y) load_bf16<8>(a.y + r * a.y_stride + at(i), v[i]);
+        if (a.y) load_bf16(a.y + r * a.y_stride + at(i), v[i]);
         res[i].load(a.residual, R, r * a.residual_stride + at(i));
         if (a.gate && a.gate_cols) g[i].load(a.gate, a.gate_bf16, r * a.gate_row_stride + at(i));
       }
@@ -431,10 +407,6 @@ __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const BlockArgs 
 }
 
 // ----------------------------------------- rows that are not whole 16 bytes
-
-__device__ __forceinline__ float load_one(const void* p, bool bf16, int64_t at) {
-  return bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
-}
 
 // A CTA a row, values one by one; the row is in shared memory, where a thread only touches its own.
 // Loops of few instructions: with a row unrolled in registers (8 values a thread, each with its types
@@ -452,7 +424,7 @@ __device__ __forceinline__ void any_rows(const BlockArgs& a, float* v, uint32_t*
     __device__ __forceinline__ float operator()(float v) const { return fmaf(v - c, factor, shift); }
   };
   auto factors = [&](const NormArgs& n) {
-    float c = n.layer ? row.first(v[0]) : 0.0f;
+    float c = n.layer ? row.first(mine == 0 ? v[0] : 0.0f) : 0.0f;
     for (Resum re{n.eps};;) {
       float mean = 0.0f, s = 0.0f;
       if (n.layer) {
@@ -885,9 +857,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
   for (int r = first; r < m; r += step) {
     float g1 = 1.0f;  // the row's gate
     if (a.gate && !a.gate_cols) {
-      float t[1];
-      load_any<1>(a.gate, a.gate_bf16, (int64_t)r * a.gate_row_stride, t);
-      g1 = gate_value(t[0], a.gate_activation);
+      g1 = gate_value(load_one(a.gate, a.gate_bf16, (int64_t)r * a.gate_row_stride), a.gate_activation);
     }
     // The group agrees that the row's copy has landed before it uses any of it: a row that is given up is not stored.
     if (!row.all(mbar_wait(&bar[s], parity, abort_flag, &g_norm_device_error, 1))) {
@@ -1038,7 +1008,7 @@ cudaError_t allow_shared(Kernel kern, int bytes) {
 
 int stream_coefs(const BlockArgs& a, bool shift) { return (shift ? 4 : 2) * 4 * a.hidden; }
 
-// As many groups as fit (15 named barriers, 1024 threads), and a second slot for each where there is room;
+// As many groups as fit (15 named barriers, kStreamThreads), and a second slot for each where there is room;
 // no groups where even two rows do not fit.
 StreamPlan plan_stream(const BlockArgs& a, bool bf16) {
   StreamPlan p = {};
