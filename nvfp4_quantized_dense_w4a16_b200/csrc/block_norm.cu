@@ -1132,7 +1132,7 @@ extern "C" ffn_status ffn_block_norm(const ffn_block_norm_args* b, int64_t m, in
   if (!b->residual || (b->pre && !b->out) || (b->y && !b->residual_out && !b->pre)) return FFN_ERR_INVALID_ARG;
   const unsigned rs = size_of(b->residual_type);
   if (!aligned(b->y, 2) || !aligned(b->residual, rs) || !aligned(b->residual_out, rs) || !aligned(b->out_scales, 4) ||
-      (b->out && !aligned(b->out, b->out_scales ? 8 : 2)) || (b->gate && !aligned(b->gate, size_of(b->gate_type))))
+      !aligned(b->out, b->out_scales ? 1 : 2) || (b->gate && !aligned(b->gate, size_of(b->gate_type))))
     return FFN_ERR_ALIGNMENT;
   bool vec = hidden % 8 == 0 && whole(b->y, b->y_stride) && whole(b->residual, b->residual_stride) &&
              whole(b->residual_out, b->residual_out_stride) && whole(b->out, b->out_stride) &&

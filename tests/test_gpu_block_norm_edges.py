@@ -211,3 +211,17 @@ def test_infinities_in_what_a_norm_reads(native, m, hidden, kind):
     z = native.ffn_block_norm(torch.zeros_like(r).cuda(), y=y.cuda(), post=n)[0]
     with np.errstate(invalid="ignore"):
         same_kind(z, I.norm(y.double().numpy(), **p), 2.0 ** -3)
+
+
+@pytest.mark.parametrize("m,hidden", [(3, 96), (5, 2048), (700, 1024)])
+def test_codes_at_any_address(native, m, hidden):
+    """Tensors are aligned to their elements, and a code is one byte."""
+    r, n = rows(m, hidden, 1).cuda(), make_norm(native, hidden)[0]
+    for offset in (1, 4, 8):
+        buffer = torch.full((m * hidden + 16,), 55, dtype=torch.int8, device="cuda")
+        out = buffer[offset:offset + m * hidden].view(m, hidden)
+        c, s = native.ffn_block_norm(r, pre=n, quantize=True, out=out)[1:]
+        rc, rs = native.ffn_int8_quantize(native.ffn_block_norm(r.clone(), pre=n)[1])
+        assert c is out and torch.all(buffer[:offset] == 55) and torch.all(buffer[offset + m * hidden:] == 55)
+        step = rs[:, None] * 127 * 2.0 ** -7 + rs[:, None]  # (sums in another order: a bf16 step, and a code)
+        assert torch.all(torch.isfinite(s)) and torch.all((c.float() * s[:, None] - rc.float() * rs[:, None]).abs() <= step)
