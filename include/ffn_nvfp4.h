@@ -413,7 +413,8 @@ ffn_status ffn_nvfp4_moe_forward(const void* x, int64_t m, int64_t hidden, int64
  * layers/dense_ffn_fixed.rs", forward_fixed, has such an 8-bit arm, of FP8
  * rows; this integer format and its definitions are this library's.)
  * The sums are exact in 32-bit integers and what follows them is the same in
- * every kernel: each output row is bit-identical whatever m is.
+ * every kernel: each output row is bit-identical whatever m is, for the rows and
+ * scales that the call is given (rows that ffn_block_norm made need not be: below).
  * ------------------------------------------------------------------------- */
 #define FFN_INT8_MAX_K 131040 /* sums of k products of magnitude 128^2 fit 32 bits */
 
@@ -460,7 +461,10 @@ ffn_status ffn_int8_linear(const void* x, const float* x_scales, int64_t m, cons
  *   out      [m, hidden] bf16; only rows 0..m-1 are written; may be x (bf16)
  * Numerics: gate and up stay fp32 (their exact sums times the two scales);
  * h = silu(gate) * up is rounded to bf16 and quantised as ffn_int8_quantize
- * does; the down projection is ffn_int8_linear's.  Everything else (workspace,
+ * does; the down projection is ffn_int8_linear's.  silu takes the hardware's
+ * exponential and reciprocal, two steps of fp32 off each (the exponential one
+ * more for each unit of |gate|), and is 0 where the sigmoid is below 2^-126:
+ * an h next to a rounding may take the other neighbour of the exact formula's.  Everything else (workspace,
  * stream order, m == 0, errors) as for ffn_int8_linear, with
  * ffn_int8_workspace_size bytes, which are always needed. */
 ffn_status ffn_int8_workspace_size(int64_t m, int64_t hidden, int64_t inter, size_t* bytes);
@@ -523,7 +527,12 @@ typedef struct ffn_norm {
  *   x'   = pre norm of r' (as rounded), in bf16            -> out
  * with out_scales: x' is quantised as ffn_int8_quantize does -> out (int8 codes)
  * and out_scales.  Without y (the first layer) r' is the residual itself: there
- * is no gate and no residual_out, and the scales are 1.  Statistics are fp32.
+ * is no gate and no residual_out, and the scales are 1.  Statistics are fp32, a
+ * layer norm's mean of what differs from the row's first value; sigmoid and tanh are
+ * within 8 half steps of fp32, sigmoids below 2^-126 are zeros.  Sums are taken in an
+ * order that goes with the kernel, which is chosen by m, hidden and the tensors'
+ * alignment: a row's r', x' and codes may differ in their last bit from those that the
+ * same row has in another batch.
  * Rows are strided: row i of a tensor starts at i * stride elements. */
 typedef struct ffn_block_norm_args {
   const void* y;            /* bf16 [m, hidden], or NULL                      */

@@ -11,11 +11,12 @@
 // sum (one row of 4096, both norms: 5.2 -> 3.8 us in a graph).  Many are bound by their
 // memory traffic if the instructions allow: 4096 rows of 5120, fp32 residual, both
 // norms, a gate for each channel (252 MB) take 47 us, 5.3 TB/s, 81% of the measured copy
-// rate; 16384 rows of 2048 with tanh gates of their own (336 MB) 69 us, 74%.  With a CTA
-// a row and plain loads those took 142 and 177 us (one or two rows under way in an SM,
-// 88 instructions a value); rows prefetched into a ring 93 and 139; 32 values a thread
-// and packed fp32 arithmetic 59 and 79; groups of one CTA that share the columns'
-// coefficients 47 and 77; the hardware's exponential and quotient in tanh 69.
+// rate; 16384 rows of 2048 with tanh gates of their own (336 MB) 67 us, 77% (47
+// instructions a value, 38 in the former).  With a CTA a row and plain loads those
+// took 142 and 177 us (one or two rows under way in an SM); rows prefetched into a ring
+// 93 and 139; 32 values a thread and packed fp32 arithmetic 59 and 79; groups of one CTA
+// that share the columns' coefficients 47 and 77; the hardware's exponential and quotient
+// in tanh 69; no registers spilled, as RMS norms are compiled apart, 67.
 #include <algorithm>
 
 #include "ffn_nvfp4.h"

@@ -6,9 +6,10 @@
 // itself from a bf16 row (whose largest magnitude is a maximum over the CTA), and the
 // first weights are under way before it waits for the kernel ahead that makes the row.
 // Four products an instruction; a warp's sum is one reduction of integers.
-// In a graph, from a bf16 row (from codes): 4096 x 4096 6.6 us (5.7), 24576 x 4096 19.6
-// (18.1, 5.6 TB/s), 4096 x 12288 12.4 (10.0); quantisation and the product on the tensor
-// cores take 9.0, 21 and 14.  Two rows so took 8.3, 23.6 and 16.1, four 12.5, 37 and 14.
+// In a graph, from a bf16 row (from codes): 4096 x 4096 5.4 us (4.5), 24576 x 4096 18.3
+// (17.3, 5.8 TB/s), 4096 x 12288 11.2 (9.0); two rows, quantised and multiplied on the
+// tensor cores, take 8.9, 21.0 and 13.9.  Two rows so took 8.3, 23.6 and 16.1, four 12.5,
+// 37 and 14.
 #include <algorithm>
 
 #include "int8.cuh"

@@ -655,9 +655,9 @@ struct PairPlan {
 };
 
 // The columns of a tile: wide ones take fewer cycles a product, but may leave pairs of SMs idle in the last wave.
-// A chunk of K measures 400 cycles for up to 80 columns, and 300 + 1.25 a column from there (64 pairs of SMs at a time:
-// the traffic from L2, 12 TB/s, and 390 cycles of barriers a stage that even an empty one takes; 512 at 256 columns by
-// the MMAs alone).  512 rows, 5120 x 17408, tiles of 96, 128, 160, 192, 256: 63, 64, 42, 44, 48 us.
+// A chunk of K measures 400 cycles for up to 80 columns, and 300 + 1.25 a column from there (64 pairs of SMs at a time; 512
+// at 256 columns by the MMAs alone).  512 rows, 5120 x 17408, tiles of 96, 128, 160, 192, 256: 63, 64, 42, 44, 48 us; with 160
+// the tensor pipe is 57% busy, and 450 MB come through L2, 10.5 TB/s.
 PairPlan pair_plan(int64_t m, int64_t cols, int64_t k, bool silu) {
   const int clusters = device_sms() / 2;
   const int64_t kc = ceil_div(k, kChunkK), m_tiles = ceil_div(m, kPairRows);
@@ -681,8 +681,8 @@ struct FewPlan {
 
 constexpr int64_t kFewBlock = 128;  // rows of a CTA, at most: their sums are two thirds of the ring
 
-// Clusters of 1, 2, ... CTAs that are resident at a time, an SM each or two an SM (measured; a cluster stays
-// within a part of the GPU).  The most CTAs that start at once: with one more wave of clusters 5120 x 17408 takes
+// Clusters of 1, 2, ... CTAs that are resident at a time, an SM each or two an SM (measured on 148 SMs; a cluster stays
+// within a part of the GPU; elsewhere the estimate, and with it the cut, is only less good).  The most CTAs that start at once: with one more wave of clusters 5120 x 17408 takes
 // 24 us, cut into 8, and 18.0, cut into 6.  Short ranges of K do better with one CTA an SM, beside which the next
 // kernel's can start: 4096 x 4096 cut into 4 and 8 6.5 and 7.2 us, 4096 x 12288 13.7 and 12.0.
 FewPlan few_plan(int64_t m, int64_t cols, int64_t k, bool silu) {
