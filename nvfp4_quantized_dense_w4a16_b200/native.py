@@ -742,9 +742,10 @@ class Norm:
         self._bind(self.__dict__)
 
     def __setattr__(self, name, value):
-        if name not in ("weight", "bias", "kind", "eps", "offset"):
-            raise AttributeError(f"{name} of a Norm cannot be set")
-        self._bind({**self.__dict__, name: value})  # (refuses what does not fit the others)
+        if name in ("hidden", "device_index"):
+            raise AttributeError(f"{name} of a Norm is that of its tensors")
+        if name in ("weight", "bias", "kind", "eps", "offset"):
+            self._bind({**self.__dict__, name: value})  # (refuses what does not fit the others)
         self.__dict__[name] = value
 
     def _bind(self, given):

@@ -65,9 +65,11 @@ def test_attributes_that_are_set_hold_from_the_next_call_on(native):
     n.bias = None
     n.weight = None
     assert bound(native, n, 7)[:2] == (None, None)
-    for name in ("hidden", "weights"):
+    for name in ("hidden", "device_index"):
         with pytest.raises(AttributeError):
             setattr(n, name, 3)
+    n.name = "before the first layer"  # (a caller's own)
+    assert n.name == "before the first layer"
 
 
 def test_a_call_keeps_the_struct_that_it_was_given(native):
