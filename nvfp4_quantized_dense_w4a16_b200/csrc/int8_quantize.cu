@@ -14,11 +14,12 @@ using namespace sm100;
 // A row stays in registers between its largest magnitude and its codes: a group of
 // `threads` threads (a warp or more of a CTA's 256, or the CTA) holds N vectors of 8
 // values each; longer rows are read twice.  Bound by memory traffic, 3 bytes a value,
-// for many rows; by its latency for few.
+// for many rows; by its latency for few.  x is no __restrict__ pointer: the kernel ahead may be
+// writing it while this one starts, which loads of data that never changes do not allow.
 template <int N>
 __global__ void __launch_bounds__(512)
-    int8_quantize_kernel(const uint16_t* __restrict__ x, int64_t m, int64_t k, int64_t stride, int threads,
-                         int8_t* __restrict__ codes, float* __restrict__ scales) {
+    int8_quantize_kernel(const uint16_t* x, int64_t m, int64_t k, int64_t stride, int threads,
+                         int8_t* codes, float* scales) {
   griddep_wait();
   griddep_launch_dependents();
   __shared__ uint32_t part[16];

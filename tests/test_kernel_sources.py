@@ -43,3 +43,9 @@ def test_warps_are_whole_at_aligned_barriers():
     for m in re.finditer(r"cluster_sync\(\);|named_bar_sync\(", kernels):
         before = kernels[:m.start()].rstrip().splitlines()[-1].strip()
         assert before.startswith(("__syncwarp();", "__syncthreads();", "tc_fence")), before
+
+
+def test_rows_that_the_kernel_ahead_writes_are_not_read_only_data():
+    """const __restrict__ lets a load pass the wait for the kernel ahead, and its caches keep what that kernel changes."""
+    for name in ("int8_quantize.cu", "int8_gemv.cu", "int8_tc.cu", "block_norm.cu"):
+        assert "__restrict__" not in code(name), name
