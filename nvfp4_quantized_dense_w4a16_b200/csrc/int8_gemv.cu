@@ -41,6 +41,8 @@ struct GemvArgs {
   bool first;        // (Int8Product::first)
 };
 
+// Past L1, as read-only data: what the kernel ahead of a call's first launch may still write is not read before its end,
+// by nobody on this SM (ordinary loads: 4096 x 4096 6.3 us for 5.3, 24576 x 4096 19.4 for 18.1).
 __device__ __forceinline__ int4 load_weights(const int8_t* p) {
   int4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
