@@ -804,6 +804,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
       bulk_load(to + y_bytes + r_bytes, static_cast<const uint8_t*>(a.gate) + r * a.gate_row_stride * (a.gate_bf16 ? 2 : 4),
                 g_bytes, &bar[s]);
   };
+  // A copy of a row that is given up lands before the CTA leaves.
+  auto landed = [&](int s, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(&bar[s], parity) && clock64() - t0 < kWaitLimitCycles) {
+    }
+  };
   // (rows in 32 bits: of 80 registers none is left, and what is spilled comes back from L2)
   const int m = (int)a.m, first = blockIdx.x + g * gridDim.x, step = gridDim.x * p.groups;
   griddep_wait();
@@ -848,7 +854,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
     // value is 0): these rows are computed in the order of their definition, once the copies have landed.
     if (mine == 0)
       for (int s = 0; s < p.slots && first + s * step < m; ++s)
-        mbar_wait(&bar[s], 0, abort_flag, &g_norm_device_error, 1);
+        if (!mbar_wait(&bar[s], 0, abort_flag, &g_norm_device_error, 1)) landed(s, 0);
     if (__syncthreads_and(*abort_flag == 0)) rows_apart<R>(a, reinterpret_cast<float*>(smem), parts);
     return;
   }
@@ -862,11 +868,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) block_norm_stream_kernel(co
     }
     // The group agrees that the row's copy has landed before it uses any of it: a row that is given up is not stored.
     if (!row.all(mbar_wait(&bar[s], parity, abort_flag, &g_norm_device_error, 1))) {
-      if (mine == 0)  // (the copies in flight land before the CTA leaves)
+      if (mine == 0)
         for (int q = r; q < m && q < r + p.slots * step; q += step) {
-          const long long t0 = clock64();
-          while (!mbar_try_wait(&bar[s], parity) && clock64() - t0 < kWaitLimitCycles) {
-          }
+          landed(s, parity);
           if (++s == p.slots) s = 0, parity ^= 1;
         }
       return;

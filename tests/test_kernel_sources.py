@@ -29,7 +29,7 @@ def test_the_streaming_norm_stores_nothing_of_a_copy_that_has_not_landed():
     wait, use, store = loop.index("mbar_wait("), loop.index("from = ring"), loop.index("residual_out)")
     vote = loop.index("row.all(")
     assert abs(vote - wait) < 20 and wait < use < store
-    assert "return;" in loop[wait:use] and "mbar_try_wait" in loop[wait:use]
+    assert "return;" in loop[wait:use] and "landed(s, parity)" in loop[wait:use]
 
 
 def test_warps_are_whole_at_aligned_barriers():
