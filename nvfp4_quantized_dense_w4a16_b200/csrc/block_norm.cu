@@ -296,17 +296,15 @@ __device__ __forceinline__ void residual_row(Row<WARP>& row, const BlockArgs& a,
     w.load(a.post, a.hidden, at);
     f = norm_factors<LAYER, WARP, N>(row, a.post, a.hidden, v, at);
   }
-  float g1 = 1.0f;  // the row's gate
-  if (a.gate && !a.gate_cols) {
-    g1 = gate_value(load_one(a.gate, a.gate_bf16, r * a.gate_row_stride), a.gate_activation);
-  }
+  float scale = a.branch_scale;  // with the row's gate
+  if (a.gate && !a.gate_cols) scale *= gate_value(load_one(a.gate, a.gate_bf16, r * a.gate_row_stride), a.gate_activation);
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (at(i) < a.hidden) {
       float t[8];
       if (a.post.on) w.apply(a.post, f, i, v[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= a.branch_scale;
+      for (int j = 0; j < 8; ++j) v[i][j] *= scale;
       if (a.gate && a.gate_cols) {
         load_gate(i, t);
         if (a.gate_activation != FFN_GATE_NONE)
@@ -314,9 +312,6 @@ __device__ __forceinline__ void residual_row(Row<WARP>& row, const BlockArgs& a,
           for (int j = 0; j < 8; ++j) t[j] = gate_value(t[j], a.gate_activation);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] *= t[j];
-      } else if (a.gate) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] *= g1;
       }
       load_res(i, t);
 #pragma unroll
